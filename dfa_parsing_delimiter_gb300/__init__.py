@@ -13,6 +13,9 @@ Names follow the C ABI in ``include/pp.h``:
   pp_tags / tags                per-byte state and tag (test hook)
   pp_count_byte / count_byte    byte count (record-capacity bound)
   desc_csv, desc_json_lexer     DFA descriptors
+
+and, from the module lm, the operators at the two ends of a language model:
+vocab_grammar, grammar_states, process_logits, embed, embed_grad.
 """
 from __future__ import annotations
 
@@ -126,6 +129,7 @@ def lib() -> ctypes.CDLL:
         L.pp_debug_parse_tags.argtypes = [_vp, _sz, ctypes.POINTER(DfaDesc), _vp, _vp, _vp]
         L.pp_debug_long_fields.restype = ctypes.c_int
         L.pp_debug_long_fields.argtypes = [ctypes.POINTER(ctypes.c_uint64), ctypes.c_int]
+        lm.declare(L)
         _lib = L
     return _lib
 
@@ -603,3 +607,8 @@ def tokenize_host(h_in: torch.Tensor, desc: DfaDesc | None = None, stream=None):
             out.append(h)
         s.synchronize()
     return tuple(out), st, int(h_in.numel()), int(d2h)
+
+
+from . import lm  # noqa: E402
+from .lm import (Grammar, embed, embed_grad, grammar_states, process_logits,  # noqa: E402,F401
+                 vocab_grammar)

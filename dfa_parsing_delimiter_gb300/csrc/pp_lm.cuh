@@ -1,0 +1,51 @@
+// Shared by the language-model entry points (pp_grammar.cu, pp_logits.cu,
+// pp_embed.cu): element types, id loads and 16-byte packs.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pp.h"
+
+namespace ppl {
+
+constexpr uint64_t MAX_DIM = (uint64_t(1) << 31) - 65536;
+
+inline pp_rc rc_of(cudaError_t e) {
+  if (e == cudaSuccess) return PP_OK;
+  return e == cudaErrorMemoryAllocation ? PP_ENOMEM : PP_ECUDA;
+}
+inline bool ftype_ok(int t) { return t >= PP_F32 && t <= PP_BF16; }
+inline bool itype_ok(int t) { return t >= PP_U8 && t <= PP_I64; }
+inline size_t fsize(int t) { return t == PP_F32 ? 4 : 2; }
+inline size_t isize(int t) { return t == PP_I64 ? 8 : t == PP_I32 ? 4 : 1; }
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// The id at index i as int64.
+__device__ __forceinline__ int64_t load_id(const void* p, int type, uint64_t i) {
+  switch (type) {
+    case PP_U8: return static_cast<const uint8_t*>(p)[i];
+    case PP_I8: return static_cast<const int8_t*>(p)[i];
+    case PP_I32: return static_cast<const int32_t*>(p)[i];
+    default: return static_cast<const int64_t*>(p)[i];
+  }
+}
+
+// N elements moved in accesses of at most 16 bytes (p aligned to that).
+template <class T, int N>
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
+  T v[N];
+};
+
+}  // namespace ppl

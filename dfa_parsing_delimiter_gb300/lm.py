@@ -1,0 +1,318 @@
+"""The operators at the two ends of a language model (pp.h, "language models").
+
+  pp_vocab_grammar / vocab_grammar    a vocabulary under a DFA -> Grammar
+  pp_grammar_states / grammar_states  the DFA's state along token sequences
+  pp_logits / process_logits          penalties, biases and the grammar's mask
+  pp_embed / embed                    rows of a table by id (differentiable)
+  pp_embed_grad / embed_grad          the gradient for the table
+
+Argument marshalling only, as in the rest of the binding: shapes and types
+are checked here, everything is computed by libpp's kernels on the given
+stream (default: the current one).  New outputs belong to that stream; the
+caller orders the use of every tensor on other streams, as with any kernel
+launch.  Arguments that do not fit raise ValueError, errors of the library
+RuntimeError.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import dfa_parsing_delimiter_gb300 as pp
+
+FTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ITYPE = {torch.uint8: 0, torch.int8: 1, torch.int32: 2, torch.int64: 3}
+STATE_NONE = 0xFF
+
+_vp, _sz, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
+
+
+class LogitOpts(ctypes.Structure):
+    """pp_logit_opts."""
+    _fields_ = [("d_history", _vp), ("d_history_row", _vp), ("d_history_len", _vp),
+                ("d_prompt_len", _vp), ("history_rows", _sz), ("history_cols", _sz),
+                ("history_stride", _sz), ("d_repetition", _vp), ("d_presence", _vp),
+                ("d_frequency", _vp), ("d_bias_offsets", _vp), ("d_bias_tokens", _vp),
+                ("d_bias_values", _vp), ("n_bias", _sz), ("d_allowed", _vp),
+                ("allowed_stride", _sz), ("d_state", _vp), ("state_stride", _sz),
+                ("n_states", ctypes.c_int32), ("history_type", ctypes.c_int32)]
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """The entry points' argument types."""
+    sigs = {
+        "pp_vocab_grammar": [_vp, _vp, _sz, _sz, ctypes.POINTER(pp.DfaDesc), _i64, _vp, _vp, _sz, _vp],
+        "pp_grammar_states": [_vp, _sz, _int, _vp, _int, _sz, _sz, _sz, _vp, _vp, _sz,
+                              ctypes.c_uint8, _vp, _sz, _vp],
+        "pp_logits": [_vp, _int, _sz, _sz, _sz, ctypes.POINTER(LogitOpts), _vp, _sz, _vp],
+        "pp_embed": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _vp, _int, _sz, _vp],
+        "pp_embed_grad": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _int, _vp,
+                          _int, _sz, _vp],
+    }
+    for name, args in sigs.items():
+        getattr(L, name).restype = _int
+        getattr(L, name).argtypes = args
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(t: torch.Tensor, like: torch.Tensor, name: str, dtypes, ndim: int) -> None:
+    if t.dtype not in dtypes or t.dim() != ndim or t.device != like.device:
+        raise ValueError(f"{name}: want {ndim} dimensions of {[str(d) for d in dtypes]} on "
+                         f"{like.device}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
+def _vector(t, like, name: str, dtypes, n: int) -> int:
+    """Address of a contiguous vector of at least n elements (None: 0)."""
+    if t is None:
+        return 0
+    _on(t, like, name, dtypes, 1)
+    _need(t.size(0) >= n and (n <= 1 or t.stride(0) == 1), f"{name}: want {n} contiguous elements")
+    return t.data_ptr()
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _matrix_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a matrix with contiguous rows."""
+    _need(t.size(1) <= 1 or t.stride(1) == 1 or not t.numel(), f"{name}: the last dimension has to be contiguous")
+    return t.stride(0)
+
+
+def _call(fn, what: str, like: torch.Tensor, stream, *args) -> None:
+    """One library call on the tensors' device and the stream."""
+    _need(like.is_cuda, f"{what}: want tensors on a GPU, got {like.device}")
+    if like.device.index == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream()
+        rc = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(like.device):
+            s = stream if stream is not None else torch.cuda.current_stream()
+            rc = fn(*args, s.cuda_stream)
+    if rc:
+        pp._check(rc, what)
+
+
+# ------------------------------------------------------------------ grammars
+class Grammar:
+    """A vocabulary under a DFA: `vectors` (int64 [n_vocab], a nibble per
+    state), `allowed` (int32 [n_states, words], a bit per token), and the
+    DFA's `start_state` and `accept_mask`.  vocab_grammar makes one."""
+
+    def __init__(self, vectors: torch.Tensor, allowed: torch.Tensor, n_vocab: int, desc):
+        _on(vectors, allowed, "vectors", (torch.int64,), 1)
+        _on(allowed, allowed, "allowed", (torch.int32,), 2)
+        self.vectors, self.allowed, self.n_vocab = vectors, allowed, int(n_vocab)
+        self.n_states, self.start_state = int(desc.n_states), int(desc.start_state)
+        self.accept_mask = int(desc.accept_mask)
+        _need(vectors.is_contiguous() and vectors.size(0) == self.n_vocab, "vectors: want one a token")
+        _need(allowed.size(0) == self.n_states and allowed.size(1) * 32 >= self.n_vocab
+              and _matrix_stride(allowed, "allowed") >= allowed.size(1), "allowed: want a row a state")
+
+    def accepts(self, states: torch.Tensor) -> torch.Tensor:
+        """Whether texts that end in these states are complete."""
+        s = states.to(torch.int64)
+        return (s < self.n_states) & ((self.accept_mask >> s.clamp(max=31)) & 1).bool()
+
+
+def vocab_grammar(offsets: torch.Tensor, chars: torch.Tensor, desc=None, end_id=None, stream=None) -> Grammar:
+    """pp_vocab_grammar of a string column (int32 offsets and uint8 chars, as
+    pp_parse writes one: token v is chars[offsets[v]:offsets[v + 1]]).
+    end_id: the token that ends a text (None: there is none)."""
+    desc = desc if desc is not None else pp.desc_csv()
+    _on(offsets, chars, "offsets", (torch.int32,), 1)
+    _on(chars, offsets, "chars", (torch.uint8,), 1)
+    _need(offsets.size(0) >= 1 and offsets.is_contiguous() and chars.is_contiguous(),
+          "want contiguous offsets (one more than tokens) and chars")
+    n = offsets.size(0) - 1
+    _need(end_id is None or 0 <= end_id < n, f"end_id: want a token of the {n}, got {end_id}")
+    words = -(-n // 128) * 4
+    vectors = _new((n,), torch.int64, offsets, stream)
+    allowed = _new((int(desc.n_states), words), torch.int32, offsets, stream)
+    _call(pp.lib().pp_vocab_grammar, "pp_vocab_grammar", offsets, stream, offsets.data_ptr(),
+          chars.data_ptr(), chars.size(0), n, ctypes.byref(desc), -1 if end_id is None else int(end_id),
+          vectors.data_ptr(), allowed.data_ptr(), words)
+    return Grammar(vectors, allowed, n, desc)
+
+
+def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=None, out=None,
+                   stream=None) -> torch.Tensor:
+    """pp_grammar_states: uint8 [rows, cols + 1], the state before each token
+    of [rows, cols] token ids and after the last one.  start: uint8 [rows]
+    (for instance an earlier result's last column) or None for the DFA's
+    start state; lengths: int32 [rows], the tokens of each row that count."""
+    _on(tokens, grammar.vectors, "tokens", ITYPE, 2)
+    rows, cols = tokens.shape
+    if out is None:
+        out = _new((rows, cols + 1), torch.uint8, tokens, stream)
+    else:
+        _on(out, tokens, "out", (torch.uint8,), 2)
+        _need(tuple(out.shape) == (rows, cols + 1), f"out: want {(rows, cols + 1)}")
+    ps, ss = 0, 0
+    if start is not None:
+        _on(start, tokens, "start", (torch.uint8,), 1)
+        _need(start.size(0) == rows, f"start: want {rows} states")
+        ps, ss = start.data_ptr(), start.stride(0)
+    if not rows:
+        return out
+    _call(pp.lib().pp_grammar_states, "pp_grammar_states", tokens, stream, grammar.vectors.data_ptr(),
+          grammar.n_vocab, grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype], rows, cols,
+          _matrix_stride(tokens, "tokens"), _vector(lengths, tokens, "lengths", (torch.int32,), rows),
+          ps, ss, grammar.start_state, out.data_ptr(), _matrix_stride(out, "out"))
+    return out
+
+
+# ------------------------------------------------------------------ logits
+def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_len=None, history_row=None,
+                   repetition=None, presence=None, frequency=None, bias=None, grammar=None, states=None,
+                   out=None, stream=None) -> torch.Tensor:
+    """pp_logits of [rows, n_vocab] logits; `out` may be `logits` itself.
+    history: [sequences, cols] token ids, of which row r counts the first
+    history_len[r] of sequence history_row[r] (default: r), the first
+    prompt_len[r] of them as given and the rest as answered.  repetition,
+    presence, frequency: float32 [rows].  bias: (offsets int32 [rows + 1],
+    tokens int32, values float32), an entry list per row.  grammar and states
+    (uint8 [rows]): tokens that the state does not allow become -inf."""
+    _need(logits.dtype in FTYPE and logits.dim() == 2, "logits: want 2 dimensions of float32, float16 or bfloat16")
+    rows, vocab = logits.shape
+    if out is None:
+        out = _new((rows, vocab), logits.dtype, logits, stream)
+    else:
+        _on(out, logits, "out", (logits.dtype,), 2)
+        _need(out.shape == logits.shape, f"out: want {tuple(logits.shape)}")
+    o = LogitOpts()
+    if history is not None:
+        _on(history, logits, "history", ITYPE, 2)
+        o.d_history, o.history_type = history.data_ptr(), ITYPE[history.dtype]
+        o.history_rows, o.history_cols = history.shape
+        o.history_stride = _matrix_stride(history, "history")
+        _need(history_row is not None or o.history_rows >= rows, "history: want a row for each row of logits")
+        ints = (torch.int32,)
+        o.d_history_row = _vector(history_row, logits, "history_row", ints, rows)
+        o.d_history_len = _vector(history_len, logits, "history_len", ints, rows)
+        o.d_prompt_len = _vector(prompt_len, logits, "prompt_len", ints, rows)
+        floats = (torch.float32,)
+        o.d_repetition = _vector(repetition, logits, "repetition", floats, rows)
+        o.d_presence = _vector(presence, logits, "presence", floats, rows)
+        o.d_frequency = _vector(frequency, logits, "frequency", floats, rows)
+    else:
+        _need(repetition is None and presence is None and frequency is None, "penalties need a history")
+    if bias is not None:
+        at, tokens, values = bias
+        o.n_bias = tokens.size(0)
+        _need(values.size(0) == o.n_bias, "bias: want as many values as tokens")
+        o.d_bias_offsets = _vector(at, logits, "bias offsets", (torch.int32,), rows + 1)
+        o.d_bias_tokens = _vector(tokens, logits, "bias tokens", (torch.int32,), o.n_bias)
+        o.d_bias_values = _vector(values, logits, "bias values", (torch.float32,), o.n_bias)
+    _need((grammar is None) == (states is None), "a grammar needs states, and states a grammar")
+    if grammar is not None:
+        _on(states, logits, "states", (torch.uint8,), 1)
+        _need(states.size(0) == rows, f"states: want {rows}")
+        _need(grammar.n_vocab == vocab, f"the grammar has {grammar.n_vocab} tokens, the logits {vocab}")
+        _on(grammar.allowed, logits, "allowed", (torch.int32,), 2)
+        o.d_allowed, o.allowed_stride = grammar.allowed.data_ptr(), grammar.allowed.stride(0)
+        o.d_state, o.state_stride, o.n_states = states.data_ptr(), states.stride(0), grammar.n_states
+    if rows and vocab:
+        _call(pp.lib().pp_logits, "pp_logits", logits, stream, logits.data_ptr(), FTYPE[logits.dtype],
+              rows, vocab, _matrix_stride(logits, "logits"), ctypes.byref(o), out.data_ptr(),
+              _matrix_stride(out, "out"))
+    return out
+
+
+# ------------------------------------------------------------------ embedding
+def _flat_ids(ids: torch.Tensor) -> tuple[int, int]:
+    """(number of ids, their stride) of ids that lie at one stride."""
+    _need(ids.dtype in ITYPE, f"ids: want uint8, int8, int32 or int64, got {ids.dtype}")
+    n = ids.numel()
+    if ids.is_contiguous():
+        return n, 1
+    stride, want = None, 0
+    for size, step in zip(reversed(ids.shape), reversed(ids.stride())):
+        if size == 1:
+            continue
+        if stride is None:
+            stride, want = step, step
+        _need(step == want, "ids: want one stride over all dimensions")
+        want = step * size
+    return n, 1 if stride is None else stride
+
+
+def _embed(ids, table, scale, padding_id, out, dtype, stream) -> torch.Tensor:
+    n, stride = _flat_ids(ids)
+    _on(table, ids, "table", FTYPE, 2)
+    vocab, dim = table.shape
+    shape = (*ids.shape, dim)
+    if out is None:
+        out = _new(shape, dtype if dtype is not None else table.dtype, ids, stream)
+    else:
+        _need(out.dtype in FTYPE and out.device == ids.device and out.shape == shape and
+              out.is_contiguous() and dtype in (None, out.dtype), f"out: want contiguous {shape}")
+    _need(out.dtype in FTYPE, f"dtype: want float32, float16 or bfloat16, got {out.dtype}")
+    if n and dim:
+        _call(pp.lib().pp_embed, "pp_embed", ids, stream, ids.data_ptr(), ITYPE[ids.dtype], stride, n,
+              table.data_ptr(), FTYPE[table.dtype], vocab, dim, _matrix_stride(table, "table"), scale,
+              -1 if padding_id is None else padding_id, out.data_ptr(), FTYPE[out.dtype], dim)
+    return out
+
+
+class _Embed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, ids, scale, padding_id, dtype, stream):
+        ctx.save_for_backward(ids)
+        ctx.rest = (table.size(0), scale, padding_id, table.dtype)
+        return _embed(ids, table, scale, padding_id, None, dtype, stream)
+
+    @staticmethod
+    def backward(ctx, grad):
+        vocab, scale, padding_id, dtype = ctx.rest
+        if grad.stride(-1) != 1:
+            grad = grad.contiguous()
+        return embed_grad(ctx.saved_tensors[0], grad, vocab, scale, padding_id, dtype=dtype), *[None] * 5
+
+
+def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, padding_id=None, out=None, dtype=None,
+          stream=None) -> torch.Tensor:
+    """pp_embed: scale * table[ids], [*ids.shape, dim] in `dtype` (default:
+    the table's).  ids: integers of any shape at one stride; padding_id and
+    ids outside the table give zeros.  A table that requires a gradient gets
+    it through embed_grad (then without `out`)."""
+    if table.requires_grad and torch.is_grad_enabled():
+        _need(out is None, "out: not for a table that requires a gradient")
+        return _Embed.apply(table, ids, scale, padding_id, dtype, stream)
+    return _embed(ids, table, scale, padding_id, out, dtype, stream)
+
+
+def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float = 1.0, padding_id=None,
+               out=None, accumulate: bool = False, dtype=None, stream=None) -> torch.Tensor:
+    """pp_embed_grad: [n_vocab, dim], the gradient of embed's table from that
+    of its result ([*ids.shape, dim]), in `dtype` (default: the gradient's).
+    With accumulate it is added to `out`; else `out` is overwritten."""
+    n, stride = _flat_ids(ids)
+    _need(grad.dtype in FTYPE and grad.device == ids.device and grad.dim() == ids.dim() + 1
+          and grad.shape[:-1] == ids.shape, f"grad: want {tuple(ids.shape)} and a last dimension, got {tuple(grad.shape)}")
+    dim = grad.size(-1)
+    if grad.dim() != 2:
+        grad = grad.reshape(n, dim)
+    if out is None:
+        _need(not accumulate, "accumulate: needs an out")
+        out = _new((n_vocab, dim), dtype if dtype is not None else grad.dtype, ids, stream)
+    else:
+        _on(out, ids, "out", FTYPE, 2)
+        _need(tuple(out.shape) == (n_vocab, dim) and dtype in (None, out.dtype), f"out: want {(n_vocab, dim)}")
+    _need(out.dtype in FTYPE, f"dtype: want float32, float16 or bfloat16, got {out.dtype}")
+    if n_vocab and dim:
+        _call(pp.lib().pp_embed_grad, "pp_embed_grad", ids, stream, ids.data_ptr(), ITYPE[ids.dtype],
+              stride, n, grad.data_ptr(), FTYPE[grad.dtype], _matrix_stride(grad, "grad"), n_vocab, dim,
+              scale, -1 if padding_id is None else padding_id, int(bool(accumulate)), out.data_ptr(),
+              FTYPE[out.dtype], _matrix_stride(out, "out"))
+    return out

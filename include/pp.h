@@ -534,6 +534,171 @@ pp_rc pp_debug_parse_tags(const uint8_t* d_in, size_t n_bytes, const pp_dfa_desc
  * Synchronous (waits for the device).  Returns PP_ECUDA on a CUDA error. */
 pp_rc pp_debug_long_fields(uint64_t* out, int reset);
 
+/* ------------------------------------------------------ language models
+ * The same DFAs at the two ends of a language model: what it answers with
+ * is held to a pp_dfa_desc while it is sampled (pp_vocab_grammar,
+ * pp_grammar_states, pp_logits), and the id columns that pp_parse writes, or
+ * token ids, become vectors (pp_embed, pp_embed_grad).  The conventions at
+ * the top of this file hold, except that these entry points have no
+ * pp_status: every value of every input has a defined result, stated below.
+ * Tensors are element arrays of the types below at their natural alignment;
+ * strides count elements and the innermost dimension is contiguous unless a
+ * stride for it is given. */
+typedef enum { PP_F32 = 0, PP_F16 = 1, PP_BF16 = 2 } pp_ftype; /* values, weights */
+typedef enum { PP_U8 = 0, PP_I8 = 1, PP_I32 = 2, PP_I64 = 3 } pp_itype; /* ids, tokens */
+
+/* The state of a token sequence that left the vocabulary (a token outside
+ * 0..n_vocab-1): it allows nothing and is never left. */
+#define PP_STATE_NONE 0xFF
+
+/*
+ * pp_vocab_grammar — a vocabulary under a DFA: what each token does to each
+ * state, and which tokens each state allows.
+ *   d_offsets, d_chars  device; the vocabulary as a string column (int32
+ *                   offsets[n_vocab + 1] into chars_len bytes, as pp_parse
+ *                   writes one).  A token whose range is not inside the
+ *                   chars counts as empty.
+ *   dfa             host; any descriptor over bytes (PP_ENC_BYTES).
+ *   end_token       the token that ends a text, or -1: allowed in the
+ *                   accepting states only and changing no state, whatever
+ *                   its bytes.
+ *   d_vectors       device uint64[n_vocab]: the token's state-transition
+ *                   vector (ParPaRaw Section 3.1); nibble s = the state
+ *                   that state s reaches over the token's bytes.  Nibbles of
+ *                   states the DFA does not have hold s.
+ *   d_allowed       device uint32[n_states][allowed_stride]; bit v % 32 of
+ *                   word v / 32 of row s: state s allows token v, that is v
+ *                   has bytes, and an accepting state can still be reached,
+ *                   by some bytes and not through the invalid state, from
+ *                   the one that v leads to.  Bits past n_vocab are 0 up to
+ *                   the next multiple of 256 tokens or the stride; words
+ *                   past both are not written.
+ *   allowed_stride  words per row, at least ceil(n_vocab / 32).
+ * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n_vocab of 2^31 -
+ * 65536 or more, PP_ECUDA on CUDA errors.  No scratch.
+ */
+pp_rc pp_vocab_grammar(const int32_t* d_offsets, const uint8_t* d_chars, size_t chars_len,
+                       size_t n_vocab, const pp_dfa_desc* dfa, int64_t end_token,
+                       uint64_t* d_vectors, uint32_t* d_allowed, size_t allowed_stride,
+                       cudaStream_t stream);
+
+/*
+ * pp_grammar_states — the DFA's state along token sequences: a scan with
+ * the composite operation over the tokens' vectors.
+ *   d_vectors       device uint64[n_vocab], from pp_vocab_grammar.
+ *   d_tokens        device [n_rows][tokens_stride], n_cols tokens a row.
+ *   d_lengths       device int32[n_rows], or NULL: tokens of each row (cut
+ *                   to 0..n_cols); the state does not change after them.
+ *   d_start         device uint8[n_rows], start_stride elements apart, or
+ *                   NULL: each row's first state; NULL: start_state.  A state
+ *                   of n_states or more counts as PP_STATE_NONE.
+ *   d_states        device uint8[n_rows][states_stride], n_cols + 1 a row:
+ *                   the state before each token, and after the last one.
+ * d_start may be a column of d_states' own earlier output, but not overlap
+ * d_states.  Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n_rows,
+ * n_cols or n_vocab of 2^31 - 65536 or more, PP_ECUDA on CUDA errors.  No scratch.
+ */
+pp_rc pp_grammar_states(const uint64_t* d_vectors, size_t n_vocab, int n_states,
+                        const void* d_tokens, pp_itype token_type, size_t n_rows, size_t n_cols,
+                        size_t tokens_stride, const int32_t* d_lengths, const uint8_t* d_start,
+                        size_t start_stride, uint8_t start_state, uint8_t* d_states,
+                        size_t states_stride, cudaStream_t stream);
+
+/* pp_logits options; every pointer may be NULL (device memory). */
+typedef struct {
+  /* what was said so far: row r's history is row history_row[r] of
+   * d_history (row r without a list), its first history_len[r] tokens
+   * (without a list history_cols), of which the first prompt_len[r]
+   * (0 without a list) were given and the others answered.  Lengths are cut
+   * to 0..history_cols; a history row outside 0..history_rows-1 counts as
+   * empty, and tokens outside the vocabulary count for nothing. */
+  const void* d_history;
+  const int32_t* d_history_row;
+  const int32_t* d_history_len;
+  const int32_t* d_prompt_len;
+  size_t history_rows, history_cols, history_stride;
+  /* float[n_rows] each: */
+  const float* d_repetition; /* NULL: 1 */
+  const float* d_presence;   /* NULL: 0 */
+  const float* d_frequency;  /* NULL: 0 */
+  /* biases: entries bias_offsets[r] .. bias_offsets[r + 1] - 1 (cut to
+   * 0..n_bias) of row r; of several for one token the last counts. */
+  const int32_t* d_bias_offsets;
+  const int32_t* d_bias_tokens;
+  const float* d_bias_values;
+  size_t n_bias;
+  /* the grammar: rows of pp_vocab_grammar's d_allowed, and each row's state
+   * (state_stride elements apart); a state of n_states or more allows
+   * nothing. */
+  const uint32_t* d_allowed;
+  size_t allowed_stride;
+  const uint8_t* d_state;
+  size_t state_stride;
+  int32_t n_states;
+  int32_t history_type; /* pp_itype of d_history */
+} pp_logit_opts;
+
+/*
+ * pp_logits — a model's logits under penalties, biases and a grammar, in
+ * one pass.  For every row r and token v, in 32 bits and in this order:
+ *   x = in[r][v]
+ *   x = x > 0 ? x / repetition : x * repetition   if v is in the history
+ *   x = x - frequency * answered(v) - (answered(v) > 0 ? presence : 0)
+ *   x = x + bias                                  if v has one
+ *   x = -infinity                                 if the grammar does not
+ *                                                 allow v (whatever x is)
+ * where answered(v) counts v in the answered part of the history; then one
+ * rounding to the type.  A row whose state allows nothing is all -infinity.
+ *   d_in, d_out     device [n_rows][stride], n_vocab values a row; d_out may
+ *                   be d_in (with the same stride), but not overlap it
+ *                   otherwise.
+ * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n_vocab or
+ * history_cols of 2^31 - 65536 or more, or more rows than the grid holds,
+ * PP_ECUDA on CUDA errors.  No scratch.
+ */
+pp_rc pp_logits(const void* d_in, pp_ftype type, size_t n_rows, size_t n_vocab, size_t in_stride,
+                const pp_logit_opts* opts, void* d_out, size_t out_stride, cudaStream_t stream);
+
+/*
+ * pp_embed — rows of a table by id: out[i] = scale * table[ids[i]], in 32
+ * bits and rounded once.  An id equal to padding_id (-1 or any id outside
+ * the table: none) or outside 0..n_vocab-1 gives a row of zeros.
+ *   d_ids           device, n ids, id_stride elements apart (0: one for
+ *                   all); any column type of pp_parse that holds integers,
+ *                   or bytes.
+ *   d_table         device [n_vocab][table_stride], dim values a row.
+ *   d_out           device [n][out_stride]; must not overlap the table.
+ * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for sizes of
+ * 2^31 - 65536 or more, PP_ECUDA on CUDA errors.  No scratch.
+ */
+pp_rc pp_embed(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
+               const void* d_table, pp_ftype table_type, size_t n_vocab, size_t dim,
+               size_t table_stride, float scale, int64_t padding_id, void* d_out,
+               pp_ftype out_type, size_t out_stride, cudaStream_t stream);
+
+/*
+ * pp_embed_grad — the gradient of pp_embed for its table: out[v] = scale *
+ * the sum of grad[i] over the i with ids[i] = v, for v other than
+ * padding_id.  The positions are sorted by id (stable), and each id's rows
+ * are summed in 32 bits in an order that depends on ids alone, so the same
+ * inputs give the same bits.
+ *   d_grad          device [n][grad_stride] (stride 0: one row for all).
+ *   d_out           device [n_vocab][out_stride]; every row is written.  With
+ *                   accumulate != 0 the sums are added to what is there, in
+ *                   32 bits and rounded once, and only rows of ids that
+ *                   occur are touched.
+ * Scratch (stream-ordered): 16 bytes an id, 1 KiB or 2 KiB of counters per
+ * 4096 ids, and for ids with long runs partial sums of up to dim * n / 8
+ * bytes; the device's default memory pool is set to keep it (release
+ * threshold: unlimited), so later calls reuse it.
+ * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n or n_vocab of 2^31
+ * - 65536 or a dim of 2^27 - 2048 or more, PP_ENOMEM / PP_ECUDA on CUDA errors.
+ */
+pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
+                    const void* d_grad, pp_ftype grad_type, size_t grad_stride, size_t n_vocab,
+                    size_t dim, float scale, int64_t padding_id, int accumulate, void* d_out,
+                    pp_ftype out_type, size_t out_stride, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
