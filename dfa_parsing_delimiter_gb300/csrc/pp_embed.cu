@@ -8,6 +8,9 @@
 // run of equal ids in registers and writes the sum once.  A run that ends by
 // the end of the next chunk is finished by the chunk it begins in; a longer
 // one leaves a partial sum per chunk, added up in order by a last kernel.
+// Up to SORT_CAP positions one thread-block cluster sorts in distributed
+// shared memory, while the other blocks of the same launch write the zeros
+// of the rows that no id names; more go through global memory in passes.
 #include <algorithm>
 #include <cstring>
 
@@ -115,10 +118,11 @@ struct SortArgs {
   int shift;
 };
 
-__device__ __forceinline__ uint32_t sort_key(const SortArgs& p, uint64_t i) {
-  if (!p.ids) return p.key_in[i];
-  const int64_t id = load_id(p.ids, p.type, i * p.id_stride);
+__device__ __forceinline__ uint32_t key_of(const SortArgs& p, int64_t id) {
   return id >= 0 && id < p.n_vocab && id != p.pad ? uint32_t(id) : p.n_vocab;
+}
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& p, uint64_t i) {
+  return p.ids ? key_of(p, load_id(p.ids, p.type, i * p.id_stride)) : p.key_in[i];
 }
 
 __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_constant__ SortArgs p) {
@@ -208,23 +212,240 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_move_kernel(const __grid_co
     }
 }
 
+// ------------------------------------------------------------ zero rows
+struct ZeroArgs {
+  void* out;
+  uint64_t row_bytes, stride_bytes;  // of a row of the gradient
+  uint32_t n_vocab;
+  int32_t wide;       // rows in whole 16-byte pieces
+  int32_t elem_size;  // otherwise: 2 or 4
+};
+
+// Rows base + i, i < span, whose bit is clear become zeros; every thread of
+// the block takes part.
+template <int THREADS>
+__device__ void zero_rows(const ZeroArgs& z, const uint32_t* bits, uint64_t base, uint32_t span) {
+  const uint32_t units = uint32_t(z.wide ? z.row_bytes / 16 : z.row_bytes / z.elem_size);
+  uint32_t per = 1;  // threads a row
+  while (per < THREADS && per < units) per *= 2;
+  const uint32_t me = threadIdx.x % per;
+  for (uint32_t i = threadIdx.x / per; i < span; i += THREADS / per) {
+    if (bits[i / 32] >> (i % 32) & 1) continue;
+    char* row = static_cast<char*>(z.out) + (base + i) * z.stride_bytes;
+    if (z.wide)
+      for (uint32_t u = me; u < units; u += per) reinterpret_cast<uint4*>(row)[u] = make_uint4(0, 0, 0, 0);
+    else if (z.elem_size == 4)
+      for (uint32_t u = me; u < units; u += per) reinterpret_cast<uint32_t*>(row)[u] = 0;
+    else
+      for (uint32_t u = me; u < units; u += per) reinterpret_cast<uint16_t*>(row)[u] = 0;
+  }
+}
+
+// From a sorted list: a thread looks for each of ZERO_SPAN rows.
+constexpr int ZERO_SPAN = 256;
+__global__ void __launch_bounds__(256)
+zero_kernel(const __grid_constant__ ZeroArgs z, const uint32_t* key, uint32_t n) {
+  __shared__ uint32_t bits[ZERO_SPAN / 32];
+  const uint64_t base = uint64_t(blockIdx.x) * ZERO_SPAN, v = base + threadIdx.x;
+  uint32_t lo = 0, hi = n;  // the first index whose key is v or more
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (key[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  const uint32_t word = __ballot_sync(FULL, lo < n && key[lo] == v);
+  if ((threadIdx.x & 31) == 0) bits[threadIdx.x / 32] = word;
+  __syncthreads();
+  zero_rows<256>(z, bits, base, uint32_t(min(uint64_t(ZERO_SPAN), z.n_vocab - base)));
+}
+
+// ------------------------------------------------- sort in one cluster
+// Block r of the cluster holds pairs r PER .. (r + 1) PER - 1 of the list,
+// PER = 1024 ITEMS.  Per pass a block ranks its pairs' digits (per warp by
+// ballots, in order), tells every block its digit totals, and after a
+// cluster barrier each pair goes straight to its place in the shared memory
+// of the block that owns it (the last pass: to global memory).
+constexpr int CS_THREADS = 1024, CS_WARPS = 32, CS_BITS = 9, CS_BINS = 1 << CS_BITS;
+constexpr int CS_BLOCKS = 16, CS_ITEMS = 8;
+constexpr uint32_t SORT_CAP = CS_THREADS * CS_ITEMS * CS_BLOCKS;
+constexpr uint32_t CS_SPAN = 1u << 18;  // rows that a zeroing block looks at together
+
+struct ClusterArgs {
+  SortArgs s;  // key_out, pos_out: the sorted list
+  int32_t blocks, bits, passes;
+  uint32_t* n_long;  // set to 0 for the sums
+  int32_t zero;      // write the rows that no id names
+  ZeroArgs z;
+};
+
+__device__ __forceinline__ uint32_t smem_of(const void* p, uint32_t rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+// The kernels of one pp_embed_grad follow each other by programmatic
+// dependent launch: each lets the next one's blocks start, and waits for
+// the end of the one before it here, before it reads what that one wrote.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(CS_THREADS, 1) cluster_sort_kernel(const __grid_constant__ ClusterArgs p) {
+  constexpr uint32_t PER = CS_THREADS * ITEMS;
+  extern __shared__ uint2 item[];  // [PER], then the arrays below
+  uint32_t* totals = reinterpret_cast<uint32_t*>(item + PER);                  // [CS_BLOCKS][CS_BINS]
+  uint16_t* place = reinterpret_cast<uint16_t*>(totals + CS_BLOCKS * CS_BINS);  // [CS_WARPS][CS_BINS]
+  __shared__ uint32_t start[CS_BINS];
+  __shared__ uint32_t sums[CS_BINS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  let_next_start();
+  if (blockIdx.x >= uint32_t(p.blocks)) {  // zeros
+    uint32_t* bits = reinterpret_cast<uint32_t*>(item);
+    const uint64_t each = (p.z.n_vocab + gridDim.x - p.blocks - 1) / (gridDim.x - p.blocks);
+    const uint64_t v0 = (blockIdx.x - p.blocks) * each, v1 = min(v0 + each, uint64_t(p.z.n_vocab));
+    for (uint64_t base = v0; base < v1; base += CS_SPAN) {
+      const uint32_t span = uint32_t(min(uint64_t(CS_SPAN), v1 - base));
+      for (uint32_t w = threadIdx.x; w * 32 < span; w += CS_THREADS) bits[w] = 0;
+      __syncthreads();
+      // from a place of its own on, as blocks that read the same ids at the
+      // same time wait for the same lines
+      const uint32_t turn = uint32_t(uint64_t(p.s.n) * blockIdx.x / gridDim.x);
+      auto mark = [&](uint32_t, auto id) {
+        // an id below 0 turns into one far past the span
+        const uint64_t j = sizeof(id) == 8 ? uint64_t(id) - base : uint32_t(id) - uint32_t(base);
+        if (j < span) atomicOr(&bits[j / 32], 1u << (j % 32));
+      };
+      ppl::for_ids<8>(p.s.ids, p.s.type, p.s.id_stride, turn + threadIdx.x, p.s.n, CS_THREADS, mark);
+      ppl::for_ids<8>(p.s.ids, p.s.type, p.s.id_stride, threadIdx.x, turn, CS_THREADS, mark);
+      __syncthreads();
+      const uint64_t pad = uint64_t(p.s.pad) - base;  // has no gradient, so its row is zeros
+      if (pad < span && threadIdx.x == 0) bits[pad / 32] &= ~(1u << (pad % 32));
+      __syncthreads();
+      zero_rows<CS_THREADS>(p.z, bits, base, span);
+      __syncthreads();
+    }
+    return;
+  }
+  const uint32_t rank = blockIdx.x, n_bins = 1u << p.bits;
+  if (rank == 0 && threadIdx.x == 0) *p.n_long = 0;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    for (uint32_t k = threadIdx.x; k < CS_WARPS * CS_BINS / 2; k += CS_THREADS)
+      reinterpret_cast<uint32_t*>(place)[k] = 0;
+    uint2 it[ITEMS];
+    uint16_t nth[ITEMS];
+    const uint32_t i0 = warp * (32 * ITEMS) + lane;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)  // past the list's end: after everything else
+      it[k] = pass ? item[i0 + k * 32] : make_uint2(p.s.n_vocab, rank * PER + i0 + k * 32);
+    if (!pass) {
+      auto read = [&](auto* ids) {
+        int64_t id[ITEMS];
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) id[k] = it[k].y < p.s.n ? int64_t(ids[it[k].y * p.s.id_stride]) : -1;
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) it[k].x = key_of(p.s, id[k]);
+      };
+      switch (p.s.type) {
+        case PP_U8: read(static_cast<const uint8_t*>(p.s.ids)); break;
+        case PP_I8: read(static_cast<const int8_t*>(p.s.ids)); break;
+        case PP_I32: read(static_cast<const int32_t*>(p.s.ids)); break;
+        default: read(static_cast<const int64_t*>(p.s.ids)); break;
+      }
+    }
+    __syncthreads();
+    uint16_t* mine = place + warp * CS_BINS;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const uint32_t d = it[k].x >> shift & (n_bins - 1);
+      uint32_t same = FULL;
+      for (int b = 0; b < p.bits; ++b) {
+        const uint32_t set = __ballot_sync(FULL, d >> b & 1);
+        same &= d >> b & 1 ? set : ~set;
+      }
+      const uint32_t before = mine[d], below = __popc(same & ((1u << lane) - 1));
+      nth[k] = uint16_t(before + below);
+      __syncwarp();
+      if (below == 0) mine[d] = uint16_t(before + __popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    if (threadIdx.x < n_bins) {  // the warps' counts to places within the block
+      uint32_t run = 0;
+#pragma unroll 8
+      for (int w = 0; w < CS_WARPS; ++w) {
+        const uint32_t c = place[w * CS_BINS + threadIdx.x];
+        place[w * CS_BINS + threadIdx.x] = uint16_t(run);
+        run += c;
+      }
+      for (int q = 0; q < p.blocks; ++q)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(smem_of(&totals[rank * CS_BINS + threadIdx.x], q)), "r"(run) : "memory");
+    }
+    cluster_sync();
+    uint32_t all = 0, before = 0, inc = 0;
+    if (threadIdx.x < CS_BINS) {
+      if (threadIdx.x < n_bins)
+        for (int q = 0; q < p.blocks; ++q) {
+          const uint32_t c = totals[q * CS_BINS + threadIdx.x];
+          if (q < int(rank)) before += c;
+          all += c;
+        }
+      inc = all;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const uint32_t up = __shfl_up_sync(FULL, inc, d);
+        if (lane >= d) inc += up;
+      }
+      if (lane == 31) sums[warp] = inc;
+    }
+    __syncthreads();
+    if (threadIdx.x < CS_BINS) {
+      for (int w = 0; w < warp; ++w) before += sums[w];
+      start[threadIdx.x] = before + inc - all;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const uint32_t d = it[k].x >> shift & (n_bins - 1);
+      const uint32_t to = start[d] + mine[d] + nth[k];
+      if (pass + 1 < p.passes) {
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(smem_of(&item[to % PER], to / PER)), "r"(it[k].x), "r"(it[k].y) : "memory");
+      } else if (to < p.s.n) {
+        p.s.key_out[to] = it[k].x;
+        p.s.pos_out[to] = it[k].y;
+      }
+    }
+    if (pass + 1 < p.passes) cluster_sync();
+  }
+}
+
+constexpr size_t cluster_smem(int items) {
+  return size_t(CS_THREADS) * items * 8 + CS_BLOCKS * CS_BINS * 4 + CS_WARPS * CS_BINS * 2;
+}
+
 // ------------------------------------------------------------ sums of runs
 struct SumArgs {
   const uint32_t *key, *pos;  // sorted by (key, position)
   uint32_t n, n_vocab;
   const void* grad;
   uint64_t gstride;
-  uint32_t dim;
+  uint32_t dim, slices;  // columns, and groups of SUM_COLS of them
   float scale;
   int32_t accumulate;
   void* out;
   uint64_t ostride;
-  float* part;  // [n_chunks][2][dim]: sums of a chunk's first and last run
+  float* part;  // [n_chunks][2][width]: sums of a chunk's first and last run
+  uint64_t width;
   uint32_t n_chunks, chunk;
+  uint32_t *n_long, *longs;  // chunks in which long runs begin
 };
 
 constexpr int SUM_WARPS = 8;
 constexpr int SUM_COLS = 32 * UNIT;  // columns a warp
+constexpr uint32_t NO_KEY = 0xFFFFFFFFu;
 
 // Columns of a warp: a lane has 8 consecutive ones (aligned rows) or every
 // 32nd one (any rows).
@@ -235,14 +456,12 @@ __device__ __forceinline__ uint64_t col_of(uint64_t c0, int k) {
 }
 
 template <class T, bool WIDE>
-__device__ __forceinline__ void load_row(const T* row, uint64_t c0, uint32_t dim, float (&x)[UNIT]) {
+__device__ __forceinline__ void load_row(const T* row, uint64_t c0, uint32_t dim, Pack<T, UNIT>& x) {
   if (WIDE && col_of<WIDE>(c0, UNIT) <= dim) {
-    const Pack<T, UNIT> v = *reinterpret_cast<const Pack<T, UNIT>*>(row + col_of<WIDE>(c0, 0));
-#pragma unroll
-    for (int k = 0; k < UNIT; ++k) x[k] = to_f(v.v[k]);
+    x = *reinterpret_cast<const Pack<T, UNIT>*>(row + col_of<WIDE>(c0, 0));
   } else {
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) x[k] = col_of<WIDE>(c0, k) < dim ? to_f(row[col_of<WIDE>(c0, k)]) : 0.f;
+    for (int k = 0; k < UNIT; ++k) x.v[k] = col_of<WIDE>(c0, k) < dim ? row[col_of<WIDE>(c0, k)] : from_f<T>(0.f);
   }
 }
 
@@ -266,101 +485,180 @@ __device__ __forceinline__ void write_sum(const SumArgs& p, uint32_t id, uint64_
 #pragma unroll
   for (int k = 0; k < UNIT; ++k) a[k] *= p.scale;
   if (p.accumulate) {
-    float old[UNIT];
+    Pack<O, UNIT> old;
     load_row<O, WIDE>(row, c0, p.dim, old);
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) a[k] += old[k];
+    for (int k = 0; k < UNIT; ++k) a[k] += to_f(old.v[k]);
   }
   store_row<O, WIDE>(row, c0, p.dim, a);
 }
 
-// Of the sorted list, chunk c holds [c L, (c + 1) L).  A run is long if it
-// begins in chunk c and goes on past the end of chunk c + 1.
-struct Runs {
-  const uint32_t* key;
-  uint64_t n, L;
-  // whether the run that holds index i (the first of chunk c > 0) began
-  // before it
-  __device__ bool goes_on(uint64_t c) const { return c > 0 && c * L < n && key[c * L - 1] == key[c * L]; }
-  // whether the run that crosses from chunk c - 1 into chunk c is long
-  __device__ bool long_into(uint64_t c) const {
-    const uint32_t id = key[c * L];
-    if (c >= 2 && key[(c - 1) * L - 1] == id) return true;          // began before chunk c - 1
-    return (c + 1) * L < n && key[(c + 1) * L] == id;               // passes the end of chunk c
-  }
-};
+// 16 (or 4) bytes from global to shared memory, asynchronously.
+template <int N>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(a), "l"(from) : "memory");
+}
 
+// A lane's columns of a row into its own place in shared memory: lane l's
+// piece g of 16 bytes at [g][l] (aligned rows), its element k at [k][l].
+template <class T, bool WIDE>
+__device__ __forceinline__ void stage_row(T* at, const T* row, uint64_t c0, uint32_t dim) {
+  const int lane = threadIdx.x & 31;
+  constexpr int EACH = 16 / sizeof(T);  // elements a piece
+  if (WIDE && col_of<WIDE>(c0, UNIT) <= dim) {
+#pragma unroll
+    for (int g = 0; g < UNIT / EACH; ++g)
+      copy_async<16>(at + (g * 32 + lane) * EACH, row + col_of<WIDE>(c0, g * EACH));
+  } else {
+#pragma unroll
+    for (int k = 0; k < UNIT; ++k) {
+      T* to = WIDE ? at + (k / EACH * 32 + lane) * EACH + k % EACH : at + k * 32 + lane;
+      const uint64_t c = col_of<WIDE>(c0, k);
+      if (c >= dim) *to = from_f<T>(0.f);
+      else if (sizeof(T) == 4) copy_async<4>(to, row + c);
+      else *to = row[c];
+    }
+  }
+}
+template <class T, bool WIDE>
+__device__ __forceinline__ void add_staged(const T* at, float (&a)[UNIT]) {
+  const int lane = threadIdx.x & 31;
+  constexpr int EACH = 16 / sizeof(T);
+  if (WIDE) {
+#pragma unroll
+    for (int g = 0; g < UNIT / EACH; ++g) {
+      const Pack<T, EACH> x = *reinterpret_cast<const Pack<T, EACH>*>(at + (g * 32 + lane) * EACH);
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) a[g * EACH + k] += to_f(x.v[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < UNIT; ++k) a[k] += to_f(at[k * 32 + lane]);
+  }
+}
+
+// Of the sorted list, chunk c holds [c L, (c + 1) L), L <= 32.  A run is long
+// if it begins in chunk c and goes on past the end of chunk c + 1.  A warp
+// per chunk and SUM_COLS columns; the chunk's keys and the next one's are in
+// its lanes, and 4 KiB of rows are on their way in a ring in shared memory
+// (a lane reads back what it copied itself, so nothing synchronises).
+constexpr int RING_BYTES = 4096;  // a warp
 template <class T, class O, bool WIDE>
 __global__ void __launch_bounds__(SUM_WARPS * 32) sum_kernel(const __grid_constant__ SumArgs p) {
-  const uint64_t c = blockIdx.x;
-  const uint64_t c0 = (uint64_t(blockIdx.y) * SUM_WARPS + threadIdx.x / 32) * SUM_COLS;
-  if (c0 >= p.dim) return;
-  const Runs runs = {p.key, p.n, p.chunk};
-  const uint64_t L = p.chunk, lo = c * L, hi = min(lo + L, uint64_t(p.n));
+  constexpr uint32_t DEPTH = RING_BYTES / (SUM_COLS * sizeof(T));  // rows: 8, of 32-bit values 4
+  __shared__ __align__(16) char ring_mem[SUM_WARPS][RING_BYTES];
+  const int lane = threadIdx.x & 31;
+  const uint64_t me = uint64_t(blockIdx.x) * SUM_WARPS + threadIdx.x / 32;
+  const uint64_t c = me / p.slices, c0 = me % p.slices * SUM_COLS;
+  let_next_start();
+  wait_for_previous();
+  if (c >= p.n_chunks) return;
+  const uint32_t L = p.chunk, n = p.n;
+  const uint32_t lo = uint32_t(c) * L, size = min(L, n - lo);
+  const bool in0 = uint32_t(lane) < size, in1 = uint32_t(lane) < L && uint64_t(lo) + L + lane < n;
+  const uint32_t key0 = in0 ? p.key[lo + lane] : NO_KEY, key1 = in1 ? p.key[lo + L + lane] : NO_KEY;
+  const uint32_t pos0 = in0 ? p.pos[lo + lane] : 0, pos1 = in1 ? p.pos[lo + L + lane] : 0;
+  const uint32_t prev = lo ? p.key[lo - 1] : NO_KEY, prev2 = lo > L ? p.key[lo - L - 1] : NO_KEY;
+  const uint32_t far = uint64_t(lo) + 2 * L < n ? p.key[lo + 2 * L] : NO_KEY;
+  const uint32_t first = __shfl_sync(FULL, key0, 0), last = __shfl_sync(FULL, key0, size - 1);
+  const uint32_t next = __shfl_sync(FULL, key1, 0);
+  const bool goes_on = prev == first;                                  // the first run began earlier
+  const bool head = goes_on && (prev2 == first || next == first);      // and is long
+  uint32_t i = goes_on && !head ? __popc(__ballot_sync(FULL, in0 && key0 == first)) : 0;
+  uint32_t end = __popc(__ballot_sync(FULL, key0 < p.n_vocab));
+  const bool crosses = size == L && next == last && last < p.n_vocab && !(goes_on && first == last);
+  const bool tail = crosses && far == last;  // the last run is long and begins here
+  if (crosses && !tail) end += __popc(__ballot_sync(FULL, key1 == last));
+  if (tail && c0 == 0 && lane == 0) p.longs[atomicAdd(p.n_long, 1u)] = uint32_t(c);
+  if (i >= end) return;
   const T* grad = static_cast<const T*>(p.grad);
-  uint64_t i = lo;
-  float a[UNIT], x[UNIT];
-  bool part = false;  // the current run is a piece of a long one
-  if (runs.goes_on(c)) {
-    part = runs.long_into(c);
-    if (!part)  // finished by the chunk before
-      while (i < hi && p.key[i] == p.key[lo]) ++i;
-  }
-  while (i < hi) {
-    const uint32_t id = p.key[i];
-    if (id >= p.n_vocab) break;
-#pragma unroll
-    for (int k = 0; k < UNIT; ++k) a[k] = 0.f;
-    const bool head = part;
-    // to the run's end, which is past the chunk's where that makes it whole
-    const bool tail = !head && (c + 2) * L < p.n && p.key[(c + 2) * L] == id;
-    const uint64_t end = head || tail ? hi : min(hi + L, uint64_t(p.n));
-    for (; i < end && p.key[i] == id; ++i) {
-      load_row<T, WIDE>(grad + uint64_t(p.pos[i]) * p.gstride, c0, p.dim, x);
-#pragma unroll
-      for (int k = 0; k < UNIT; ++k) a[k] += x[k];
+  float a[UNIT] = {};
+  bool piece = head;  // the current run is the long one that began earlier
+  uint32_t id = __shfl_sync(FULL, key0, i);
+  T* ring = reinterpret_cast<T*>(ring_mem[threadIdx.x / 32]);
+  auto stage = [&](uint32_t e) {
+    if (e < end) {
+      const uint32_t at = __shfl_sync(FULL, e < L ? pos0 : pos1, e < L ? e : e - L);
+      stage_row<T, WIDE>(ring + e % DEPTH * SUM_COLS, grad + uint64_t(at) * p.gstride, c0, p.dim);
     }
-    if (head || tail) store_row<float, WIDE>(p.part + (2 * c + (tail ? 1 : 0)) * uint64_t((p.dim + 7) / 8 * 8), c0, p.dim, a);
-    else write_sum<O, WIDE>(p, id, c0, a);
-    part = false;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (uint32_t k = 0; k + 1 < DEPTH; ++k) stage(i + k);
+#pragma unroll 1
+  for (; i < end; ++i) {
+    stage(i + DEPTH - 1);
+    const uint32_t now = __shfl_sync(FULL, i < L ? key0 : key1, i < L ? i : i - L);
+    if (now != id) {
+      if (piece) store_row<float, WIDE>(p.part + 2 * c * p.width, c0, p.dim, a);
+      else write_sum<O, WIDE>(p, id, c0, a);
+      piece = false;
+      id = now;
+#pragma unroll
+      for (int j = 0; j < UNIT; ++j) a[j] = 0.f;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    add_staged<T, WIDE>(ring + i % DEPTH * SUM_COLS, a);
   }
+  if (piece || tail) store_row<float, WIDE>(p.part + (2 * c + (piece ? 0 : 1)) * p.width, c0, p.dim, a);
+  else write_sum<O, WIDE>(p, id, c0, a);
 }
 
-// Adds the pieces of the long run that begins in chunk c, in order.
+// Adds the pieces of each long run: a block per run and SUM_COLS columns,
+// a warp per eighth of the pieces, in order.
+constexpr int JOIN_BLOCKS = 256;
 template <class O, bool WIDE>
 __global__ void __launch_bounds__(SUM_WARPS * 32) join_kernel(const __grid_constant__ SumArgs p) {
-  const uint64_t c = blockIdx.x, L = p.chunk;
-  const uint64_t c0 = (uint64_t(blockIdx.y) * SUM_WARPS + threadIdx.x / 32) * SUM_COLS;
-  if (c0 >= p.dim || (c + 2) * L >= p.n) return;
-  const uint32_t id = p.key[(c + 1) * L - 1];
-  if (id >= p.n_vocab || p.key[(c + 2) * L] != id) return;
-  if (c > 0 && p.key[c * L - 1] == id) return;  // it began earlier
-  const uint64_t width = (p.dim + 7) / 8 * 8;
-  float a[UNIT], x[UNIT];
-  load_row<float, WIDE>(p.part + (2 * c + 1) * width, c0, p.dim, a);
-  for (uint64_t d = c + 1; d * L < p.n && p.key[d * L] == id; ++d) {
-    load_row<float, WIDE>(p.part + 2 * d * width, c0, p.dim, x);
+  __shared__ float part[SUM_WARPS][SUM_COLS];
+  __shared__ uint32_t more;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const uint64_t c0 = uint64_t(blockIdx.y) * SUM_COLS, L = p.chunk;
+  wait_for_previous();
+  const uint32_t n_long = *p.n_long;
+  for (uint32_t r = blockIdx.x; r < n_long; r += gridDim.x) {
+    const uint64_t c = p.longs[r];
+    const uint32_t id = p.key[(c + 1) * L - 1];
+    // pieces in the chunks after the one that the run begins in
+    uint32_t n = 0;
+    for (bool go = true; go;) {
+      if (threadIdx.x == 0) more = 0;
+      __syncthreads();
+      const uint64_t at = (c + 1 + n + threadIdx.x) * L;
+      const uint32_t got = __ballot_sync(FULL, at < p.n && p.key[at] == id);
+      if (lane == 0) atomicAdd(&more, uint32_t(__popc(got)));
+      __syncthreads();
+      const uint32_t m = more;
+      n += m;
+      go = m == blockDim.x;
+      __syncthreads();
+    }
+    const uint32_t each = (n + 1 + SUM_WARPS - 1) / SUM_WARPS;
+    const uint32_t lo = min(warp * each, n + 1), hi = min(lo + each, n + 1);
+    float a[UNIT] = {};
+    for (uint32_t q = lo; q < hi; q += 6) {
+      Pack<float, UNIT> x[6];
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) a[k] += x[k];
+      for (int j = 0; j < 6; ++j)
+        if (q + j < hi) load_row<float, WIDE>(p.part + (q + j ? 2 * (c + q + j) : 2 * c + 1) * p.width, c0, p.dim, x[j]);
+#pragma unroll
+      for (int j = 0; j < 6; ++j)
+        if (q + j < hi) {
+#pragma unroll
+          for (int k = 0; k < UNIT; ++k) a[k] += x[j].v[k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < UNIT; ++k) part[warp][k * 32 + lane] = a[k];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int k = 0; k < UNIT; ++k)
+        for (int w = 1; w < SUM_WARPS; ++w) a[k] += part[w][k * 32 + lane];
+      write_sum<O, WIDE>(p, id, c0, a);
+    }
+    __syncthreads();
   }
-  write_sum<O, WIDE>(p, id, c0, a);
-}
-
-// Rows of ids that do not occur become zeros.
-template <class O, bool WIDE>
-__global__ void __launch_bounds__(256) fill_kernel(const __grid_constant__ SumArgs p) {
-  const uint64_t v = blockIdx.x;
-  uint32_t lo = 0, hi = p.n;  // the first sorted index whose key is v or more
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (p.key[mid] < v) lo = mid + 1;
-    else hi = mid;
-  }
-  if (lo < p.n && p.key[lo] == v) return;
-  const float zero[UNIT] = {};
-  O* row = static_cast<O*>(p.out) + v * p.ostride;
-  for (uint64_t c0 = (threadIdx.x / 32) * SUM_COLS; c0 < p.dim; c0 += 8 * SUM_COLS)
-    store_row<O, WIDE>(row, c0, p.dim, zero);
 }
 
 // Keep freed stream-ordered memory in the device's default pool across
@@ -379,9 +677,85 @@ cudaError_t keep_pool_memory() {
   });
 }
 
-cudaError_t launch_sort(SortArgs s, uint32_t* key[2], uint32_t* pos[2], int* at, cudaStream_t stream) {
+// Per device: attributes of the cluster sort, and how many clusters of each
+// kind run at a time.
+struct ClusterSetup {
+  int blocks;        // of the largest cluster
+  int active[3][5];  // [kind of cluster_sort_kernel][log2 of the blocks]
+};
+constexpr int CLUSTER_ITEMS[3] = {1, 2, 8};
+using ClusterKernel = void (*)(ClusterArgs);
+const ClusterKernel CLUSTER_KERNEL[3] = {cluster_sort_kernel<1>, cluster_sort_kernel<2>, cluster_sort_kernel<8>};
+
+cudaLaunchConfig_t cluster_config(int kind, int blocks, int grid, cudaLaunchAttribute* at, cudaStream_t stream) {
+  std::memset(at, 0, sizeof *at);
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = blocks;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(CS_THREADS);
+  cfg.dynamicSmemBytes = cluster_smem(CLUSTER_ITEMS[kind]);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+cudaError_t cluster_setup(const ClusterSetup** out) {
+  static ppi::DeviceOnce once;
+  static ClusterSetup setup[ppi::MAX_DEVICES];
+  int dev;
+  cudaError_t e = ppi::current_device(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run(dev, [](int d) {
+    ClusterSetup& s = setup[d];
+    for (int k = 0; k < 3; ++k) {
+      cudaError_t e = cudaFuncSetAttribute(CLUSTER_KERNEL[k], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           int(cluster_smem(CLUSTER_ITEMS[k])));
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(CLUSTER_KERNEL[k], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      for (int c = 0; e == cudaSuccess && c < 5; ++c) {
+        cudaLaunchAttribute at;
+        const cudaLaunchConfig_t cfg = cluster_config(k, 1 << c, 1 << c, &at, nullptr);
+        e = cudaOccupancyMaxActiveClusters(&s.active[k][c], CLUSTER_KERNEL[k], &cfg);
+      }
+      if (e != cudaSuccess) return e;
+    }
+    s.blocks = CS_BLOCKS;
+    while (s.blocks > 8 && s.active[2][4] < 1) s.blocks /= 2;
+    return cudaSuccess;
+  });
+  *out = &setup[dev];
+  return e;
+}
+
+int key_bits(uint32_t n_vocab) {
   int bits = 1;
-  while (bits < 32 && (uint64_t(s.n_vocab) >> bits)) ++bits;
+  while (bits < 32 && (uint64_t(n_vocab) >> bits)) ++bits;
+  return bits;
+}
+
+cudaError_t launch_cluster_sort(ClusterArgs& p, const ClusterSetup& setup, cudaStream_t stream) {
+  // pairs a thread: the fewest that the blocks hold, as the sort is bound by
+  // its steps' latencies
+  const uint32_t n = p.s.n, threads = uint32_t(CS_THREADS * setup.blocks);
+  const int kind = n <= threads ? 0 : n <= 2 * threads ? 1 : 2;
+  int c = 0;
+  while ((1 << c) < setup.blocks && uint32_t(CLUSTER_ITEMS[kind] * CS_THREADS << c) < n) ++c;
+  const int bits = key_bits(p.s.n_vocab);
+  p.passes = (bits + CS_BITS - 1) / CS_BITS;
+  p.bits = (bits + p.passes - 1) / p.passes;
+  p.blocks = 1 << c;
+  // the zeroing blocks are as many as run beside the sort at once: the rows
+  // are dealt out evenly, so blocks of a second wave would double the time
+  const int clusters = p.zero ? std::max(setup.active[kind][c], 2) : 1;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = cluster_config(kind, 1 << c, clusters << c, &at, stream);
+  return cudaLaunchKernelEx(&cfg, CLUSTER_KERNEL[kind], p);
+}
+
+cudaError_t launch_sort(SortArgs s, uint32_t* key[2], uint32_t* pos[2], int* at, cudaStream_t stream) {
+  const int bits = key_bits(s.n_vocab);
   int to = 0;
   for (int shift = 0; shift < bits; shift += DIGIT_BITS) {
     s.shift = shift;
@@ -399,25 +773,31 @@ cudaError_t launch_sort(SortArgs s, uint32_t* key[2], uint32_t* pos[2], int* at,
   return cudaGetLastError();
 }
 
+template <class K>
+cudaError_t launch_next(K kernel, dim3 grid, dim3 block, const SumArgs& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <class T, class O>
 cudaError_t launch_sums(const SumArgs& p, cudaStream_t stream) {
   const bool wide = rows_aligned(p.grad, sizeof(T), p.gstride, p.n) &&
                     rows_aligned(p.out, sizeof(O), p.ostride, p.n_vocab);
-  const unsigned y = unsigned((uint64_t(p.dim) + SUM_COLS * SUM_WARPS - 1) / (SUM_COLS * SUM_WARPS));
-  const dim3 grid(p.n_chunks, y);
-  if (!p.accumulate) {
-    if (wide) fill_kernel<O, true><<<p.n_vocab, 256, 0, stream>>>(p);
-    else fill_kernel<O, false><<<p.n_vocab, 256, 0, stream>>>(p);
-  }
-  if (!p.n) return cudaGetLastError();
-  if (wide) {
-    sum_kernel<T, O, true><<<grid, SUM_WARPS * 32, 0, stream>>>(p);
-    if (p.n_chunks > 2) join_kernel<O, true><<<grid, SUM_WARPS * 32, 0, stream>>>(p);
-  } else {
-    sum_kernel<T, O, false><<<grid, SUM_WARPS * 32, 0, stream>>>(p);
-    if (p.n_chunks > 2) join_kernel<O, false><<<grid, SUM_WARPS * 32, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  const unsigned grid = unsigned((uint64_t(p.n_chunks) * p.slices + SUM_WARPS - 1) / SUM_WARPS);
+  const dim3 join(std::min(p.n_chunks, uint32_t(JOIN_BLOCKS)), p.slices);
+  const dim3 block(SUM_WARPS * 32);
+  cudaError_t e = launch_next(wide ? sum_kernel<T, O, true> : sum_kernel<T, O, false>, grid, block, p, stream);
+  if (e == cudaSuccess && p.n_chunks > 2)
+    e = launch_next(wide ? join_kernel<O, true> : join_kernel<O, false>, join, block, p, stream);
+  return e;
 }
 
 }  // namespace
@@ -454,10 +834,13 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
       !ppl::aligned(d_out, ppl::fsize(out_type)))
     return PP_EINVAL;
   if (n >= ppl::MAX_DIM || n_vocab >= ppl::MAX_DIM || dim >= ppl::MAX_DIM) return PP_ETOOLARGE;
-  if (dim > uint64_t(65535) * SUM_COLS * SUM_WARPS) return PP_ETOOLARGE;  // the grid's second dimension
+  if (dim > uint64_t(65535) * SUM_COLS) return PP_ETOOLARGE;  // the grid's second dimension
   if (!n_vocab || !dim || (!n && accumulate)) return PP_OK;
   cudaError_t e = keep_pool_memory();
   if (e != cudaSuccess) return ppl::rc_of(e);
+  const ClusterSetup* setup;
+  if ((e = cluster_setup(&setup)) != cudaSuccess) return ppl::rc_of(e);
+  const size_t size = ppl::fsize(out_type);
   SumArgs p;
   std::memset(&p, 0, sizeof p);
   p.n = uint32_t(n);
@@ -465,12 +848,25 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   p.grad = d_grad;
   p.gstride = grad_stride;
   p.dim = uint32_t(dim);
+  p.slices = uint32_t((dim + SUM_COLS - 1) / SUM_COLS);
   p.scale = scale;
   p.accumulate = accumulate;
   p.out = d_out;
   p.ostride = out_stride;
-  p.chunk = 64;
+  p.width = (dim + 7) / 8 * 8;
+  // chunks of 32 where they make enough warps to fill the machine (24 on
+  // each of 152 multiprocessors), else shorter ones
+  p.chunk = 32;
+  while (p.chunk > 8 && uint64_t(n) / p.chunk * p.slices < 152 * 24) p.chunk /= 2;
   p.n_chunks = uint32_t((n + p.chunk - 1) / p.chunk);
+  if (uint64_t(p.n_chunks) * p.slices / SUM_WARPS >= ppl::MAX_DIM) return PP_ETOOLARGE;
+  ZeroArgs z;
+  z.out = d_out;
+  z.row_bytes = dim * size;
+  z.stride_bytes = out_stride * size;
+  z.n_vocab = uint32_t(n_vocab);
+  z.wide = z.row_bytes % 16 == 0 && rows_aligned(d_out, size, out_stride, n_vocab);
+  z.elem_size = int(size);
   SortArgs s;
   std::memset(&s, 0, sizeof s);
   s.ids = d_ids;
@@ -480,22 +876,41 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   s.n_vocab = uint32_t(n_vocab);
   s.pad = padding_id;
   s.n_tiles = uint32_t((n + SORT_TILE - 1) / SORT_TILE);
-  const size_t width = (dim + 7) / 8 * 8;
-  const size_t counts = size_t(s.n_tiles) * DIGITS, pairs = (n + 3) / 4 * 4;
-  const size_t parts = p.n_chunks > 2 ? size_t(p.n_chunks) * 2 * width : 0;
+  const bool one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * setup->blocks;  // one cluster sorts
+  const size_t counts = one ? 0 : size_t(s.n_tiles) * DIGITS, pairs = (n + 3) / 4 * 4;
+  const size_t parts = p.n_chunks > 2 ? size_t(p.n_chunks) * 2 * p.width : 0;
   void* scratch = nullptr;
-  e = cudaMallocAsync(&scratch, 4 * (parts + 4 * pairs + counts) + 16, stream);
+  e = cudaMallocAsync(&scratch, 4 * (parts + (one ? 2 : 4) * pairs + counts + p.n_chunks + 4), stream);
   if (e != cudaSuccess) return ppl::rc_of(e);
   p.part = static_cast<float*>(scratch);
   uint32_t* u = reinterpret_cast<uint32_t*>(p.part + parts);
-  uint32_t* key[2] = {u, u + pairs};
-  uint32_t* pos[2] = {u + 2 * pairs, u + 3 * pairs};
+  p.n_long = u;
+  p.longs = u + 4;
+  u = p.longs + p.n_chunks;
+  uint32_t* key[2] = {u, u + 2 * pairs};
+  uint32_t* pos[2] = {u + pairs, u + 3 * pairs};
   s.counts = u + 4 * pairs;
   int at = 0;
-  if (n) e = launch_sort(s, key, pos, &at, stream);
+  if (one) {
+    ClusterArgs c;
+    c.s = s;
+    c.s.key_out = key[0];
+    c.s.pos_out = pos[0];
+    c.n_long = p.n_long;
+    c.zero = !accumulate;
+    c.z = z;
+    e = launch_cluster_sort(c, *setup, stream);
+  } else {
+    e = cudaMemsetAsync(p.n_long, 0, 4, stream);
+    if (e == cudaSuccess) e = launch_sort(s, key, pos, &at, stream);
+    if (e == cudaSuccess && !accumulate) {
+      zero_kernel<<<unsigned((n_vocab + ZERO_SPAN - 1) / ZERO_SPAN), 256, 0, stream>>>(z, key[at], s.n);
+      e = cudaGetLastError();
+    }
+  }
   p.key = key[at];
   p.pos = pos[at];
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && n)
     e = with_type(grad_type, [&](auto t) {
       return with_type(out_type, [&](auto o) { return launch_sums<decltype(t), decltype(o)>(p, stream); });
     });

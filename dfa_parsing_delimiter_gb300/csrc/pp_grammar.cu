@@ -137,68 +137,175 @@ __global__ void __launch_bounds__(128) states_short_kernel(const __grid_constant
   }
 }
 
-// A block per row: tiles of STATES_THREADS x STATES_K tokens; a thread
-// composes its tokens' vectors, the warp scans them, and the state that
-// enters the tile passes through the warps' totals.
-constexpr int STATES_THREADS = 256, STATES_K = 8;
-__global__ void __launch_bounds__(STATES_THREADS)
-states_kernel(const __grid_constant__ StateArgs p) {
-  constexpr int WARPS = STATES_THREADS / 32;
-  __shared__ uint64_t total[WARPS];
-  __shared__ uint32_t lost[WARPS];
+// Longer rows: the blocks of a cluster share a row, a part each.  A thread
+// composes K tokens' vectors, the warp scans them, the block composes its
+// warps' totals; each block tells the later ones its part's total, and after
+// a cluster barrier the state that enters a part is known and passes through
+// the warps' totals to the threads.  A part of up to STATES_THREADS x K
+// tokens keeps its vectors in registers between the two steps; a longer one
+// reads them twice.
+constexpr int STATES_THREADS = 1024, STATES_WARPS = 32, STATES_BLOCKS = 8;
+
+struct StateShared {
+  uint64_t total[STATES_WARPS];  // the warps' vectors
+  uint32_t lost[STATES_WARPS];   // a token outside the vocabulary among a warp's
+  uint64_t part[STATES_BLOCKS];  // the earlier blocks' vectors, written by them
+  uint32_t part_lost[STATES_BLOCKS];
+  uint64_t tile;
+  uint32_t tile_lost;
+};
+
+// One tile's vectors into registers and its warps' totals into shared memory.
+template <int K, class I>
+__device__ __forceinline__ void states_tile(const StateArgs& p, const I* tokens, uint64_t t0, uint64_t len,
+                                            uint64_t (&vec)[K], uint32_t* bad, Stv16* before, uint32_t* dead,
+                                            StateShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const uint64_t row = blockIdx.x;
-  const uint32_t len = row_length(p, row);
-  uint32_t carry = first_state(p, row);
-  uint8_t* out = p.states + row * p.sstride;
-  if (threadIdx.x == 0) out[0] = uint8_t(carry);
-  const uint64_t id = stv16_pack(stv16_id());
-  for (uint64_t base = 0; base < p.n_cols; base += STATES_THREADS * STATES_K) {
-    const uint64_t t0 = base + uint64_t(threadIdx.x) * STATES_K;
-    uint64_t vec[STATES_K];
-    uint32_t bad = STATES_K;  // this thread's first token outside the vocabulary
-    Stv16 a = stv16_id();
+  int64_t tok[K];
 #pragma unroll
-    for (int k = 0; k < STATES_K; ++k) {
-      vec[k] = id;
-      if (t0 + k < len) {
-        const int64_t tok = load_id(p.tokens, p.type, row * p.tstride + t0 + k);
-        if (tok >= 0 && tok < p.n_vocab) vec[k] = p.vectors[tok];
-        else if (bad == STATES_K) bad = k;
-      }
-    }
+  for (int k = 0; k < K; ++k) tok[k] = t0 + k < len ? int64_t(tokens[t0 + k]) : -1;
+  *bad = K;  // this thread's first token outside the vocabulary
 #pragma unroll
-    for (int k = 0; k < STATES_K; ++k) a = stv16_compose(a, stv16_unpack(vec[k]));
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const Stv16 up = shfl_up16(a, d);
-      if (lane >= d) a = stv16_compose(up, a);
-    }
-    const Stv16 before = shfl_up16(a, 1);
-    const uint32_t dead = __ballot_sync(FULL, bad < STATES_K);
-    if (lane == 31) {
-      total[warp] = stv16_pack(a);
-      lost[warp] = dead;
-    }
-    __syncthreads();
-    uint32_t s = carry;
-    for (int w = 0; w < WARPS; ++w) {
-      if (w == warp) {
-        uint32_t q = s;
-        if (q != PP_STATE_NONE && lane > 0) q = stv16_apply(before, q);
-        if (dead & ((1u << lane) - 1)) q = PP_STATE_NONE;
-#pragma unroll
-        for (int k = 0; k < STATES_K; ++k) {
-          if (uint32_t(k) >= bad) q = PP_STATE_NONE;
-          if (q != PP_STATE_NONE) q = nib_apply(vec[k], q);
-          if (t0 + k < p.n_cols) out[t0 + k + 1] = uint8_t(q);
-        }
-      }
-      if (s != PP_STATE_NONE) s = lost[w] ? uint32_t(PP_STATE_NONE) : nib_apply(total[w], s);
-    }
-    carry = s;
-    __syncthreads();
+  for (int k = K - 1; k >= 0; --k) {
+    const bool fine = tok[k] >= 0 && tok[k] < p.n_vocab;
+    vec[k] = fine ? p.vectors[tok[k]] : 0xFEDCBA9876543210ull;  // the identity
+    if (!fine && t0 + k < len) *bad = k;
   }
+  Stv16 a = stv16_id();
+  if (t0 < len) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) a = stv16_compose(a, stv16_unpack(vec[k]));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const Stv16 up = shfl_up16(a, d);
+    if (lane >= d) a = stv16_compose(up, a);
+  }
+  *before = shfl_up16(a, 1);
+  *dead = __ballot_sync(FULL, *bad < K);
+  if (lane == 31) {
+    sh.total[warp] = stv16_pack(a);
+    sh.lost[warp] = *dead;
+  }
+}
+
+template <int K, class I>
+__device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, StateShared& sh, uint32_t* staged) {
+  constexpr uint32_t TILE = STATES_THREADS * K;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const uint64_t row = blockIdx.x / blocks;
+  const uint32_t rank = blockIdx.x % blocks;
+  const uint64_t begin = min(uint64_t(rank) * each, uint64_t(p.n_cols)), end = min(begin + each, uint64_t(p.n_cols));
+  const uint64_t len = min(uint64_t(row_length(p, row)), end);
+  const I* tokens = static_cast<const I*>(p.tokens) + row * p.tstride;
+  uint8_t* out = p.states + row * p.sstride;
+  uint64_t vec[K];
+  uint32_t bad, dead, s = first_state(p, row);
+  Stv16 before;
+  if (rank == 0 && threadIdx.x == 0) out[0] = uint8_t(s);
+  if (blocks > 1) {
+    // the part's total, by warp 0
+    Stv16 all = stv16_id();
+    uint32_t gone = 0;
+    for (uint64_t base = begin; base < end; base += TILE) {
+      states_tile<K>(p, tokens, base + uint64_t(threadIdx.x) * K, len, vec, &bad, &before, &dead, sh);
+      __syncthreads();
+      if (warp == 0) {
+        Stv16 a = stv16_unpack(sh.total[lane]);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const Stv16 up = shfl_up16(a, d);
+          if (lane >= d) a = stv16_compose(up, a);
+        }
+        all = stv16_compose(all, a);  // lane 31 has them all
+        gone |= __ballot_sync(FULL, sh.lost[lane] != 0);
+      }
+      if (base + TILE < end) __syncthreads();
+    }
+    if (warp == 0 && lane == 31)
+      for (uint32_t q = rank + 1; q < blocks; ++q) {
+        const uint64_t v = stv16_pack(all);
+        uint32_t a, b;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part[rank]))), "r"(q));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part_lost[rank]))), "r"(q));
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(gone) : "memory");
+      }
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+    for (uint32_t q = 0; q < rank; ++q)
+      if (s != PP_STATE_NONE) s = sh.part_lost[q] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.part[q], s);
+  }
+  const bool kept = blocks > 1 && end - begin <= TILE;  // the one tile's vectors are still here
+  for (uint64_t base = begin; base < end; base += TILE) {
+    const uint64_t t0 = base + uint64_t(threadIdx.x) * K;
+    if (!kept) {
+      states_tile<K>(p, tokens, t0, len, vec, &bad, &before, &dead, sh);
+      __syncthreads();
+    }
+    uint32_t q = s;
+    for (int w = 0; w < STATES_WARPS; ++w) {
+      if (w == warp) q = s;
+      if (s != PP_STATE_NONE) s = sh.lost[w] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.total[w], s);
+    }
+    if (q != PP_STATE_NONE && lane > 0) q = stv16_apply(before, q);
+    if (dead & ((1u << lane) - 1)) q = PP_STATE_NONE;
+#pragma unroll
+    for (int g = 0; g < K / 4; ++g) {
+      uint32_t four = 0;
+#pragma unroll
+      for (int k = 4 * g; k < 4 * g + 4; ++k) {
+        if (uint32_t(k) >= bad) q = PP_STATE_NONE;
+        if (q != PP_STATE_NONE) q = nib_apply(vec[k], q);
+        four |= q << (8 * (k - 4 * g));
+      }
+      staged[threadIdx.x * (K / 4) + g] = four;
+    }
+    __syncthreads();
+    // the tile's states, which begin at any byte, in words of memory
+    uint8_t* to = out + base + 1;
+    const uint32_t n = uint32_t(min(uint64_t(TILE), end - base));
+    const uint32_t skip = min(uint32_t(-reinterpret_cast<intptr_t>(to)) & 3u, n), words = (n - skip) / 4;
+    for (uint32_t w = threadIdx.x; w < words; w += STATES_THREADS)
+      reinterpret_cast<uint32_t*>(to + skip)[w] = __funnelshift_r(staged[w], staged[w + 1], 8 * skip);
+    const uint32_t rest = n - skip - 4 * words;
+    if (threadIdx.x < skip) to[threadIdx.x] = reinterpret_cast<uint8_t*>(staged)[threadIdx.x];
+    if (threadIdx.x < rest) to[n - rest + threadIdx.x] = reinterpret_cast<uint8_t*>(staged)[n - rest + threadIdx.x];
+    if (base + TILE < end) __syncthreads();
+  }
+}
+
+template <int K>
+__global__ void __launch_bounds__(STATES_THREADS, 1)
+states_kernel(const __grid_constant__ StateArgs p, uint32_t blocks, uint32_t each) {
+  __shared__ StateShared sh;
+  __shared__ __align__(16) uint32_t staged[STATES_THREADS * K / 4 + 1];
+  switch (p.type) {
+    case PP_U8: return states_row<K, uint8_t>(p, blocks, each, sh, staged);
+    case PP_I8: return states_row<K, int8_t>(p, blocks, each, sh, staged);
+    case PP_I32: return states_row<K, int32_t>(p, blocks, each, sh, staged);
+    default: return states_row<K, int64_t>(p, blocks, each, sh, staged);
+  }
+}
+
+cudaError_t launch_states(const StateArgs& p, cudaStream_t stream) {
+  // a cluster shares a row while there are fewer blocks than 152
+  // multiprocessors and a part keeps 1024 tokens
+  uint32_t blocks = 1;
+  while (blocks < STATES_BLOCKS && uint64_t(p.n_rows) * blocks < 152 && p.n_cols / (2 * blocks) >= 1024) blocks *= 2;
+  const uint32_t each = uint32_t((uint64_t(p.n_cols) + blocks - 1) / blocks);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  std::memset(&at, 0, sizeof at);
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = blocks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(p.n_rows * blocks);
+  cfg.blockDim = dim3(STATES_THREADS);
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, each <= STATES_THREADS * 4 ? states_kernel<4> : states_kernel<16>, p, blocks, each);
 }
 
 // Per state, whether an accepting state can be reached from it without
@@ -207,11 +314,15 @@ uint32_t live_states(const pp_dfa_desc* d) {
   uint32_t in = 0, live = 0;
   for (int s = 0; s < d->n_states; ++s)
     if (s != d->invalid_state) in |= 1u << s;
+  uint32_t used = 0;  // groups that some byte has
+  for (int b = 0; b < 256; ++b) used |= 1u << d->byte_to_group[b];
   live = d->accept_mask & in;
-  for (int round = 0; round < d->n_states; ++round)
+  for (uint32_t before = ~live; before != live;) {
+    before = live;
     for (int s = 0; s < d->n_states; ++s)
-      for (int b = 0; b < 256; ++b)
-        if ((in >> s & 1) && (live >> d->delta[d->byte_to_group[b]][s] & 1)) live |= 1u << s;
+      for (int g = 0; g < d->n_groups; ++g)
+        if ((in >> s & 1) && (used >> g & 1) && (live >> d->delta[g][s] & 1)) live |= 1u << s;
+  }
   return live;
 }
 
@@ -264,7 +375,7 @@ pp_rc pp_grammar_states(const uint64_t* d_vectors, size_t n_vocab, int n_states,
   if (n_cols <= STATES_SHORT)
     states_short_kernel<<<unsigned((n_rows + 127) / 128), 128, 0, stream>>>(p);
   else
-    states_kernel<<<unsigned(n_rows), STATES_THREADS, 0, stream>>>(p);
+    return ppl::rc_of(launch_states(p, stream));
   return ppl::rc_of(cudaGetLastError());
 }
 

@@ -42,6 +42,39 @@ __device__ __forceinline__ int64_t load_id(const void* p, int type, uint64_t i) 
   }
 }
 
+// f(position, id) for the ids at positions first, first + step, ... below n,
+// BATCH loads on their way at a time (a load per iteration would wait for
+// each: the id feeds a shared-memory atomic that later loads stay behind).
+template <int BATCH, class I, class F>
+__device__ __forceinline__ void for_ids_of(const I* p, uint64_t stride, uint32_t first, uint32_t n, uint32_t step, F&& f) {
+  const I* q = p + first * stride;
+  const uint64_t d = step * stride;
+  uint64_t i = first;
+  for (; i + uint64_t(BATCH - 1) * step < n; i += uint64_t(BATCH) * step, q += BATCH * d) {
+    I v[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) v[k] = q[k * d];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) f(uint32_t(i) + k * step, v[k]);
+  }
+  I v[BATCH];
+#pragma unroll
+  for (int k = 0; k < BATCH; ++k)
+    if (i + uint64_t(k) * step < n) v[k] = q[k * d];
+#pragma unroll
+  for (int k = 0; k < BATCH; ++k)
+    if (i + uint64_t(k) * step < n) f(uint32_t(i) + k * step, v[k]);
+}
+template <int BATCH, class F>
+__device__ __forceinline__ void for_ids(const void* p, int type, uint64_t stride, uint32_t first, uint32_t n, uint32_t step, F&& f) {
+  switch (type) {
+    case PP_U8: return for_ids_of<BATCH>(static_cast<const uint8_t*>(p), stride, first, n, step, f);
+    case PP_I8: return for_ids_of<BATCH>(static_cast<const int8_t*>(p), stride, first, n, step, f);
+    case PP_I32: return for_ids_of<BATCH>(static_cast<const int32_t*>(p), stride, first, n, step, f);
+    default: return for_ids_of<BATCH>(static_cast<const int64_t*>(p), stride, first, n, step, f);
+  }
+}
+
 // N elements moved in accesses of at most 16 bytes (p aligned to that).
 template <class T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {

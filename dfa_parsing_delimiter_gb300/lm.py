@@ -16,6 +16,7 @@ RuntimeError.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -40,13 +41,18 @@ class LogitOpts(ctypes.Structure):
                 ("n_states", ctypes.c_int32), ("history_type", ctypes.c_int32)]
 
 
+# The same struct from values in order: one pack costs a tenth of setting the
+# fields one by one, which is felt where a call's kernel takes microseconds.
+_pack_opts = struct.Struct("@18Q2i").pack
+
+
 def declare(L: ctypes.CDLL) -> None:
     """The entry points' argument types."""
     sigs = {
         "pp_vocab_grammar": [_vp, _vp, _sz, _sz, ctypes.POINTER(pp.DfaDesc), _i64, _vp, _vp, _sz, _vp],
         "pp_grammar_states": [_vp, _sz, _int, _vp, _int, _sz, _sz, _sz, _vp, _vp, _sz,
                               ctypes.c_uint8, _vp, _sz, _vp],
-        "pp_logits": [_vp, _int, _sz, _sz, _sz, ctypes.POINTER(LogitOpts), _vp, _sz, _vp],
+        "pp_logits": [_vp, _int, _sz, _sz, _sz, _vp, _vp, _sz, _vp],
         "pp_embed": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _vp, _int, _sz, _vp],
         "pp_embed_grad": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _int, _vp,
                           _int, _sz, _vp],
@@ -61,18 +67,24 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+def _wrong(t, like, name: str, dtypes, ndim) -> None:
+    raise ValueError(f"{name}: want {ndim} dimensions of {[str(d) for d in dtypes]} on {like.device}, "
+                     f"got {tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
 def _on(t: torch.Tensor, like: torch.Tensor, name: str, dtypes, ndim: int) -> None:
-    if t.dtype not in dtypes or t.dim() != ndim or t.device != like.device:
-        raise ValueError(f"{name}: want {ndim} dimensions of {[str(d) for d in dtypes]} on "
-                         f"{like.device}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+    if t.dtype not in dtypes or t.dim() != ndim or t.get_device() != like.get_device():
+        _wrong(t, like, name, dtypes, ndim)
 
 
-def _vector(t, like, name: str, dtypes, n: int) -> int:
+def _vector(t, like, name: str, dtype, n: int) -> int:
     """Address of a contiguous vector of at least n elements (None: 0)."""
     if t is None:
         return 0
-    _on(t, like, name, dtypes, 1)
-    _need(t.size(0) >= n and (n <= 1 or t.stride(0) == 1), f"{name}: want {n} contiguous elements")
+    if t.dtype is not dtype or t.dim() != 1 or t.get_device() != like.get_device():
+        _wrong(t, like, name, (dtype,), 1)
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: want {n} contiguous elements")
     return t.data_ptr()
 
 
@@ -85,20 +97,22 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
 
 def _matrix_stride(t: torch.Tensor, name: str) -> int:
     """Row stride of a matrix with contiguous rows."""
-    _need(t.size(1) <= 1 or t.stride(1) == 1 or not t.numel(), f"{name}: the last dimension has to be contiguous")
-    return t.stride(0)
+    stride = t.stride()
+    if stride[1] != 1 and t.size(1) > 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension has to be contiguous")
+    return stride[0]
 
 
 def _call(fn, what: str, like: torch.Tensor, stream, *args) -> None:
     """One library call on the tensors' device and the stream."""
-    _need(like.is_cuda, f"{what}: want tensors on a GPU, got {like.device}")
-    if like.device.index == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream()
-        rc = fn(*args, s.cuda_stream)
+    dev = like.get_device()
+    if dev < 0:
+        raise ValueError(f"{what}: want tensors on a GPU, got {like.device}")
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(like.device):
-            s = stream if stream is not None else torch.cuda.current_stream()
-            rc = fn(*args, s.cuda_stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if rc:
         pp._check(rc, what)
 
@@ -157,17 +171,17 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
         out = _new((rows, cols + 1), torch.uint8, tokens, stream)
     else:
         _on(out, tokens, "out", (torch.uint8,), 2)
-        _need(tuple(out.shape) == (rows, cols + 1), f"out: want {(rows, cols + 1)}")
+        _need(out.shape == (rows, cols + 1), "out: want one column more than tokens")
     ps, ss = 0, 0
     if start is not None:
         _on(start, tokens, "start", (torch.uint8,), 1)
-        _need(start.size(0) == rows, f"start: want {rows} states")
+        _need(start.size(0) == rows, "start: want one state a row")
         ps, ss = start.data_ptr(), start.stride(0)
     if not rows:
         return out
     _call(pp.lib().pp_grammar_states, "pp_grammar_states", tokens, stream, grammar.vectors.data_ptr(),
           grammar.n_vocab, grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype], rows, cols,
-          _matrix_stride(tokens, "tokens"), _vector(lengths, tokens, "lengths", (torch.int32,), rows),
+          _matrix_stride(tokens, "tokens"), _vector(lengths, tokens, "lengths", torch.int32, rows),
           ps, ss, grammar.start_state, out.data_ptr(), _matrix_stride(out, "out"))
     return out
 
@@ -189,50 +203,52 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
         out = _new((rows, vocab), logits.dtype, logits, stream)
     else:
         _on(out, logits, "out", (logits.dtype,), 2)
-        _need(out.shape == logits.shape, f"out: want {tuple(logits.shape)}")
-    o = LogitOpts()
+        _need(out.shape == logits.shape, "out: want the shape of the logits")
+    hist = (0,) * 10
+    itype = 0
     if history is not None:
         _on(history, logits, "history", ITYPE, 2)
-        o.d_history, o.history_type = history.data_ptr(), ITYPE[history.dtype]
-        o.history_rows, o.history_cols = history.shape
-        o.history_stride = _matrix_stride(history, "history")
-        _need(history_row is not None or o.history_rows >= rows, "history: want a row for each row of logits")
-        ints = (torch.int32,)
-        o.d_history_row = _vector(history_row, logits, "history_row", ints, rows)
-        o.d_history_len = _vector(history_len, logits, "history_len", ints, rows)
-        o.d_prompt_len = _vector(prompt_len, logits, "prompt_len", ints, rows)
-        floats = (torch.float32,)
-        o.d_repetition = _vector(repetition, logits, "repetition", floats, rows)
-        o.d_presence = _vector(presence, logits, "presence", floats, rows)
-        o.d_frequency = _vector(frequency, logits, "frequency", floats, rows)
+        itype = ITYPE[history.dtype]
+        lines, cols = history.shape
+        _need(history_row is not None or lines >= rows, "history: want a row for each row of logits")
+        i32, f32 = torch.int32, torch.float32
+        hist = (history.data_ptr(), _vector(history_row, logits, "history_row", i32, rows),
+                _vector(history_len, logits, "history_len", i32, rows),
+                _vector(prompt_len, logits, "prompt_len", i32, rows),
+                lines, cols, _matrix_stride(history, "history"),
+                _vector(repetition, logits, "repetition", f32, rows),
+                _vector(presence, logits, "presence", f32, rows),
+                _vector(frequency, logits, "frequency", f32, rows))
     else:
         _need(repetition is None and presence is None and frequency is None, "penalties need a history")
+    lists = (0,) * 4
     if bias is not None:
         at, tokens, values = bias
-        o.n_bias = tokens.size(0)
-        _need(values.size(0) == o.n_bias, "bias: want as many values as tokens")
-        o.d_bias_offsets = _vector(at, logits, "bias offsets", (torch.int32,), rows + 1)
-        o.d_bias_tokens = _vector(tokens, logits, "bias tokens", (torch.int32,), o.n_bias)
-        o.d_bias_values = _vector(values, logits, "bias values", (torch.float32,), o.n_bias)
+        n = tokens.size(0)
+        _need(values.size(0) == n, "bias: want as many values as tokens")
+        lists = (_vector(at, logits, "bias offsets", torch.int32, rows + 1),
+                 _vector(tokens, logits, "bias tokens", torch.int32, n),
+                 _vector(values, logits, "bias values", torch.float32, n), n)
     _need((grammar is None) == (states is None), "a grammar needs states, and states a grammar")
+    mask = (0,) * 5
     if grammar is not None:
         _on(states, logits, "states", (torch.uint8,), 1)
-        _need(states.size(0) == rows, f"states: want {rows}")
-        _need(grammar.n_vocab == vocab, f"the grammar has {grammar.n_vocab} tokens, the logits {vocab}")
-        _on(grammar.allowed, logits, "allowed", (torch.int32,), 2)
-        o.d_allowed, o.allowed_stride = grammar.allowed.data_ptr(), grammar.allowed.stride(0)
-        o.d_state, o.state_stride, o.n_states = states.data_ptr(), states.stride(0), grammar.n_states
+        _need(states.size(0) == rows, "states: want one a row")
+        _need(grammar.n_vocab == vocab, "the grammar has another number of tokens than the logits")
+        allowed = grammar.allowed
+        _need(allowed.get_device() == logits.get_device(), "the grammar is on another device")
+        mask = (allowed.data_ptr(), allowed.stride(0), states.data_ptr(), states.stride(0), grammar.n_states)
     if rows and vocab:
         _call(pp.lib().pp_logits, "pp_logits", logits, stream, logits.data_ptr(), FTYPE[logits.dtype],
-              rows, vocab, _matrix_stride(logits, "logits"), ctypes.byref(o), out.data_ptr(),
-              _matrix_stride(out, "out"))
+              rows, vocab, _matrix_stride(logits, "logits"), _pack_opts(*hist, *lists, *mask, itype),
+              out.data_ptr(), _matrix_stride(out, "out"))
     return out
 
 
 # ------------------------------------------------------------------ embedding
 def _flat_ids(ids: torch.Tensor) -> tuple[int, int]:
     """(number of ids, their stride) of ids that lie at one stride."""
-    _need(ids.dtype in ITYPE, f"ids: want uint8, int8, int32 or int64, got {ids.dtype}")
+    _need(ids.dtype in ITYPE, "ids: want uint8, int8, int32 or int64")
     n = ids.numel()
     if ids.is_contiguous():
         return n, 1
@@ -256,8 +272,8 @@ def _embed(ids, table, scale, padding_id, out, dtype, stream) -> torch.Tensor:
         out = _new(shape, dtype if dtype is not None else table.dtype, ids, stream)
     else:
         _need(out.dtype in FTYPE and out.device == ids.device and out.shape == shape and
-              out.is_contiguous() and dtype in (None, out.dtype), f"out: want contiguous {shape}")
-    _need(out.dtype in FTYPE, f"dtype: want float32, float16 or bfloat16, got {out.dtype}")
+              out.is_contiguous() and dtype in (None, out.dtype), "out: want the ids' shape and the width, contiguous")
+    _need(out.dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
     if n and dim:
         _call(pp.lib().pp_embed, "pp_embed", ids, stream, ids.data_ptr(), ITYPE[ids.dtype], stride, n,
               table.data_ptr(), FTYPE[table.dtype], vocab, dim, _matrix_stride(table, "table"), scale,
@@ -299,7 +315,7 @@ def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float
     With accumulate it is added to `out`; else `out` is overwritten."""
     n, stride = _flat_ids(ids)
     _need(grad.dtype in FTYPE and grad.device == ids.device and grad.dim() == ids.dim() + 1
-          and grad.shape[:-1] == ids.shape, f"grad: want {tuple(ids.shape)} and a last dimension, got {tuple(grad.shape)}")
+          and grad.shape[:-1] == ids.shape, "grad: want the ids' shape and a last dimension")
     dim = grad.size(-1)
     if grad.dim() != 2:
         grad = grad.reshape(n, dim)
@@ -308,8 +324,8 @@ def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float
         out = _new((n_vocab, dim), dtype if dtype is not None else grad.dtype, ids, stream)
     else:
         _on(out, ids, "out", FTYPE, 2)
-        _need(tuple(out.shape) == (n_vocab, dim) and dtype in (None, out.dtype), f"out: want {(n_vocab, dim)}")
-    _need(out.dtype in FTYPE, f"dtype: want float32, float16 or bfloat16, got {out.dtype}")
+        _need(out.shape == (n_vocab, dim) and dtype in (None, out.dtype), "out: want a row a token, of the width")
+    _need(out.dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
     if n_vocab and dim:
         _call(pp.lib().pp_embed_grad, "pp_embed_grad", ids, stream, ids.data_ptr(), ITYPE[ids.dtype],
               stride, n, grad.data_ptr(), FTYPE[grad.dtype], _matrix_stride(grad, "grad"), n_vocab, dim,

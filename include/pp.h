@@ -652,7 +652,7 @@ typedef struct {
  *   d_in, d_out     device [n_rows][stride], n_vocab values a row; d_out may
  *                   be d_in (with the same stride), but not overlap it
  *                   otherwise.
- * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n_vocab or
+ * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n_vocab of 2^30,
  * history_cols of 2^31 - 65536 or more, or more rows than the grid holds,
  * PP_ECUDA on CUDA errors.  No scratch.
  */
@@ -687,12 +687,12 @@ pp_rc pp_embed(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
  *                   accumulate != 0 the sums are added to what is there, in
  *                   32 bits and rounded once, and only rows of ids that
  *                   occur are touched.
- * Scratch (stream-ordered): 16 bytes an id, 1 KiB or 2 KiB of counters per
- * 4096 ids, and for ids with long runs partial sums of up to dim * n / 8
- * bytes; the device's default memory pool is set to keep it (release
- * threshold: unlimited), so later calls reuse it.
+ * Scratch (stream-ordered): 8 bytes an id up to 131072 ids and 17 beyond,
+ * and for ids with long runs partial sums of up to dim * n bytes; the
+ * device's default memory pool is set to keep it (release threshold:
+ * unlimited), so later calls reuse it.
  * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n or n_vocab of 2^31
- * - 65536 or a dim of 2^27 - 2048 or more, PP_ENOMEM / PP_ECUDA on CUDA errors.
+ * - 65536 or a dim of 2^24 - 255 or more, PP_ENOMEM / PP_ECUDA on CUDA errors.
  */
 pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
                     const void* d_grad, pp_ftype grad_type, size_t grad_stride, size_t n_vocab,

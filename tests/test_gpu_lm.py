@@ -367,6 +367,22 @@ def test_logits_bias_entries_outside_and_repeated():
     assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("hist", [20, 40000])
+def test_logits_long_bias_lists(hist):
+    """Lists of more entries than 16 bits count, with every token twice; with
+    a short history and one that needs counts of more than 15 bits."""
+    rng = np.random.default_rng(11)
+    vocab = 50000
+    tokens = np.concatenate([rng.permutation(vocab), rng.permutation(vocab)[:49000], [7, 7]]).astype(np.int32)
+    values = rng.normal(0, 3, tokens.size).astype(np.float32)
+    x = rng.normal(0, 2, (3, vocab)).astype(np.float32)
+    c = {"bias": (np.array([0, 5, 5, tokens.size], np.int32), tokens, values),
+         "history": rng.integers(0, 300, (3, hist)).astype(np.int32),
+         "frequency": np.full(3, 0.125, np.float32)}
+    ref, error = R.logits(x, **c)
+    R.check(pp.process_logits(dev(x), **on_gpu(c)), ref, error, torch.float32)
+
+
 @pytest.mark.parametrize("dtype", FT)
 def test_logits_infinities_and_nan(dtype):
     rng = np.random.default_rng(9)
@@ -533,6 +549,30 @@ def test_grad_ids(n, how):
     R.check(got, ref, error, torch.float32)
     again = pp.embed_grad(dev(ids.astype(np.int32)), grad.cuda(), vocab, scale=0.5, padding_id=2)
     assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("how", ["zipf", "runs", "one"])
+@pytest.mark.parametrize("n", [1024, 1025, 8192, 8193, 16384, 16385, 32769, 65537, 131072, 131073, 140001])
+def test_grad_many_ids(n, how):
+    """The sizes at which another sort takes over, and their neighbours."""
+    rng = np.random.default_rng(n)
+    vocab, dim = 2500, 12
+    ids = grad_ids(rng, n, vocab, how)
+    ids[::1000] = -1
+    grad = rng.normal(0, 1, (n, dim)).astype(np.float32)
+    for accumulate in (False, True):
+        old = rng.normal(0, 1, (vocab, dim)).astype(np.float32)
+        got = pp.embed_grad(dev(ids), dev(grad), vocab, out=dev(old), accumulate=accumulate)
+        ref, size, count = np.zeros((vocab, dim)), np.zeros((vocab, dim)), np.zeros(vocab)
+        ok = ids >= 0
+        np.add.at(ref, ids[ok], grad[ok].astype(np.float64))
+        np.add.at(size, ids[ok], np.abs(grad[ok]).astype(np.float64))
+        np.add.at(count, ids[ok], 1)
+        error = (count[:, None] + 2) * R.U32 * size
+        if accumulate:
+            ref = ref + old
+            error = error + 2 * R.U32 * (np.abs(ref) + np.abs(old)) * (count[:, None] > 0)
+        R.check(got, ref, error, torch.float32)
 
 
 @pytest.mark.parametrize("vocab", [1, 2, 255, 256, 257, 65535, 65536, 70000, 300000])
