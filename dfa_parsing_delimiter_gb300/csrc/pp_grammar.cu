@@ -17,6 +17,59 @@ namespace {
 using namespace ppd;
 using ppl::load_id;
 
+// State-transition vectors of DFAs with up to 8 states: the low half of the
+// 16-lane form of pp_stv16.cuh, at 8 instead of 28 instructions a
+// composition.  Map<16> is that form itself.
+template <int S> struct Map;
+template <> struct Map<16> {
+  using Packed = uint64_t;
+  Stv16 g;
+  static constexpr Packed ID = 0xFEDCBA9876543210ull;
+  static __device__ __forceinline__ Map id() { return {stv16_id()}; }
+  static __device__ __forceinline__ Map unpack(Packed v) { return {stv16_unpack(v)}; }
+  __device__ __forceinline__ Packed pack() const { return stv16_pack(g); }
+  __device__ __forceinline__ Map then(const Map& b) const { return {stv16_compose(g, b.g)}; }
+  __device__ __forceinline__ Map up(int d) const { return {shfl_up16(g, d)}; }
+  __device__ __forceinline__ uint32_t apply(uint32_t s) const { return stv16_apply(g, s); }
+  static __device__ __forceinline__ Packed load(const uint64_t* v, uint64_t i) { return v[i]; }
+};
+template <> struct Map<8> {
+  using Packed = uint32_t;
+  uint32_t w[2];  // lanes 0-3, 4-7, a byte each
+  static constexpr Packed ID = 0x76543210u;
+  static __device__ __forceinline__ Map id() { return {{0x03020100u, 0x07060504u}}; }
+  static __device__ __forceinline__ Map unpack(Packed v) {
+    const uint32_t ev = v & 0x0F0F0F0Fu, od = (v >> 4) & 0x0F0F0F0Fu;
+    return {{prmt(ev, od, 0x5140u), prmt(ev, od, 0x7362u)}};
+  }
+  __device__ __forceinline__ Packed pack() const { return prmt(w[0] | (w[0] >> 4), w[1] | (w[1] >> 4), 0x6420u); }
+  __device__ __forceinline__ Map then(const Map& b) const {
+    Map r;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) r.w[k] = prmt(b.w[0], b.w[1], prmt(w[k] | (w[k] >> 4), 0u, 0x0020u));
+    return r;
+  }
+  __device__ __forceinline__ Map up(int d) const {
+    return {{__shfl_up_sync(FULL, w[0], d), __shfl_up_sync(FULL, w[1], d)}};
+  }
+  __device__ __forceinline__ uint32_t apply(uint32_t s) const { return ((s & 4 ? w[1] : w[0]) >> (8 * (s & 3))) & 0xFFu; }
+  static __device__ __forceinline__ Packed load(const uint64_t* v, uint64_t i) {
+    return reinterpret_cast<const uint32_t*>(v)[2 * i];  // the low half
+  }
+};
+
+// Inclusive scan of a warp's maps.
+template <class M>
+__device__ __forceinline__ M warp_scan(M a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int d = 1; d < 32; d *= 2) {
+    const M up = a.up(d);
+    if (lane >= d) a = up.then(a);
+  }
+  return a;
+}
+
 struct VocabDfa {
   uint8_t byte_to_group[256];
   uint64_t row[PP_MAX_GROUPS];  // nibble s of row g: delta[g][s]
@@ -39,19 +92,82 @@ struct VocabArgs {
 constexpr int VOCAB_THREADS = 256;
 constexpr int VOCAB_LONG = 64;  // bytes from which a warp reads a token together
 
-__device__ __forceinline__ Stv16 vocab_walk(const uint8_t* p, int64_t n, const Stv16* step) {
-  Stv16 a = stv16_id();
-  for (int64_t k = 0; k < n; ++k) a = stv16_compose(a, step[p[k]]);
+template <class M>
+__device__ __forceinline__ M vocab_walk(const uint8_t* p, int64_t n, const M* step) {
+  M a = M::id();
+  for (int64_t k = 0; k < n; ++k) a = a.then(step[p[k]]);
   return a;
 }
 
-// A thread per token: its bytes composed one by one, then a ballot per state
-// writes 32 tokens' bits.  A token of VOCAB_LONG bytes or more is read by
-// its whole warp, a piece a lane, and the pieces are composed in order.
+// The vectors of a warp's 32 tokens (n bytes at lo each, one behind the
+// other, `all` in total, at most VOCAB_BYTES): every lane composes an equal
+// share of the bytes, whatever tokens they belong to.  What a lane has of the
+// token that it begins in is completed by a segmented scan of what the lanes
+// before it left open.  marks: the tokens' last bytes; done: the vectors of
+// the tokens that have bytes, in order.
+constexpr uint32_t VOCAB_BYTES = 2048;
+template <class M>
+__device__ __forceinline__ typename M::Packed vocab_share(const uint8_t* p, uint32_t at, uint32_t n, uint32_t all,
+                                                          const M* step, uint32_t* marks, typename M::Packed* done) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1;
+  marks[lane] = marks[lane + 32] = 0;
+  __syncwarp();
+  if (n) atomicOr(&marks[(at + n - 1) / 32], 1u << ((at + n - 1) % 32));
+  const uint32_t some = __ballot_sync(FULL, n > 0), each = (all + 31) / 32;
+  __syncwarp();
+  const uint32_t begin = min(lane * each, all), end = min(begin + each, all);
+  int l = 0;  // the token that holds byte `begin`: the first that ends after it
+#pragma unroll
+  for (int d = 16; d; d /= 2)
+    if (__shfl_sync(FULL, at + n, l + d - 1) <= begin) l += d;
+  uint32_t r = __popc(some & ((1u << (l & 31)) - 1)), first = r;
+  M a = M::id(), head = a;
+  bool ended = false;  // the lane's first token
+  for (uint32_t k = begin; k < end; ++k) {
+    a = a.then(step[p[k]]);
+    if (marks[k / 32] >> (k % 32) & 1) {
+      if (ended) done[r] = a.pack();
+      else head = a;
+      ended = true;
+      a = M::id();
+      ++r;
+    }
+  }
+  __syncwarp();
+  uint32_t cut = ended;  // a holds what is open since an end, not since the lane's first byte
+#pragma unroll 1
+  for (int d = 1; d < 32; d *= 2) {
+    const M up = a.up(d);
+    const uint32_t up_cut = __shfl_up_sync(FULL, cut, d);
+    if (lane >= d && !cut) {
+      a = up.then(a);
+      cut = up_cut;
+    }
+  }
+  const M open = a.up(1);
+  if (ended) done[first] = lane ? open.then(head).pack() : head.pack();
+  __syncwarp();
+  return n ? done[__popc(some & below)] : M::ID;
+}
+
+// A warp's 32 tokens together where they lie one behind the other with no
+// more than VOCAB_BYTES bytes, as in any ordinary vocabulary; else a thread a
+// token, but tokens of VOCAB_LONG bytes or more by their whole warp, a piece
+// a lane, the pieces composed in order.  Then a ballot per state writes 32
+// tokens' bits.
+//
+// Bound by instructions, the byte permutes of the compositions: with a thread
+// a token a warp takes as long as its longest token, 24 us for 262144 tokens
+// of 8 bytes on average under 16 states.
+template <int S>
 __global__ void __launch_bounds__(VOCAB_THREADS)
 vocab_kernel(const __grid_constant__ VocabArgs p, const __grid_constant__ VocabDfa dfa) {
-  __shared__ Stv16 step[256];
-  step[threadIdx.x] = stv16_unpack(dfa.row[dfa.byte_to_group[threadIdx.x]]);
+  using M = Map<S>;
+  __shared__ M step[256];
+  __shared__ uint32_t marks[VOCAB_THREADS / 32][VOCAB_BYTES / 32];
+  __shared__ typename M::Packed done[VOCAB_THREADS / 32][32];
+  step[threadIdx.x] = M::unpack(typename M::Packed(dfa.row[dfa.byte_to_group[threadIdx.x]]));
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const uint64_t v = uint64_t(blockIdx.x) * VOCAB_THREADS + threadIdx.x;
@@ -63,26 +179,29 @@ vocab_kernel(const __grid_constant__ VocabArgs p, const __grid_constant__ VocabD
     n = lo >= 0 && hi >= lo && hi <= p.chars_len ? hi - lo : 0;
   }
   const bool ends = there && int64_t(v) == p.end;
-  if (ends) n = 0;
-  Stv16 a = stv16_id();
-  if (n < VOCAB_LONG) a = vocab_walk(p.chars + lo, n, step);
-  for (uint32_t todo = __ballot_sync(FULL, n >= VOCAB_LONG); todo; todo &= todo - 1) {
-    const int src = __ffs(todo) - 1;
-    const int64_t at = __shfl_sync(FULL, lo, src), all = __shfl_sync(FULL, n, src);
-    const int64_t each = (all + 31) / 32, b = min(int64_t(lane) * each, all);
-    Stv16 g = vocab_walk(p.chars + at + b, min(each, all - b), step);
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const Stv16 up = shfl_up16(g, d);
-      if (lane >= d) g = stv16_compose(up, g);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = __shfl_sync(FULL, g.w[k], 31);
-      if (lane == src) a.w[k] = w;
+  const int64_t lo0 = __shfl_sync(FULL, lo, 0), hi = lo + n, before = __shfl_up_sync(FULL, hi, 1);
+  const int64_t all = __shfl_sync(FULL, hi, 31) - lo0;
+  const bool together = __all_sync(FULL, there && (lane == 0 || lo == before)) && all <= VOCAB_BYTES;
+  typename M::Packed packed;
+  if (together) {
+    packed = vocab_share<M>(p.chars + lo0, uint32_t(lo - lo0), uint32_t(n), uint32_t(all), step, marks[threadIdx.x / 32],
+                            done[threadIdx.x / 32]);
+  } else {
+    packed = (n < VOCAB_LONG ? vocab_walk(p.chars + lo, n, step) : M::id()).pack();
+    for (uint32_t todo = __ballot_sync(FULL, n >= VOCAB_LONG); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int64_t at = __shfl_sync(FULL, lo, src), size = __shfl_sync(FULL, n, src);
+      const int64_t each = (size + 31) / 32, b = min(int64_t(lane) * each, size);
+      const M g = warp_scan(vocab_walk(p.chars + at + b, min(each, size - b), step));
+      const typename M::Packed whole = __shfl_sync(FULL, g.pack(), 31);
+      if (lane == src) packed = whole;
     }
   }
-  const uint64_t vec = stv16_pack(a);
+  if (ends) {
+    n = 0;
+    packed = M::ID;
+  }
+  const uint64_t vec = S == 8 ? 0xFEDCBA9800000000ull | packed : packed;
   if (there) p.vectors[v] = vec;
   uint32_t mine = 0;
   for (int s = 0; s < dfa.n_states; ++s) {
@@ -144,21 +263,26 @@ __global__ void __launch_bounds__(128) states_short_kernel(const __grid_constant
 // the warps' totals to the threads.  A part of up to STATES_THREADS x K
 // tokens keeps its vectors in registers between the two steps; a longer one
 // reads them twice.
-constexpr int STATES_THREADS = 1024, STATES_WARPS = 32, STATES_BLOCKS = 8;
+//
+// Bound by instructions (the byte permutes of the compositions go at half
+// rate) and by the latency of its steps, not by memory.  640 threads, so that two blocks
+// share a multiprocessor and clusters of 16 fill the machine (with one block
+// a multiprocessor only 15 clusters of 8 ran at once, and the 16 rows of
+// 65537 tokens took two waves: 27 us), and so that a row of a few tokens more
+// than a power of two still has one tile a block.
+constexpr int STATES_THREADS = 640, STATES_WARPS = STATES_THREADS / 32, STATES_BLOCKS = 16;
 
 struct StateShared {
   uint64_t total[STATES_WARPS];  // the warps' vectors
   uint32_t lost[STATES_WARPS];   // a token outside the vocabulary among a warp's
   uint64_t part[STATES_BLOCKS];  // the earlier blocks' vectors, written by them
   uint32_t part_lost[STATES_BLOCKS];
-  uint64_t tile;
-  uint32_t tile_lost;
 };
 
 // One tile's vectors into registers and its warps' totals into shared memory.
-template <int K, class I>
+template <class M, int K, class I>
 __device__ __forceinline__ void states_tile(const StateArgs& p, const I* tokens, uint64_t t0, uint64_t len,
-                                            uint64_t (&vec)[K], uint32_t* bad, Stv16* before, uint32_t* dead,
+                                            typename M::Packed (&vec)[K], uint32_t* bad, M* before, uint32_t* dead,
                                             StateShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   int64_t tok[K];
@@ -168,29 +292,25 @@ __device__ __forceinline__ void states_tile(const StateArgs& p, const I* tokens,
 #pragma unroll
   for (int k = K - 1; k >= 0; --k) {
     const bool fine = tok[k] >= 0 && tok[k] < p.n_vocab;
-    vec[k] = fine ? p.vectors[tok[k]] : 0xFEDCBA9876543210ull;  // the identity
+    vec[k] = fine ? M::load(p.vectors, tok[k]) : M::ID;
     if (!fine && t0 + k < len) *bad = k;
   }
-  Stv16 a = stv16_id();
+  M a = M::id();
   if (t0 < len) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) a = stv16_compose(a, stv16_unpack(vec[k]));
+    for (int k = 0; k < K; ++k) a = a.then(M::unpack(vec[k]));
   }
   __syncwarp();
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const Stv16 up = shfl_up16(a, d);
-    if (lane >= d) a = stv16_compose(up, a);
-  }
-  *before = shfl_up16(a, 1);
+  a = warp_scan(a);
+  *before = a.up(1);
   *dead = __ballot_sync(FULL, *bad < K);
   if (lane == 31) {
-    sh.total[warp] = stv16_pack(a);
+    sh.total[warp] = a.pack();
     sh.lost[warp] = *dead;
   }
 }
 
-template <int K, class I>
+template <class M, int K, class I>
 __device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, StateShared& sh, uint32_t* staged) {
   constexpr uint32_t TILE = STATES_THREADS * K;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -200,112 +320,135 @@ __device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, S
   const uint64_t len = min(uint64_t(row_length(p, row)), end);
   const I* tokens = static_cast<const I*>(p.tokens) + row * p.tstride;
   uint8_t* out = p.states + row * p.sstride;
-  uint64_t vec[K];
-  uint32_t bad, dead, s = first_state(p, row);
-  Stv16 before;
+  typename M::Packed vec[K];
+  uint32_t bad = K, dead = 0, s = first_state(p, row);
+  M before = M::id(), all = M::id();
+  uint32_t gone = 0;
   if (rank == 0 && threadIdx.x == 0) out[0] = uint8_t(s);
-  if (blocks > 1) {
-    // the part's total, by warp 0
-    Stv16 all = stv16_id();
-    uint32_t gone = 0;
+  const bool kept = blocks > 1 && end - begin <= TILE;  // one tile, whose vectors stay
+#pragma unroll 1
+  for (int pass = blocks > 1 ? 0 : 1; pass < 2; ++pass) {
+#pragma unroll 1
     for (uint64_t base = begin; base < end; base += TILE) {
-      states_tile<K>(p, tokens, base + uint64_t(threadIdx.x) * K, len, vec, &bad, &before, &dead, sh);
-      __syncthreads();
-      if (warp == 0) {
-        Stv16 a = stv16_unpack(sh.total[lane]);
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const Stv16 up = shfl_up16(a, d);
-          if (lane >= d) a = stv16_compose(up, a);
-        }
-        all = stv16_compose(all, a);  // lane 31 has them all
-        gone |= __ballot_sync(FULL, sh.lost[lane] != 0);
+      const uint64_t t0 = base + uint64_t(threadIdx.x) * K;
+      if (pass == 0 || !kept) {
+        states_tile(p, tokens, t0, len, vec, &bad, &before, &dead, sh);
+        __syncthreads();
       }
+      if (pass == 0) {  // the part's total, by warp 0
+        if (warp == 0) {
+          const M a = warp_scan(lane < STATES_WARPS ? M::unpack(typename M::Packed(sh.total[lane])) : M::id());
+          all = all.then(a);  // lane 31 has them all
+          gone |= __ballot_sync(FULL, lane < STATES_WARPS && sh.lost[lane] != 0);
+        }
+        if (base + TILE < end) __syncthreads();
+        continue;
+      }
+      uint32_t q = s;
+#pragma unroll 4
+      for (int w = 0; w < STATES_WARPS; ++w) {
+        if (w == warp) q = s;
+        if (s != PP_STATE_NONE) s = sh.lost[w] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.total[w], s);
+      }
+      if (q != PP_STATE_NONE && lane > 0) q = before.apply(q);
+      if (dead & ((1u << lane) - 1)) q = PP_STATE_NONE;
+#pragma unroll
+      for (int g = 0; g < K / 4; ++g) {
+        uint32_t four = 0;
+#pragma unroll
+        for (int k = 4 * g; k < 4 * g + 4; ++k) {
+          if (uint32_t(k) >= bad) q = PP_STATE_NONE;
+          if (q != PP_STATE_NONE) q = nib_apply(vec[k], q);
+          four |= q << (8 * (k - 4 * g));
+        }
+        staged[threadIdx.x * (K / 4) + g] = four;
+      }
+      __syncthreads();
+      // the tile's states, which begin at any byte, in words of memory
+      uint8_t* to = out + base + 1;
+      const uint32_t n = uint32_t(min(uint64_t(TILE), end - base));
+      const uint32_t skip = min(uint32_t(-reinterpret_cast<intptr_t>(to)) & 3u, n), words = (n - skip) / 4;
+      for (uint32_t w = threadIdx.x; w < words; w += STATES_THREADS)
+        reinterpret_cast<uint32_t*>(to + skip)[w] = __funnelshift_r(staged[w], staged[w + 1], 8 * skip);
+      const uint32_t rest = n - skip - 4 * words;
+      if (threadIdx.x < skip) to[threadIdx.x] = reinterpret_cast<uint8_t*>(staged)[threadIdx.x];
+      if (threadIdx.x < rest) to[n - rest + threadIdx.x] = reinterpret_cast<uint8_t*>(staged)[n - rest + threadIdx.x];
       if (base + TILE < end) __syncthreads();
     }
-    if (warp == 0 && lane == 31)
-      for (uint32_t q = rank + 1; q < blocks; ++q) {
-        const uint64_t v = stv16_pack(all);
-        uint32_t a, b;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part[rank]))), "r"(q));
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part_lost[rank]))), "r"(q));
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(gone) : "memory");
-      }
-    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-    for (uint32_t q = 0; q < rank; ++q)
-      if (s != PP_STATE_NONE) s = sh.part_lost[q] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.part[q], s);
-  }
-  const bool kept = blocks > 1 && end - begin <= TILE;  // the one tile's vectors are still here
-  for (uint64_t base = begin; base < end; base += TILE) {
-    const uint64_t t0 = base + uint64_t(threadIdx.x) * K;
-    if (!kept) {
-      states_tile<K>(p, tokens, t0, len, vec, &bad, &before, &dead, sh);
-      __syncthreads();
+    if (pass == 0) {
+      if (warp == 0 && lane == 31)
+        for (uint32_t q = rank + 1; q < blocks; ++q) {
+          const uint64_t v = all.pack();
+          uint32_t a, b;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part[rank]))), "r"(q));
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part_lost[rank]))), "r"(q));
+          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(gone) : "memory");
+        }
+      asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+      for (uint32_t q = 0; q < rank; ++q)
+        if (s != PP_STATE_NONE) s = sh.part_lost[q] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.part[q], s);
     }
-    uint32_t q = s;
-    for (int w = 0; w < STATES_WARPS; ++w) {
-      if (w == warp) q = s;
-      if (s != PP_STATE_NONE) s = sh.lost[w] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.total[w], s);
-    }
-    if (q != PP_STATE_NONE && lane > 0) q = stv16_apply(before, q);
-    if (dead & ((1u << lane) - 1)) q = PP_STATE_NONE;
-#pragma unroll
-    for (int g = 0; g < K / 4; ++g) {
-      uint32_t four = 0;
-#pragma unroll
-      for (int k = 4 * g; k < 4 * g + 4; ++k) {
-        if (uint32_t(k) >= bad) q = PP_STATE_NONE;
-        if (q != PP_STATE_NONE) q = nib_apply(vec[k], q);
-        four |= q << (8 * (k - 4 * g));
-      }
-      staged[threadIdx.x * (K / 4) + g] = four;
-    }
-    __syncthreads();
-    // the tile's states, which begin at any byte, in words of memory
-    uint8_t* to = out + base + 1;
-    const uint32_t n = uint32_t(min(uint64_t(TILE), end - base));
-    const uint32_t skip = min(uint32_t(-reinterpret_cast<intptr_t>(to)) & 3u, n), words = (n - skip) / 4;
-    for (uint32_t w = threadIdx.x; w < words; w += STATES_THREADS)
-      reinterpret_cast<uint32_t*>(to + skip)[w] = __funnelshift_r(staged[w], staged[w + 1], 8 * skip);
-    const uint32_t rest = n - skip - 4 * words;
-    if (threadIdx.x < skip) to[threadIdx.x] = reinterpret_cast<uint8_t*>(staged)[threadIdx.x];
-    if (threadIdx.x < rest) to[n - rest + threadIdx.x] = reinterpret_cast<uint8_t*>(staged)[n - rest + threadIdx.x];
-    if (base + TILE < end) __syncthreads();
   }
 }
 
-template <int K>
-__global__ void __launch_bounds__(STATES_THREADS, 1)
+template <int S, int K>
+__global__ void __launch_bounds__(STATES_THREADS, 2)
 states_kernel(const __grid_constant__ StateArgs p, uint32_t blocks, uint32_t each) {
   __shared__ StateShared sh;
   __shared__ __align__(16) uint32_t staged[STATES_THREADS * K / 4 + 1];
   switch (p.type) {
-    case PP_U8: return states_row<K, uint8_t>(p, blocks, each, sh, staged);
-    case PP_I8: return states_row<K, int8_t>(p, blocks, each, sh, staged);
-    case PP_I32: return states_row<K, int32_t>(p, blocks, each, sh, staged);
-    default: return states_row<K, int64_t>(p, blocks, each, sh, staged);
+    case PP_U8: return states_row<Map<S>, K, uint8_t>(p, blocks, each, sh, staged);
+    case PP_I8: return states_row<Map<S>, K, int8_t>(p, blocks, each, sh, staged);
+    case PP_I32: return states_row<Map<S>, K, int32_t>(p, blocks, each, sh, staged);
+    default: return states_row<Map<S>, K, int64_t>(p, blocks, each, sh, staged);
   }
+}
+using StatesKernel = void (*)(StateArgs, uint32_t, uint32_t);
+const StatesKernel STATES_KERNEL[4] = {states_kernel<8, 4>, states_kernel<8, 8>, states_kernel<16, 4>, states_kernel<16, 8>};
+
+cudaLaunchConfig_t states_config(uint32_t blocks, uint32_t grid, cudaLaunchAttribute* at, cudaStream_t stream) {
+  std::memset(at, 0, sizeof *at);
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = blocks;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(STATES_THREADS);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
 }
 
 cudaError_t launch_states(const StateArgs& p, cudaStream_t stream) {
-  // a cluster shares a row while there are fewer blocks than 152
-  // multiprocessors and a part keeps 1024 tokens
+  static ppi::DeviceOnce once;
+  static uint32_t most[ppi::MAX_DEVICES];  // blocks of the largest cluster
+  int dev;
+  cudaError_t e = ppi::current_device(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run(dev, [](int d) {
+    cudaError_t e = cudaSuccess;
+    for (int k = 0; k < 4 && e == cudaSuccess; ++k)
+      e = cudaFuncSetAttribute(STATES_KERNEL[k], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = states_config(STATES_BLOCKS, STATES_BLOCKS, &at, nullptr);
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, STATES_KERNEL[3], &cfg);
+    most[d] = n > 0 ? STATES_BLOCKS : 8;
+    return e;
+  });
+  if (e != cudaSuccess) return e;
+  // a cluster shares a row while there are fewer than two blocks for each of
+  // 152 multiprocessors and a part keeps 1024 tokens
   uint32_t blocks = 1;
-  while (blocks < STATES_BLOCKS && uint64_t(p.n_rows) * blocks < 152 && p.n_cols / (2 * blocks) >= 1024) blocks *= 2;
+  while (blocks < most[dev] && uint64_t(p.n_rows) * blocks < 304 && p.n_cols / (2 * blocks) >= 1024) blocks *= 2;
+  if (uint64_t(p.n_rows) * blocks >= (uint64_t(1) << 31)) blocks = 1;
   const uint32_t each = uint32_t((uint64_t(p.n_cols) + blocks - 1) / blocks);
-  cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at;
-  std::memset(&at, 0, sizeof at);
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = blocks;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.gridDim = dim3(p.n_rows * blocks);
-  cfg.blockDim = dim3(STATES_THREADS);
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, each <= STATES_THREADS * 4 ? states_kernel<4> : states_kernel<16>, p, blocks, each);
+  const cudaLaunchConfig_t cfg = states_config(blocks, p.n_rows * blocks, &at, stream);
+  return cudaLaunchKernelEx(&cfg, STATES_KERNEL[(p.n_states > 8 ? 2 : 0) + (each > STATES_THREADS * 4 ? 1 : 0)], p, blocks, each);
 }
 
 // Per state, whether an accepting state can be reached from it without
@@ -354,7 +497,8 @@ pp_rc pp_vocab_grammar(const int32_t* d_offsets, const uint8_t* d_chars, size_t 
   const VocabArgs p = {d_offsets, d_chars, int64_t(chars_len), uint32_t(n_vocab), end_token,
                        d_vectors, d_allowed, allowed_stride};
   const uint64_t blocks = (n_vocab + VOCAB_THREADS - 1) / VOCAB_THREADS;
-  vocab_kernel<<<unsigned(blocks), VOCAB_THREADS, 0, stream>>>(p, g);
+  if (dfa->n_states <= 8) vocab_kernel<8><<<unsigned(blocks), VOCAB_THREADS, 0, stream>>>(p, g);
+  else vocab_kernel<16><<<unsigned(blocks), VOCAB_THREADS, 0, stream>>>(p, g);
   return ppl::rc_of(cudaGetLastError());
 }
 

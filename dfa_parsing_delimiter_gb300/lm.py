@@ -126,12 +126,20 @@ class Grammar:
     def __init__(self, vectors: torch.Tensor, allowed: torch.Tensor, n_vocab: int, desc):
         _on(vectors, allowed, "vectors", (torch.int64,), 1)
         _on(allowed, allowed, "allowed", (torch.int32,), 2)
-        self.vectors, self.allowed, self.n_vocab = vectors, allowed, int(n_vocab)
-        self.n_states, self.start_state = int(desc.n_states), int(desc.start_state)
-        self.accept_mask = int(desc.accept_mask)
+        self._set(vectors, allowed, int(n_vocab), desc)
         _need(vectors.is_contiguous() and vectors.size(0) == self.n_vocab, "vectors: want one a token")
         _need(allowed.size(0) == self.n_states and allowed.size(1) * 32 >= self.n_vocab
               and _matrix_stride(allowed, "allowed") >= allowed.size(1), "allowed: want a row a state")
+
+    def _set(self, vectors, allowed, n_vocab, desc) -> None:
+        self.vectors, self.allowed, self.n_vocab = vectors, allowed, n_vocab
+        self.n_states, self.start_state, self.accept_mask = desc.n_states, desc.start_state, desc.accept_mask
+
+    @classmethod
+    def _of(cls, vectors, allowed, n_vocab, desc) -> "Grammar":
+        g = cls.__new__(cls)
+        g._set(vectors, allowed, n_vocab, desc)
+        return g
 
     def accepts(self, states: torch.Tensor) -> torch.Tensor:
         """Whether texts that end in these states are complete."""
@@ -156,7 +164,7 @@ def vocab_grammar(offsets: torch.Tensor, chars: torch.Tensor, desc=None, end_id=
     _call(pp.lib().pp_vocab_grammar, "pp_vocab_grammar", offsets, stream, offsets.data_ptr(),
           chars.data_ptr(), chars.size(0), n, ctypes.byref(desc), -1 if end_id is None else int(end_id),
           vectors.data_ptr(), allowed.data_ptr(), words)
-    return Grammar(vectors, allowed, n, desc)
+    return Grammar._of(vectors, allowed, n, desc)
 
 
 def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=None, out=None,
