@@ -9,7 +9,7 @@
 // the end of the next chunk is finished by the chunk it begins in; a longer
 // one leaves a partial sum per chunk, added up in order by a last kernel.
 // Up to SORT_CAP positions one thread-block cluster sorts in distributed
-// shared memory, while the other blocks of the same launch write the zeros
+// shared memory, while the first blocks of the next kernel write the zeros
 // of the rows that no id names; more go through global memory in passes.
 #include <algorithm>
 #include <cstring>
@@ -213,6 +213,12 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_move_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------ zero rows
+// The kernels of one pp_embed_grad follow each other by programmatic
+// dependent launch: each lets the next one's blocks start early, and a block
+// that needs what the kernel before wrote waits for that one's end first.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct ZeroArgs {
   void* out;
   uint64_t row_bytes, stride_bytes;  // of a row of the gradient
@@ -259,6 +265,36 @@ zero_kernel(const __grid_constant__ ZeroArgs z, const uint32_t* key, uint32_t n)
   zero_rows<256>(z, bits, base, uint32_t(min(uint64_t(ZERO_SPAN), z.n_vocab - base)));
 }
 
+// From the ids themselves: block `me` of `all` looks at its share of the rows
+// against every id, `SPAN` rows at a time (bits: that many).
+constexpr uint32_t SPAN = 1u << 18;
+template <int THREADS>
+__device__ __noinline__ void zero_scan(const ZeroArgs& z, const SortArgs& s, uint32_t me, uint32_t all, uint32_t* bits) {
+  const uint64_t each = (z.n_vocab + all - 1) / all;
+  const uint64_t v0 = me * each, v1 = min(v0 + each, uint64_t(z.n_vocab));
+  // from a place of its own on, as blocks that read the same ids at the same
+  // time wait for the same lines
+  const uint32_t turn = uint32_t(uint64_t(s.n) * me / all);
+  for (uint64_t base = v0; base < v1; base += SPAN) {
+    const uint32_t span = uint32_t(min(uint64_t(SPAN), v1 - base));
+    for (uint32_t w = threadIdx.x; w * 32 < span; w += THREADS) bits[w] = 0;
+    __syncthreads();
+    auto mark = [&](uint32_t, auto id) {
+      // an id below 0 turns into one far past the span
+      const uint64_t j = sizeof(id) == 8 ? uint64_t(id) - base : uint32_t(id) - uint32_t(base);
+      if (j < span) atomicOr(&bits[j / 32], 1u << (j % 32));
+    };
+    ppl::for_ids<8>(s.ids, s.type, s.id_stride, turn + threadIdx.x, s.n, THREADS, mark);
+    ppl::for_ids<8>(s.ids, s.type, s.id_stride, threadIdx.x, turn, THREADS, mark);
+    __syncthreads();
+    const uint64_t pad = uint64_t(s.pad) - base;  // has no gradient, so its row is zeros
+    if (pad < span && threadIdx.x == 0) bits[pad / 32] &= ~(1u << (pad % 32));
+    __syncthreads();
+    zero_rows<THREADS>(z, bits, base, span);
+    __syncthreads();
+  }
+}
+
 // ------------------------------------------------- sort in one cluster
 // Block r of the cluster holds pairs r PER .. (r + 1) PER - 1 of the list,
 // PER = 1024 ITEMS.  Per pass a block ranks its pairs' digits (per warp by
@@ -268,14 +304,11 @@ zero_kernel(const __grid_constant__ ZeroArgs z, const uint32_t* key, uint32_t n)
 constexpr int CS_THREADS = 1024, CS_WARPS = 32, CS_BITS = 9, CS_BINS = 1 << CS_BITS;
 constexpr int CS_BLOCKS = 16, CS_ITEMS = 8;
 constexpr uint32_t SORT_CAP = CS_THREADS * CS_ITEMS * CS_BLOCKS;
-constexpr uint32_t CS_SPAN = 1u << 18;  // rows that a zeroing block looks at together
 
 struct ClusterArgs {
   SortArgs s;  // key_out, pos_out: the sorted list
   int32_t blocks, bits, passes;
   uint32_t* n_long;  // set to 0 for the sums
-  int32_t zero;      // write the rows that no id names
-  ZeroArgs z;
 };
 
 __device__ __forceinline__ uint32_t smem_of(const void* p, uint32_t rank) {
@@ -283,11 +316,6 @@ __device__ __forceinline__ uint32_t smem_of(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   return r;
 }
-// The kernels of one pp_embed_grad follow each other by programmatic
-// dependent launch: each lets the next one's blocks start, and waits for
-// the end of the one before it here, before it reads what that one wrote.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -302,33 +330,6 @@ __global__ void __launch_bounds__(CS_THREADS, 1) cluster_sort_kernel(const __gri
   __shared__ uint32_t sums[CS_BINS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   let_next_start();
-  if (blockIdx.x >= uint32_t(p.blocks)) {  // zeros
-    uint32_t* bits = reinterpret_cast<uint32_t*>(item);
-    const uint64_t each = (p.z.n_vocab + gridDim.x - p.blocks - 1) / (gridDim.x - p.blocks);
-    const uint64_t v0 = (blockIdx.x - p.blocks) * each, v1 = min(v0 + each, uint64_t(p.z.n_vocab));
-    for (uint64_t base = v0; base < v1; base += CS_SPAN) {
-      const uint32_t span = uint32_t(min(uint64_t(CS_SPAN), v1 - base));
-      for (uint32_t w = threadIdx.x; w * 32 < span; w += CS_THREADS) bits[w] = 0;
-      __syncthreads();
-      // from a place of its own on, as blocks that read the same ids at the
-      // same time wait for the same lines
-      const uint32_t turn = uint32_t(uint64_t(p.s.n) * blockIdx.x / gridDim.x);
-      auto mark = [&](uint32_t, auto id) {
-        // an id below 0 turns into one far past the span
-        const uint64_t j = sizeof(id) == 8 ? uint64_t(id) - base : uint32_t(id) - uint32_t(base);
-        if (j < span) atomicOr(&bits[j / 32], 1u << (j % 32));
-      };
-      ppl::for_ids<8>(p.s.ids, p.s.type, p.s.id_stride, turn + threadIdx.x, p.s.n, CS_THREADS, mark);
-      ppl::for_ids<8>(p.s.ids, p.s.type, p.s.id_stride, threadIdx.x, turn, CS_THREADS, mark);
-      __syncthreads();
-      const uint64_t pad = uint64_t(p.s.pad) - base;  // has no gradient, so its row is zeros
-      if (pad < span && threadIdx.x == 0) bits[pad / 32] &= ~(1u << (pad % 32));
-      __syncthreads();
-      zero_rows<CS_THREADS>(p.z, bits, base, span);
-      __syncthreads();
-    }
-    return;
-  }
   const uint32_t rank = blockIdx.x, n_bins = 1u << p.bits;
   if (rank == 0 && threadIdx.x == 0) *p.n_long = 0;
   for (int pass = 0; pass < p.passes; ++pass) {
@@ -441,9 +442,12 @@ struct SumArgs {
   uint64_t width;
   uint32_t n_chunks, chunk;
   uint32_t *n_long, *longs;  // chunks in which long runs begin
+  uint32_t n_zero;           // blocks that write zeros, before those that sum
+  ZeroArgs z;
+  SortArgs s;
 };
 
-constexpr int SUM_WARPS = 8;
+constexpr int SUM_WARPS = 16, JOIN_WARPS = 8;
 constexpr int SUM_COLS = 32 * UNIT;  // columns a warp
 constexpr uint32_t NO_KEY = 0xFFFFFFFFu;
 
@@ -546,13 +550,19 @@ __device__ __forceinline__ void add_staged(const T* at, float (&a)[UNIT]) {
 // (a lane reads back what it copied itself, so nothing synchronises).
 constexpr int RING_BYTES = 4096;  // a warp
 template <class T, class O, bool WIDE>
-__global__ void __launch_bounds__(SUM_WARPS * 32) sum_kernel(const __grid_constant__ SumArgs p) {
-  constexpr uint32_t DEPTH = RING_BYTES / (SUM_COLS * sizeof(T));  // rows: 8, of 32-bit values 4
+__global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_constant__ SumArgs p) {
+  constexpr uint32_t DEPTH = RING_BYTES / (SUM_COLS * sizeof(T));  // rows: 6, of 32-bit values 3
   __shared__ __align__(16) char ring_mem[SUM_WARPS][RING_BYTES];
   const int lane = threadIdx.x & 31;
-  const uint64_t me = uint64_t(blockIdx.x) * SUM_WARPS + threadIdx.x / 32;
-  const uint64_t c = me / p.slices, c0 = me % p.slices * SUM_COLS;
   let_next_start();
+  if (blockIdx.x < p.n_zero) {
+    static_assert(sizeof ring_mem >= SPAN / 8, "the ring's memory holds the rows' bits");
+    zero_scan<SUM_WARPS * 32>(p.z, p.s, blockIdx.x, p.n_zero, reinterpret_cast<uint32_t*>(&ring_mem[0][0]));
+    wait_for_previous();  // so that the end of this kernel is the end of both
+    return;
+  }
+  const uint64_t me = uint64_t(blockIdx.x - p.n_zero) * SUM_WARPS + threadIdx.x / 32;
+  const uint64_t c = me / p.slices, c0 = me % p.slices * SUM_COLS;
   wait_for_previous();
   if (c >= p.n_chunks) return;
   const uint32_t L = p.chunk, n = p.n;
@@ -609,8 +619,8 @@ __global__ void __launch_bounds__(SUM_WARPS * 32) sum_kernel(const __grid_consta
 // a warp per eighth of the pieces, in order.
 constexpr int JOIN_BLOCKS = 256;
 template <class O, bool WIDE>
-__global__ void __launch_bounds__(SUM_WARPS * 32) join_kernel(const __grid_constant__ SumArgs p) {
-  __shared__ float part[SUM_WARPS][SUM_COLS];
+__global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ SumArgs p) {
+  __shared__ float part[JOIN_WARPS][SUM_COLS];
   __shared__ uint32_t more;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const uint64_t c0 = uint64_t(blockIdx.y) * SUM_COLS, L = p.chunk;
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(SUM_WARPS * 32) join_kernel(const __grid_const
       go = m == blockDim.x;
       __syncthreads();
     }
-    const uint32_t each = (n + 1 + SUM_WARPS - 1) / SUM_WARPS;
+    const uint32_t each = (n + 1 + JOIN_WARPS - 1) / JOIN_WARPS;
     const uint32_t lo = min(warp * each, n + 1), hi = min(lo + each, n + 1);
     float a[UNIT] = {};
     for (uint32_t q = lo; q < hi; q += 6) {
@@ -654,7 +664,7 @@ __global__ void __launch_bounds__(SUM_WARPS * 32) join_kernel(const __grid_const
     if (warp == 0) {
 #pragma unroll
       for (int k = 0; k < UNIT; ++k)
-        for (int w = 1; w < SUM_WARPS; ++w) a[k] += part[w][k * 32 + lane];
+        for (int w = 1; w < JOIN_WARPS; ++w) a[k] += part[w][k * 32 + lane];
       write_sum<O, WIDE>(p, id, c0, a);
     }
     __syncthreads();
@@ -677,23 +687,18 @@ cudaError_t keep_pool_memory() {
   });
 }
 
-// Per device: attributes of the cluster sort, and how many clusters of each
-// kind run at a time.
-struct ClusterSetup {
-  int blocks;        // of the largest cluster
-  int active[3][5];  // [kind of cluster_sort_kernel][log2 of the blocks]
-};
+// Per device: attributes of the cluster sort, and its largest cluster.
 constexpr int CLUSTER_ITEMS[3] = {1, 2, 8};
 using ClusterKernel = void (*)(ClusterArgs);
 const ClusterKernel CLUSTER_KERNEL[3] = {cluster_sort_kernel<1>, cluster_sort_kernel<2>, cluster_sort_kernel<8>};
 
-cudaLaunchConfig_t cluster_config(int kind, int blocks, int grid, cudaLaunchAttribute* at, cudaStream_t stream) {
+cudaLaunchConfig_t cluster_config(int kind, int blocks, cudaLaunchAttribute* at, cudaStream_t stream) {
   std::memset(at, 0, sizeof *at);
   at->id = cudaLaunchAttributeClusterDimension;
   at->val.clusterDim.x = blocks;
   at->val.clusterDim.y = at->val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(CS_THREADS);
   cfg.dynamicSmemBytes = cluster_smem(CLUSTER_ITEMS[kind]);
   cfg.stream = stream;
@@ -702,30 +707,27 @@ cudaLaunchConfig_t cluster_config(int kind, int blocks, int grid, cudaLaunchAttr
   return cfg;
 }
 
-cudaError_t cluster_setup(const ClusterSetup** out) {
+cudaError_t cluster_setup(int* blocks) {
   static ppi::DeviceOnce once;
-  static ClusterSetup setup[ppi::MAX_DEVICES];
+  static int most[ppi::MAX_DEVICES];
   int dev;
   cudaError_t e = ppi::current_device(&dev);
   if (e != cudaSuccess) return e;
   e = once.run(dev, [](int d) {
-    ClusterSetup& s = setup[d];
     for (int k = 0; k < 3; ++k) {
       cudaError_t e = cudaFuncSetAttribute(CLUSTER_KERNEL[k], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            int(cluster_smem(CLUSTER_ITEMS[k])));
       if (e == cudaSuccess) e = cudaFuncSetAttribute(CLUSTER_KERNEL[k], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      for (int c = 0; e == cudaSuccess && c < 5; ++c) {
-        cudaLaunchAttribute at;
-        const cudaLaunchConfig_t cfg = cluster_config(k, 1 << c, 1 << c, &at, nullptr);
-        e = cudaOccupancyMaxActiveClusters(&s.active[k][c], CLUSTER_KERNEL[k], &cfg);
-      }
       if (e != cudaSuccess) return e;
     }
-    s.blocks = CS_BLOCKS;
-    while (s.blocks > 8 && s.active[2][4] < 1) s.blocks /= 2;
-    return cudaSuccess;
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = cluster_config(2, CS_BLOCKS, &at, nullptr);
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, CLUSTER_KERNEL[2], &cfg);
+    most[d] = n > 0 ? CS_BLOCKS : 8;  // 8 blocks run on any device
+    return e;
   });
-  *out = &setup[dev];
+  *blocks = most[dev];
   return e;
 }
 
@@ -735,22 +737,19 @@ int key_bits(uint32_t n_vocab) {
   return bits;
 }
 
-cudaError_t launch_cluster_sort(ClusterArgs& p, const ClusterSetup& setup, cudaStream_t stream) {
+cudaError_t launch_cluster_sort(ClusterArgs& p, int blocks, cudaStream_t stream) {
   // pairs a thread: the fewest that the blocks hold, as the sort is bound by
   // its steps' latencies
-  const uint32_t n = p.s.n, threads = uint32_t(CS_THREADS * setup.blocks);
+  const uint32_t n = p.s.n, threads = uint32_t(CS_THREADS * blocks);
   const int kind = n <= threads ? 0 : n <= 2 * threads ? 1 : 2;
-  int c = 0;
-  while ((1 << c) < setup.blocks && uint32_t(CLUSTER_ITEMS[kind] * CS_THREADS << c) < n) ++c;
+  int c = 1;
+  while (c < blocks && uint32_t(CLUSTER_ITEMS[kind] * CS_THREADS * c) < n) c *= 2;
   const int bits = key_bits(p.s.n_vocab);
   p.passes = (bits + CS_BITS - 1) / CS_BITS;
   p.bits = (bits + p.passes - 1) / p.passes;
-  p.blocks = 1 << c;
-  // the zeroing blocks are as many as run beside the sort at once: the rows
-  // are dealt out evenly, so blocks of a second wave would double the time
-  const int clusters = p.zero ? std::max(setup.active[kind][c], 2) : 1;
+  p.blocks = c;
   cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = cluster_config(kind, 1 << c, clusters << c, &at, stream);
+  const cudaLaunchConfig_t cfg = cluster_config(kind, c, &at, stream);
   return cudaLaunchKernelEx(&cfg, CLUSTER_KERNEL[kind], p);
 }
 
@@ -791,12 +790,11 @@ template <class T, class O>
 cudaError_t launch_sums(const SumArgs& p, cudaStream_t stream) {
   const bool wide = rows_aligned(p.grad, sizeof(T), p.gstride, p.n) &&
                     rows_aligned(p.out, sizeof(O), p.ostride, p.n_vocab);
-  const unsigned grid = unsigned((uint64_t(p.n_chunks) * p.slices + SUM_WARPS - 1) / SUM_WARPS);
+  const unsigned grid = unsigned(p.n_zero + (uint64_t(p.n_chunks) * p.slices + SUM_WARPS - 1) / SUM_WARPS);
   const dim3 join(std::min(p.n_chunks, uint32_t(JOIN_BLOCKS)), p.slices);
-  const dim3 block(SUM_WARPS * 32);
-  cudaError_t e = launch_next(wide ? sum_kernel<T, O, true> : sum_kernel<T, O, false>, grid, block, p, stream);
+  cudaError_t e = launch_next(wide ? sum_kernel<T, O, true> : sum_kernel<T, O, false>, grid, SUM_WARPS * 32, p, stream);
   if (e == cudaSuccess && p.n_chunks > 2)
-    e = launch_next(wide ? join_kernel<O, true> : join_kernel<O, false>, join, block, p, stream);
+    e = launch_next(wide ? join_kernel<O, true> : join_kernel<O, false>, join, JOIN_WARPS * 32, p, stream);
   return e;
 }
 
@@ -838,8 +836,8 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   if (!n_vocab || !dim || (!n && accumulate)) return PP_OK;
   cudaError_t e = keep_pool_memory();
   if (e != cudaSuccess) return ppl::rc_of(e);
-  const ClusterSetup* setup;
-  if ((e = cluster_setup(&setup)) != cudaSuccess) return ppl::rc_of(e);
+  int blocks, n_sm;
+  if ((e = cluster_setup(&blocks)) != cudaSuccess || (e = ppi::sm_count(&n_sm)) != cudaSuccess) return ppl::rc_of(e);
   const size_t size = ppl::fsize(out_type);
   SumArgs p;
   std::memset(&p, 0, sizeof p);
@@ -876,7 +874,7 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   s.n_vocab = uint32_t(n_vocab);
   s.pad = padding_id;
   s.n_tiles = uint32_t((n + SORT_TILE - 1) / SORT_TILE);
-  const bool one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * setup->blocks;  // one cluster sorts
+  const bool one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * blocks;  // one cluster sorts
   const size_t counts = one ? 0 : size_t(s.n_tiles) * DIGITS, pairs = (n + 3) / 4 * 4;
   const size_t parts = p.n_chunks > 2 ? size_t(p.n_chunks) * 2 * p.width : 0;
   void* scratch = nullptr;
@@ -897,9 +895,12 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
     c.s.key_out = key[0];
     c.s.pos_out = pos[0];
     c.n_long = p.n_long;
-    c.zero = !accumulate;
-    c.z = z;
-    e = launch_cluster_sort(c, *setup, stream);
+    e = launch_cluster_sort(c, blocks, stream);
+    if (!accumulate) {  // two blocks a multiprocessor, but none for less than 64 KiB
+      p.z = z;
+      p.s = s;
+      p.n_zero = uint32_t(std::min<uint64_t>(2 * n_sm, n_vocab * dim * size / 65536 + 1));
+    }
   } else {
     e = cudaMemsetAsync(p.n_long, 0, 4, stream);
     if (e == cudaSuccess) e = launch_sort(s, key, pos, &at, stream);
@@ -910,7 +911,7 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   }
   p.key = key[at];
   p.pos = pos[at];
-  if (e == cudaSuccess && n)
+  if (e == cudaSuccess)
     e = with_type(grad_type, [&](auto t) {
       return with_type(out_type, [&](auto o) { return launch_sums<decltype(t), decltype(o)>(p, stream); });
     });
