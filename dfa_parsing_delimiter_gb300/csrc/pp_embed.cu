@@ -53,26 +53,35 @@ struct EmbedArgs {
 };
 
 // blockDim.x threads move a row, blockDim.y rows a block; U columns a thread
-// and step (8 where rows are aligned to 16 bytes in both arrays).
+// and step (8 where rows are aligned to 16 bytes in both arrays), AHEAD
+// steps' loads on their way before the first store: the compiler cannot know
+// that the arrays do not overlap.
+constexpr int EMBED_THREADS = 256, AHEAD = 4;
 template <class T, class O, int U>
-__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedArgs p) {
+__global__ void __launch_bounds__(EMBED_THREADS) embed_kernel(const __grid_constant__ EmbedArgs p) {
   const uint64_t i = uint64_t(blockIdx.x) * blockDim.y + threadIdx.y;
   if (i >= p.n) return;
   const int64_t id = load_id(p.ids, p.type, i * p.id_stride);
   const bool there = id >= 0 && id < p.n_vocab && id != p.pad;
   const T* row = static_cast<const T*>(p.table) + (there ? uint64_t(id) * p.tstride : 0);
   O* out = static_cast<O*>(p.out) + i * p.ostride;
-  for (uint64_t c = uint64_t(threadIdx.x) * U; c < p.dim; c += uint64_t(blockDim.x) * U) {
-    if (U > 1 && c + U <= p.dim) {
-      Pack<T, U> x;
-      Pack<O, U> y;
-      if (there) x = *reinterpret_cast<const Pack<T, U>*>(row + c);
+  const uint64_t step = uint64_t(blockDim.x) * U;
+  for (uint64_t c = uint64_t(threadIdx.x) * U; c < p.dim; c += step * AHEAD) {
+    Pack<T, U> x[AHEAD];
 #pragma unroll
-      for (int k = 0; k < U; ++k) y.v[k] = from_f<O>(there ? to_f(x.v[k]) * p.scale : 0.f);
-      *reinterpret_cast<Pack<O, U>*>(out + c) = y;
-    } else {
-      for (uint64_t k = c; k < c + U && k < p.dim; ++k)
-        out[k] = from_f<O>(there ? to_f(row[k]) * p.scale : 0.f);
+    for (int g = 0; g < AHEAD; ++g)
+      if (there && c + g * step + U <= p.dim) x[g] = *reinterpret_cast<const Pack<T, U>*>(row + c + g * step);
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+      const uint64_t at = c + g * step;
+      if (at + U <= p.dim) {
+        Pack<O, U> y;
+#pragma unroll
+        for (int k = 0; k < U; ++k) y.v[k] = from_f<O>(there ? to_f(x[g].v[k]) * p.scale : 0.f);
+        *reinterpret_cast<Pack<O, U>*>(out + at) = y;
+      } else if (U > 1) {
+        for (uint64_t k = at; k < p.dim; ++k) out[k] = from_f<O>(there ? to_f(row[k]) * p.scale : 0.f);
+      }
     }
   }
 }
@@ -87,9 +96,12 @@ cudaError_t launch_embed(const EmbedArgs& p, cudaStream_t stream) {
   const bool wide = rows_aligned(p.table, sizeof(T), p.tstride, p.n_vocab) &&
                     rows_aligned(p.out, sizeof(O), p.ostride, p.n);
   const uint32_t steps = wide ? (p.dim + UNIT - 1) / UNIT : p.dim;
+  // threads a row: enough for one step each, but with a large n only a
+  // quarter, whose AHEAD steps are loaded at once
+  const uint32_t want = p.n >= 2048 ? (steps + AHEAD - 1) / AHEAD : steps;
   uint32_t x = 1;
-  while (x < 256 && x < steps) x *= 2;
-  const dim3 block(x, 256 / x);
+  while (x < EMBED_THREADS && x < want) x *= 2;
+  const dim3 block(x, EMBED_THREADS / x);
   const unsigned grid = unsigned((uint64_t(p.n) + block.y - 1) / block.y);
   if (wide) embed_kernel<T, O, UNIT><<<grid, block, 0, stream>>>(p);
   else embed_kernel<T, O, 1><<<grid, block, 0, stream>>>(p);

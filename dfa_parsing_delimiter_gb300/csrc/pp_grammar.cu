@@ -273,27 +273,30 @@ __global__ void __launch_bounds__(128) states_short_kernel(const __grid_constant
 constexpr int STATES_THREADS = 640, STATES_WARPS = STATES_THREADS / 32, STATES_BLOCKS = 16;
 
 struct StateShared {
-  uint64_t total[STATES_WARPS];  // the warps' vectors
+  uint64_t total[STATES_WARPS];  // the warps' vectors, then those of all up to each
   uint32_t lost[STATES_WARPS];   // a token outside the vocabulary among a warp's
+  uint32_t lost_mask;            // bit w: warp w has one
   uint64_t part[STATES_BLOCKS];  // the earlier blocks' vectors, written by them
   uint32_t part_lost[STATES_BLOCKS];
 };
 
-// One tile's vectors into registers and its warps' totals into shared memory.
+// One tile's vectors into registers, and the vectors from the tile's begin to
+// each warp's end into shared memory.
 template <class M, int K, class I>
-__device__ __forceinline__ void states_tile(const StateArgs& p, const I* tokens, uint64_t t0, uint64_t len,
+__device__ __forceinline__ void states_tile(const StateArgs& p, const I* tokens, uint32_t t0, uint32_t len,
                                             typename M::Packed (&vec)[K], uint32_t* bad, M* before, uint32_t* dead,
                                             StateShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  int64_t tok[K];
+  I tok[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) tok[k] = t0 + k < len ? int64_t(tokens[t0 + k]) : -1;
+  for (int k = 0; k < K; ++k) tok[k] = t0 + k < len ? tokens[t0 + k] : I(0);
   *bad = K;  // this thread's first token outside the vocabulary
 #pragma unroll
   for (int k = K - 1; k >= 0; --k) {
-    const bool fine = tok[k] >= 0 && tok[k] < p.n_vocab;
-    vec[k] = fine ? M::load(p.vectors, tok[k]) : M::ID;
-    if (!fine && t0 + k < len) *bad = k;
+    // an id below 0 turns into one past the vocabulary
+    const bool there = t0 + k < len, fine = sizeof(I) == 8 ? uint64_t(tok[k]) < p.n_vocab : uint32_t(tok[k]) < p.n_vocab;
+    vec[k] = there && fine ? M::load(p.vectors, uint32_t(tok[k])) : M::ID;
+    if (there && !fine) *bad = k;
   }
   M a = M::id();
   if (t0 < len) {
@@ -308,65 +311,78 @@ __device__ __forceinline__ void states_tile(const StateArgs& p, const I* tokens,
     sh.total[warp] = a.pack();
     sh.lost[warp] = *dead;
   }
+  __syncthreads();
+  if (warp == 0) {
+    const bool in = lane < STATES_WARPS;
+    const M t = warp_scan(in ? M::unpack(typename M::Packed(sh.total[lane])) : M::id());
+    const uint32_t mask = __ballot_sync(FULL, in && sh.lost[lane] != 0);
+    if (in) sh.total[lane] = t.pack();
+    if (lane == 0) sh.lost_mask = mask;
+  }
+  __syncthreads();
 }
 
 template <class M, int K, class I>
 __device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, StateShared& sh, uint32_t* staged) {
+  using Packed = typename M::Packed;
   constexpr uint32_t TILE = STATES_THREADS * K;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const uint64_t row = blockIdx.x / blocks;
   const uint32_t rank = blockIdx.x % blocks;
-  const uint64_t begin = min(uint64_t(rank) * each, uint64_t(p.n_cols)), end = min(begin + each, uint64_t(p.n_cols));
-  const uint64_t len = min(uint64_t(row_length(p, row)), end);
+  const uint32_t begin = uint32_t(min(uint64_t(rank) * each, uint64_t(p.n_cols)));
+  const uint32_t end = uint32_t(min(uint64_t(begin) + each, uint64_t(p.n_cols)));
+  const uint32_t len = min(row_length(p, row), end);
   const I* tokens = static_cast<const I*>(p.tokens) + row * p.tstride;
   uint8_t* out = p.states + row * p.sstride;
-  typename M::Packed vec[K];
-  uint32_t bad = K, dead = 0, s = first_state(p, row);
+  Packed vec[K];
+  uint32_t bad = K, dead = 0, gone = 0, s = first_state(p, row);
   M before = M::id(), all = M::id();
-  uint32_t gone = 0;
   if (rank == 0 && threadIdx.x == 0) out[0] = uint8_t(s);
   const bool kept = blocks > 1 && end - begin <= TILE;  // one tile, whose vectors stay
 #pragma unroll 1
   for (int pass = blocks > 1 ? 0 : 1; pass < 2; ++pass) {
 #pragma unroll 1
-    for (uint64_t base = begin; base < end; base += TILE) {
-      const uint64_t t0 = base + uint64_t(threadIdx.x) * K;
-      if (pass == 0 || !kept) {
-        states_tile(p, tokens, t0, len, vec, &bad, &before, &dead, sh);
-        __syncthreads();
-      }
-      if (pass == 0) {  // the part's total, by warp 0
-        if (warp == 0) {
-          const M a = warp_scan(lane < STATES_WARPS ? M::unpack(typename M::Packed(sh.total[lane])) : M::id());
-          all = all.then(a);  // lane 31 has them all
-          gone |= __ballot_sync(FULL, lane < STATES_WARPS && sh.lost[lane] != 0);
-        }
+    for (uint32_t base = begin; base < end; base += TILE) {  // TILE is far below 2^16: no overflow
+      const uint32_t t0 = base + threadIdx.x * K;
+      if (pass == 0 || !kept) states_tile(p, tokens, t0, len, vec, &bad, &before, &dead, sh);
+      const M whole = M::unpack(Packed(sh.total[STATES_WARPS - 1]));
+      const uint32_t lost = sh.lost_mask;
+      if (pass == 0) {
+        all = all.then(whole);
+        gone |= lost;
         if (base + TILE < end) __syncthreads();
         continue;
       }
       uint32_t q = s;
-#pragma unroll 4
-      for (int w = 0; w < STATES_WARPS; ++w) {
-        if (w == warp) q = s;
-        if (s != PP_STATE_NONE) s = sh.lost[w] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.total[w], s);
+      if (q != PP_STATE_NONE) {
+        if (warp > 0) q = nib_apply(sh.total[warp - 1], q);
+        if (lane > 0) q = before.apply(q);
       }
-      if (q != PP_STATE_NONE && lane > 0) q = before.apply(q);
-      if (dead & ((1u << lane) - 1)) q = PP_STATE_NONE;
+      if ((lost & ((1u << warp) - 1)) || (dead & ((1u << lane) - 1))) q = PP_STATE_NONE;
+      if (q != PP_STATE_NONE && bad == K) {
 #pragma unroll
-      for (int g = 0; g < K / 4; ++g) {
-        uint32_t four = 0;
+        for (int g = 0; g < K / 4; ++g) {
+          uint32_t four = 0;
 #pragma unroll
-        for (int k = 4 * g; k < 4 * g + 4; ++k) {
-          if (uint32_t(k) >= bad) q = PP_STATE_NONE;
-          if (q != PP_STATE_NONE) q = nib_apply(vec[k], q);
-          four |= q << (8 * (k - 4 * g));
+          for (int k = 4 * g; k < 4 * g + 4; ++k) {
+            q = uint32_t(vec[k] >> (4 * q)) & 15;
+            four |= q << (8 * (k - 4 * g));
+          }
+          staged[threadIdx.x * (K / 4) + g] = four;
         }
-        staged[threadIdx.x * (K / 4) + g] = four;
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (uint32_t(k) >= bad) q = PP_STATE_NONE;
+          if (q != PP_STATE_NONE) q = uint32_t(vec[k] >> (4 * q)) & 15;
+          reinterpret_cast<uint8_t*>(staged)[threadIdx.x * K + k] = uint8_t(q);
+        }
       }
+      if (s != PP_STATE_NONE) s = lost ? uint32_t(PP_STATE_NONE) : whole.apply(s);
       __syncthreads();
       // the tile's states, which begin at any byte, in words of memory
-      uint8_t* to = out + base + 1;
-      const uint32_t n = uint32_t(min(uint64_t(TILE), end - base));
+      uint8_t* to = out + uint64_t(base) + 1;
+      const uint32_t n = min(TILE, end - base);
       const uint32_t skip = min(uint32_t(-reinterpret_cast<intptr_t>(to)) & 3u, n), words = (n - skip) / 4;
       for (uint32_t w = threadIdx.x; w < words; w += STATES_THREADS)
         reinterpret_cast<uint32_t*>(to + skip)[w] = __funnelshift_r(staged[w], staged[w + 1], 8 * skip);
@@ -376,18 +392,20 @@ __device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, S
       if (base + TILE < end) __syncthreads();
     }
     if (pass == 0) {
-      if (warp == 0 && lane == 31)
-        for (uint32_t q = rank + 1; q < blocks; ++q) {
-          const uint64_t v = all.pack();
-          uint32_t a, b;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part[rank]))), "r"(q));
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part_lost[rank]))), "r"(q));
-          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(gone) : "memory");
-        }
+      if (warp == 0 && uint32_t(lane) > rank && uint32_t(lane) < blocks) {  // a lane per later block
+        const uint64_t v = all.pack();
+        uint32_t a, b;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part[rank]))), "r"(lane));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(uint32_t(__cvta_generic_to_shared(&sh.part_lost[rank]))), "r"(lane));
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(gone) : "memory");
+      }
       asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-      for (uint32_t q = 0; q < rank; ++q)
-        if (s != PP_STATE_NONE) s = sh.part_lost[q] ? uint32_t(PP_STATE_NONE) : nib_apply(sh.part[q], s);
+#pragma unroll 4
+      for (uint32_t q = 0; q < rank; ++q) {
+        const uint32_t next = uint32_t(sh.part[q] >> (4 * (s & 15))) & 15;
+        s = s == PP_STATE_NONE || sh.part_lost[q] ? uint32_t(PP_STATE_NONE) : next;
+      }
     }
   }
 }
