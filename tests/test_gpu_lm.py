@@ -428,6 +428,19 @@ def test_logits_long_history_counts_exactly():
     assert np.array_equal(got[1], -np.bincount(history[1], minlength=vocab).astype(float))
 
 
+@pytest.mark.parametrize("n", [65535, 65536])
+def test_logits_counts_at_16_bits(n):
+    """One token alone, beside one that is never said, at both widths of the
+    counts."""
+    history = np.full((2, n), 5, np.int32)
+    history[1] = 4
+    got = pp.process_logits(dev(np.zeros((2, 1100)), torch.float32), history=dev(history),
+                            frequency=dev(np.ones(2, np.float32))).cpu().numpy()
+    want = np.zeros((2, 1100))
+    want[0, 5], want[1, 4] = -n, -n
+    assert np.array_equal(got, want)
+
+
 @pytest.mark.parametrize("rows,vocab", [(1, 200000), (70000, 9), (3000, 257)])
 def test_logits_shapes(rows, vocab):
     rng = np.random.default_rng(rows)
@@ -708,3 +721,17 @@ def test_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_the_example_learns_and_answers_rows_that_parse():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "grammar_rows.py")
+    spec = importlib.util.spec_from_file_location("grammar_rows", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    out = example.run()
+    assert out["losses"][-1] < 0.6 * out["losses"][0] and out["same_states"]
+    done = [p for p in out["parsed"] if p is not None]
+    assert done and all(p["error"] & pp.ERR_FATAL == 0 for p in done)  # what the grammar lets end, parses
+    assert all(p is not None for p, over in zip(out["parsed"], out["over"]) if over)
