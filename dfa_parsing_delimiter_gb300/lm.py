@@ -25,6 +25,7 @@ import dfa_parsing_delimiter_gb300 as pp
 FTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ITYPE = {torch.uint8: 0, torch.int8: 1, torch.int32: 2, torch.int64: 3}
 STATE_NONE = 0xFF
+_U8 = (torch.uint8,)
 
 _vp, _sz, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _i64, _f32 = ctypes.c_int64, ctypes.c_float
@@ -44,6 +45,7 @@ class LogitOpts(ctypes.Structure):
 # The same struct from values in order: one pack costs a tenth of setting the
 # fields one by one, which is felt where a call's kernel takes microseconds.
 _pack_opts = struct.Struct("@18Q2i").pack
+_NO_HISTORY, _NO_BIAS, _NO_GRAMMAR = (0,) * 10, (0,) * 4, (0,) * 5
 
 
 def declare(L: ctypes.CDLL) -> None:
@@ -77,15 +79,15 @@ def _on(t: torch.Tensor, like: torch.Tensor, name: str, dtypes, ndim: int) -> No
         _wrong(t, like, name, dtypes, ndim)
 
 
-def _vector(t, like, name: str, dtype, n: int) -> int:
+def _vector(t, dev: int, name: str, dtype, n: int) -> int:
     """Address of a contiguous vector of at least n elements (None: 0)."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.dim() != 1 or t.get_device() != like.get_device():
-        _wrong(t, like, name, (dtype,), 1)
-    if t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: want {n} contiguous elements")
-    return t.data_ptr()
+    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.numel() >= n
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError(f"{name}: want {n} contiguous elements of {dtype} on the other tensors' device, "
+                     f"got {tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -153,7 +155,7 @@ def vocab_grammar(offsets: torch.Tensor, chars: torch.Tensor, desc=None, end_id=
     end_id: the token that ends a text (None: there is none)."""
     desc = desc if desc is not None else pp.desc_csv()
     _on(offsets, chars, "offsets", (torch.int32,), 1)
-    _on(chars, offsets, "chars", (torch.uint8,), 1)
+    _on(chars, offsets, "chars", _U8, 1)
     _need(offsets.size(0) >= 1 and offsets.is_contiguous() and chars.is_contiguous(),
           "want contiguous offsets (one more than tokens) and chars")
     n = offsets.size(0) - 1
@@ -178,18 +180,18 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
     if out is None:
         out = _new((rows, cols + 1), torch.uint8, tokens, stream)
     else:
-        _on(out, tokens, "out", (torch.uint8,), 2)
+        _on(out, tokens, "out", _U8, 2)
         _need(out.shape == (rows, cols + 1), "out: want one column more than tokens")
     ps, ss = 0, 0
     if start is not None:
-        _on(start, tokens, "start", (torch.uint8,), 1)
+        _on(start, tokens, "start", _U8, 1)
         _need(start.size(0) == rows, "start: want one state a row")
         ps, ss = start.data_ptr(), start.stride(0)
     if not rows:
         return out
     _call(pp.lib().pp_grammar_states, "pp_grammar_states", tokens, stream, grammar.vectors.data_ptr(),
           grammar.n_vocab, grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype], rows, cols,
-          _matrix_stride(tokens, "tokens"), _vector(lengths, tokens, "lengths", torch.int32, rows),
+          _matrix_stride(tokens, "tokens"), _vector(lengths, tokens.get_device(), "lengths", torch.int32, rows),
           ps, ss, grammar.start_state, out.data_ptr(), _matrix_stride(out, "out"))
     return out
 
@@ -207,45 +209,43 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     (uint8 [rows]): tokens that the state does not allow become -inf."""
     _need(logits.dtype in FTYPE and logits.dim() == 2, "logits: want 2 dimensions of float32, float16 or bfloat16")
     rows, vocab = logits.shape
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
     if out is None:
         out = _new((rows, vocab), logits.dtype, logits, stream)
     else:
         _on(out, logits, "out", (logits.dtype,), 2)
         _need(out.shape == logits.shape, "out: want the shape of the logits")
-    hist = (0,) * 10
-    itype = 0
+    hist, itype = _NO_HISTORY, 0
     if history is not None:
         _on(history, logits, "history", ITYPE, 2)
         itype = ITYPE[history.dtype]
         lines, cols = history.shape
         _need(history_row is not None or lines >= rows, "history: want a row for each row of logits")
-        i32, f32 = torch.int32, torch.float32
-        hist = (history.data_ptr(), _vector(history_row, logits, "history_row", i32, rows),
-                _vector(history_len, logits, "history_len", i32, rows),
-                _vector(prompt_len, logits, "prompt_len", i32, rows),
+        hist = (history.data_ptr(), _vector(history_row, dev, "history_row", i32, rows),
+                _vector(history_len, dev, "history_len", i32, rows),
+                _vector(prompt_len, dev, "prompt_len", i32, rows),
                 lines, cols, _matrix_stride(history, "history"),
-                _vector(repetition, logits, "repetition", f32, rows),
-                _vector(presence, logits, "presence", f32, rows),
-                _vector(frequency, logits, "frequency", f32, rows))
-    else:
-        _need(repetition is None and presence is None and frequency is None, "penalties need a history")
-    lists = (0,) * 4
+                _vector(repetition, dev, "repetition", f32, rows),
+                _vector(presence, dev, "presence", f32, rows),
+                _vector(frequency, dev, "frequency", f32, rows))
+    elif repetition is not None or presence is not None or frequency is not None:
+        raise ValueError("penalties need a history")
+    lists = _NO_BIAS
     if bias is not None:
         at, tokens, values = bias
-        n = tokens.size(0)
-        _need(values.size(0) == n, "bias: want as many values as tokens")
-        lists = (_vector(at, logits, "bias offsets", torch.int32, rows + 1),
-                 _vector(tokens, logits, "bias tokens", torch.int32, n),
-                 _vector(values, logits, "bias values", torch.float32, n), n)
-    _need((grammar is None) == (states is None), "a grammar needs states, and states a grammar")
-    mask = (0,) * 5
-    if grammar is not None:
-        _on(states, logits, "states", (torch.uint8,), 1)
-        _need(states.size(0) == rows, "states: want one a row")
-        _need(grammar.n_vocab == vocab, "the grammar has another number of tokens than the logits")
+        n = tokens.numel()
+        _need(values.numel() == n, "bias: want as many values as tokens")
+        lists = (_vector(at, dev, "bias offsets", i32, rows + 1), _vector(tokens, dev, "bias tokens", i32, n),
+                 _vector(values, dev, "bias values", f32, n), n)
+    mask = _NO_GRAMMAR
+    if grammar is not None and states is not None:
+        _on(states, logits, "states", _U8, 1)
         allowed = grammar.allowed
-        _need(allowed.get_device() == logits.get_device(), "the grammar is on another device")
+        if states.numel() != rows or grammar.n_vocab != vocab or allowed.get_device() != dev:
+            raise ValueError(f"want {rows} states, and a grammar of {vocab} tokens on the logits' device")
         mask = (allowed.data_ptr(), allowed.stride(0), states.data_ptr(), states.stride(0), grammar.n_states)
+    elif grammar is not states:
+        raise ValueError("a grammar needs states, and states a grammar")
     if rows and vocab:
         _call(pp.lib().pp_logits, "pp_logits", logits, stream, logits.data_ptr(), FTYPE[logits.dtype],
               rows, vocab, _matrix_stride(logits, "logits"), _pack_opts(*hist, *lists, *mask, itype),
