@@ -159,7 +159,7 @@ __device__ __forceinline__ typename M::Packed vocab_share(const uint8_t* p, uint
 //
 // Bound by instructions, the byte permutes of the compositions: with a thread
 // a token a warp takes as long as its longest token, 24 us for 262144 tokens
-// of 8 bytes on average under 16 states.
+// of 8 bytes on average under 16 states; together 16 to 19.
 template <int S>
 __global__ void __launch_bounds__(VOCAB_THREADS)
 vocab_kernel(const __grid_constant__ VocabArgs p, const __grid_constant__ VocabDfa dfa) {
@@ -238,8 +238,13 @@ __device__ __forceinline__ uint32_t row_length(const StateArgs& p, uint64_t row)
   return p.lengths ? uint32_t(min(max(p.lengths[row], 0), int32_t(p.n_cols))) : p.n_cols;
 }
 
-// Few tokens a row (STATES_SHORT or fewer): a thread walks its row.
-constexpr uint32_t STATES_SHORT = 16;
+// Few tokens a row, or many rows: a thread walks its row, the vectors of
+// STATES_BATCH tokens on their way at a time.  That takes 0.28 us a column
+// while the rows fit the machine, and a block a row 0.0135 us a row (of up to
+// 2560 tokens): 8192 rows of 64 tokens take 21 us here and 113 there, 2048
+// rows of 256 75 and 33, so rows of up to a 20th of their number go here.
+constexpr uint32_t STATES_SHORT = 16, STATES_MANY = 20;
+constexpr int STATES_BATCH = 4;
 __global__ void __launch_bounds__(128) states_short_kernel(const __grid_constant__ StateArgs p) {
   const uint64_t row = uint64_t(blockIdx.x) * 128 + threadIdx.x;
   if (row >= p.n_rows) return;
@@ -247,12 +252,19 @@ __global__ void __launch_bounds__(128) states_short_kernel(const __grid_constant
   const uint32_t len = row_length(p, row);
   uint8_t* out = p.states + row * p.sstride;
   out[0] = uint8_t(s);
-  for (uint32_t t = 0; t < p.n_cols; ++t) {
-    if (t < len && s != PP_STATE_NONE) {
-      const int64_t tok = load_id(p.tokens, p.type, row * p.tstride + t);
-      s = tok >= 0 && tok < p.n_vocab ? nib_apply(p.vectors[tok], s) : PP_STATE_NONE;
+  for (uint32_t t = 0; t < p.n_cols; t += STATES_BATCH) {
+    int64_t tok[STATES_BATCH];
+    uint64_t vec[STATES_BATCH];
+#pragma unroll
+    for (int k = 0; k < STATES_BATCH; ++k) tok[k] = t + k < len ? load_id(p.tokens, p.type, row * p.tstride + t + k) : -1;
+#pragma unroll
+    for (int k = 0; k < STATES_BATCH; ++k) vec[k] = tok[k] >= 0 && tok[k] < p.n_vocab ? p.vectors[tok[k]] : 0;
+#pragma unroll
+    for (int k = 0; k < STATES_BATCH; ++k) {
+      if (t + k < len && s != PP_STATE_NONE)
+        s = tok[k] >= 0 && tok[k] < p.n_vocab ? nib_apply(vec[k], s) : PP_STATE_NONE;
+      if (t + k < p.n_cols) out[t + k + 1] = uint8_t(s);
     }
-    out[t + 1] = uint8_t(s);
   }
 }
 
@@ -267,9 +279,9 @@ __global__ void __launch_bounds__(128) states_short_kernel(const __grid_constant
 // Bound by instructions (the byte permutes of the compositions go at half
 // rate) and by the latency of its steps, not by memory.  640 threads, so that two blocks
 // share a multiprocessor and clusters of 16 fill the machine (with one block
-// a multiprocessor only 15 clusters of 8 ran at once, and the 16 rows of
-// 65537 tokens took two waves: 27 us), and so that a row of a few tokens more
-// than a power of two still has one tile a block.
+// a multiprocessor only 15 clusters of 8 run at once, and 16 rows of 65537
+// tokens take two waves, 27 us; this way 13), and so that a row of a few
+// tokens more than a power of two still has one tile a block.
 constexpr int STATES_THREADS = 640, STATES_WARPS = STATES_THREADS / 32, STATES_BLOCKS = 16;
 
 struct StateShared {
@@ -534,7 +546,7 @@ pp_rc pp_grammar_states(const uint64_t* d_vectors, size_t n_vocab, int n_states,
   const StateArgs p = {d_vectors, uint32_t(n_vocab), n_states, d_tokens, token_type,
                        uint32_t(n_rows), uint32_t(n_cols), tokens_stride, d_lengths, d_start,
                        start_stride, start_state, d_states, states_stride};
-  if (n_cols <= STATES_SHORT)
+  if (n_cols <= STATES_SHORT || n_cols * STATES_MANY <= n_rows)
     states_short_kernel<<<unsigned((n_rows + 127) / 128), 128, 0, stream>>>(p);
   else
     return ppl::rc_of(launch_states(p, stream));

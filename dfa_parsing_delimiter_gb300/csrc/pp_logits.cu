@@ -12,9 +12,10 @@
 // order of the atomics changes a count.
 //
 // 512 rows of 131075 f16 with histories of up to 8191, biases and a grammar
-// take 84 us, of which the stream alone is 44 (its 268 MB at the copy rate:
-// 40), the mask 8, counting and turning 25 and the biases 6; bound by
-// instructions.
+// take 81 us, of which the stream alone is 44 (its 268 MB at the copy rate:
+// 40), the mask 4, counting and turning 26 and the biases 6; bound by the
+// latency of a block's steps one after the other, so many blocks at once (four
+// on a multiprocessor) count for more than loads in flight in each.
 //
 // What was measured against it (512 rows of 131075 f16, histories of 8191,
 // biases, a grammar): turning marked elements within their vectors takes 8
@@ -32,7 +33,8 @@ namespace {
 using ppl::from_f;
 using ppl::to_f;
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 512, BLOCKS = 4;  // a multiprocessor
+constexpr int NV = 2;  // vectors that a thread holds
 
 struct LogitArgs {
   const void* in;
@@ -77,10 +79,22 @@ __device__ __forceinline__ History history_of(const pp_logit_opts& o, uint64_t r
   return r;
 }
 
+// A row's biases.
+struct Biases {
+  const int32_t* tokens;
+  const float* values;
+  uint32_t n;
+};
+__device__ __forceinline__ Biases biases_of(const pp_logit_opts& o, uint64_t row) {
+  if (!o.d_bias_offsets) return {nullptr, nullptr, 0};
+  const int64_t lo = cut(o.d_bias_offsets[row], o.n_bias), hi = cut(o.d_bias_offsets[row + 1], o.n_bias);
+  return {o.d_bias_tokens + lo, o.d_bias_values + lo, hi > lo ? uint32_t(hi - lo) : 0};
+}
+
 template <int HIST>
 __device__ __forceinline__ void count_history(const History& h, int type, int first, uint32_t size, uint32_t* counts,
                                               uint32_t* marks) {
-  ppl::for_ids<8>(h.line, type, 1, threadIdx.x, h.len, THREADS, [&](uint32_t t, auto tok) {
+  ppl::for_ids<4>(h.line, type, 1, threadIdx.x, h.len, THREADS, [&](uint32_t t, auto tok) {
     if (sizeof(tok) == 8 && uint64_t(tok) >= 0x7FFFFFFFu) return;
     const uint32_t j = uint32_t(int32_t(tok) - first);  // before the slice: past its end
     if (j >= size) return;
@@ -119,7 +133,8 @@ __device__ __forceinline__ uint4 forbid(uint4 v, uint32_t need) {
 // The 32 bits of `bits` from column c on (c > -32).
 __device__ __forceinline__ uint32_t allowed_from(const uint32_t* bits, int c, int n_vocab) {
   if (c < 0) return bits[0] << -c;
-  return __funnelshift_r(bits[c / 32], bits[min(c / 32 + 1, (n_vocab - 1) / 32)], c);
+  const uint32_t w = uint32_t(c) / 32, last = uint32_t(n_vocab - 1) / 32;
+  return __funnelshift_r(bits[w], bits[min(w + 1, last)], c);
 }
 
 // f(j) for the set bits j of marks that `without` (if any) has not, restricted
@@ -192,8 +207,7 @@ __device__ __forceinline__ void for_marked(const uint32_t* marks, const uint32_t
 // elements before column 0; a row's incomplete first and last vectors go
 // element by element, as everything does with VEC 1.
 template <class T, int VEC, int HIST, bool BIAS, bool MASK>
-__global__ void __launch_bounds__(THREADS, 3) logits_kernel(const __grid_constant__ LogitArgs p) {
-  constexpr int NV = 2;  // vectors that a thread holds
+__global__ void __launch_bounds__(THREADS, BLOCKS) logits_kernel(const __grid_constant__ LogitArgs p) {
   constexpr uint32_t ALL = (1u << VEC) - 1;
   using C = Counts<HIST>;
   extern __shared__ __align__(16) uint32_t counts[];
@@ -218,37 +232,42 @@ __global__ void __launch_bounds__(THREADS, 3) logits_kernel(const __grid_constan
 
   History h;
   if (HIST) h = history_of(o, row);
-  int64_t b_lo = 0, b_hi = 0;
-  if (BIAS && o.d_bias_offsets) {
-    b_lo = cut(o.d_bias_offsets[row], o.n_bias);
-    b_hi = cut(o.d_bias_offsets[row + 1], o.n_bias);
-  }
+  Biases bias = {};
+  if (BIAS) bias = biases_of(o, row);
 
   // the complete vectors of the row that this slice holds: v_lo .. v_hi - 1
   const int n_vec = int(p.slice) / VEC;
   const int v_lo = first < 0 ? 1 : 0, v_hi = min(n_vec, (n_vocab - first) / VEC);
+  // this thread's first one, and how many vectors from there to v_hi; its
+  // vectors are THREADS apart, whole words of bits, so that its place within
+  // a word stays
+  const int c_first = first + (v_lo + int(threadIdx.x)) * VEC;
+  int left = VEC > 1 ? v_hi - v_lo - int(threadIdx.x) : 0;
+  const uint4* src = reinterpret_cast<const uint4*>(in + c_first);
+  uint4* dst = reinterpret_cast<uint4*>(out + c_first);
+  const uint32_t* word = bits + uint32_t(c_first) / 32;
+  const uint32_t shift = uint32_t(c_first) % 32;
+  const bool across = shift + VEC > 32;  // into the next word
   uint4 x[NV];
   uint32_t need[NV];  // bit k: the grammar allows element k
   // what the grammar forbids is not even read
-  auto load = [&](int v0) {
+  auto load = [&]() {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = v0 + i * THREADS + int(threadIdx.x);
-      need[i] = 0;
-      if (v < v_hi) {
-        const int c = first + v * VEC;
+    for (int i = 0; i < NV; ++i)
+      if (i * THREADS < left) {
         need[i] = ALL;
         if (masked) {
-          need[i] = 0;
-          if (bits) need[i] = allowed_from(bits, c, n_vocab) & ALL;
+          uint32_t lo = 0, hi = 0;
+          if (bits) {
+            lo = word[i * (THREADS * VEC / 32)];
+            if (across) hi = word[i * (THREADS * VEC / 32) + 1];
+          }
+          need[i] = __funnelshift_r(lo, hi, shift) & ALL;
         }
-        if (need[i]) x[i] = *reinterpret_cast<const uint4*>(in + c);
+        if (need[i]) x[i] = src[i * THREADS];
       }
-    }
   };
-  if (VEC > 1) load(v_lo);
-  const uint32_t n_bias = b_hi > b_lo ? uint32_t(b_hi - b_lo) : 0;
-  const int32_t* b_tokens = o.d_bias_tokens + b_lo;
+  if (VEC > 1) load();
   if (HIST || BIAS) {
     const uint32_t n = C::words(p.slice) + n_marks * ((HIST ? 1 : 0) + (BIAS ? 1 : 0));  // a multiple of 4
     for (uint32_t j = threadIdx.x * 4; j < n; j += THREADS * 4)
@@ -257,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 3) logits_kernel(const __grid_constan
     __syncthreads();
     if (HIST) count_history<HIST>(h, o.history_type, first, p.slice, counts, marks);
     if (BIAS)
-      ppl::for_ids_of<2>(b_tokens, 1, threadIdx.x, n_bias, THREADS, [&](uint32_t, int32_t tok) {
+      ppl::for_ids_of<2>(bias.tokens, 1, threadIdx.x, bias.n, THREADS, [&](uint32_t, int32_t tok) {
         const uint32_t j = uint32_t(tok - first);
         if (tok < 0 || j >= p.slice) return;
         if (atomicOr(&biased[j / 32], 1u << (j % 32)) >> (j % 32) & 1) twice = 1;
@@ -267,19 +286,20 @@ __global__ void __launch_bounds__(THREADS, 3) logits_kernel(const __grid_constan
   auto single = [&](int j) {
     const int c = first + j;
     if (c < 0 || c >= n_vocab) return;
-    const bool fine = !masked || (bits && (bits[c / 32] >> (c % 32) & 1));
+    const bool fine = !masked || (bits && (bits[uint32_t(c) / 32] >> (c & 31) & 1));
     out[c] = fine ? in[c] : from_f<T>(-INFINITY);
   };
   if (VEC == 1)
     for (int j = threadIdx.x; j < int(p.slice); j += THREADS) single(j);
-  for (int v0 = v_lo; VEC > 1 && v0 < v_hi;) {
+  while (VEC > 1 && left > 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = v0 + i * THREADS + int(threadIdx.x);
-      if (v < v_hi) *reinterpret_cast<uint4*>(out + first + v * VEC) = masked ? forbid<T>(x[i], need[i]) : x[i];
-    }
-    v0 += NV * THREADS;
-    if (v0 < v_hi) load(v0);
+    for (int i = 0; i < NV; ++i)
+      if (i * THREADS < left) dst[i * THREADS] = masked ? forbid<T>(x[i], need[i]) : x[i];
+    src += NV * THREADS;
+    dst += NV * THREADS;
+    word += NV * THREADS * VEC / 32;
+    left -= NV * THREADS;
+    load();
   }
   if (VEC > 1) {  // the incomplete vectors: before v_lo and from v_hi on
     if (first < 0 && int(threadIdx.x) < VEC) single(threadIdx.x);
@@ -302,20 +322,22 @@ __global__ void __launch_bounds__(THREADS, 3) logits_kernel(const __grid_constan
   if (HIST)  // but for tokens with a bias, which come next
     for_marked(marks, BIAS ? biased : nullptr, n_marks, first, n_vocab, masked, bits,
                [&](int j) { out[first + j] = from_f<T>(turn(j, true)); });
-  if (BIAS)
-    for (uint32_t e = threadIdx.x; e < n_bias; e += THREADS) {
-      const int tok = b_tokens[e];
+  if (BIAS) {
+    bias = biases_of(o, row);  // again, rather than kept in registers meanwhile
+    for (uint32_t e = threadIdx.x; e < bias.n; e += THREADS) {
+      const int tok = bias.tokens[e];
       const uint32_t j = uint32_t(tok - first);
       if (tok < 0 || tok >= n_vocab || j >= p.slice) continue;
-      if (masked && !(bits && (bits[tok / 32] >> (tok % 32) & 1))) continue;
+      if (masked && !(bits && (bits[uint32_t(tok) / 32] >> (tok & 31) & 1))) continue;
       bool last = true;  // the last entry of a token counts
       if (twice)
-        for (uint32_t k = e + 1; last && k < n_bias; ++k) last = b_tokens[k] != tok;
-      if (last) out[tok] = from_f<T>(turn(j, HIST && marks[j / 32] >> (j % 32) & 1) + o.d_bias_values[b_lo + e]);
+        for (uint32_t k = e + 1; last && k < bias.n; ++k) last = bias.tokens[k] != tok;
+      if (last) out[tok] = from_f<T>(turn(j, HIST && marks[j / 32] >> (j % 32) & 1) + bias.values[e]);
     }
+  }
 }
 
-constexpr uint32_t SLICE_MOST = 32768 + 128;
+constexpr uint32_t SLICE_MOST = 24576 + 128;  // 55 KiB with counts of 16 bits: BLOCKS of them fit
 constexpr uint32_t SLICE_LEAST = 1024;
 constexpr size_t SMEM_MOST = SLICE_MOST * 4 + SLICE_MOST / 4;
 
@@ -339,11 +361,11 @@ template <class T, int VEC>
 cudaError_t launch_kind(LogitArgs& p, uint64_t n_rows, int hist, bool bias, bool mask, cudaStream_t stream) {
   // Slices of up to SLICE_MOST tokens, since every block reads its row's
   // history; smaller ones where there are few rows, as many as run at once
-  // (three on each of 152 multiprocessors; for 64 rows of 131072 7 slices
-  // take 10.9 us, 5 take 12.4 and 14, two waves, 14.6), but none of fewer
-  // than SLICE_LEAST tokens.
+  // (four on each of 152 multiprocessors; for 64 rows of 131072, 9 slices
+  // take 10.9 us and 14, two waves, 14.6), but none of fewer than SLICE_LEAST
+  // tokens.
   const uint64_t n = uint64_t(p.n_vocab) + VEC - 1;
-  const uint64_t s = std::max((n + 32767) / 32768, std::min(std::max<uint64_t>(456 / n_rows, 1), (n + SLICE_LEAST - 1) / SLICE_LEAST));
+  const uint64_t s = std::max((n + 24575) / 24576, std::min(std::max<uint64_t>(608 / n_rows, 1), (n + SLICE_LEAST - 1) / SLICE_LEAST));
   p.slice = uint32_t(((n + s - 1) / s + 127) / 128 * 128);  // whole words of marks, in fours
   p.n_slices = uint32_t((n + p.slice - 1) / p.slice);
   const uint64_t blocks = n_rows * p.n_slices;

@@ -92,9 +92,9 @@ def _vector(t, dev: int, name: str, dtype, n: int) -> int:
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _matrix_stride(t: torch.Tensor, name: str) -> int:
@@ -211,7 +211,8 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     rows, vocab = logits.shape
     dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
     if out is None:
-        out = _new((rows, vocab), logits.dtype, logits, stream)
+        out = torch.empty_like(logits) if stream is None and logits.is_contiguous() else \
+            _new((rows, vocab), logits.dtype, logits, stream)
     else:
         _on(out, logits, "out", (logits.dtype,), 2)
         _need(out.shape == logits.shape, "out: want the shape of the logits")

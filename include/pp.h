@@ -541,6 +541,8 @@ pp_rc pp_debug_long_fields(uint64_t* out, int reset);
  * token ids, become vectors (pp_embed, pp_embed_grad).  The conventions at
  * the top of this file hold, except that these entry points have no
  * pp_status: every value of every input has a defined result, stated below.
+ * They can be captured into graphs; make the first call of each on a device,
+ * which sets kernel attributes, before any stream capture starts on it.
  * Tensors are element arrays of the types below at their natural alignment;
  * strides count elements and the innermost dimension is contiguous unless a
  * stride for it is given. */

@@ -216,7 +216,8 @@ def test_states_types_strides_and_continuation(dtype, cols):
     assert np.array_equal(torch.cat([one[:, :-1], two], 1).cpu().numpy(), ref)
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 70001), (3, 40000), (700, 1), (300, 16), (200, 17), (1, 400000)])
+@pytest.mark.parametrize("rows,cols", [(1, 70001), (3, 40000), (700, 1), (300, 16), (200, 17), (1, 400000),
+                                       (339, 17), (340, 17), (2001, 90), (5000, 250)])
 def test_states_many(rows, cols):
     g, to, desc = make_grammar("csv", n=3000, seed=2)
     rng = np.random.default_rng(3)
