@@ -8,7 +8,8 @@
 // run of equal ids in registers and writes the sum once.  A run that ends by
 // the end of the next chunk is finished by the chunk it begins in; a longer
 // one leaves a partial sum per chunk, added up in order by a last kernel.
-// Up to SORT_CAP positions one thread-block cluster sorts in distributed
+// Up to SMALL_IDS positions one kernel does it all (small_kernel).  Up to
+// SORT_CAP positions one thread-block cluster sorts in distributed
 // shared memory, while the first blocks of the next kernel write the zeros
 // of the rows that no id names; more go through global memory in passes.
 #include <algorithm>
@@ -470,103 +471,117 @@ constexpr int SUM_WARPS = 16, JOIN_WARPS = 8;
 constexpr int SUM_COLS = 32 * UNIT;  // columns a warp
 constexpr uint32_t NO_KEY = 0xFFFFFFFFu;
 
-// Columns of a warp: a lane has 8 consecutive ones (aligned rows) or every
-// 32nd one (any rows).
-template <bool WIDE>
-__device__ __forceinline__ uint64_t col_of(uint64_t c0, int k) {
-  const int lane = threadIdx.x & 31;
-  return WIDE ? c0 + lane * UNIT + k : c0 + lane + 32 * k;
-}
+// A lane's columns of the 32 N from c0 on: N consecutive ones (WIDE: aligned
+// rows) or every 32nd one (any rows), n of which exist.
+template <bool WIDE, int N = UNIT>
+struct Cols {
+  static constexpr int STEP = WIDE ? 1 : 32;
+  uint32_t first;
+  int n;
+  __device__ __forceinline__ Cols(uint32_t c0, uint32_t dim) {
+    const uint32_t lane = threadIdx.x & 31;
+    first = c0 + lane * (WIDE ? N : 1);
+    const int left = int(dim) - int(first);
+    n = left <= 0 ? 0 : min((left + STEP - 1) / STEP, N);
+  }
+};
 
-template <class T, bool WIDE>
-__device__ __forceinline__ void load_row(const T* row, uint64_t c0, uint32_t dim, Pack<T, UNIT>& x) {
-  if (WIDE && col_of<WIDE>(c0, UNIT) <= dim) {
-    x = *reinterpret_cast<const Pack<T, UNIT>*>(row + col_of<WIDE>(c0, 0));
+// Loads and stores of a lane's columns; row: at its first one.
+template <class T, bool WIDE, int N>
+__device__ __forceinline__ void load_row(const T* row, int n, Pack<T, N>& x) {
+  if (WIDE && n == N) {
+    x = *reinterpret_cast<const Pack<T, N>*>(row);
   } else {
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) x.v[k] = col_of<WIDE>(c0, k) < dim ? row[col_of<WIDE>(c0, k)] : from_f<T>(0.f);
+    for (int k = 0; k < N; ++k) x.v[k] = k < n ? row[k * Cols<WIDE>::STEP] : from_f<T>(0.f);
   }
 }
 
-template <class O, bool WIDE>
-__device__ __forceinline__ void store_row(O* row, uint64_t c0, uint32_t dim, const float (&x)[UNIT]) {
-  if (WIDE && col_of<WIDE>(c0, UNIT) <= dim) {
-    Pack<O, UNIT> v;
+template <class O, bool WIDE, int N>
+__device__ __forceinline__ void store_row(O* row, int n, const float (&x)[N]) {
+  if (WIDE && n == N) {
+    Pack<O, N> v;
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) v.v[k] = from_f<O>(x[k]);
-    *reinterpret_cast<Pack<O, UNIT>*>(row + col_of<WIDE>(c0, 0)) = v;
+    for (int k = 0; k < N; ++k) v.v[k] = from_f<O>(x[k]);
+    *reinterpret_cast<Pack<O, N>*>(row) = v;
   } else {
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k)
-      if (col_of<WIDE>(c0, k) < dim) row[col_of<WIDE>(c0, k)] = from_f<O>(x[k]);
+    for (int k = 0; k < N; ++k)
+      if (k < n) row[k * Cols<WIDE>::STEP] = from_f<O>(x[k]);
   }
 }
 
-template <class O, bool WIDE>
-__device__ __forceinline__ void write_sum(const SumArgs& p, uint32_t id, uint64_t c0, float (&a)[UNIT]) {
-  O* row = static_cast<O*>(p.out) + uint64_t(id) * p.ostride;
+template <class O, bool WIDE, int N>
+__device__ __forceinline__ void write_sum(const SumArgs& p, uint32_t id, const Cols<WIDE, N>& at, float (&a)[N]) {
+  O* row = static_cast<O*>(p.out) + (uint64_t(id) * p.ostride + at.first);
 #pragma unroll
-  for (int k = 0; k < UNIT; ++k) a[k] *= p.scale;
+  for (int k = 0; k < N; ++k) a[k] *= p.scale;
   if (p.accumulate) {
-    Pack<O, UNIT> old;
-    load_row<O, WIDE>(row, c0, p.dim, old);
+    Pack<O, N> old;
+    load_row<O, WIDE>(row, at.n, old);
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) a[k] += to_f(old.v[k]);
+    for (int k = 0; k < N; ++k) a[k] += to_f(old.v[k]);
   }
-  store_row<O, WIDE>(row, c0, p.dim, a);
+  store_row<O, WIDE>(row, at.n, a);
 }
 
-// 16 (or 4) bytes from global to shared memory, asynchronously.
-template <int N>
+// 16, 8 or 4 bytes from global to shared memory, asynchronously.
+template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
   const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-  if (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(a), "l"(from) : "memory");
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(a), "l"(from), "n"(BYTES) : "memory");
 }
 
-// A lane's columns of a row into its own place in shared memory: lane l's
-// piece g of 16 bytes at [g][l] (aligned rows), its element k at [k][l].
-template <class T, bool WIDE>
-__device__ __forceinline__ void stage_row(T* at, const T* row, uint64_t c0, uint32_t dim) {
-  const int lane = threadIdx.x & 31;
-  constexpr int EACH = 16 / sizeof(T);  // elements a piece
-  if (WIDE && col_of<WIDE>(c0, UNIT) <= dim) {
+// Rows on their way to a warp: a ring of DEPTH rows of 32 N columns in shared
+// memory, BYTES in all.  A lane copies its own columns and reads them back
+// itself, so nothing synchronises.  The lanes' pieces of up to 16 bytes
+// (WIDE) or their elements lie side by side.
+template <class T, bool WIDE, int BYTES, int N = UNIT>
+struct Ring {
+  static constexpr int PIECE = !WIDE ? int(sizeof(T)) : N * sizeof(T) < 16 ? int(N * sizeof(T)) : 16;
+  static constexpr int EACH = PIECE / int(sizeof(T));  // elements a piece
+  static constexpr uint32_t ROW = 32 * N * sizeof(T), DEPTH = BYTES / ROW, END = DEPTH * ROW;
+  char* mine;
+  uint32_t in = 0, out = 0;  // where the next row is copied to, and read from
+  __device__ __forceinline__ explicit Ring(char* warp) : mine(warp + (threadIdx.x & 31) * PIECE) {}
+  static __device__ __forceinline__ constexpr int place(int k) { return k / EACH * 32 * PIECE + k % EACH * int(sizeof(T)); }
+  // one group of copies a call; row null: none
+  __device__ __forceinline__ void copy(const T* row, int n) {
+    if (row) {
+      if (WIDE && n == N) {
 #pragma unroll
-    for (int g = 0; g < UNIT / EACH; ++g)
-      copy_async<16>(at + (g * 32 + lane) * EACH, row + col_of<WIDE>(c0, g * EACH));
-  } else {
+        for (int k = 0; k < N; k += EACH) copy_async<PIECE < 4 ? 4 : PIECE>(mine + in + place(k), row + k);
+      } else {
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) {
-      T* to = WIDE ? at + (k / EACH * 32 + lane) * EACH + k % EACH : at + k * 32 + lane;
-      const uint64_t c = col_of<WIDE>(c0, k);
-      if (c >= dim) *to = from_f<T>(0.f);
-      else if (sizeof(T) == 4) copy_async<4>(to, row + c);
-      else *to = row[c];
+        for (int k = 0; k < N; ++k) {
+          T* to = reinterpret_cast<T*>(mine + in + place(k));
+          if (k >= n) *to = from_f<T>(0.f);
+          else if (sizeof(T) == 4) copy_async<4>(to, row + k * Cols<WIDE, N>::STEP);
+          else *to = row[k * Cols<WIDE, N>::STEP];
+        }
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    in = in + ROW == END ? 0 : in + ROW;
   }
-}
-template <class T, bool WIDE>
-__device__ __forceinline__ void add_staged(const T* at, float (&a)[UNIT]) {
-  const int lane = threadIdx.x & 31;
-  constexpr int EACH = 16 / sizeof(T);
-  if (WIDE) {
+  // the oldest row, with DEPTH - 1 groups after it, is added to a
+  __device__ __forceinline__ void add(float (&a)[N]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
 #pragma unroll
-    for (int g = 0; g < UNIT / EACH; ++g) {
-      const Pack<T, EACH> x = *reinterpret_cast<const Pack<T, EACH>*>(at + (g * 32 + lane) * EACH);
+    for (int g = 0; g < N; g += EACH) {
+      const Pack<T, EACH> x = *reinterpret_cast<const Pack<T, EACH>*>(mine + out + place(g));
 #pragma unroll
-      for (int k = 0; k < EACH; ++k) a[g * EACH + k] += to_f(x.v[k]);
+      for (int k = 0; k < EACH; ++k) a[g + k] += to_f(x.v[k]);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < UNIT; ++k) a[k] += to_f(at[k * 32 + lane]);
+    out = out + ROW == END ? 0 : out + ROW;
   }
-}
+};
 
 // Of the sorted list, chunk c holds [c L, (c + 1) L), L <= 32.  A run is long
 // if it begins in chunk c and goes on past the end of chunk c + 1.  A warp
 // per chunk and SUM_COLS columns; the chunk's keys and the next one's are in
-// its lanes, and 3 KiB of rows are on their way in a ring in shared memory
-// (a lane reads back what it copied itself, so nothing synchronises).
+// its lanes, and RING_BYTES of rows are on their way.
 // The first n_zero blocks write the rows that no id names.  They need the
 // ids alone and so run beside the sort; the sums follow on the slots that
 // they leave, and the memory is never idle.
@@ -579,7 +594,7 @@ __device__ __forceinline__ void add_staged(const T* at, float (&a)[UNIT]) {
 constexpr int RING_BYTES = 3072;  // a warp; 4096 measures the same, 2048 up to 6 % slower on f32
 template <class T, class O, bool WIDE>
 __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_constant__ SumArgs p) {
-  constexpr uint32_t DEPTH = RING_BYTES / (SUM_COLS * sizeof(T));  // rows: 6, of 32-bit values 3
+  using R = Ring<T, WIDE, RING_BYTES>;  // 6 rows, of 32-bit values 3
   __shared__ __align__(16) char ring_mem[SUM_WARPS][RING_BYTES];
   const int lane = threadIdx.x & 31;
   let_next_start();
@@ -590,7 +605,9 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_con
     return;
   }
   const uint64_t me = uint64_t(blockIdx.x - p.n_zero) * SUM_WARPS + threadIdx.x / 32;
-  const uint64_t c = me / p.slices, c0 = me % p.slices * SUM_COLS;
+  const uint64_t c = me / p.slices;
+  const uint32_t c0 = uint32_t(me % p.slices) * SUM_COLS;
+  const Cols<WIDE> at(c0, p.dim);
   wait_for_previous();
   if (c >= p.n_chunks) return;
   const uint32_t L = p.chunk, n = p.n;
@@ -611,36 +628,34 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_con
   if (crosses && !tail) end += __popc(__ballot_sync(FULL, key1 == last));
   if (tail && c0 == 0 && lane == 0) p.longs[atomicAdd(p.n_long, 1u)] = uint32_t(c);
   if (i >= end) return;
-  const T* grad = static_cast<const T*>(p.grad);
+  const T* grad = static_cast<const T*>(p.grad) + at.first;
+  float* part = p.part + 2 * c * p.width + at.first;
   float a[UNIT] = {};
   bool piece = head;  // the current run is the long one that began earlier
   uint32_t id = __shfl_sync(FULL, key0, i);
-  T* ring = reinterpret_cast<T*>(ring_mem[threadIdx.x / 32]);
-  auto stage = [&](uint32_t e) {
-    if (e < end) {
-      const uint32_t at = __shfl_sync(FULL, e < L ? pos0 : pos1, e < L ? e : e - L);
-      stage_row<T, WIDE>(ring + e % DEPTH * SUM_COLS, grad + uint64_t(at) * p.gstride, c0, p.dim);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  R ring(ring_mem[threadIdx.x / 32]);
+  auto copy = [&](uint32_t e) {
+    const T* row = nullptr;
+    if (e < end) row = grad + uint64_t(__shfl_sync(FULL, e < L ? pos0 : pos1, e < L ? e : e - L)) * p.gstride;
+    ring.copy(row, at.n);
   };
-  for (uint32_t k = 0; k + 1 < DEPTH; ++k) stage(i + k);
+  for (uint32_t k = 0; k + 1 < R::DEPTH; ++k) copy(i + k);
 #pragma unroll 1
   for (; i < end; ++i) {
-    stage(i + DEPTH - 1);
+    copy(i + R::DEPTH - 1);
     const uint32_t now = __shfl_sync(FULL, i < L ? key0 : key1, i < L ? i : i - L);
     if (now != id) {
-      if (piece) store_row<float, WIDE>(p.part + 2 * c * p.width, c0, p.dim, a);
-      else write_sum<O, WIDE>(p, id, c0, a);
+      if (piece) store_row<float, WIDE>(part, at.n, a);
+      else write_sum<O, WIDE>(p, id, at, a);
       piece = false;
       id = now;
 #pragma unroll
       for (int j = 0; j < UNIT; ++j) a[j] = 0.f;
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-    add_staged<T, WIDE>(ring + i % DEPTH * SUM_COLS, a);
+    ring.add(a);
   }
-  if (piece || tail) store_row<float, WIDE>(p.part + (2 * c + (piece ? 0 : 1)) * p.width, c0, p.dim, a);
-  else write_sum<O, WIDE>(p, id, c0, a);
+  if (piece || tail) store_row<float, WIDE>(part + (piece ? 0 : p.width), at.n, a);
+  else write_sum<O, WIDE>(p, id, at, a);
 }
 
 // Adds the pieces of each long run: a block per run and SUM_COLS columns,
@@ -652,7 +667,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
   __shared__ float part[JOIN_WARPS][SUM_COLS];
   __shared__ uint32_t more;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const uint64_t c0 = uint64_t(blockIdx.y) * SUM_COLS, L = p.chunk;
+  const uint64_t L = p.chunk;
+  const Cols<WIDE> cols(blockIdx.y * SUM_COLS, p.dim);
   wait_for_previous();
   const uint32_t n_long = *p.n_long;
   for (uint32_t r = blockIdx.x; r < n_long; r += gridDim.x) {
@@ -679,7 +695,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
       Pack<float, UNIT> x[6];
 #pragma unroll
       for (int j = 0; j < 6; ++j)
-        if (q + j < hi) load_row<float, WIDE>(p.part + (q + j ? 2 * (c + q + j) : 2 * c + 1) * p.width, c0, p.dim, x[j]);
+        if (q + j < hi)
+          load_row<float, WIDE>(p.part + (q + j ? 2 * (c + q + j) : 2 * c + 1) * p.width + cols.first, cols.n, x[j]);
 #pragma unroll
       for (int j = 0; j < 6; ++j)
         if (q + j < hi) {
@@ -694,10 +711,111 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
 #pragma unroll
       for (int k = 0; k < UNIT; ++k)
         for (int w = 1; w < JOIN_WARPS; ++w) a[k] += part[w][k * 32 + lane];
-      write_sum<O, WIDE>(p, id, c0, a);
+      write_sum<O, WIDE>(p, id, cols, a);
     }
     __syncthreads();
   }
+}
+
+// ------------------------------------------------------------ small batches
+// Up to SMALL_IDS ids in one launch without scratch: every block that sums
+// sorts the (id, position) pairs for itself (bitonic, in shared memory) and
+// has 64 columns, its warps equal shares of the sorted list.  So few columns,
+// two a lane, since a multiprocessor moves 50 to 60 GB/s at most and a block
+// has all rows of its columns.  The
+// pieces of runs that cross shares are kept in shared memory and added in
+// order by the warp that a run begins in.  Other blocks write zero rows as
+// in sum_kernel.
+//
+// Rows of 256 f32 or 2048 bf16 for 4000 ids: 128 ids take 7 and 13 us, and 15
+// and 13 in three kernels, a call from Python 8 and 14 against 19 and 18; 512
+// ids 14 and 24, and 16 and 17 in three kernels.
+constexpr int SMALL_IDS = 384, SMALL_PAIRS = 512;
+constexpr int SMALL_UNIT = 2, SMALL_COLS = 32 * SMALL_UNIT;
+constexpr int SMALL_RING = 2048;  // bytes a warp
+
+template <class T, class O, bool WIDE>
+__global__ void __launch_bounds__(SUM_WARPS * 32, 2) small_kernel(const __grid_constant__ SumArgs p) {
+  using R = Ring<T, WIDE, SMALL_RING, SMALL_UNIT>;
+  constexpr uint32_t THREADS = SUM_WARPS * 32;
+  __shared__ __align__(16) char small_mem[SUM_WARPS * SMALL_RING];  // the rings; zero rows: the bits
+  __shared__ uint64_t pair[SMALL_PAIRS];                            // key << 32 | position
+  static_assert(sizeof small_mem >= SPAN / 8, "the rings' memory holds the rows' bits");
+  if (blockIdx.x < p.n_zero) return zero_scan<THREADS>(p.z, p.s, blockIdx.x, p.n_zero, reinterpret_cast<uint32_t*>(small_mem));
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, n = p.n;
+  const Cols<WIDE, SMALL_UNIT> at((blockIdx.x - p.n_zero) * SMALL_COLS, p.dim);
+  uint32_t size = 2;
+  while (size < n) size *= 2;
+  for (uint32_t i = threadIdx.x; i < size; i += THREADS)
+    pair[i] = i < n ? uint64_t(sort_key(p.s, i)) << 32 | i : ~0ull;
+  for (uint32_t k = 2; k <= size; k *= 2)
+    for (uint32_t j = k / 2; j; j /= 2) {
+      __syncthreads();
+      for (uint32_t t = threadIdx.x; t < size / 2; t += THREADS) {
+        const uint32_t a = 2 * t - (t & (j - 1)), b = a + j;
+        const uint64_t x = pair[a], y = pair[b];
+        if ((x > y) == ((a & k) == 0)) {
+          pair[a] = y;
+          pair[b] = x;
+        }
+      }
+    }
+  __syncthreads();
+  auto key = [&](uint32_t i) { return uint32_t(pair[i] >> 32); };
+  uint32_t m = 0, top = n;  // the ids that take part: the first key of n_vocab
+  while (m < top) {
+    const uint32_t mid = (m + top) / 2;
+    if (key(mid) < p.n_vocab) m = mid + 1;
+    else top = mid;
+  }
+  const uint32_t each = (m + SUM_WARPS - 1) / SUM_WARPS;
+  auto share = [&](uint32_t w) { return min(w * each, m); };
+  const uint32_t lo = share(warp), hi = share(warp + 1);
+  // this share's first run began before it, its last one goes on after it
+  const bool head = lo < hi && lo > 0 && key(lo - 1) == key(lo);
+  const bool tail = lo < hi && hi < m && key(hi) == key(hi - 1) && !(head && key(lo) == key(hi - 1));
+  const T* grad = static_cast<const T*>(p.grad) + at.first;
+  R ring(small_mem + warp * SMALL_RING);
+  auto copy = [&](uint32_t e) { ring.copy(e < hi ? grad + uint64_t(uint32_t(pair[e])) * p.gstride : nullptr, at.n); };
+  float a[SMALL_UNIT] = {}, first[SMALL_UNIT] = {};
+  bool piece = head;
+  uint32_t id = lo < hi ? key(lo) : 0;
+  for (uint32_t k = 0; k + 1 < R::DEPTH; ++k) copy(lo + k);
+#pragma unroll 1
+  for (uint32_t i = lo; i < hi; ++i) {
+    copy(i + R::DEPTH - 1);
+    const uint32_t now = key(i);
+    if (now != id) {
+      if (!piece) write_sum<O, WIDE>(p, id, at, a);
+#pragma unroll
+      for (int j = 0; j < SMALL_UNIT; ++j) {
+        if (piece) first[j] = a[j];
+        a[j] = 0.f;
+      }
+      piece = false;
+      id = now;
+    }
+    ring.add(a);
+  }
+  if (piece) {  // one run is all of the share
+#pragma unroll
+    for (int j = 0; j < SMALL_UNIT; ++j) first[j] = a[j];
+  } else if (lo < hi && !tail) {
+    write_sum<O, WIDE>(p, id, at, a);
+  }
+  // the pieces that other warps add up: the first run's, where the ring was
+  __syncwarp();
+  float* mine = reinterpret_cast<float*>(small_mem + warp * SMALL_RING);
+#pragma unroll
+  for (int j = 0; j < SMALL_UNIT; ++j) mine[j * 32 + lane] = first[j];
+  __syncthreads();
+  if (!tail) return;
+  for (uint32_t w = warp + 1; w < SUM_WARPS && share(w) < m && key(share(w)) == id; ++w) {
+    const float* piece_of = reinterpret_cast<const float*>(small_mem + w * SMALL_RING);
+#pragma unroll
+    for (int j = 0; j < SMALL_UNIT; ++j) a[j] += piece_of[j * 32 + lane];
+  }
+  write_sum<O, WIDE>(p, id, at, a);
 }
 
 // Keep freed stream-ordered memory in the device's default pool across
@@ -816,9 +934,20 @@ cudaError_t launch_next(K kernel, dim3 grid, dim3 block, const SumArgs& p, cudaS
 }
 
 template <class T, class O>
+bool wide_rows(const SumArgs& p) {
+  return rows_aligned(p.grad, sizeof(T), p.gstride, p.n) && rows_aligned(p.out, sizeof(O), p.ostride, p.n_vocab);
+}
+
+template <class T, class O, bool WIDE>
+cudaError_t launch_small(const SumArgs& p, cudaStream_t stream) {
+  const uint32_t sums = p.n ? (p.dim + SMALL_COLS - 1) / SMALL_COLS : 0;
+  small_kernel<T, O, WIDE><<<p.n_zero + sums, SUM_WARPS * 32, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <class T, class O>
 cudaError_t launch_sums(const SumArgs& p, cudaStream_t stream) {
-  const bool wide = rows_aligned(p.grad, sizeof(T), p.gstride, p.n) &&
-                    rows_aligned(p.out, sizeof(O), p.ostride, p.n_vocab);
+  const bool wide = wide_rows<T, O>(p);
   const unsigned grid = unsigned(p.n_zero + (uint64_t(p.n_chunks) * p.slices + SUM_WARPS - 1) / SUM_WARPS);
   const dim3 join(std::min(p.n_chunks, uint32_t(JOIN_BLOCKS)), p.slices);
   cudaError_t e = launch_next(wide ? sum_kernel<T, O, true> : sum_kernel<T, O, false>, grid, SUM_WARPS * 32, p, stream);
@@ -863,10 +992,9 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   if (n >= ppl::MAX_DIM || n_vocab >= ppl::MAX_DIM || dim >= ppl::MAX_DIM) return PP_ETOOLARGE;
   if (dim > uint64_t(65535) * SUM_COLS) return PP_ETOOLARGE;  // the grid's second dimension
   if (!n_vocab || !dim || (!n && accumulate)) return PP_OK;
-  cudaError_t e = keep_pool_memory();
+  int n_sm;
+  cudaError_t e = ppi::sm_count(&n_sm);
   if (e != cudaSuccess) return ppl::rc_of(e);
-  int blocks, n_sm;
-  if ((e = cluster_setup(&blocks)) != cudaSuccess || (e = ppi::sm_count(&n_sm)) != cudaSuccess) return ppl::rc_of(e);
   const size_t size = ppl::fsize(out_type);
   SumArgs p;
   std::memset(&p, 0, sizeof p);
@@ -905,6 +1033,23 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   s.n = uint32_t(n);
   s.n_vocab = uint32_t(n_vocab);
   s.pad = padding_id;
+  if (!accumulate) {  // two blocks a multiprocessor, but none for less than 64 KiB
+    p.z = z;
+    p.s = s;
+    p.n_zero = uint32_t(std::min<uint64_t>(2 * n_sm, n_vocab * dim * size / 65536 + 1));
+  }
+  if (n <= SMALL_IDS) {
+    p.s = s;
+    return ppl::rc_of(with_type(grad_type, [&](auto t) {
+      return with_type(out_type, [&](auto o) {
+        using T = decltype(t);
+        using O = decltype(o);
+        return wide_rows<T, O>(p) ? launch_small<T, O, true>(p, stream) : launch_small<T, O, false>(p, stream);
+      });
+    }));
+  }
+  int blocks;
+  if ((e = keep_pool_memory()) != cudaSuccess || (e = cluster_setup(&blocks)) != cudaSuccess) return ppl::rc_of(e);
   s.n_tiles = uint32_t((n + SORT_TILE - 1) / SORT_TILE);
   const bool one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * blocks;  // one cluster sorts
   const size_t counts = one ? 0 : size_t(s.n_tiles) * DIGITS, pairs = (n + 3) / 4 * 4;
@@ -928,12 +1073,8 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
     c.s.pos_out = pos[0];
     c.n_long = p.n_long;
     e = launch_cluster_sort(c, blocks, stream);
-    if (!accumulate) {  // two blocks a multiprocessor, but none for less than 64 KiB
-      p.z = z;
-      p.s = s;
-      p.n_zero = uint32_t(std::min<uint64_t>(2 * n_sm, n_vocab * dim * size / 65536 + 1));
-    }
   } else {
+    p.n_zero = 0;  // from the sorted list
     e = cudaMemsetAsync(p.n_long, 0, 4, stream);
     if (e == cudaSuccess) e = launch_sort(s, key, pos, &at, stream);
     if (e == cudaSuccess && !accumulate) {

@@ -96,7 +96,7 @@ __device__ __forceinline__ void count_history(const History& h, int type, int fi
                                               uint32_t* marks) {
   ppl::for_ids<4>(h.line, type, 1, threadIdx.x, h.len, THREADS, [&](uint32_t t, auto tok) {
     if (sizeof(tok) == 8 && uint64_t(tok) >= 0x7FFFFFFFu) return;
-    const uint32_t j = uint32_t(int32_t(tok) - first);  // before the slice: past its end
+    const uint32_t j = uint32_t(tok) - uint32_t(first);  // before the slice: past its end
     if (j >= size) return;
     atomicOr(&marks[j / 32], 1u << (j % 32));
     if (t >= h.given) Counts<HIST>::add(counts, j);
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) logits_kernel(const __grid_co
     if (HIST) count_history<HIST>(h, o.history_type, first, p.slice, counts, marks);
     if (BIAS)
       ppl::for_ids_of<2>(bias.tokens, 1, threadIdx.x, bias.n, THREADS, [&](uint32_t, int32_t tok) {
-        const uint32_t j = uint32_t(tok - first);
+        const uint32_t j = uint32_t(tok) - uint32_t(first);
         if (tok < 0 || j >= p.slice) return;
         if (atomicOr(&biased[j / 32], 1u << (j % 32)) >> (j % 32) & 1) twice = 1;
       });
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) logits_kernel(const __grid_co
     bias = biases_of(o, row);  // again, rather than kept in registers meanwhile
     for (uint32_t e = threadIdx.x; e < bias.n; e += THREADS) {
       const int tok = bias.tokens[e];
-      const uint32_t j = uint32_t(tok - first);
+      const uint32_t j = uint32_t(tok) - uint32_t(first);
       if (tok < 0 || tok >= n_vocab || j >= p.slice) continue;
       if (masked && !(bits && (bits[uint32_t(tok) / 32] >> (tok & 31) & 1))) continue;
       bool last = true;  // the last entry of a token counts

@@ -689,10 +689,10 @@ pp_rc pp_embed(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
  *                   accumulate != 0 the sums are added to what is there, in
  *                   32 bits and rounded once, and only rows of ids that
  *                   occur are touched.
- * Scratch (stream-ordered): 8 bytes an id up to 131072 ids and 17 beyond,
- * and for ids with long runs partial sums of up to dim * n bytes; the
- * device's default memory pool is set to keep it (release threshold:
- * unlimited), so later calls reuse it.
+ * Scratch (stream-ordered): none up to 384 ids; else 8 bytes an id up to
+ * 131072 ids and 17 beyond, and for ids with long runs partial sums of up to
+ * dim * n bytes; the device's default memory pool is then set to keep it
+ * (release threshold: unlimited), so later calls reuse it.
  * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n or n_vocab of 2^31
  * - 65536 or a dim of 2^24 - 255 or more, PP_ENOMEM / PP_ECUDA on CUDA errors.
  */

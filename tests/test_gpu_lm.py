@@ -531,7 +531,7 @@ def test_embed_offsets_past_32_bits():
     assert table[2:-1].abs().max() == 0
 
 
-GRAD_N = [0, 1, 2, 3, 63, 64, 65, 127, 128, 129, 191, 192, 193, 1000, 4095, 4096, 4097, 9000]
+GRAD_N = [0, 1, 2, 3, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 191, 192, 193, 257, 383, 384, 385, 512, 1000, 4095, 4096, 4097, 9000]
 
 
 def grad_ids(rng, n, vocab, how):
@@ -601,12 +601,13 @@ def test_grad_vocabularies(vocab):
     R.check(got, ref, error, torch.float32)
 
 
+@pytest.mark.parametrize("n", [100, 700])
 @pytest.mark.parametrize("out", FT)
 @pytest.mark.parametrize("dtype", FT)
-@pytest.mark.parametrize("dim", [1, 7, 8, 9, 255, 256, 257, 1000, 2051])
-def test_grad_types_and_widths(dtype, out, dim):
+@pytest.mark.parametrize("dim", [1, 7, 8, 9, 63, 64, 65, 255, 256, 257, 1000, 2051])
+def test_grad_types_and_widths(dtype, out, dim, n):
     rng = np.random.default_rng(dim)
-    n, vocab = 700, 90
+    vocab = 90
     ids = grad_ids(rng, n, vocab, "zipf")
     ids[::7] = 11
     grad = torch.from_numpy(rng.normal(0, 1, (n, dim))).to(dtype)
