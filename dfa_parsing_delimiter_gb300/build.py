@@ -1,9 +1,11 @@
-"""Build libpp.so in-tree for sm_103a (nvcc, translation units in parallel)."""
+"""Build libpp.so in-tree for sm_103a (nvcc, translation units in parallel),
+and pp_bind.so, the C half of the Python binding's lm module."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -11,6 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpp.so")
+BIND = os.path.join(PKG, "pp_bind.so")
 SOURCES = ["pp_api.cu", "pp_parse.cu", "pp_tokenize.cu", "pp_generic.cu", "pp_noalloc.cu",
            "pp_stream.cu", "pp_options.cu", "pp_grammar.cu", "pp_logits.cu", "pp_embed.cu"]
 HEADERS = ["pp_device.cuh", "pp_numeric.cuh", "pp_stv16.cuh", "pp_internal.h", "pp_lm.cuh"]
@@ -63,6 +66,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + ".tmp"
         subprocess.check_call([nvcc, "-shared"] + ARCH + ["-o", tmp] + objs)
         os.replace(tmp, LIB)
+    bind_src = os.path.join(CSRC, "pp_bind.c")
+    if force or _stale(BIND, [bind_src, common[0]]):
+        tmp = BIND + ".tmp"
+        subprocess.check_call([nvcc, "-shared", "-cudart", "none", "-O2", "-Xcompiler", "-fPIC",
+                               "-I" + os.path.join(ROOT, "include"),
+                               "-I" + sysconfig.get_paths()["include"], "-o", tmp, bind_src])
+        os.replace(tmp, BIND)
     return LIB
 
 

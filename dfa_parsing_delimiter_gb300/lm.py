@@ -7,7 +7,8 @@
   pp_embed_grad / embed_grad          the gradient for the table
 
 Argument marshalling only, as in the rest of the binding: shapes and types
-are checked here, everything is computed by libpp's kernels on the given
+are checked here (the vectors' in pp_bind.so, whose calls also take less of the
+time than ctypes'), everything is computed by libpp's kernels on the given
 stream (default: the current one).  New outputs belong to that stream; the
 caller orders the use of every tensor on other streams, as with any kernel
 launch.  Arguments that do not fit raise ValueError, errors of the library
@@ -16,7 +17,6 @@ RuntimeError.
 from __future__ import annotations
 
 import ctypes
-import struct
 
 import torch
 
@@ -42,9 +42,6 @@ class LogitOpts(ctypes.Structure):
                 ("n_states", ctypes.c_int32), ("history_type", ctypes.c_int32)]
 
 
-# The same struct from values in order: one pack costs a tenth of setting the
-# fields one by one, which is felt where a call's kernel takes microseconds.
-_pack_opts = struct.Struct("@18Q2i").pack
 _NO_HISTORY, _NO_BIAS, _NO_GRAMMAR = (0,) * 10, (0,) * 4, (0,) * 5
 
 
@@ -62,6 +59,21 @@ def declare(L: ctypes.CDLL) -> None:
     for name, args in sigs.items():
         getattr(L, name).restype = _int
         getattr(L, name).argtypes = args
+    global _c
+    try:
+        from . import pp_bind as _c
+    except ImportError as e:
+        raise RuntimeError("pp_bind.so not built; run __graft_entry__.build()") from e
+    _c.init(*[ctypes.cast(getattr(L, name), _vp).value for name in sigs])
+
+
+_c = None  # pp_bind, once the library is loaded: checks and calls without ctypes' share of the time
+
+
+def _lib():
+    if _c is None:
+        pp.lib()
+    return _c
 
 
 def _need(ok: bool, what: str) -> None:
@@ -79,22 +91,11 @@ def _on(t: torch.Tensor, like: torch.Tensor, name: str, dtypes, ndim: int) -> No
         _wrong(t, like, name, dtypes, ndim)
 
 
-def _vector(t, dev: int, name: str, dtype, n: int) -> int:
-    """Address of a contiguous vector of at least n elements (None: 0)."""
-    if t is None:
-        return 0
-    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.numel() >= n
-            and t.is_contiguous()):
-        return t.data_ptr()
-    raise ValueError(f"{name}: want {n} contiguous elements of {dtype} on the other tensors' device, "
-                     f"got {tuple(t.shape)} of {t.dtype} on {t.device}")
-
-
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _matrix_stride(t: torch.Tensor, name: str) -> int:
@@ -163,8 +164,8 @@ def vocab_grammar(offsets: torch.Tensor, chars: torch.Tensor, desc=None, end_id=
     words = -(-n // 128) * 4
     vectors = _new((n,), torch.int64, offsets, stream)
     allowed = _new((int(desc.n_states), words), torch.int32, offsets, stream)
-    _call(pp.lib().pp_vocab_grammar, "pp_vocab_grammar", offsets, stream, offsets.data_ptr(),
-          chars.data_ptr(), chars.size(0), n, ctypes.byref(desc), -1 if end_id is None else int(end_id),
+    _call(_lib().vocab_grammar, "pp_vocab_grammar", offsets, stream, offsets.data_ptr(),
+          chars.data_ptr(), chars.size(0), n, ctypes.addressof(desc), -1 if end_id is None else int(end_id),
           vectors.data_ptr(), allowed.data_ptr(), words)
     return Grammar._of(vectors, allowed, n, desc)
 
@@ -189,9 +190,10 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
         ps, ss = start.data_ptr(), start.stride(0)
     if not rows:
         return out
-    _call(pp.lib().pp_grammar_states, "pp_grammar_states", tokens, stream, grammar.vectors.data_ptr(),
+    c = _lib()
+    _call(c.grammar_states, "pp_grammar_states", tokens, stream, grammar.vectors.data_ptr(),
           grammar.n_vocab, grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype], rows, cols,
-          _matrix_stride(tokens, "tokens"), _vector(lengths, tokens.get_device(), "lengths", torch.int32, rows),
+          _matrix_stride(tokens, "tokens"), c.vec(lengths, torch.int32, tokens.get_device(), rows, "lengths"),
           ps, ss, grammar.start_state, out.data_ptr(), _matrix_stride(out, "out"))
     return out
 
@@ -210,6 +212,8 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     _need(logits.dtype in FTYPE and logits.dim() == 2, "logits: want 2 dimensions of float32, float16 or bfloat16")
     rows, vocab = logits.shape
     dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
+    c = _lib()
+    vec = c.vec
     if out is None:
         out = torch.empty_like(logits) if stream is None and logits.is_contiguous() else \
             _new((rows, vocab), logits.dtype, logits, stream)
@@ -222,13 +226,13 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
         itype = ITYPE[history.dtype]
         lines, cols = history.shape
         _need(history_row is not None or lines >= rows, "history: want a row for each row of logits")
-        hist = (history.data_ptr(), _vector(history_row, dev, "history_row", i32, rows),
-                _vector(history_len, dev, "history_len", i32, rows),
-                _vector(prompt_len, dev, "prompt_len", i32, rows),
+        hist = (history.data_ptr(), vec(history_row, i32, dev, rows, "history_row"),
+                vec(history_len, i32, dev, rows, "history_len"),
+                vec(prompt_len, i32, dev, rows, "prompt_len"),
                 lines, cols, _matrix_stride(history, "history"),
-                _vector(repetition, dev, "repetition", f32, rows),
-                _vector(presence, dev, "presence", f32, rows),
-                _vector(frequency, dev, "frequency", f32, rows))
+                vec(repetition, f32, dev, rows, "repetition"),
+                vec(presence, f32, dev, rows, "presence"),
+                vec(frequency, f32, dev, rows, "frequency"))
     elif repetition is not None or presence is not None or frequency is not None:
         raise ValueError("penalties need a history")
     lists = _NO_BIAS
@@ -236,8 +240,8 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
         at, tokens, values = bias
         n = tokens.numel()
         _need(values.numel() == n, "bias: want as many values as tokens")
-        lists = (_vector(at, dev, "bias offsets", i32, rows + 1), _vector(tokens, dev, "bias tokens", i32, n),
-                 _vector(values, dev, "bias values", f32, n), n)
+        lists = (vec(at, i32, dev, rows + 1, "bias offsets"), vec(tokens, i32, dev, n, "bias tokens"),
+                 vec(values, f32, dev, n, "bias values"), n)
     mask = _NO_GRAMMAR
     if grammar is not None and states is not None:
         _on(states, logits, "states", _U8, 1)
@@ -248,9 +252,9 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     elif grammar is not states:
         raise ValueError("a grammar needs states, and states a grammar")
     if rows and vocab:
-        _call(pp.lib().pp_logits, "pp_logits", logits, stream, logits.data_ptr(), FTYPE[logits.dtype],
-              rows, vocab, _matrix_stride(logits, "logits"), _pack_opts(*hist, *lists, *mask, itype),
-              out.data_ptr(), _matrix_stride(out, "out"))
+        _call(c.logits, "pp_logits", logits, stream, logits.data_ptr(), FTYPE[logits.dtype], rows, vocab,
+              _matrix_stride(logits, "logits"), *hist, *lists, *mask, itype, out.data_ptr(),
+              _matrix_stride(out, "out"))
     return out
 
 
@@ -284,7 +288,7 @@ def _embed(ids, table, scale, padding_id, out, dtype, stream) -> torch.Tensor:
               out.is_contiguous() and dtype in (None, out.dtype), "out: want the ids' shape and the width, contiguous")
     _need(out.dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
     if n and dim:
-        _call(pp.lib().pp_embed, "pp_embed", ids, stream, ids.data_ptr(), ITYPE[ids.dtype], stride, n,
+        _call(_lib().embed, "pp_embed", ids, stream, ids.data_ptr(), ITYPE[ids.dtype], stride, n,
               table.data_ptr(), FTYPE[table.dtype], vocab, dim, _matrix_stride(table, "table"), scale,
               -1 if padding_id is None else padding_id, out.data_ptr(), FTYPE[out.dtype], dim)
     return out
@@ -336,7 +340,7 @@ def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float
         _need(out.shape == (n_vocab, dim) and dtype in (None, out.dtype), "out: want a row a token, of the width")
     _need(out.dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
     if n_vocab and dim:
-        _call(pp.lib().pp_embed_grad, "pp_embed_grad", ids, stream, ids.data_ptr(), ITYPE[ids.dtype],
+        _call(_lib().embed_grad, "pp_embed_grad", ids, stream, ids.data_ptr(), ITYPE[ids.dtype],
               stride, n, grad.data_ptr(), FTYPE[grad.dtype], _matrix_stride(grad, "grad"), n_vocab, dim,
               scale, -1 if padding_id is None else padding_id, int(bool(accumulate)), out.data_ptr(),
               FTYPE[out.dtype], _matrix_stride(out, "out"))
