@@ -203,10 +203,15 @@ vocab_kernel(const __grid_constant__ VocabArgs p, const __grid_constant__ VocabD
   }
   const uint64_t vec = S == 8 ? 0xFEDCBA9800000000ull | packed : packed;
   if (there) p.vectors[v] = vec;
+  // bit s: state s allows the token
+  uint32_t set = 0;
+#pragma unroll
+  for (int s = 0; s < S; ++s) set |= (dfa.live >> (uint32_t(packed >> (4 * s)) & 15) & 1) << s;
+  set = ends ? dfa.accept : n > 0 ? set & dfa.live : 0;
   uint32_t mine = 0;
-  for (int s = 0; s < dfa.n_states; ++s) {
-    const uint32_t set = ends ? dfa.accept >> s : n > 0 && (dfa.live >> s & 1) ? dfa.live >> nib_apply(vec, s) : 0;
-    const uint32_t word = __ballot_sync(FULL, set & 1);
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const uint32_t word = __ballot_sync(FULL, set >> s & 1);
     if (lane == s) mine = word;
   }
   const uint64_t w = v / 32;
