@@ -159,7 +159,7 @@ __device__ __forceinline__ typename M::Packed vocab_share(const uint8_t* p, uint
 //
 // Bound by instructions, the byte permutes of the compositions: with a thread
 // a token a warp takes as long as its longest token, 24 us for 262144 tokens
-// of 8 bytes on average under 16 states; together 16 to 19.
+// of 8 bytes on average under 16 states; together 15.
 template <int S>
 __global__ void __launch_bounds__(VOCAB_THREADS)
 vocab_kernel(const __grid_constant__ VocabArgs p, const __grid_constant__ VocabDfa dfa) {

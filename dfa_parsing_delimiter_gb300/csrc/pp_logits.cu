@@ -12,8 +12,8 @@
 // order of the atomics changes a count.
 //
 // 512 rows of 131075 f16 with histories of up to 8191, biases and a grammar
-// take 81 us, of which the stream alone is 44 (its 268 MB at the copy rate:
-// 40), the mask 4, counting and turning 26 and the biases 6; bound by the
+// take 80 us, of which the stream alone is 44 (its 268 MB at the copy rate:
+// 40), the mask 4, counting and turning 25 and the biases 7; bound by the
 // latency of a block's steps one after the other, so many blocks at once (four
 // on a multiprocessor) count for more than loads in flight in each.
 //
@@ -274,13 +274,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) logits_kernel(const __grid_co
       *reinterpret_cast<uint4*>(counts + j) = make_uint4(0, 0, 0, 0);
     if (BIAS && threadIdx.x == 0) twice = 0;
     __syncthreads();
-    if (HIST) count_history<HIST>(h, o.history_type, first, p.slice, counts, marks);
     if (BIAS)
-      ppl::for_ids_of<2>(bias.tokens, 1, threadIdx.x, bias.n, THREADS, [&](uint32_t, int32_t tok) {
+      ppl::for_ids_of<1>(bias.tokens, 1, THREADS - 1 - threadIdx.x, bias.n, THREADS, [&](uint32_t, int32_t tok) {
         const uint32_t j = uint32_t(tok) - uint32_t(first);
         if (tok < 0 || j >= p.slice) return;
         if (atomicOr(&biased[j / 32], 1u << (j % 32)) >> (j % 32) & 1) twice = 1;
       });
+    if (HIST) count_history<HIST>(h, o.history_type, first, p.slice, counts, marks);
   }
   // element j of the slice by itself
   auto single = [&](int j) {
@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) logits_kernel(const __grid_co
                [&](int j) { out[first + j] = from_f<T>(turn(j, true)); });
   if (BIAS) {
     bias = biases_of(o, row);  // again, rather than kept in registers meanwhile
-    for (uint32_t e = threadIdx.x; e < bias.n; e += THREADS) {
+    // from the last thread on: the first warps have the marks
+    for (uint32_t e = THREADS - 1 - threadIdx.x; e < bias.n; e += THREADS) {
       const int tok = bias.tokens[e];
       const uint32_t j = uint32_t(tok) - uint32_t(first);
       if (tok < 0 || tok >= n_vocab || j >= p.slice) continue;
