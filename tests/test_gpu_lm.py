@@ -637,6 +637,28 @@ def test_grad_strides_and_shared_rows(dtype):
     assert (whole[:, :4] == 4).all() and (whole[:, 4 + dim:] == 4).all()
 
 
+@pytest.mark.parametrize("dtype", FT)
+@pytest.mark.parametrize("dim", [1, 3, 5, 13, 37, 61, 127, 250])
+def test_aligned_rows_of_odd_widths(dtype, dim):
+    """Rows that begin on 16-byte boundaries and end anywhere: a table, a
+    gradient and a result inside wider arrays."""
+    rng = np.random.default_rng(dim)
+    vocab = 60
+    wide = torch.from_numpy(rng.normal(0, 1, (900, 256))).to(dtype).cuda()
+    for n in (1, 50, 900):
+        ids = grad_ids(rng, n, vocab, "zipf")
+        table = wide[:vocab, :dim]
+        got = pp.embed(dev(ids), table, scale=0.75)
+        ref = R.embed(ids, table.double().cpu().numpy(), 0.75, None)
+        R.check(got, ref, R.U32 * np.abs(ref), dtype)
+        for out in (torch.float32, dtype):
+            whole = torch.full((vocab, 256), 5.0, dtype=out, device="cuda")
+            got = pp.embed_grad(dev(ids), wide[:n, :dim], vocab, out=whole[:, :dim])
+            ref, error = R.embed_grad(ids, wide[:n, :dim].double().cpu().numpy(), vocab, 1, -1)
+            R.check(got, ref, error, out)
+            assert (whole[:, dim:] == 5).all()
+
+
 def test_grad_through_autograd():
     rng = np.random.default_rng(6)
     vocab, dim, n = 17, 12, 50
