@@ -637,6 +637,22 @@ def test_grad_strides_and_shared_rows(dtype):
     assert (whole[:, :4] == 4).all() and (whole[:, 4 + dim:] == 4).all()
 
 
+@pytest.mark.parametrize("n", [1, 300, 5000, 140000])
+def test_grad_of_a_very_large_vocabulary(n):
+    """More rows than a block looks at together, ids of 28 bits."""
+    rng = np.random.default_rng(n)
+    vocab = (1 << 27) + 3
+    ids = rng.integers(0, vocab, n)
+    ids[:min(n, 100)] = vocab - 1
+    out = torch.full((vocab, 1), 9.0, device="cuda")
+    pp.embed_grad(dev(ids), torch.ones(n, 1, device="cuda"), vocab, out=out, padding_id=int(ids[-1]) if n > 1 else None)
+    keep = ids[ids != ids[-1]] if n > 1 else ids
+    which, count = np.unique(keep, return_counts=True)
+    at = torch.nonzero(out[:, 0]).flatten()
+    assert np.array_equal(at.cpu().numpy(), which)
+    assert np.array_equal(out[at, 0].cpu().numpy(), count.astype(np.float32))
+
+
 @pytest.mark.parametrize("dtype", FT)
 @pytest.mark.parametrize("dim", [1, 3, 5, 13, 37, 61, 127, 250])
 def test_aligned_rows_of_odd_widths(dtype, dim):
