@@ -461,7 +461,8 @@ struct SumArgs {
   float* part;  // [n_chunks][2][width]: sums of a chunk's first and last run
   uint64_t width;
   uint32_t n_chunks, chunk;
-  uint32_t *n_long, *longs;  // chunks in which long runs begin
+  uint32_t* n_long;
+  uint2* longs;  // the long runs: the chunk that each begins in, and its id
   uint32_t n_zero;           // blocks that write zeros, before those that sum
   ZeroArgs z;
   SortArgs s;
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_con
   const bool crosses = size == L && next == last && last < p.n_vocab && !(goes_on && first == last);
   const bool tail = crosses && far == last;  // the last run is long and begins here
   if (crosses && !tail) end += __popc(__ballot_sync(FULL, key1 == last));
-  if (tail && c0 == 0 && lane == 0) p.longs[atomicAdd(p.n_long, 1u)] = uint32_t(c);
+  if (tail && c0 == 0 && lane == 0) p.longs[atomicAdd(p.n_long, 1u)] = make_uint2(uint32_t(c), last);
   if (i >= end) return;
   const T* grad = static_cast<const T*>(p.grad) + at.first;
   float* part = p.part + 2 * c * p.width + at.first;
@@ -671,9 +672,11 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
   const Cols<WIDE> cols(blockIdx.y * SUM_COLS, p.dim);
   wait_for_previous();
   const uint32_t n_long = *p.n_long;
+  uint2 run = p.longs[blockIdx.x];  // beside n_long, whether there is one or not
   for (uint32_t r = blockIdx.x; r < n_long; r += gridDim.x) {
-    const uint64_t c = p.longs[r];
-    const uint32_t id = p.key[(c + 1) * L - 1];
+    if (r != blockIdx.x) run = p.longs[r];
+    const uint64_t c = run.x;
+    const uint32_t id = run.y;
     // pieces in the chunks after the one that the run begins in
     uint32_t n = 0;
     for (bool go = true; go;) {
@@ -1055,13 +1058,14 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   const size_t counts = one ? 0 : size_t(s.n_tiles) * DIGITS, pairs = (n + 3) / 4 * 4;
   const size_t parts = p.n_chunks > 2 ? size_t(p.n_chunks) * 2 * p.width : 0;
   void* scratch = nullptr;
-  e = cudaMallocAsync(&scratch, 4 * (parts + (one ? 2 : 4) * pairs + counts + p.n_chunks + 4), stream);
+  const size_t longs = (size_t(p.n_chunks) + 1) / 2 * 4;  // words, in fours
+  e = cudaMallocAsync(&scratch, 4 * (parts + (one ? 2 : 4) * pairs + counts + longs + 4), stream);
   if (e != cudaSuccess) return ppl::rc_of(e);
   p.part = static_cast<float*>(scratch);
   uint32_t* u = reinterpret_cast<uint32_t*>(p.part + parts);
   p.n_long = u;
-  p.longs = u + 4;
-  u = p.longs + p.n_chunks;
+  p.longs = reinterpret_cast<uint2*>(u + 4);
+  u += 4 + longs;
   uint32_t* key[2] = {u, u + 2 * pairs};
   uint32_t* pos[2] = {u + pairs, u + 3 * pairs};
   s.counts = u + 4 * pairs;
