@@ -115,12 +115,14 @@ cudaError_t launch_embed(const EmbedArgs& p, cudaStream_t stream) {
 
 // ---------------------------------------------------------- sort by id
 // Least significant digit first; each pass counts the digits of every tile,
-// scans the counts by (digit, tile) and moves the pairs.  Keys: the id, or
-// n_vocab for a position that takes no part (sorted last).
-constexpr int SORT_THREADS = 256, SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_ITEMS = 16;  // pairs a thread
+// scans each digit's counts over the tiles and moves the pairs, whose block
+// adds up the digits before.  Keys: the id, or n_vocab for a position that
+// takes no part (sorted last).
+constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_ITEMS = 8;  // pairs a thread
 constexpr uint32_t SORT_TILE = SORT_THREADS * SORT_ITEMS;
-constexpr int DIGIT_BITS = 8, DIGITS = 1 << DIGIT_BITS;
+constexpr int DIGIT_BITS = 9, DIGITS = 1 << DIGIT_BITS;
+static_assert(DIGITS == SORT_THREADS, "a thread per digit");
 
 struct SortArgs {
   const void* ids;  // first pass: the ids; else null
@@ -130,9 +132,9 @@ struct SortArgs {
   int64_t pad;
   const uint32_t *key_in, *pos_in;
   uint32_t *key_out, *pos_out;
-  uint32_t* counts;  // [DIGITS][n_tiles]
+  uint32_t* counts;  // [1 << bits][n_tiles], then [1 << bits] totals
   uint32_t n_tiles;
-  int shift;
+  int shift, bits;
 };
 
 __device__ __forceinline__ uint32_t key_of(const SortArgs& p, int64_t id) {
@@ -142,90 +144,103 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& p, uint64_t i) {
   return p.ids ? key_of(p, load_id(p.ids, p.type, i * p.id_stride)) : p.key_in[i];
 }
 
+// This thread's keys of a tile: warp w has SORT_ITEMS x 32 consecutive ones.
+__device__ __forceinline__ void tile_keys(const SortArgs& p, uint64_t first, uint32_t (&key)[SORT_ITEMS]) {
+#pragma unroll
+  for (int k = 0; k < SORT_ITEMS; ++k) key[k] = first + k * 32 < p.n ? sort_key(p, first + k * 32) : 0;
+}
+
+// Exclusive scan of a value a thread over the block's SORT_THREADS threads.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  uint32_t inc = x;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint32_t up = __shfl_up_sync(FULL, inc, d);
+    if (lane >= d) inc += up;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  uint32_t before = inc - x;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  return before;
+}
+
 __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const __grid_constant__ SortArgs p) {
   __shared__ uint32_t count[DIGITS];
   count[threadIdx.x] = 0;
+  const uint64_t first = uint64_t(blockIdx.x) * SORT_TILE + threadIdx.x / 32 * (SORT_ITEMS * 32) + (threadIdx.x & 31);
+  uint32_t key[SORT_ITEMS];
+  tile_keys(p, first, key);
   __syncthreads();
-  const uint64_t base = uint64_t(blockIdx.x) * SORT_TILE;
-#pragma unroll 4
-  for (int k = 0; k < SORT_ITEMS; ++k) {
-    const uint64_t i = base + k * SORT_THREADS + threadIdx.x;
-    if (i < p.n) atomicAdd(&count[sort_key(p, i) >> p.shift & (DIGITS - 1)], 1u);
-  }
+#pragma unroll
+  for (int k = 0; k < SORT_ITEMS; ++k)
+    if (first + k * 32 < p.n) atomicAdd(&count[key[k] >> p.shift & ((1u << p.bits) - 1)], 1u);
   __syncthreads();
-  p.counts[uint64_t(threadIdx.x) * p.n_tiles + blockIdx.x] = count[threadIdx.x];
+  if (threadIdx.x < 1u << p.bits) p.counts[uint64_t(threadIdx.x) * p.n_tiles + blockIdx.x] = count[threadIdx.x];
 }
 
-// Exclusive scan of the counts in place, one block.
-__global__ void __launch_bounds__(1024) sort_scan_kernel(uint32_t* counts, uint64_t n) {
-  __shared__ uint32_t total[32];
-  __shared__ uint32_t carry;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  if (threadIdx.x == 0) carry = 0;
-  __syncthreads();
-  for (uint64_t base = 0; base < n; base += 4096) {
-    uint32_t v[4], sum = 0;
-    const uint64_t at = base + threadIdx.x * 4;
-    for (int k = 0; k < 4; ++k) {
-      v[k] = at + k < n ? counts[at + k] : 0;
-      sum += v[k];
-    }
-    uint32_t inc = sum;
-    for (int d = 1; d < 32; d *= 2) {
-      const uint32_t up = __shfl_up_sync(FULL, inc, d);
-      if (lane >= d) inc += up;
-    }
-    if (lane == 31) total[warp] = inc;
+// A block per digit: its counts become the pairs with it in earlier tiles.
+__global__ void __launch_bounds__(SORT_THREADS) sort_scan_kernel(const __grid_constant__ SortArgs p) {
+  __shared__ uint32_t sums[SORT_WARPS];
+  __shared__ uint32_t last;
+  uint32_t* counts = p.counts + uint64_t(blockIdx.x) * p.n_tiles;
+  uint32_t run = 0;
+  for (uint32_t base = 0; base < p.n_tiles; base += SORT_THREADS) {
+    const uint32_t t = base + threadIdx.x, x = t < p.n_tiles ? counts[t] : 0;
+    const uint32_t before = block_scan(x, sums);
+    if (t < p.n_tiles) counts[t] = run + before;
+    if (threadIdx.x == SORT_THREADS - 1) last = before + x;
     __syncthreads();
-    uint32_t run = carry;
-    for (int w = 0; w < warp; ++w) run += total[w];
-    run += inc - sum;
-    for (int k = 0; k < 4; ++k)
-      if (at + k < n) {
-        counts[at + k] = run;
-        run += v[k];
-      }
-    __syncthreads();
-    if (threadIdx.x == 1023) carry = run;
+    run += last;
     __syncthreads();
   }
+  if (threadIdx.x == 0) p.counts[(uint64_t(1) << p.bits) * p.n_tiles + blockIdx.x] = run;
 }
 
-// Stable move: warp w of the block owns SORT_ITEMS x 32 consecutive pairs,
-// ranks equal digits by match and adds them up per warp in order.
+// Stable move: equal digits of a warp are ranked by ballots, in order.
 __global__ void __launch_bounds__(SORT_THREADS) sort_move_kernel(const __grid_constant__ SortArgs p) {
   __shared__ uint32_t place[SORT_WARPS][DIGITS];
+  __shared__ uint32_t sums[SORT_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const uint32_t n_bins = 1u << p.bits;
   for (int w = 0; w < SORT_WARPS; ++w) place[w][threadIdx.x] = 0;
-  __syncthreads();
-  const uint64_t base = uint64_t(blockIdx.x) * SORT_TILE + warp * (SORT_ITEMS * 32) + lane;
+  const uint64_t first = uint64_t(blockIdx.x) * SORT_TILE + warp * (SORT_ITEMS * 32) + lane;
   uint32_t key[SORT_ITEMS], rank[SORT_ITEMS];
-#pragma unroll
-  for (int k = 0; k < SORT_ITEMS; ++k) key[k] = base + k * 32 < p.n ? sort_key(p, base + k * 32) : 0;
+  tile_keys(p, first, key);
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < SORT_ITEMS; ++k) {
-    const bool there = base + k * 32 < p.n;
-    const uint32_t d = there ? key[k] >> p.shift & (DIGITS - 1) : DIGITS;
-    const uint32_t same = __match_any_sync(FULL, d);
-    if (there) rank[k] = place[warp][d] + __popc(same & ((1u << lane) - 1));
+    const bool there = first + k * 32 < p.n;
+    const uint32_t d = key[k] >> p.shift & (n_bins - 1);
+    uint32_t same = __ballot_sync(FULL, there);
+    for (int b = 0; b < p.bits; ++b) {
+      const uint32_t set = __ballot_sync(FULL, d >> b & 1);
+      same &= d >> b & 1 ? set : ~set;
+    }
+    const uint32_t before = place[warp][d], below = __popc(same & ((1u << lane) - 1));
+    rank[k] = before + below;
     __syncwarp();
-    if (there && lane == 31 - __clz(same)) place[warp][d] = rank[k] + 1;
+    if (there && below == 0) place[warp][d] = before + __popc(same);
     __syncwarp();
   }
-  __syncthreads();
-  uint32_t run = p.counts[uint64_t(threadIdx.x) * p.n_tiles + blockIdx.x];
-  for (int w = 0; w < SORT_WARPS; ++w) {
-    const uint32_t c = place[w][threadIdx.x];
-    place[w][threadIdx.x] = run;
-    run += c;
+  const uint32_t total = threadIdx.x < n_bins ? p.counts[uint64_t(n_bins) * p.n_tiles + threadIdx.x] : 0;
+  uint32_t run = block_scan(total, sums);  // and all ranks are in
+  if (threadIdx.x < n_bins) {
+    run += p.counts[uint64_t(threadIdx.x) * p.n_tiles + blockIdx.x];
+    for (int w = 0; w < SORT_WARPS; ++w) {
+      const uint32_t c = place[w][threadIdx.x];
+      place[w][threadIdx.x] = run;
+      run += c;
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < SORT_ITEMS; ++k)
-    if (base + k * 32 < p.n) {
-      const uint32_t to = place[warp][key[k] >> p.shift & (DIGITS - 1)] + rank[k];
+    if (first + k * 32 < p.n) {
+      const uint32_t to = place[warp][key[k] >> p.shift & (n_bins - 1)] + rank[k];
       p.key_out[to] = key[k];
-      p.pos_out[to] = p.ids ? uint32_t(base + k * 32) : p.pos_in[base + k * 32];
+      p.pos_out[to] = p.ids ? uint32_t(first + k * 32) : p.pos_in[first + k * 32];
     }
 }
 
@@ -320,7 +335,7 @@ __device__ __noinline__ void zero_scan(const ZeroArgs& z, const SortArgs& s, uin
 // of the block that owns it (the last pass: to global memory).  Bound by the
 // latency of its steps: 131072 pairs in two passes of 9 bits take 29 us, 8192
 // take 9, hidden behind the zeros but when the result is accumulated.  The
-// passes through global memory take three kernels each, 90 us for the former.
+// passes through global memory take three kernels each, 42 us for 140000 pairs.
 constexpr int CS_THREADS = 1024, CS_WARPS = 32, CS_BITS = 9, CS_BINS = 1 << CS_BITS;
 constexpr int CS_BLOCKS = 16, CS_ITEMS = 8;
 constexpr uint32_t SORT_CAP = CS_THREADS * CS_ITEMS * CS_BLOCKS;
@@ -904,14 +919,15 @@ cudaError_t launch_cluster_sort(ClusterArgs& p, int blocks, cudaStream_t stream)
 }
 
 cudaError_t launch_sort(SortArgs s, uint32_t* key[2], uint32_t* pos[2], int* at, cudaStream_t stream) {
-  const int bits = key_bits(s.n_vocab);
+  const int bits = key_bits(s.n_vocab), passes = (bits + DIGIT_BITS - 1) / DIGIT_BITS;
+  s.bits = (bits + passes - 1) / passes;
   int to = 0;
-  for (int shift = 0; shift < bits; shift += DIGIT_BITS) {
-    s.shift = shift;
+  for (int pass = 0; pass < passes; ++pass) {
+    s.shift = pass * s.bits;
     s.key_out = key[to];
     s.pos_out = pos[to];
     sort_count_kernel<<<s.n_tiles, SORT_THREADS, 0, stream>>>(s);
-    sort_scan_kernel<<<1, 1024, 0, stream>>>(s.counts, uint64_t(s.n_tiles) * DIGITS);
+    sort_scan_kernel<<<1u << s.bits, SORT_THREADS, 0, stream>>>(s);
     sort_move_kernel<<<s.n_tiles, SORT_THREADS, 0, stream>>>(s);
     s.ids = nullptr;
     s.key_in = key[to];
@@ -1055,7 +1071,7 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   if ((e = keep_pool_memory()) != cudaSuccess || (e = cluster_setup(&blocks)) != cudaSuccess) return ppl::rc_of(e);
   s.n_tiles = uint32_t((n + SORT_TILE - 1) / SORT_TILE);
   const bool one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * blocks;  // one cluster sorts
-  const size_t counts = one ? 0 : size_t(s.n_tiles) * DIGITS, pairs = (n + 3) / 4 * 4;
+  const size_t counts = one ? 0 : (size_t(s.n_tiles) + 1) * DIGITS, pairs = (n + 3) / 4 * 4;
   const size_t parts = p.n_chunks > 2 ? size_t(p.n_chunks) * 2 * p.width : 0;
   void* scratch = nullptr;
   const size_t longs = (size_t(p.n_chunks) + 1) / 2 * 4;  // words, in fours

@@ -566,7 +566,7 @@ def test_grad_ids(n, how):
 
 
 @pytest.mark.parametrize("how", ["zipf", "runs", "one"])
-@pytest.mark.parametrize("n", [1024, 1025, 8192, 8193, 16384, 16385, 32769, 65537, 131072, 131073, 140001])
+@pytest.mark.parametrize("n", [1024, 1025, 8192, 8193, 16384, 16385, 32769, 65537, 131072, 131073, 140001, 262144, 400003])
 def test_grad_many_ids(n, how):
     """The sizes at which another sort takes over, and their neighbours."""
     rng = np.random.default_rng(n)
