@@ -343,7 +343,7 @@ constexpr uint32_t SORT_CAP = CS_THREADS * CS_ITEMS * CS_BLOCKS;
 struct ClusterArgs {
   SortArgs s;  // key_out, pos_out: the sorted list
   int32_t blocks, bits, passes;
-  uint32_t* n_long;  // set to 0 for the sums
+  uint32_t* n_long;  // [2], set to 0 for the sums
 };
 
 __device__ __forceinline__ uint32_t smem_of(const void* p, uint32_t rank) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(CS_THREADS, 1) cluster_sort_kernel(const __gri
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   let_next_start();
   const uint32_t rank = blockIdx.x, n_bins = 1u << p.bits;
-  if (rank == 0 && threadIdx.x == 0) *p.n_long = 0;
+  if (rank == 0 && threadIdx.x == 0) p.n_long[0] = p.n_long[1] = 0;
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
     for (uint32_t k = threadIdx.x; k < CS_WARPS * CS_BINS / 2; k += CS_THREADS)
@@ -476,8 +476,8 @@ struct SumArgs {
   float* part;  // [n_chunks][2][width]: sums of a chunk's first and last run
   uint64_t width;
   uint32_t n_chunks, chunk;
-  uint32_t* n_long;
-  uint2* longs;  // the long runs: the chunk that each begins in, and its id
+  uint32_t* n_long;  // [2]: long runs, and those that blocks share
+  uint2* longs;  // the chunk that each begins in, and its id; the shared ones from the end on
   uint32_t n_zero;           // blocks that write zeros, before those that sum
   ZeroArgs z;
   SortArgs s;
@@ -594,6 +594,21 @@ struct Ring {
   }
 };
 
+// Long runs that reach this many chunks after their first are listed apart.
+// 128 measured the same on Zipf ids (271 us a call against 272); 64 is the least
+// that gives each warp of a group a piece.
+constexpr uint32_t JOIN_SHARE = 64;
+// Where piece q of the run that begins in chunk c lies, for column 0.
+__device__ __forceinline__ float* piece_of(const SumArgs& p, uint64_t c, uint32_t q) {
+  return p.part + (q ? 2 * (c + q) : 2 * c + 1) * p.width;
+}
+// How many blocks have left their sums of that run for the columns from c0
+// on: in the next chunk's second row, which is free since the run fills the
+// chunk.  Set to 0 where the run is listed.
+__device__ __forceinline__ uint32_t* joined(const SumArgs& p, uint64_t c, uint32_t c0) {
+  return reinterpret_cast<uint32_t*>(p.part + (2 * (c + 1) + 1) * p.width + c0);
+}
+
 // Of the sorted list, chunk c holds [c L, (c + 1) L), L <= 32.  A run is long
 // if it begins in chunk c and goes on past the end of chunk c + 1.  A warp
 // per chunk and SUM_COLS columns; the chunk's keys and the next one's are in
@@ -633,6 +648,8 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_con
   const uint32_t pos0 = in0 ? p.pos[lo + lane] : 0, pos1 = in1 ? p.pos[lo + L + lane] : 0;
   const uint32_t prev = lo ? p.key[lo - 1] : NO_KEY, prev2 = lo > L ? p.key[lo - L - 1] : NO_KEY;
   const uint32_t far = uint64_t(lo) + 2 * L < n ? p.key[lo + 2 * L] : NO_KEY;
+  const uint64_t share = lo + uint64_t(JOIN_SHARE) * L;
+  const uint32_t beyond = c0 == 0 && share < n ? p.key[share] : NO_KEY;
   const uint32_t first = __shfl_sync(FULL, key0, 0), last = __shfl_sync(FULL, key0, size - 1);
   const uint32_t next = __shfl_sync(FULL, key1, 0);
   const bool goes_on = prev == first;                                  // the first run began earlier
@@ -642,7 +659,14 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_con
   const bool crosses = size == L && next == last && last < p.n_vocab && !(goes_on && first == last);
   const bool tail = crosses && far == last;  // the last run is long and begins here
   if (crosses && !tail) end += __popc(__ballot_sync(FULL, key1 == last));
-  if (tail && c0 == 0 && lane == 0) p.longs[atomicAdd(p.n_long, 1u)] = make_uint2(uint32_t(c), last);
+  if (tail && lane == 0) {
+    *joined(p, c, c0) = 0;
+    const bool shared = beyond == last;
+    if (c0 == 0) {
+      const uint32_t at = atomicAdd(p.n_long + shared, 1u);
+      p.longs[shared ? p.n_chunks - 1 - at : at] = make_uint2(uint32_t(c), last);
+    }
+  }
   if (i >= end) return;
   const T* grad = static_cast<const T*>(p.grad) + at.first;
   float* part = p.part + 2 * c * p.width + at.first;
@@ -674,64 +698,103 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_con
   else write_sum<O, WIDE>(p, id, at, a);
 }
 
-// Adds the pieces of each long run: a block per run and SUM_COLS columns,
-// a warp per eighth of the pieces, in order.  Bound by latency: 15 us for the
-// long runs of 131072 Zipf ids in chunks of 32.
-constexpr int JOIN_BLOCKS = 256;
+// Adds the pieces of each long run for SUM_COLS columns: a block per run, its
+// warps one piece after another by turns.  Runs of more than JOIN_SHARE pieces
+// (a padding id that nothing masks, the first of a Zipf law) are cut among the
+// JOIN_GROUP blocks of a group; each leaves its sum in the place of its first
+// piece, and the last one to do so adds the sums, in order.  Bound by latency,
+// and for long runs by what a multiprocessor loads (50 GB/s).  An id that half
+// of 131072 positions of 2048 columns name: 192 us a call, 222 with one block a
+// run.  Two loads in flight a lane: more cost registers, and so blocks (131072
+// Zipf ids of 2048 columns: 268 us a call with 2, 272 with 4, 274 with 6).
+constexpr int JOIN_BLOCKS = 256, JOIN_GROUP = 8, JOIN_LOADS = 2;
+
 template <class O, bool WIDE>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ SumArgs p) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 4) join_kernel(const __grid_constant__ SumArgs p) {
+  static_assert(JOIN_GROUP == JOIN_WARPS, "a warp adds a block's sum in the end");
+  static_assert(JOIN_SHARE + 1 >= JOIN_GROUP * JOIN_WARPS, "a piece for each warp of a group");
   __shared__ float part[JOIN_WARPS][SUM_COLS];
-  __shared__ uint32_t more;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const uint32_t rank = blockIdx.x % JOIN_GROUP, groups = gridDim.x / JOIN_GROUP;
   const uint64_t L = p.chunk;
   const Cols<WIDE> cols(blockIdx.y * SUM_COLS, p.dim);
   wait_for_previous();
-  const uint32_t n_long = *p.n_long;
-  uint2 run = p.longs[blockIdx.x];  // beside n_long, whether there is one or not
-  for (uint32_t r = blockIdx.x; r < n_long; r += gridDim.x) {
-    if (r != blockIdx.x) run = p.longs[r];
+  const uint2 n_long = *reinterpret_cast<const uint2*>(p.n_long);
+  uint32_t r = blockIdx.x, h = groups - 1 - blockIdx.x / JOIN_GROUP;
+  const uint2 own = r < p.n_chunks ? p.longs[r] : make_uint2(0, 0);  // beside n_long, whether there is one or not
+#pragma unroll 1
+  for (;;) {
+    // first the shared runs, by the groups whose blocks have the fewest others
+    const bool shared = h < n_long.y;
+    if (!shared && r >= n_long.x) break;
+    uint2 run = own;
+    if (shared) run = p.longs[p.n_chunks - 1 - h];
+    else if (r != blockIdx.x) run = p.longs[r];
     const uint64_t c = run.x;
-    const uint32_t id = run.y;
-    // pieces in the chunks after the one that the run begins in
-    uint32_t n = 0;
-    for (bool go = true; go;) {
-      if (threadIdx.x == 0) more = 0;
-      __syncthreads();
-      const uint64_t at = (c + 1 + n + threadIdx.x) * L;
-      const uint32_t got = __ballot_sync(FULL, at < p.n && p.key[at] == id);
-      if (lane == 0) atomicAdd(&more, uint32_t(__popc(got)));
-      __syncthreads();
-      const uint32_t m = more;
-      n += m;
-      go = m == blockDim.x;
-      __syncthreads();
+    const uint32_t id = run.y, step = shared ? JOIN_GROUP * JOIN_WARPS : JOIN_WARPS;
+    uint32_t q = shared ? rank * JOIN_WARPS + warp : warp;
+    // the first piece comes beside the keys, whether the run has it or not
+    Pack<float, UNIT> x0;
+    if (c + q < p.n_chunks) load_row<float, WIDE>(piece_of(p, c, q) + cols.first, cols.n, x0);
+    uint32_t n;  // pieces in the chunks after the one that the run begins in
+    if (shared) {
+      h += groups;
+      n = JOIN_SHARE;
+      uint32_t most = uint32_t(p.n_chunks - 1 - c);
+      while (n < most) {  // each probe leaves a 257th
+        const uint32_t far = (most - n + blockDim.x - 1) / blockDim.x, at = n + (threadIdx.x + 1) * far;
+        const uint32_t m = __syncthreads_count(at <= most && p.key[(c + at) * L] == id);
+        n += m * far;
+        most = min(most, n + far - 1);
+      }
+    } else {
+      r += gridDim.x;
+      const uint64_t at = (c + 1 + threadIdx.x) * L;
+      n = __syncthreads_count(threadIdx.x < JOIN_SHARE && at < p.n && p.key[at] == id);
     }
-    const uint32_t each = (n + 1 + JOIN_WARPS - 1) / JOIN_WARPS;
-    const uint32_t lo = min(warp * each, n + 1), hi = min(lo + each, n + 1);
-    float a[UNIT] = {};
-    for (uint32_t q = lo; q < hi; q += 6) {
-      Pack<float, UNIT> x[6];
+    float a[UNIT];
 #pragma unroll
-      for (int j = 0; j < 6; ++j)
-        if (q + j < hi)
-          load_row<float, WIDE>(p.part + (q + j ? 2 * (c + q + j) : 2 * c + 1) * p.width + cols.first, cols.n, x[j]);
+    for (int k = 0; k < UNIT; ++k) a[k] = q <= n ? x0.v[k] : 0.f;
+    for (q += step; q <= n; q += JOIN_LOADS * step) {
+      Pack<float, UNIT> x[JOIN_LOADS];
 #pragma unroll
-      for (int j = 0; j < 6; ++j)
-        if (q + j < hi) {
+      for (int j = 0; j < JOIN_LOADS; ++j)
+        if (q + j * step <= n) load_row<float, WIDE>(piece_of(p, c, q + j * step) + cols.first, cols.n, x[j]);
+#pragma unroll
+      for (int j = 0; j < JOIN_LOADS; ++j)
+        if (q + j * step <= n) {
 #pragma unroll
           for (int k = 0; k < UNIT; ++k) a[k] += x[j].v[k];
         }
     }
+    bool end = !shared;
+#pragma unroll 1
+    for (;;) {
 #pragma unroll
-    for (int k = 0; k < UNIT; ++k) part[warp][k * 32 + lane] = a[k];
-    __syncthreads();
-    if (warp == 0) {
+      for (int k = 0; k < UNIT; ++k) part[warp][k * 32 + lane] = a[k];
+      __syncthreads();
+      bool go_on = false;
+      if (warp == 0) {
 #pragma unroll
-      for (int k = 0; k < UNIT; ++k)
-        for (int w = 1; w < JOIN_WARPS; ++w) a[k] += part[w][k * 32 + lane];
-      write_sum<O, WIDE>(p, id, cols, a);
+        for (int k = 0; k < UNIT; ++k)
+          for (int w = 1; w < JOIN_WARPS; ++w) a[k] += part[w][k * 32 + lane];
+        if (end) {
+          write_sum<O, WIDE>(p, id, cols, a);
+        } else {
+          store_row<float, WIDE>(piece_of(p, c, rank * JOIN_WARPS) + cols.first, cols.n, a);
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) go_on = atomicAdd(joined(p, c, blockIdx.y * SUM_COLS), 1u) == JOIN_GROUP - 1;
+          __threadfence();
+        }
+      }
+      if (!__syncthreads_or(go_on)) break;
+      __threadfence();
+      load_row<float, WIDE>(piece_of(p, c, warp * JOIN_WARPS) + cols.first, cols.n, x0);  // a block's sum
+#pragma unroll
+      for (int k = 0; k < UNIT; ++k) a[k] = x0.v[k];
+      end = true;
     }
-    __syncthreads();
   }
 }
 
@@ -968,7 +1031,8 @@ template <class T, class O>
 cudaError_t launch_sums(const SumArgs& p, cudaStream_t stream) {
   const bool wide = wide_rows<T, O>(p);
   const unsigned grid = unsigned(p.n_zero + (uint64_t(p.n_chunks) * p.slices + SUM_WARPS - 1) / SUM_WARPS);
-  const dim3 join(std::min(p.n_chunks, uint32_t(JOIN_BLOCKS)), p.slices);
+  const uint32_t runs = std::min(p.n_chunks, std::max(uint32_t(JOIN_BLOCKS), 152 * 8 / p.slices));
+  const dim3 join((runs + JOIN_GROUP - 1) / JOIN_GROUP * JOIN_GROUP, p.slices);
   cudaError_t e = launch_next(wide ? sum_kernel<T, O, true> : sum_kernel<T, O, false>, grid, SUM_WARPS * 32, p, stream);
   if (e == cudaSuccess && p.n_chunks > 2)
     e = launch_next(wide ? join_kernel<O, true> : join_kernel<O, false>, join, JOIN_WARPS * 32, p, stream);
@@ -1095,7 +1159,7 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
     e = launch_cluster_sort(c, blocks, stream);
   } else {
     p.n_zero = 0;  // from the sorted list
-    e = cudaMemsetAsync(p.n_long, 0, 4, stream);
+    e = cudaMemsetAsync(p.n_long, 0, 8, stream);
     if (e == cudaSuccess) e = launch_sort(s, key, pos, &at, stream);
     if (e == cudaSuccess && !accumulate) {
       zero_kernel<<<unsigned((n_vocab + ZERO_SPAN - 1) / ZERO_SPAN), 256, 0, stream>>>(z, key[at], s.n);

@@ -589,6 +589,23 @@ def test_grad_many_ids(n, how):
         R.check(got, ref, error, torch.float32)
 
 
+@pytest.mark.parametrize("dim", [256, 600, 601])
+@pytest.mark.parametrize("first", [0, 1, 7])
+@pytest.mark.parametrize("runs", [[500, 511, 512, 513, 520, 521, 529], [2016, 2047, 2048, 2049, 2080, 2081, 2113],
+                                  [3, 16640, 1, 40000, 5, 16639], [120000], [20, 300000]])
+def test_grad_of_long_runs(runs, first, dim):
+    """Ids that so many positions name that blocks share their sums, and those just below."""
+    rng = np.random.default_rng(first)
+    ids = np.concatenate([np.full(first, 0)] + [np.full(k, 2 * i + 1) for i, k in enumerate(runs)])
+    rng.shuffle(ids)
+    grad = rng.integers(-8, 9, (len(ids), dim)).astype(np.float32)  # sums without rounding
+    ref = np.zeros((2 * len(runs) + 3, dim))
+    for i in np.unique(ids):
+        ref[i] = grad[ids == i].sum(0, dtype=np.float64)
+    got = pp.embed_grad(dev(ids), dev(grad).to(torch.bfloat16), len(ref), dtype=torch.float32)
+    assert np.array_equal(got.cpu().numpy().astype(np.float64), ref)
+
+
 @pytest.mark.parametrize("vocab", [1, 2, 255, 256, 257, 65535, 65536, 70000, 300000])
 def test_grad_vocabularies(vocab):
     rng = np.random.default_rng(vocab)
