@@ -354,6 +354,7 @@ __device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, S
   Packed vec[K];
   uint32_t bad = K, dead = 0, gone = 0, s = first_state(p, row);
   M before = M::id(), all = M::id();
+  if (blocks > 1) ppl::cluster_arrive();
   if (rank == 0 && threadIdx.x == 0) out[0] = uint8_t(s);
   const bool kept = blocks > 1 && end - begin <= TILE;  // one tile, whose vectors stay
 #pragma unroll 1
@@ -409,6 +410,7 @@ __device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, S
       if (base + TILE < end) __syncthreads();
     }
     if (pass == 0) {
+      ppl::cluster_wait();  // the later blocks have started
       if (warp == 0 && uint32_t(lane) > rank && uint32_t(lane) < blocks) {  // a lane per later block
         const uint64_t v = all.pack();
         uint32_t a, b;
@@ -417,7 +419,7 @@ __device__ void states_row(const StateArgs& p, uint32_t blocks, uint32_t each, S
         asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(gone) : "memory");
       }
-      asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+      ppl::cluster_sync();
 #pragma unroll 4
       for (uint32_t q = 0; q < rank; ++q) {
         const uint32_t next = uint32_t(sh.part[q] >> (4 * (s & 15))) & 15;

@@ -75,6 +75,16 @@ __device__ __forceinline__ void for_ids(const void* p, int type, uint64_t stride
   }
 }
 
+// The barrier of a thread-block cluster.  A block's shared memory may be
+// accessed by others once it has started: every thread arrives when its kernel
+// begins and waits before the first such access, by which time the others'
+// arrivals are long over.  cluster_sync also orders memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // N elements moved in accesses of at most 16 bytes (p aligned to that).
 template <class T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
