@@ -22,6 +22,9 @@
 namespace {
 
 using namespace ppd;
+using ppl::cluster_arrive;
+using ppl::cluster_sync;
+using ppl::cluster_wait;
 using ppl::from_f;
 using ppl::load_id;
 using ppl::Pack;
@@ -351,9 +354,6 @@ __device__ __forceinline__ uint32_t smem_of(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
 
 template <int ITEMS>
 __global__ void __launch_bounds__(CS_THREADS, 1) cluster_sort_kernel(const __grid_constant__ ClusterArgs p) {
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(CS_THREADS, 1) cluster_sort_kernel(const __gri
   __shared__ uint32_t start[CS_BINS];
   __shared__ uint32_t sums[CS_BINS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  cluster_arrive();
   let_next_start();
   const uint32_t rank = blockIdx.x, n_bins = 1u << p.bits;
   if (rank == 0 && threadIdx.x == 0) p.n_long[0] = p.n_long[1] = 0;
@@ -409,6 +410,7 @@ __global__ void __launch_bounds__(CS_THREADS, 1) cluster_sort_kernel(const __gri
       __syncwarp();
     }
     __syncthreads();
+    if (!pass) cluster_wait();  // all blocks have started
     if (threadIdx.x < n_bins) {  // the warps' counts to places within the block
       uint32_t run = 0;
 #pragma unroll 8

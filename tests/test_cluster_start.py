@@ -19,7 +19,7 @@ def functions_with_remote_stores(name):
     return [d for d in re.split(r"(?m)^\}", text) if "st.shared::cluster" in d]
 
 
-@pytest.mark.parametrize("name", ["pp_grammar.cu"])
+@pytest.mark.parametrize("name", ["pp_grammar.cu", "pp_embed.cu"])
 def test_blocks_have_started_before_remote_stores(name):
     found = functions_with_remote_stores(name)
     assert found
