@@ -17,6 +17,7 @@ RuntimeError.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 
 import torch
 
@@ -89,6 +90,11 @@ def _wrong(t, like, name: str, dtypes, ndim) -> None:
 def _on(t: torch.Tensor, like: torch.Tensor, name: str, dtypes, ndim: int) -> None:
     if t.dtype not in dtypes or t.dim() != ndim or t.get_device() != like.get_device():
         _wrong(t, like, name, dtypes, ndim)
+
+
+def _on_stream(stream):
+    """A context in which torch's own work goes to the call's stream."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -331,7 +337,8 @@ def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float
           and grad.shape[:-1] == ids.shape, "grad: want the ids' shape and a last dimension")
     dim = grad.size(-1)
     if grad.dim() != 2:
-        grad = grad.reshape(n, dim)
+        with _on_stream(stream):  # where this copies, the copy is the stream's
+            grad = grad.reshape(n, dim)
     if out is None:
         _need(not accumulate, "accumulate: needs an out")
         out = _new((n_vocab, dim), dtype if dtype is not None else grad.dtype, ids, stream)
