@@ -300,7 +300,15 @@ def _embed(ids, table, scale, padding_id, out, dtype, stream) -> torch.Tensor:
     return out
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t with contiguous rows, as derivatives do not always come."""
+    return t if t.stride(-1) == 1 else t.contiguous()
+
+
 class _Embed(torch.autograd.Function):
+    """embed is linear in the table and embed_grad its derivative, and the
+    other way round: so derivatives of every order are calls of the two."""
+
     @staticmethod
     def forward(ctx, table, ids, scale, padding_id, dtype, stream):
         ctx.save_for_backward(ids)
@@ -310,9 +318,20 @@ class _Embed(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         vocab, scale, padding_id, dtype = ctx.rest
-        if grad.stride(-1) != 1:
-            grad = grad.contiguous()
-        return embed_grad(ctx.saved_tensors[0], grad, vocab, scale, padding_id, dtype=dtype), *[None] * 5
+        return embed_grad(ctx.saved_tensors[0], _rows(grad), vocab, scale, padding_id, dtype=dtype), *[None] * 5
+
+
+class _EmbedGrad(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad, ids, n_vocab, scale, padding_id, dtype, stream):
+        ctx.save_for_backward(ids)
+        ctx.rest = (scale, padding_id, grad.dtype)
+        return _embed_grad(ids, grad, n_vocab, scale, padding_id, None, False, dtype, stream)
+
+    @staticmethod
+    def backward(ctx, grad):
+        scale, padding_id, dtype = ctx.rest
+        return embed(ctx.saved_tensors[0], _rows(grad), scale, padding_id, dtype=dtype), *[None] * 6
 
 
 def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, padding_id=None, out=None, dtype=None,
@@ -327,11 +346,7 @@ def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, padding_id
     return _embed(ids, table, scale, padding_id, out, dtype, stream)
 
 
-def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float = 1.0, padding_id=None,
-               out=None, accumulate: bool = False, dtype=None, stream=None) -> torch.Tensor:
-    """pp_embed_grad: [n_vocab, dim], the gradient of embed's table from that
-    of its result ([*ids.shape, dim]), in `dtype` (default: the gradient's).
-    With accumulate it is added to `out`; else `out` is overwritten."""
+def _embed_grad(ids, grad, n_vocab, scale, padding_id, out, accumulate, dtype, stream) -> torch.Tensor:
     n, stride = _flat_ids(ids)
     _need(grad.dtype in FTYPE and grad.device == ids.device and grad.dim() == ids.dim() + 1
           and grad.shape[:-1] == ids.shape, "grad: want the ids' shape and a last dimension")
@@ -352,3 +367,17 @@ def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float
               scale, -1 if padding_id is None else padding_id, int(bool(accumulate)), out.data_ptr(),
               FTYPE[out.dtype], _matrix_stride(out, "out"))
     return out
+
+
+def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float = 1.0, padding_id=None,
+               out=None, accumulate: bool = False, dtype=None, stream=None) -> torch.Tensor:
+    """pp_embed_grad: [n_vocab, dim], the gradient of embed's table from that
+    of its result ([*ids.shape, dim]), in `dtype` (default: the gradient's).
+    With accumulate it is added to `out`; else `out` is overwritten.  A
+    gradient that requires one itself gets it through embed (then without
+    `out`)."""
+    if grad.requires_grad and torch.is_grad_enabled():
+        _need(out is None, "out: not for a gradient that requires a gradient")
+        _need(not accumulate, "accumulate: needs an out")
+        return _EmbedGrad.apply(grad, ids, n_vocab, scale, padding_id, dtype, stream)
+    return _embed_grad(ids, grad, n_vocab, scale, padding_id, out, accumulate, dtype, stream)

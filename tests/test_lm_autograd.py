@@ -1,0 +1,90 @@
+"""embed and embed_grad under torch's autograd: each is linear in its values
+and the other one is its derivative, of any order."""
+import numpy as np
+import pytest
+import torch
+
+import dfa_parsing_delimiter_gb300 as pp
+
+
+def plain_embed(ids, table, scale, padding_id, out=None, dtype=None, stream=None):
+    """The kernels' results by torch on the CPU, cut from its graph as theirs are."""
+    table = table.detach()
+    there = (ids >= 0) & (ids < table.size(0)) & (ids != (-1 if padding_id is None else padding_id))
+    rows = table[torch.where(there, ids, 0)] * scale
+    return torch.where(there[..., None], rows, 0.0).to(table.dtype if dtype is None else dtype)
+
+
+def plain_embed_grad(ids, grad, n_vocab, scale=1.0, padding_id=None, out=None, accumulate=False, dtype=None, stream=None):
+    grad, ids = grad.detach().reshape(-1, grad.size(-1)), ids.flatten()
+    there = (ids >= 0) & (ids < n_vocab) & (ids != (-1 if padding_id is None else padding_id))
+    full = torch.zeros(n_vocab, grad.size(-1), dtype=grad.dtype).index_add_(0, ids[there], grad[there])
+    return (full * scale).to(grad.dtype if dtype is None else dtype)
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """The two kernel calls replaced: what is tested is what autograd makes of them."""
+    monkeypatch.setattr(pp.lm, "_embed", plain_embed)
+    monkeypatch.setattr(pp.lm, "_embed_grad", plain_embed_grad, raising=False)
+
+
+IDS = torch.tensor([[3, 0, 3], [6, -1, 2], [3, 9, 6]])  # 2: padding; -1 and 9: outside
+
+
+def of(table):
+    return pp.embed(IDS, table, scale=1.5, padding_id=2)
+
+
+def test_derivatives_of_embed(on_cpu):
+    table = torch.randn(7, 5, dtype=torch.float64, requires_grad=True)
+    assert torch.autograd.gradcheck(of, (table,))
+    assert torch.autograd.gradgradcheck(lambda t: of(t) ** 2, (table,))
+
+
+def test_derivatives_of_embed_grad(on_cpu):
+    grad = torch.randn(3, 3, 5, dtype=torch.float64, requires_grad=True)
+
+    def f(g):
+        return pp.embed_grad(IDS, g, 7, scale=1.5, padding_id=2)
+
+    assert f(grad).requires_grad
+    assert torch.autograd.gradcheck(f, (grad,))
+    assert torch.autograd.gradgradcheck(lambda g: f(g) ** 2, (grad,))
+    with torch.no_grad():
+        assert not f(grad).requires_grad
+
+
+def test_refuses_a_result_tensor_for_a_gradient_that_requires_one():
+    grad = torch.zeros(4, 8, requires_grad=True)
+    with pytest.raises(ValueError, match="out"):
+        pp.embed_grad(torch.zeros(4, dtype=torch.int64), grad, 9, out=torch.zeros(9, 8))
+
+
+def penalised(table, ids, weight, look_up):
+    """A loss with the square of its own gradient, all in whole numbers."""
+    y = look_up(ids, table)
+    g, = torch.autograd.grad((weight * y * y).sum(), table, create_graph=True)
+    return (weight * y).sum() + (g * g).sum()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [30, 2000])  # one kernel, and three
+def test_gradient_penalty(n):
+    rng = np.random.default_rng(n)
+    vocab, dim = 40, 12
+    ids = torch.from_numpy(rng.integers(-1, vocab + 1, (n // 10, 10)))
+    value = torch.from_numpy(rng.integers(-3, 4, (vocab, dim))).double()
+    weight = torch.from_numpy(rng.integers(0, 2, (*ids.shape, dim))).double()
+
+    def plain(ids, table):
+        there = (ids >= 0) & (ids < vocab) & (ids != 5)
+        return torch.where(there[..., None], 2 * table[torch.where(there, ids, 0)], 0.0)
+
+    host = value.clone().requires_grad_()
+    penalised(host, ids, weight, plain).backward()
+    table = value.float().cuda().requires_grad_()
+    loss = penalised(table, ids.cuda(), weight.float().cuda(), lambda i, t: pp.embed(i, t, scale=2.0, padding_id=5))
+    loss.backward()
+    assert host.grad.abs().max() < 2 ** 24  # so that 32 bits hold every sum
+    assert torch.equal(table.grad.double().cpu(), host.grad)
