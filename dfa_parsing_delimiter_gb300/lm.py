@@ -20,6 +20,7 @@ import ctypes
 from contextlib import nullcontext
 
 import torch
+from torch.autograd import forward_ad
 
 import dfa_parsing_delimiter_gb300 as pp
 
@@ -305,6 +306,12 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     return t if t.stride(-1) == 1 else t.contiguous()
 
 
+def _followed(t: torch.Tensor) -> bool:
+    """Whether autograd follows t, backward or forward."""
+    return (t.requires_grad and torch.is_grad_enabled()) or \
+        (forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None)
+
+
 class _Embed(torch.autograd.Function):
     """embed is linear in the table and embed_grad its derivative, and the
     other way round: so derivatives of every order are calls of the two."""
@@ -312,26 +319,37 @@ class _Embed(torch.autograd.Function):
     @staticmethod
     def forward(ctx, table, ids, scale, padding_id, dtype, stream):
         ctx.save_for_backward(ids)
-        ctx.rest = (table.size(0), scale, padding_id, table.dtype)
+        ctx.save_for_forward(ids)
+        ctx.rest = (table.size(0), scale, padding_id, table.dtype, dtype)
         return _embed(ids, table, scale, padding_id, None, dtype, stream)
 
     @staticmethod
     def backward(ctx, grad):
-        vocab, scale, padding_id, dtype = ctx.rest
+        vocab, scale, padding_id, dtype, _ = ctx.rest
         return embed_grad(ctx.saved_tensors[0], _rows(grad), vocab, scale, padding_id, dtype=dtype), *[None] * 5
+
+    @staticmethod
+    def jvp(ctx, table, *rest):
+        return embed(ctx.saved_tensors[0], _rows(table), ctx.rest[1], ctx.rest[2], dtype=ctx.rest[4])
 
 
 class _EmbedGrad(torch.autograd.Function):
     @staticmethod
     def forward(ctx, grad, ids, n_vocab, scale, padding_id, dtype, stream):
         ctx.save_for_backward(ids)
-        ctx.rest = (scale, padding_id, grad.dtype)
+        ctx.save_for_forward(ids)
+        ctx.rest = (scale, padding_id, grad.dtype, n_vocab, dtype)
         return _embed_grad(ids, grad, n_vocab, scale, padding_id, None, False, dtype, stream)
 
     @staticmethod
     def backward(ctx, grad):
-        scale, padding_id, dtype = ctx.rest
+        scale, padding_id, dtype = ctx.rest[:3]
         return embed(ctx.saved_tensors[0], _rows(grad), scale, padding_id, dtype=dtype), *[None] * 6
+
+    @staticmethod
+    def jvp(ctx, grad, *rest):
+        scale, padding_id, _, vocab, dtype = ctx.rest
+        return embed_grad(ctx.saved_tensors[0], _rows(grad), vocab, scale, padding_id, dtype=dtype)
 
 
 def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, padding_id=None, out=None, dtype=None,
@@ -339,8 +357,9 @@ def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, padding_id
     """pp_embed: scale * table[ids], [*ids.shape, dim] in `dtype` (default:
     the table's).  ids: integers of any shape at one stride; padding_id and
     ids outside the table give zeros.  A table that requires a gradient gets
-    it through embed_grad (then without `out`)."""
-    if table.requires_grad and torch.is_grad_enabled():
+    it through embed_grad, and one with a tangent passes it on (then without
+    `out`)."""
+    if _followed(table):
         _need(out is None, "out: not for a table that requires a gradient")
         return _Embed.apply(table, ids, scale, padding_id, dtype, stream)
     return _embed(ids, table, scale, padding_id, out, dtype, stream)
@@ -376,7 +395,7 @@ def embed_grad(ids: torch.Tensor, grad: torch.Tensor, n_vocab: int, scale: float
     With accumulate it is added to `out`; else `out` is overwritten.  A
     gradient that requires one itself gets it through embed (then without
     `out`)."""
-    if grad.requires_grad and torch.is_grad_enabled():
+    if _followed(grad):
         _need(out is None, "out: not for a gradient that requires a gradient")
         _need(not accumulate, "accumulate: needs an out")
         return _EmbedGrad.apply(grad, ids, n_vocab, scale, padding_id, dtype, stream)

@@ -88,3 +88,37 @@ def test_gradient_penalty(n):
     loss.backward()
     assert host.grad.abs().max() < 2 ** 24  # so that 32 bits hold every sum
     assert torch.equal(table.grad.double().cpu(), host.grad)
+
+
+def test_forward_mode(on_cpu):
+    """A dual tensor does not require a gradient, and still has a tangent."""
+    import torch.autograd.forward_ad as forward
+    table, tangent = torch.randn(2, 7, 5, dtype=torch.float64)
+    grad, other = torch.randn(2, 3, 3, 5, dtype=torch.float64)
+    with forward.dual_level():
+        got = forward.unpack_dual(of(forward.make_dual(table, tangent))).tangent
+        assert got is not None and torch.equal(got, of(tangent))
+        dual = forward.make_dual(grad, other)
+        got = forward.unpack_dual(pp.embed_grad(IDS, dual, 7, scale=1.5, padding_id=2)).tangent
+        assert got is not None and torch.equal(got, pp.embed_grad(IDS, other, 7, scale=1.5, padding_id=2))
+        with pytest.raises(ValueError, match="out"):
+            pp.embed(IDS, forward.make_dual(table, tangent), out=torch.zeros(3, 3, 5, dtype=torch.float64))
+        with pytest.raises(ValueError, match="out"):
+            pp.embed_grad(IDS, dual, 7, out=torch.zeros(7, 5, dtype=torch.float64))
+    table.requires_grad_()
+    assert torch.autograd.gradcheck(of, (table,), check_forward_ad=True)
+    assert torch.autograd.gradgradcheck(lambda t: of(t) ** 2, (table,), check_fwd_over_rev=True)
+
+
+@pytest.mark.gpu
+def test_forward_mode_of_the_kernels():
+    import torch.autograd.forward_ad as forward
+    rng = np.random.default_rng(1)
+    table, tangent = torch.from_numpy(rng.integers(-9, 10, (2, 40, 12))).float().cuda()
+    ids = torch.from_numpy(rng.integers(-1, 41, 100)).cuda()
+    with forward.dual_level():
+        y = pp.embed(ids, forward.make_dual(table, tangent), scale=2.0)
+        d = pp.embed_grad(ids, y, 40, scale=0.5)
+        value, slope = forward.unpack_dual(d)
+    assert torch.equal(value, pp.embed_grad(ids, pp.embed(ids, table, scale=2.0), 40, scale=0.5))
+    assert torch.equal(slope, pp.embed_grad(ids, pp.embed(ids, tangent, scale=2.0), 40, scale=0.5))
