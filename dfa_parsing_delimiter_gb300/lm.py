@@ -127,6 +127,12 @@ def _call(fn, what: str, like: torch.Tensor, stream, *args) -> None:
         pp._check(rc, what)
 
 
+def _followed(t: torch.Tensor) -> bool:
+    """Whether autograd follows t, backward or forward."""
+    return (t.requires_grad and torch.is_grad_enabled()) or \
+        (forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None)
+
+
 # ------------------------------------------------------------------ grammars
 class Grammar:
     """A vocabulary under a DFA: `vectors` (int64 [n_vocab], a nibble per
@@ -206,6 +212,18 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
 
 
 # ------------------------------------------------------------------ logits
+class _Underived(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, arguments, *followed):
+        return process_logits(*arguments)  # autograd follows nothing in here
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("process_logits has no derivative: detach its arguments")
+
+    jvp = backward
+
+
 def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_len=None, history_row=None,
                    repetition=None, presence=None, frequency=None, bias=None, grammar=None, states=None,
                    out=None, stream=None) -> torch.Tensor:
@@ -215,7 +233,18 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     prompt_len[r] of them as given and the rest as answered.  repetition,
     presence, frequency: float32 [rows].  bias: (offsets int32 [rows + 1],
     tokens int32, values float32), an entry list per row.  grammar and states
-    (uint8 [rows]): tokens that the state does not allow become -inf."""
+    (uint8 [rows]): tokens that the state does not allow become -inf.  There
+    is no derivative: a result of values that require a gradient raises
+    RuntimeError when it is differentiated (and such values take no `out`)."""
+    if forward_ad._current_level >= 0 or logits.requires_grad or (bias is not None and bias[-1].requires_grad) or (
+            repetition is not None and repetition.requires_grad) or (presence is not None and presence.requires_grad) or (
+            frequency is not None and frequency.requires_grad):
+        given = (logits, repetition, presence, frequency, None if bias is None else bias[-1])
+        followed = [t for t in given if t is not None and _followed(t)]
+        if followed:
+            _need(out is None, "out: not for values that require a gradient")
+            return _Underived.apply((logits, history, history_len, prompt_len, history_row, repetition, presence,
+                                     frequency, bias, grammar, states, None, stream), *followed)
     _need(logits.dtype in FTYPE and logits.dim() == 2, "logits: want 2 dimensions of float32, float16 or bfloat16")
     rows, vocab = logits.shape
     dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
@@ -304,12 +333,6 @@ def _embed(ids, table, scale, padding_id, out, dtype, stream) -> torch.Tensor:
 def _rows(t: torch.Tensor) -> torch.Tensor:
     """t with contiguous rows, as derivatives do not always come."""
     return t if t.stride(-1) == 1 else t.contiguous()
-
-
-def _followed(t: torch.Tensor) -> bool:
-    """Whether autograd follows t, backward or forward."""
-    return (t.requires_grad and torch.is_grad_enabled()) or \
-        (forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None)
 
 
 class _Embed(torch.autograd.Function):

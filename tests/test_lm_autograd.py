@@ -122,3 +122,45 @@ def test_forward_mode_of_the_kernels():
         value, slope = forward.unpack_dual(d)
     assert torch.equal(value, pp.embed_grad(ids, pp.embed(ids, table, scale=2.0), 40, scale=0.5))
     assert torch.equal(slope, pp.embed_grad(ids, pp.embed(ids, tangent, scale=2.0), 40, scale=0.5))
+
+
+FLOATS = ["logits", "repetition", "presence", "frequency", "bias"]
+
+
+def logit_arguments(device, follow=lambda t: t, which=None):
+    f = {"logits": torch.ones(2, 9, device=device), "repetition": torch.ones(2, device=device),
+         "presence": torch.ones(2, device=device), "frequency": torch.ones(2, device=device),
+         "bias": torch.ones(2, device=device)}
+    if which is not None:
+        f[which] = follow(f[which])
+    at = torch.tensor([0, 1, 2], dtype=torch.int32, device=device)
+    f["bias"] = (at, at[:2], f["bias"])
+    return dict(f, history=torch.zeros(2, 3, dtype=torch.int32, device=device))
+
+
+@pytest.mark.parametrize("which", FLOATS)
+def test_process_logits_has_no_derivative_and_says_so(monkeypatch, which):
+    """Whoever differentiates its result is told; who does not, may go on."""
+    import torch.autograd.forward_ad as forward
+    monkeypatch.setattr(pp.lm, "_call", lambda *a: None)
+    y = pp.process_logits(**logit_arguments("cpu", lambda t: t.requires_grad_(), which))
+    assert y.requires_grad and y.argmax(1).shape == (2,)
+    with pytest.raises(RuntimeError, match="process_logits"):
+        (y.sum() + 1).backward()
+    with pytest.raises(ValueError, match="out"):
+        pp.process_logits(**logit_arguments("cpu", lambda t: t.requires_grad_(), which), out=torch.zeros(2, 9))
+    with torch.no_grad():
+        y = pp.process_logits(**logit_arguments("cpu", lambda t: t.requires_grad_(), which), out=torch.zeros(2, 9))
+        assert not y.requires_grad
+    with forward.dual_level(), pytest.raises(RuntimeError, match="process_logits"):
+        pp.process_logits(**logit_arguments("cpu", lambda t: forward.make_dual(t, t), which))
+    with forward.dual_level():
+        assert not pp.process_logits(**logit_arguments("cpu")).requires_grad
+
+
+@pytest.mark.gpu
+def test_process_logits_of_logits_that_require_a_gradient():
+    a = logit_arguments("cuda")
+    want = pp.process_logits(**a)
+    got = pp.process_logits(**dict(a, logits=a["logits"].clone().requires_grad_()))
+    assert got.requires_grad and torch.equal(got.detach(), want)
