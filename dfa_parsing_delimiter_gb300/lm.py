@@ -21,6 +21,7 @@ from contextlib import nullcontext
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 import dfa_parsing_delimiter_gb300 as pp
 
@@ -113,6 +114,15 @@ def _matrix_stride(t: torch.Tensor, name: str) -> int:
     return stride[0]
 
 
+def _written(out: torch.Tensor) -> None:
+    """Called where a kernel is about to write to a tensor of the caller's:
+    autograd refuses a backward pass that needs what was there."""
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out: not one that requires a gradient")
+    if not out.is_inference():
+        increment_version(out)
+
+
 def _call(fn, what: str, like: torch.Tensor, stream, *args) -> None:
     """One library call on the tensors' device and the stream."""
     dev = like.get_device()
@@ -191,6 +201,7 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
     start state; lengths: int32 [rows], the tokens of each row that count."""
     _on(tokens, grammar.vectors, "tokens", ITYPE, 2)
     rows, cols = tokens.shape
+    given = out
     if out is None:
         out = _new((rows, cols + 1), torch.uint8, tokens, stream)
     else:
@@ -204,10 +215,13 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
     if not rows:
         return out
     c = _lib()
-    _call(c.grammar_states, "pp_grammar_states", tokens, stream, grammar.vectors.data_ptr(),
-          grammar.n_vocab, grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype], rows, cols,
-          _matrix_stride(tokens, "tokens"), c.vec(lengths, torch.int32, tokens.get_device(), rows, "lengths"),
-          ps, ss, grammar.start_state, out.data_ptr(), _matrix_stride(out, "out"))
+    args = (grammar.vectors.data_ptr(), grammar.n_vocab, grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype],
+            rows, cols, _matrix_stride(tokens, "tokens"),
+            c.vec(lengths, torch.int32, tokens.get_device(), rows, "lengths"),
+            ps, ss, grammar.start_state, out.data_ptr(), _matrix_stride(out, "out"))
+    if given is not None:
+        _written(out)
+    _call(c.grammar_states, "pp_grammar_states", tokens, stream, *args)
     return out
 
 
@@ -239,8 +253,8 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     if forward_ad._current_level >= 0 or logits.requires_grad or (bias is not None and bias[-1].requires_grad) or (
             repetition is not None and repetition.requires_grad) or (presence is not None and presence.requires_grad) or (
             frequency is not None and frequency.requires_grad):
-        given = (logits, repetition, presence, frequency, None if bias is None else bias[-1])
-        followed = [t for t in given if t is not None and _followed(t)]
+        values = (logits, repetition, presence, frequency, None if bias is None else bias[-1])
+        followed = [t for t in values if t is not None and _followed(t)]
         if followed:
             _need(out is None, "out: not for values that require a gradient")
             return _Underived.apply((logits, history, history_len, prompt_len, history_row, repetition, presence,
@@ -250,6 +264,7 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
     c = _lib()
     vec = c.vec
+    given = out
     if out is None:
         out = torch.empty_like(logits) if stream is None and logits.is_contiguous() else \
             _new((rows, vocab), logits.dtype, logits, stream)
@@ -288,9 +303,11 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
     elif grammar is not states:
         raise ValueError("a grammar needs states, and states a grammar")
     if rows and vocab:
+        stride, ostride = _matrix_stride(logits, "logits"), _matrix_stride(out, "out")
+        if given is not None:
+            _written(out)
         _call(c.logits, "pp_logits", logits, stream, logits.data_ptr(), FTYPE[logits.dtype], rows, vocab,
-              _matrix_stride(logits, "logits"), *hist, *lists, *mask, itype, out.data_ptr(),
-              _matrix_stride(out, "out"))
+              stride, *hist, *lists, *mask, itype, out.data_ptr(), ostride)
     return out
 
 
@@ -317,6 +334,7 @@ def _embed(ids, table, scale, padding_id, out, dtype, stream) -> torch.Tensor:
     _on(table, ids, "table", FTYPE, 2)
     vocab, dim = table.shape
     shape = (*ids.shape, dim)
+    given = out
     if out is None:
         out = _new(shape, dtype if dtype is not None else table.dtype, ids, stream)
     else:
@@ -324,8 +342,11 @@ def _embed(ids, table, scale, padding_id, out, dtype, stream) -> torch.Tensor:
               out.is_contiguous() and dtype in (None, out.dtype), "out: want the ids' shape and the width, contiguous")
     _need(out.dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
     if n and dim:
+        tstride = _matrix_stride(table, "table")
+        if given is not None:
+            _written(out)
         _call(_lib().embed, "pp_embed", ids, stream, ids.data_ptr(), ITYPE[ids.dtype], stride, n,
-              table.data_ptr(), FTYPE[table.dtype], vocab, dim, _matrix_stride(table, "table"), scale,
+              table.data_ptr(), FTYPE[table.dtype], vocab, dim, tstride, scale,
               -1 if padding_id is None else padding_id, out.data_ptr(), FTYPE[out.dtype], dim)
     return out
 
@@ -396,6 +417,7 @@ def _embed_grad(ids, grad, n_vocab, scale, padding_id, out, accumulate, dtype, s
     if grad.dim() != 2:
         with _on_stream(stream):  # where this copies, the copy is the stream's
             grad = grad.reshape(n, dim)
+    given = out
     if out is None:
         _need(not accumulate, "accumulate: needs an out")
         out = _new((n_vocab, dim), dtype if dtype is not None else grad.dtype, ids, stream)
@@ -404,10 +426,13 @@ def _embed_grad(ids, grad, n_vocab, scale, padding_id, out, accumulate, dtype, s
         _need(out.shape == (n_vocab, dim) and dtype in (None, out.dtype), "out: want a row a token, of the width")
     _need(out.dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
     if n_vocab and dim:
+        gstride, ostride = _matrix_stride(grad, "grad"), _matrix_stride(out, "out")
+        if given is not None:
+            _written(out)
         _call(_lib().embed_grad, "pp_embed_grad", ids, stream, ids.data_ptr(), ITYPE[ids.dtype],
-              stride, n, grad.data_ptr(), FTYPE[grad.dtype], _matrix_stride(grad, "grad"), n_vocab, dim,
+              stride, n, grad.data_ptr(), FTYPE[grad.dtype], gstride, n_vocab, dim,
               scale, -1 if padding_id is None else padding_id, int(bool(accumulate)), out.data_ptr(),
-              FTYPE[out.dtype], _matrix_stride(out, "out"))
+              FTYPE[out.dtype], ostride)
     return out
 
 

@@ -164,3 +164,56 @@ def test_process_logits_of_logits_that_require_a_gradient():
     want = pp.process_logits(**a)
     got = pp.process_logits(**dict(a, logits=a["logits"].clone().requires_grad_()))
     assert got.requires_grad and torch.equal(got.detach(), want)
+
+
+def results(device):
+    """Each operator with a result tensor: (its call, the shape and type of that)."""
+    ids = torch.zeros(4, dtype=torch.int64, device=device)
+    x = torch.zeros(4, 8, device=device)
+    g = pp.Grammar(torch.zeros(9, dtype=torch.int64, device=device), torch.zeros(5, 4, dtype=torch.int32, device=device), 9,
+                   pp.desc_csv())
+    return {"grammar_states": (lambda out: pp.grammar_states(g, ids[None], out=out), (1, 5), torch.uint8),
+            "process_logits": (lambda out: pp.process_logits(x, out=out), (4, 8), torch.float32),
+            "embed": (lambda out: pp.embed(ids, x, out=out), (4, 8), torch.float32),
+            "embed_grad": (lambda out: pp.embed_grad(ids, x, 9, out=out), (9, 8), torch.float32),
+            "embed_grad added": (lambda out: pp.embed_grad(ids, x, 9, out=out, accumulate=True), (9, 8), torch.float32)}
+
+
+def write_over_what_backward_needs(which, device):
+    call, shape, dtype = results(device)[which]
+    saved = torch.ones(shape, dtype=dtype, device=device)
+    loss = (torch.ones(shape, device=device, requires_grad=True) * saved).sum()
+    call(saved)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+RESULTS = ["grammar_states", "process_logits", "embed", "embed_grad", "embed_grad added"]
+
+
+@pytest.mark.parametrize("which", RESULTS)
+def test_results_in_place_are_noticed_by_autograd(monkeypatch, which):
+    monkeypatch.setattr(pp.lm, "_call", lambda *a: None)
+    write_over_what_backward_needs(which, "cpu")
+    call, shape, dtype = results("cpu")[which]
+    if dtype == torch.float32:
+        leaf = torch.zeros(shape, requires_grad=True)
+        with pytest.raises(ValueError, match="out"):
+            call(leaf)
+        with torch.no_grad():  # as a step of an optimiser may
+            assert call(leaf) is leaf
+    with torch.inference_mode():
+        made = torch.zeros(shape, dtype=dtype)
+        call(made)
+    call(made)  # has no version to count
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", RESULTS)
+def test_results_in_place_on_the_gpu(which):
+    write_over_what_backward_needs(which, "cuda")
+    call, shape, dtype = results("cuda")[which]
+    with torch.inference_mode():
+        made = torch.zeros(shape, dtype=dtype, device="cuda")
+        call(made)
+    call(made)
