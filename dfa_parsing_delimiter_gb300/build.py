@@ -1,5 +1,5 @@
 """Build libpp.so in-tree for sm_103a (nvcc, translation units in parallel),
-and pp_bind.so, the C half of the Python binding's lm module."""
+and pp_bind, the C half of the Python binding's lm module."""
 from __future__ import annotations
 
 import os
@@ -13,7 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpp.so")
-BIND = os.path.join(PKG, "pp_bind.so")
+BIND = os.path.join(PKG, "pp_bind" + sysconfig.get_config_var("EXT_SUFFIX"))  # of this interpreter
 SOURCES = ["pp_api.cu", "pp_parse.cu", "pp_tokenize.cu", "pp_generic.cu", "pp_noalloc.cu",
            "pp_stream.cu", "pp_options.cu", "pp_grammar.cu", "pp_logits.cu", "pp_embed.cu"]
 HEADERS = ["pp_device.cuh", "pp_numeric.cuh", "pp_stv16.cuh", "pp_internal.h", "pp_lm.cuh"]
@@ -66,12 +66,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + ".tmp"
         subprocess.check_call([nvcc, "-shared"] + ARCH + ["-o", tmp] + objs)
         os.replace(tmp, LIB)
-    bind_src = os.path.join(CSRC, "pp_bind.c")
-    if force or _stale(BIND, [bind_src, common[0]]):
+    bind_src, include = os.path.join(CSRC, "pp_bind.c"), sysconfig.get_path("include")
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        sys.stderr.write(f"no Python.h in {include}: built without pp_bind, which the lm module's calls need\n")
+    elif force or _stale(BIND, [bind_src, common[0]]):
         tmp = BIND + ".tmp"
         subprocess.check_call([nvcc, "-shared", "-cudart", "none", "-O2", "-Xcompiler", "-fPIC",
-                               "-I" + os.path.join(ROOT, "include"),
-                               "-I" + sysconfig.get_paths()["include"], "-o", tmp, bind_src])
+                               "-I" + os.path.join(ROOT, "include"), "-I" + include, "-o", tmp, bind_src])
         os.replace(tmp, BIND)
     return LIB
 

@@ -7,7 +7,7 @@
   pp_embed_grad / embed_grad          the gradient for the table
 
 Argument marshalling only, as in the rest of the binding: shapes and types
-are checked here (the vectors' in pp_bind.so, whose calls also take less of the
+are checked here (the vectors' in pp_bind, whose calls also take less of the
 time than ctypes'), everything is computed by libpp's kernels on the given
 stream (default: the current one).  New outputs belong to that stream; the
 caller orders the use of every tensor on other streams, as with any kernel
@@ -17,6 +17,8 @@ RuntimeError.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from contextlib import nullcontext
 
 import torch
@@ -62,21 +64,28 @@ def declare(L: ctypes.CDLL) -> None:
     for name, args in sigs.items():
         getattr(L, name).restype = _int
         getattr(L, name).argtypes = args
-    global _c
-    try:
-        from . import pp_bind as _c
-    except ImportError as e:
-        raise RuntimeError("pp_bind.so not built; run __graft_entry__.build()") from e
-    _c.init(*[ctypes.cast(getattr(L, name), _vp).value for name in sigs])
 
 
-_c = None  # pp_bind, once the library is loaded: checks and calls without ctypes' share of the time
+_c = None  # pp_bind, from the first call on: checks and calls without ctypes' share of the time
 
 
 def _lib():
-    if _c is None:
-        pp.lib()
-    return _c
+    return _c if _c is not None else _load()
+
+
+def _load():
+    global _c
+    from .build import BIND
+    L = pp.lib()
+    if not os.path.exists(BIND):
+        raise RuntimeError(f"{BIND} not built; run __graft_entry__.build() (it needs Python's headers)")
+    spec = importlib.util.spec_from_file_location(__package__ + ".pp_bind", BIND)
+    bind = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(bind)
+    bind.init(*[ctypes.cast(getattr(L, "pp_" + name), _vp).value
+                for name in ("vocab_grammar", "grammar_states", "logits", "embed", "embed_grad")])
+    _c = bind
+    return bind
 
 
 def _need(ok: bool, what: str) -> None:
