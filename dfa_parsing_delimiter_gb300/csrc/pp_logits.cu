@@ -202,6 +202,73 @@ __device__ __forceinline__ void for_marked(const uint32_t* marks, const uint32_t
   }
 }
 
+// A logit under its row's penalties; said: how often its token was answered.
+struct Penalties {
+  float rep, pres, freq;
+  __device__ __forceinline__ Penalties(const pp_logit_opts& o, bool history, uint64_t row)
+      : rep(history && o.d_repetition ? o.d_repetition[row] : 1.f),
+        pres(history && o.d_presence ? o.d_presence[row] : 0.f),
+        freq(history && o.d_frequency ? o.d_frequency[row] : 0.f) {}
+  __device__ __forceinline__ float on(float f, uint32_t said) const {
+    f = f > 0.f ? f / rep : f * rep;
+    return said ? f - freq * float(said) - pres : f;
+  }
+};
+
+// The biases of a row some of whose tokens have several entries, of which the
+// last counts: THREADS of the list at a time, from its end, and a bit for each
+// token that a later lot had.  Entries of one lot for one token clash on their
+// bit; only those are compared with the lot's later entries, a warp for each.
+// So this is linear in the list, where a search of what follows each entry
+// took 102 ms for 100000 entries with one pair among them (75 us without a
+// pair, 132 us with it).  As a function of its own it costs every row of the
+// kernel with biases 1 % (its calls' stack), inlined nothing.
+template <class T, int HIST>
+__device__ __forceinline__ void repeated_biases(const LogitArgs& p, uint64_t row, int first, uint32_t* counts) {
+  const uint32_t n_marks = p.slice / 32, lane = threadIdx.x & 31;
+  const uint32_t* marks = counts + Counts<HIST>::words(p.slice);
+  uint32_t* done = counts + Counts<HIST>::words(p.slice) + (HIST ? n_marks : 0);
+  const T* in = static_cast<const T*>(p.in) + row * p.in_stride;
+  T* out = static_cast<T*>(p.out) + row * p.out_stride;
+  const uint32_t* bits = nullptr;
+  if (p.o.d_allowed) {
+    const uint32_t s = p.o.d_state[row * p.o.state_stride];
+    if (s < uint32_t(p.o.n_states)) bits = p.o.d_allowed + s * p.o.allowed_stride;
+  }
+  const Biases bias = biases_of(p.o, row);
+  const Penalties pen(p.o, HIST != 0, row);
+  for (uint32_t w = threadIdx.x; w < n_marks; w += THREADS) done[w] = 0;
+  __syncthreads();
+  for (uint32_t top = bias.n, base; top; top = base) {
+    base = top > THREADS ? top - THREADS : 0;
+    const uint32_t e = base + threadIdx.x;
+    const int tok = e < top ? bias.tokens[e] : -1;
+    const uint32_t j = uint32_t(tok) - uint32_t(first), bit = 1u << (j % 32);
+    bool last = tok >= 0 && tok < int(p.n_vocab) && j < p.slice && !(done[j / 32] & bit);
+    __syncthreads();
+    const bool clash = last && atomicOr(&done[j / 32], bit) & bit;
+    if (__syncthreads_or(clash)) {
+      if (clash) atomicAnd(&done[j / 32], ~bit);  // now clear for all entries of such a token
+      __syncthreads();
+      const bool shared = last && !(done[j / 32] & bit);
+      __syncthreads();
+      if (shared) atomicOr(&done[j / 32], bit);
+      for (uint32_t todo = __ballot_sync(~0u, shared); todo; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1, same = __shfl_sync(~0u, tok, src);
+        bool later = false;
+        for (uint32_t k = e + src + 1; k < top; k += 32) later |= bias.tokens[k] == same;
+        if (__any_sync(~0u, later) && int(lane) == src) last = false;
+      }
+      __syncthreads();
+    }
+    if (last && (!p.o.d_allowed || (bits && (bits[uint32_t(tok) / 32] >> (tok & 31) & 1)))) {
+      float f = to_f(in[tok]);
+      if (HIST && marks[j / 32] >> (j % 32) & 1) f = pen.on(f, Counts<HIST>::get(counts, j));
+      out[tok] = from_f<T>(f + bias.values[e]);
+    }
+  }
+}
+
 // Rows start at any element, so a vector access begins at a multiple of VEC
 // of a place counted from the last 16-byte boundary before the row, `lead`
 // elements before column 0; a row's incomplete first and last vectors go
@@ -307,22 +374,18 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) logits_kernel(const __grid_co
   }
   if (!HIST && !BIAS) return;
   __syncthreads();
-  const float rep = HIST && o.d_repetition ? o.d_repetition[row] : 1.f;
-  const float pres = HIST && o.d_presence ? o.d_presence[row] : 0.f;
-  const float freq = HIST && o.d_frequency ? o.d_frequency[row] : 0.f;
+  const Penalties pen(o, HIST != 0, row);
   auto turn = [&](int j, bool seen) {
-    float f = to_f(in[first + j]);
-    if (HIST && seen) {
-      f = f > 0.f ? f / rep : f * rep;
-      const uint32_t said = C::get(counts, j);
-      if (said) f = f - freq * float(said) - pres;
-    }
-    return f;
+    const float f = to_f(in[first + j]);
+    return HIST && seen ? pen.on(f, C::get(counts, j)) : f;
   };
   if (HIST)  // but for tokens with a bias, which come next
     for_marked(marks, BIAS ? biased : nullptr, n_marks, first, n_vocab, masked, bits,
                [&](int j) { out[first + j] = from_f<T>(turn(j, true)); });
-  if (BIAS) {
+  if (BIAS && twice) {
+    __syncthreads();  // the marked logits are done with the bits of the biases
+    repeated_biases<T, HIST>(p, row, first, counts);
+  } else if (BIAS) {
     bias = biases_of(o, row);  // again, rather than kept in registers meanwhile
     // from the last thread on: the first warps have the marks
     for (uint32_t e = THREADS - 1 - threadIdx.x; e < bias.n; e += THREADS) {
@@ -330,10 +393,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) logits_kernel(const __grid_co
       const uint32_t j = uint32_t(tok) - uint32_t(first);
       if (tok < 0 || tok >= n_vocab || j >= p.slice) continue;
       if (masked && !(bits && (bits[uint32_t(tok) / 32] >> (tok & 31) & 1))) continue;
-      bool last = true;  // the last entry of a token counts
-      if (twice)
-        for (uint32_t k = e + 1; last && k < bias.n; ++k) last = bias.tokens[k] != tok;
-      if (last) out[tok] = from_f<T>(turn(j, HIST && marks[j / 32] >> (j % 32) & 1) + bias.values[e]);
+      out[tok] = from_f<T>(turn(j, HIST && marks[j / 32] >> (j % 32) & 1) + bias.values[e]);
     }
   }
 }
