@@ -11,7 +11,8 @@ static __typeof__(&pp_vocab_grammar) f_vocab;
 static __typeof__(&pp_grammar_states) f_states;
 static __typeof__(&pp_logits) f_logits;
 static __typeof__(&pp_embed) f_embed;
-static __typeof__(&pp_embed_grad) f_grad;
+static __typeof__(&pp_embed_grad_noalloc) f_grad;
+static __typeof__(&pp_embed_grad_scratch) f_scratch;
 static PyObject *s_dtype, *s_get_device, *s_numel, *s_is_contiguous, *s_dim, *s_data_ptr;
 
 /* a method without arguments that gives an integer; -1 and an error set on failure */
@@ -97,27 +98,35 @@ static PyObject* embed(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 static PyObject* embed_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  long long v[16];
+  long long v[18];
   double scale = 0;
-  if (!want(n, 16) || !numbers(a, n, v, 9, &scale)) return NULL;
+  if (!want(n, 18) || !numbers(a, n, v, 9, &scale)) return NULL;
   CALL(f_grad(PTR(0), (pp_itype)v[1], SIZE(2), SIZE(3), PTR(4), (pp_ftype)v[5], SIZE(6), SIZE(7), SIZE(8), (float)scale,
-              v[10], (int)v[11], PTR(12), (pp_ftype)v[13], SIZE(14), PTR(15)));
+              v[10], (int)v[11], PTR(12), (pp_ftype)v[13], SIZE(14), PTR(15), SIZE(16), PTR(17)));
+}
+
+static PyObject* embed_grad_scratch(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  long long v[3];
+  if (!want(n, 3) || !numbers(a, n, v, -1, NULL)) return NULL;
+  return PyLong_FromSize_t(f_scratch(SIZE(0), SIZE(1), SIZE(2)));
 }
 
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  long long v[5];
-  if (!want(n, 5) || !numbers(a, n, v, -1, NULL)) return NULL;
+  long long v[6];
+  if (!want(n, 6) || !numbers(a, n, v, -1, NULL)) return NULL;
   f_vocab = (__typeof__(f_vocab))(uintptr_t)v[0];
   f_states = (__typeof__(f_states))(uintptr_t)v[1];
   f_logits = (__typeof__(f_logits))(uintptr_t)v[2];
   f_embed = (__typeof__(f_embed))(uintptr_t)v[3];
   f_grad = (__typeof__(f_grad))(uintptr_t)v[4];
+  f_scratch = (__typeof__(f_scratch))(uintptr_t)v[5];
   Py_RETURN_NONE;
 }
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {FAST(init), FAST(vec), FAST(vocab_grammar), FAST(grammar_states),
-                                FAST(logits), FAST(embed), FAST(embed_grad), {NULL, NULL, 0, NULL}};
+                                FAST(logits), FAST(embed), FAST(embed_grad), FAST(embed_grad_scratch),
+                                {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "pp_bind", NULL, -1, methods};
 
 PyMODINIT_FUNC PyInit_pp_bind(void) {

@@ -1041,33 +1041,39 @@ cudaError_t launch_sums(const SumArgs& p, cudaStream_t stream) {
   return e;
 }
 
-}  // namespace
+// What a gradient's sorted list and partial sums take, in 32-bit words.
+struct GradPlan {
+  uint32_t slices, chunk, n_chunks, n_tiles;
+  size_t width, parts, longs, pairs, counts;
+  bool one;  // one cluster sorts
+  size_t bytes() const { return 4 * (parts + 4 + longs + (one ? 2 : 4) * pairs + (one ? 0 : counts)); }
+};
 
-extern "C" {
-
-pp_rc pp_embed(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
-               const void* d_table, pp_ftype table_type, size_t n_vocab, size_t dim,
-               size_t table_stride, float scale, int64_t padding_id, void* d_out,
-               pp_ftype out_type, size_t out_stride, cudaStream_t stream) {
-  if (!ppl::itype_ok(id_type) || !ppl::ftype_ok(table_type) || !ppl::ftype_ok(out_type)) return PP_EINVAL;
-  if (n && dim && (!d_ids || !d_out || (n_vocab && !d_table))) return PP_EINVAL;
-  if (n > 1 && out_stride < dim) return PP_EINVAL;
-  if (!ppl::aligned(d_ids, ppl::isize(id_type)) || !ppl::aligned(d_table, ppl::fsize(table_type)) ||
-      !ppl::aligned(d_out, ppl::fsize(out_type)))
-    return PP_EINVAL;
-  if (n >= ppl::MAX_DIM || n_vocab >= ppl::MAX_DIM || dim >= ppl::MAX_DIM) return PP_ETOOLARGE;
-  if (!n || !dim) return PP_OK;
-  const EmbedArgs p = {d_ids, id_type, id_stride, uint32_t(n), d_table, uint32_t(n_vocab),
-                       uint32_t(dim), table_stride, scale, padding_id, d_out, out_stride};
-  return ppl::rc_of(with_type(table_type, [&](auto t) {
-    return with_type(out_type, [&](auto o) { return launch_embed<decltype(t), decltype(o)>(p, stream); });
-  }));
+GradPlan grad_plan(size_t n, size_t dim, int cluster_blocks) {
+  GradPlan g;
+  g.slices = uint32_t((dim + SUM_COLS - 1) / SUM_COLS);
+  // chunks of 32 where they make enough warps to fill the machine (24 on
+  // each of 152 multiprocessors), else shorter ones: 8192 rows of 1024 take
+  // 34 us in chunks of 8, 37 in 16 and 45 in 32; but shorter ones leave more
+  // pieces of long runs, and 100000 rows of 512 for 1000 ids take 95 us in
+  // chunks of 32, 109 in 16 and 119 in 8
+  g.chunk = 32;
+  while (g.chunk > 8 && uint64_t(n) / g.chunk * g.slices < 152 * 24) g.chunk /= 2;
+  g.n_chunks = uint32_t((n + g.chunk - 1) / g.chunk);
+  g.n_tiles = uint32_t((n + SORT_TILE - 1) / SORT_TILE);
+  g.one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * cluster_blocks;
+  g.width = (dim + 7) / 8 * 8;
+  g.parts = g.n_chunks > 2 ? size_t(g.n_chunks) * 2 * g.width : 0;
+  g.longs = (size_t(g.n_chunks) + 1) / 2 * 4;  // in fours
+  g.pairs = (n + 3) / 4 * 4;
+  g.counts = (size_t(g.n_tiles) + 1) * DIGITS;
+  return g;
 }
 
-pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
-                    const void* d_grad, pp_ftype grad_type, size_t grad_stride, size_t n_vocab,
-                    size_t dim, float scale, int64_t padding_id, int accumulate, void* d_out,
-                    pp_ftype out_type, size_t out_stride, cudaStream_t stream) {
+// pp_embed_grad and its form with the caller's scratch (given).
+pp_rc embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n, const void* d_grad, pp_ftype grad_type,
+                 size_t grad_stride, size_t n_vocab, size_t dim, float scale, int64_t padding_id, int accumulate, void* d_out,
+                 pp_ftype out_type, size_t out_stride, bool given, void* scratch, size_t scratch_bytes, cudaStream_t stream) {
   if (!ppl::itype_ok(id_type) || !ppl::ftype_ok(grad_type) || !ppl::ftype_ok(out_type)) return PP_EINVAL;
   if (n_vocab && dim && (!d_out || (n && (!d_ids || !d_grad)))) return PP_EINVAL;
   if (n_vocab > 1 && out_stride < dim) return PP_EINVAL;
@@ -1077,10 +1083,16 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   if (n >= ppl::MAX_DIM || n_vocab >= ppl::MAX_DIM || dim >= ppl::MAX_DIM) return PP_ETOOLARGE;
   if (dim > uint64_t(65535) * SUM_COLS) return PP_ETOOLARGE;  // the grid's second dimension
   if (!n_vocab || !dim || (!n && accumulate)) return PP_OK;
+  if (given && (scratch_bytes < pp_embed_grad_scratch(n, n_vocab, dim) || !ppl::aligned(scratch, 16) ||
+                (!scratch && pp_embed_grad_scratch(n, n_vocab, dim))))
+    return PP_EINVAL;
   int n_sm;
   cudaError_t e = ppi::sm_count(&n_sm);
   if (e != cudaSuccess) return ppl::rc_of(e);
   const size_t size = ppl::fsize(out_type);
+  int blocks = CS_BLOCKS;
+  if (n > SMALL_IDS && (e = cluster_setup(&blocks)) != cudaSuccess) return ppl::rc_of(e);
+  const GradPlan plan = grad_plan(n, dim, blocks);
   SumArgs p;
   std::memset(&p, 0, sizeof p);
   p.n = uint32_t(n);
@@ -1088,20 +1100,14 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
   p.grad = d_grad;
   p.gstride = grad_stride;
   p.dim = uint32_t(dim);
-  p.slices = uint32_t((dim + SUM_COLS - 1) / SUM_COLS);
   p.scale = scale;
   p.accumulate = accumulate;
   p.out = d_out;
   p.ostride = out_stride;
-  p.width = (dim + 7) / 8 * 8;
-  // chunks of 32 where they make enough warps to fill the machine (24 on
-  // each of 152 multiprocessors), else shorter ones: 8192 rows of 1024 take
-  // 34 us in chunks of 8, 37 in 16 and 45 in 32; but shorter ones leave more
-  // pieces of long runs, and 100000 rows of 512 for 1000 ids take 95 us in
-  // chunks of 32, 109 in 16 and 119 in 8
-  p.chunk = 32;
-  while (p.chunk > 8 && uint64_t(n) / p.chunk * p.slices < 152 * 24) p.chunk /= 2;
-  p.n_chunks = uint32_t((n + p.chunk - 1) / p.chunk);
+  p.slices = plan.slices;
+  p.width = plan.width;
+  p.chunk = plan.chunk;
+  p.n_chunks = plan.n_chunks;
   if (uint64_t(p.n_chunks) * p.slices / SUM_WARPS >= ppl::MAX_DIM) return PP_ETOOLARGE;
   ZeroArgs z;
   z.out = d_out;
@@ -1133,26 +1139,22 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
       });
     }));
   }
-  int blocks;
-  if ((e = keep_pool_memory()) != cudaSuccess || (e = cluster_setup(&blocks)) != cudaSuccess) return ppl::rc_of(e);
-  s.n_tiles = uint32_t((n + SORT_TILE - 1) / SORT_TILE);
-  const bool one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * blocks;  // one cluster sorts
-  const size_t counts = one ? 0 : (size_t(s.n_tiles) + 1) * DIGITS, pairs = (n + 3) / 4 * 4;
-  const size_t parts = p.n_chunks > 2 ? size_t(p.n_chunks) * 2 * p.width : 0;
-  void* scratch = nullptr;
-  const size_t longs = (size_t(p.n_chunks) + 1) / 2 * 4;  // words, in fours
-  e = cudaMallocAsync(&scratch, 4 * (parts + (one ? 2 : 4) * pairs + counts + longs + 4), stream);
-  if (e != cudaSuccess) return ppl::rc_of(e);
+  s.n_tiles = plan.n_tiles;
+  if (!given) {
+    if ((e = keep_pool_memory()) != cudaSuccess) return ppl::rc_of(e);
+    e = cudaMallocAsync(&scratch, plan.bytes(), stream);
+    if (e != cudaSuccess) return ppl::rc_of(e);
+  }
   p.part = static_cast<float*>(scratch);
-  uint32_t* u = reinterpret_cast<uint32_t*>(p.part + parts);
+  uint32_t* u = reinterpret_cast<uint32_t*>(p.part + plan.parts);
   p.n_long = u;
   p.longs = reinterpret_cast<uint2*>(u + 4);
-  u += 4 + longs;
-  uint32_t* key[2] = {u, u + 2 * pairs};
-  uint32_t* pos[2] = {u + pairs, u + 3 * pairs};
-  s.counts = u + 4 * pairs;
+  u += 4 + plan.longs;
+  uint32_t* key[2] = {u, u + 2 * plan.pairs};
+  uint32_t* pos[2] = {u + plan.pairs, u + 3 * plan.pairs};
+  s.counts = u + 4 * plan.pairs;
   int at = 0;
-  if (one) {
+  if (plan.one) {
     ClusterArgs c;
     c.s = s;
     c.s.key_out = key[0];
@@ -1174,8 +1176,53 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
     e = with_type(grad_type, [&](auto t) {
       return with_type(out_type, [&](auto o) { return launch_sums<decltype(t), decltype(o)>(p, stream); });
     });
-  const cudaError_t ef = cudaFreeAsync(scratch, stream);
+  const cudaError_t ef = given ? cudaSuccess : cudaFreeAsync(scratch, stream);
   return ppl::rc_of(e == cudaSuccess ? ef : e);
+}
+
+}  // namespace
+
+extern "C" {
+
+pp_rc pp_embed(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
+               const void* d_table, pp_ftype table_type, size_t n_vocab, size_t dim,
+               size_t table_stride, float scale, int64_t padding_id, void* d_out,
+               pp_ftype out_type, size_t out_stride, cudaStream_t stream) {
+  if (!ppl::itype_ok(id_type) || !ppl::ftype_ok(table_type) || !ppl::ftype_ok(out_type)) return PP_EINVAL;
+  if (n && dim && (!d_ids || !d_out || (n_vocab && !d_table))) return PP_EINVAL;
+  if (n > 1 && out_stride < dim) return PP_EINVAL;
+  if (!ppl::aligned(d_ids, ppl::isize(id_type)) || !ppl::aligned(d_table, ppl::fsize(table_type)) ||
+      !ppl::aligned(d_out, ppl::fsize(out_type)))
+    return PP_EINVAL;
+  if (n >= ppl::MAX_DIM || n_vocab >= ppl::MAX_DIM || dim >= ppl::MAX_DIM) return PP_ETOOLARGE;
+  if (!n || !dim) return PP_OK;
+  const EmbedArgs p = {d_ids, id_type, id_stride, uint32_t(n), d_table, uint32_t(n_vocab),
+                       uint32_t(dim), table_stride, scale, padding_id, d_out, out_stride};
+  return ppl::rc_of(with_type(table_type, [&](auto t) {
+    return with_type(out_type, [&](auto o) { return launch_embed<decltype(t), decltype(o)>(p, stream); });
+  }));
+}
+
+size_t pp_embed_grad_scratch(size_t n, size_t n_vocab, size_t dim) {
+  if (n <= SMALL_IDS || !n_vocab || !dim || n >= ppl::MAX_DIM || dim >= ppl::MAX_DIM) return 0;
+  return grad_plan(n, dim, CS_BLOCKS / 2).bytes();  // no less than with clusters of CS_BLOCKS
+}
+
+pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
+                    const void* d_grad, pp_ftype grad_type, size_t grad_stride, size_t n_vocab,
+                    size_t dim, float scale, int64_t padding_id, int accumulate, void* d_out,
+                    pp_ftype out_type, size_t out_stride, cudaStream_t stream) {
+  return embed_grad(d_ids, id_type, id_stride, n, d_grad, grad_type, grad_stride, n_vocab, dim, scale, padding_id,
+                    accumulate, d_out, out_type, out_stride, false, nullptr, 0, stream);
+}
+
+pp_rc pp_embed_grad_noalloc(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
+                            const void* d_grad, pp_ftype grad_type, size_t grad_stride, size_t n_vocab,
+                            size_t dim, float scale, int64_t padding_id, int accumulate, void* d_out,
+                            pp_ftype out_type, size_t out_stride, void* d_scratch, size_t scratch_bytes,
+                            cudaStream_t stream) {
+  return embed_grad(d_ids, id_type, id_stride, n, d_grad, grad_type, grad_stride, n_vocab, dim, scale, padding_id,
+                    accumulate, d_out, out_type, out_stride, true, d_scratch, scratch_bytes, stream);
 }
 
 }  // extern "C"

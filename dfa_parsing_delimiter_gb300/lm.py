@@ -60,9 +60,12 @@ def declare(L: ctypes.CDLL) -> None:
         "pp_embed": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _vp, _int, _sz, _vp],
         "pp_embed_grad": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _int, _vp,
                           _int, _sz, _vp],
+        "pp_embed_grad_noalloc": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _int, _vp,
+                                  _int, _sz, _vp, _sz, _vp],
+        "pp_embed_grad_scratch": [_sz, _sz, _sz],
     }
     for name, args in sigs.items():
-        getattr(L, name).restype = _int
+        getattr(L, name).restype = _sz if name == "pp_embed_grad_scratch" else _int
         getattr(L, name).argtypes = args
 
 
@@ -83,7 +86,7 @@ def _load():
     bind = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(bind)
     bind.init(*[ctypes.cast(getattr(L, "pp_" + name), _vp).value
-                for name in ("vocab_grammar", "grammar_states", "logits", "embed", "embed_grad")])
+                for name in ("vocab_grammar", "grammar_states", "logits", "embed", "embed_grad_noalloc", "embed_grad_scratch")])
     _c = bind
     return bind
 
@@ -436,12 +439,15 @@ def _embed_grad(ids, grad, n_vocab, scale, padding_id, out, accumulate, dtype, s
     _need(out.dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
     if n_vocab and dim:
         gstride, ostride = _matrix_stride(grad, "grad"), _matrix_stride(out, "out")
+        c = _lib()
+        size = c.embed_grad_scratch(n, n_vocab, dim)
+        scratch = _new((size,), torch.uint8, ids, stream) if size else None
         if given is not None:
             _written(out)
-        _call(_lib().embed_grad, "pp_embed_grad", ids, stream, ids.data_ptr(), ITYPE[ids.dtype],
+        _call(c.embed_grad, "pp_embed_grad", ids, stream, ids.data_ptr(), ITYPE[ids.dtype],
               stride, n, grad.data_ptr(), FTYPE[grad.dtype], gstride, n_vocab, dim,
               scale, -1 if padding_id is None else padding_id, int(bool(accumulate)), out.data_ptr(),
-              FTYPE[out.dtype], ostride)
+              FTYPE[out.dtype], ostride, 0 if scratch is None else scratch.data_ptr(), size)
     return out
 
 

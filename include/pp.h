@@ -701,6 +701,24 @@ pp_rc pp_embed_grad(const void* d_ids, pp_itype id_type, size_t id_stride, size_
                     size_t dim, float scale, int64_t padding_id, int accumulate, void* d_out,
                     pp_ftype out_type, size_t out_stride, cudaStream_t stream);
 
+/*
+ * pp_embed_grad_noalloc — pp_embed_grad with the caller's scratch: it
+ * allocates nothing and leaves the device's memory pool as it is, for callers
+ * with an allocator of their own (the Python binding takes its scratch from
+ * PyTorch's) and for captured graphs without memory nodes.
+ *   d_scratch       device, aligned to 16 bytes, used on `stream` until the
+ *                   call's work is done; NULL where none is needed.
+ *   scratch_bytes   at least pp_embed_grad_scratch of the call's sizes.
+ * Returns PP_EINVAL for too little scratch; otherwise as pp_embed_grad.
+ */
+pp_rc pp_embed_grad_noalloc(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
+                            const void* d_grad, pp_ftype grad_type, size_t grad_stride, size_t n_vocab,
+                            size_t dim, float scale, int64_t padding_id, int accumulate, void* d_out,
+                            pp_ftype out_type, size_t out_stride, void* d_scratch, size_t scratch_bytes,
+                            cudaStream_t stream);
+/* Bytes of scratch that pp_embed_grad_noalloc needs (0: none).  Host only. */
+size_t pp_embed_grad_scratch(size_t n, size_t n_vocab, size_t dim);
+
 #ifdef __cplusplus
 }
 #endif
