@@ -1036,7 +1036,7 @@ cudaError_t launch_sums(const SumArgs& p, cudaStream_t stream) {
   const uint32_t runs = std::min(p.n_chunks, std::max(uint32_t(JOIN_BLOCKS), 152 * 8 / p.slices));
   const dim3 join((runs + JOIN_GROUP - 1) / JOIN_GROUP * JOIN_GROUP, p.slices);
   cudaError_t e = launch_next(wide ? sum_kernel<T, O, true> : sum_kernel<T, O, false>, grid, SUM_WARPS * 32, p, stream);
-  if (e == cudaSuccess && p.n_chunks > 2)
+  if (e == cudaSuccess)
     e = launch_next(wide ? join_kernel<O, true> : join_kernel<O, false>, join, JOIN_WARPS * 32, p, stream);
   return e;
 }
@@ -1063,7 +1063,7 @@ GradPlan grad_plan(size_t n, size_t dim, int cluster_blocks) {
   g.n_tiles = uint32_t((n + SORT_TILE - 1) / SORT_TILE);
   g.one = n <= uint64_t(SORT_CAP) / CS_BLOCKS * cluster_blocks;
   g.width = (dim + 7) / 8 * 8;
-  g.parts = g.n_chunks > 2 ? size_t(g.n_chunks) * 2 * g.width : 0;
+  g.parts = size_t(g.n_chunks) * 2 * g.width;
   g.longs = (size_t(g.n_chunks) + 1) / 2 * 4;  // in fours
   g.pairs = (n + 3) / 4 * 4;
   g.counts = (size_t(g.n_tiles) + 1) * DIGITS;

@@ -689,10 +689,15 @@ pp_rc pp_embed(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
  *                   accumulate != 0 the sums are added to what is there, in
  *                   32 bits and rounded once, and only rows of ids that
  *                   occur are touched.
- * Scratch (stream-ordered): none up to 384 ids; else 8 bytes an id up to
- * 131072 ids and 17 beyond, and for ids with long runs partial sums of up to
- * dim * n bytes; the device's default memory pool is then set to keep it
- * (release threshold: unlimited), so later calls reuse it.
+ * Scratch (stream-ordered): none up to 384 ids.  Beyond, on every call:
+ * partial sums of 8 ceil(n / L) dim' bytes, dim' being dim rounded up to 8 and
+ * L the positions a warp sums, 32 (0.25 dim' n bytes) where n / 32 of them in
+ * steps of 256 columns are 3648 warps or more, else 16 or 8 (1 dim' n bytes);
+ * the sorted list, 8 bytes an id up to 131072 ids (65536 where the device has
+ * no clusters of 16 blocks), and beyond 16 and 2 KiB for every 4096 begun; 8
+ * bytes for every L begun; 4 KiB.  The device's default memory pool is set to
+ * keep it for good (release threshold: unlimited), so later calls reuse it;
+ * pp_embed_grad_noalloc does neither.
  * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n or n_vocab of 2^31
  * - 65536 or a dim of 2^24 - 255 or more, PP_ENOMEM / PP_ECUDA on CUDA errors.
  */

@@ -64,3 +64,16 @@ def test_both_entry_points_agree_and_stay_inside_the_scratch(n):
     assert L.pp_embed_grad_noalloc(*args, b.data_ptr(), 0, dim, room[256:].data_ptr(), need, s) == pp.PP_OK
     assert torch.equal(a, b) and torch.equal(a, pp.embed_grad(ids, grad, vocab, 1.5, 3))
     assert (room[:256] == 77).all() and (room[256 + need:] == 77).all()
+
+
+@pytest.mark.parametrize("n", [385, 386, 1000, 4096, 65536, 65537, 131072, 131073, 1 << 20, 3000001])
+@pytest.mark.parametrize("dim", [1, 7, 8, 9, 256, 257, 2048])
+def test_no_more_than_the_header_states(n, dim):
+    """Partial sums 8 ceil(n / L) dim' with L = 32 where that many chunks fill
+    the machine, and 8 at the least; the sorted list 8 bytes an id, or from
+    65537 ids on 16 and 2 KiB for every 4096 begun; 8 bytes a chunk; 4 KiB."""
+    size = pp.lib().pp_embed_grad_scratch(n, 9, dim)
+    least = 32 if n // 32 * ((dim + 255) // 256) >= 3648 else 8
+    chunks, width = -(-n // least), -(-dim // 8) * 8
+    assert size <= 8 * chunks * width + (8 * n if n <= 65536 else 16 * n + 2048 * -(-n // 4096)) + 8 * chunks + 4096
+    assert size >= 8 * -(-n // 32) * width + 8 * n
