@@ -519,6 +519,7 @@ pp_rc pp_vocab_grammar(const int32_t* d_offsets, const uint8_t* d_chars, size_t 
   if (end_token < -1 || (end_token >= 0 && uint64_t(end_token) >= n_vocab)) return PP_EINVAL;
   if (n_vocab >= ppl::MAX_DIM) return PP_ETOOLARGE;
   if (allowed_stride < (n_vocab + 31) / 32) return PP_EINVAL;
+  if (!ppl::aligned(d_offsets, 4) || !ppl::aligned(d_vectors, 8) || !ppl::aligned(d_allowed, 4)) return PP_EINVAL;
   if (!n_vocab) return PP_OK;
   VocabDfa g;
   std::memset(&g, 0, sizeof g);
@@ -550,6 +551,8 @@ pp_rc pp_grammar_states(const uint64_t* d_vectors, size_t n_vocab, int n_states,
   if (n_rows >= ppl::MAX_DIM || n_cols >= ppl::MAX_DIM || n_vocab >= ppl::MAX_DIM)
     return PP_ETOOLARGE;
   if (!n_rows) return PP_OK;
+  if (!ppl::aligned(d_vectors, 8) || !ppl::aligned(d_tokens, ppl::isize(token_type)) || !ppl::aligned(d_lengths, 4))
+    return PP_EINVAL;
   const StateArgs p = {d_vectors, uint32_t(n_vocab), n_states, d_tokens, token_type,
                        uint32_t(n_rows), uint32_t(n_cols), tokens_stride, d_lengths, d_start,
                        start_stride, start_state, d_states, states_stride};

@@ -491,6 +491,13 @@ extern "C" pp_rc pp_logits(const void* d_in, pp_ftype type, size_t n_rows, size_
     return PP_EINVAL;
   if (n_rows >= ppl::MAX_DIM || n_vocab >= (size_t(1) << 30)) return PP_ETOOLARGE;
   if (!n_rows || !n_vocab) return PP_OK;
+  if (o.d_history && !ppl::aligned(o.d_history, ppl::isize(o.history_type))) return PP_EINVAL;
+  for (const void* four : {static_cast<const void*>(o.d_history_row), static_cast<const void*>(o.d_history_len),
+                           static_cast<const void*>(o.d_prompt_len), static_cast<const void*>(o.d_repetition),
+                           static_cast<const void*>(o.d_presence), static_cast<const void*>(o.d_frequency),
+                           static_cast<const void*>(o.d_bias_offsets), static_cast<const void*>(o.d_bias_tokens),
+                           static_cast<const void*>(o.d_bias_values), static_cast<const void*>(o.d_allowed)})
+    if (!ppl::aligned(four, 4)) return PP_EINVAL;
   p.in = d_in;
   p.out = d_out;
   p.in_stride = in_stride;
