@@ -619,7 +619,7 @@ __device__ __forceinline__ uint32_t* joined(const SumArgs& p, uint64_t c, uint32
 // ids alone and so run beside the sort; the sums follow on the slots that
 // they leave, and the memory is never idle.
 //
-// 131072 rows of 2048 bf16 for 131072 Zipf ids: 1.59 GB in 256 us, 91 % of
+// 131072 rows of 2048 bf16 for 131072 Zipf ids: 1.59 GB in 253 us, 92 % of
 // the copy rate (zeros 794 MB, rows read 537 MB, sums 280 MB); bound by
 // memory.  A run's sum is written in one place of a loop that is not
 // unrolled: with 8 rows in registers and as many places the code does not
@@ -705,9 +705,10 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 2) sum_kernel(const __grid_con
 // (a padding id that nothing masks, the first of a Zipf law) are cut among the
 // JOIN_GROUP blocks of a group; each leaves its sum in the place of its first
 // piece, and the last one to do so adds the sums, in order.  Bound by latency,
-// and for long runs by what a multiprocessor loads (50 GB/s).  An id that half
-// of 131072 positions of 2048 columns name: 192 us a call, 222 with one block a
-// run.  Two loads in flight a lane: more cost registers, and so blocks (131072
+// and for long runs by what a block with so few loads in flight reads (50 GB/s;
+// a multiprocessor reads 137 with 1024 threads of eight 16-byte loads).  An id
+// that half of 131072 positions of 2048 columns name: 190 us a call, 222 with
+// one block a run.  Two loads in flight a lane: more cost registers, and so blocks (131072
 // Zipf ids of 2048 columns: 268 us a call with 2, 272 with 4, 274 with 6).
 constexpr int JOIN_BLOCKS = 256, JOIN_GROUP = 8, JOIN_LOADS = 2;
 
@@ -804,11 +805,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) join_kernel(const __grid_c
 // Up to SMALL_IDS ids in one launch without scratch: every block that sums
 // sorts the (id, position) pairs for itself (bitonic, in shared memory) and
 // has 64 columns, its warps equal shares of the sorted list.  So few columns,
-// two a lane, since a multiprocessor moves 50 to 60 GB/s at most and a block
-// has all rows of its columns.  The
-// pieces of runs that cross shares are kept in shared memory and added in
-// order by the warp that a run begins in.  Other blocks write zero rows as
-// in sum_kernel.
+// two a lane, since a block of this size reads 50 to 70 GB/s and each has all
+// rows of its columns.  The pieces of runs that cross shares are kept in shared
+// memory and added in order by the warp that a run begins in.  Other blocks
+// write zero rows as in sum_kernel.
 //
 // Rows of 256 f32 or 2048 bf16 for 4000 ids: 128 ids take 7 and 13 us, and 15
 // and 13 in three kernels, a call from Python 8 and 14 against 19 and 18; 512

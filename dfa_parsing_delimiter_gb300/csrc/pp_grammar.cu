@@ -157,9 +157,11 @@ __device__ __forceinline__ typename M::Packed vocab_share(const uint8_t* p, uint
 // a lane, the pieces composed in order.  Then a ballot per state writes 32
 // tokens' bits.
 //
-// Bound by instructions, the byte permutes of the compositions: with a thread
-// a token a warp takes as long as its longest token, 24 us for 262144 tokens
-// of 8 bytes on average under 16 states; together 15.
+// Bound by instructions: 262144 tokens of 8 bytes on average under 16 states
+// take 9.9 M of a warp, 6.0 M of them on the ALU pipe (71 % of its rate), in 15
+// us; a third are the compositions of bytes and of the scan, the rest the
+// bytes, the marks, the branch at a token's end and the ballots around them.
+// With a thread a token a warp takes as long as its longest token: 24 us.
 template <int S>
 __global__ void __launch_bounds__(VOCAB_THREADS)
 vocab_kernel(const __grid_constant__ VocabArgs p, const __grid_constant__ VocabDfa dfa) {
@@ -281,12 +283,18 @@ __global__ void __launch_bounds__(128) states_short_kernel(const __grid_constant
 // tokens keeps its vectors in registers between the two steps; a longer one
 // reads them twice.
 //
-// Bound by instructions (the byte permutes of the compositions go at half
-// rate) and by the latency of its steps, not by memory.  640 threads, so that two blocks
-// share a multiprocessor and clusters of 16 fill the machine (with one block
-// a multiprocessor only 15 clusters of 8 run at once, and 16 rows of 65537
-// tokens take two waves, 27 us; this way 13), and so that a row of a few
-// tokens more than a power of two still has one tile a block.
+// Bound by the latency of its steps, barriers first (16 rows of 65537 tokens
+// under 5 states: 13.4 us, issue 38 %), not by memory.  Two blocks share a
+// multiprocessor, so that clusters of 16 fill the machine (with one, only 15
+// clusters of 8 run at once, and 16 rows take two waves, 27 us).  Threads a
+// block: more of them hold a longer part in one tile, whose tokens are read
+// once, and pay more for their barriers.  16 rows under 5 and 16 states, us:
+//   tokens a row   20000        50000        65537        100000       200000
+//   512 threads     9.1, 12.0   12.2, 15.9   26.8, 40.3   30.7, 44.7   55.2, 84.0
+//   640            10.1, 13.3   13.4, 18.6   14.1, 19.5   32.4, 51.3   49.9, 78.0
+//   768            12.0, 15.8   15.4, 18.3   16.5, 19.3   37.9, 55.5   59.4, 85.5
+// (one tile up to 65536, 81920 and 98304).  The 16-lane form of 8 tokens a
+// thread spills 88 bytes at the 48 registers that two blocks leave.
 constexpr int STATES_THREADS = 640, STATES_WARPS = STATES_THREADS / 32, STATES_BLOCKS = 16;
 
 struct StateShared {

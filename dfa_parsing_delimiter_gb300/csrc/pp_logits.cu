@@ -12,7 +12,7 @@
 // order of the atomics changes a count.
 //
 // 512 rows of 131075 f16 with histories of up to 8191, biases and a grammar
-// take 80 us, of which the stream alone is 44 (its 268 MB at the copy rate:
+// take 79 us, of which the stream alone is 44 (its 268 MB at the copy rate:
 // 40), the mask 4, counting and turning 25 and the biases 7; bound by the
 // latency of a block's steps one after the other, so many blocks at once (four
 // on a multiprocessor) count for more than loads in flight in each.

@@ -3,16 +3,17 @@
   pp_vocab_grammar / vocab_grammar    a vocabulary under a DFA -> Grammar
   pp_grammar_states / grammar_states  the DFA's state along token sequences
   pp_logits / process_logits          penalties, biases and the grammar's mask
-  pp_embed / embed                    rows of a table by id (differentiable)
-  pp_embed_grad / embed_grad          the gradient for the table
+  pp_embed / embed                    rows of a table by id
+  pp_embed_grad / embed_grad          the gradient for the table (both differentiable)
 
 Argument marshalling only, as in the rest of the binding: shapes and types
 are checked here (the vectors' in pp_bind, whose calls also take less of the
 time than ctypes'), everything is computed by libpp's kernels on the given
 stream (default: the current one).  New outputs belong to that stream; the
 caller orders the use of every tensor on other streams, as with any kernel
-launch.  Arguments that do not fit raise ValueError, errors of the library
-RuntimeError.
+launch.  Result tensors that are given count as written to in place: they may
+not require a gradient while gradients are recorded.  Arguments that do not fit
+raise ValueError, errors of the library RuntimeError.
 """
 from __future__ import annotations
 

@@ -685,10 +685,10 @@ pp_rc pp_embed(const void* d_ids, pp_itype id_type, size_t id_stride, size_t n,
  * are summed in 32 bits in an order that depends on ids alone, so the same
  * inputs give the same bits.
  *   d_grad          device [n][grad_stride] (stride 0: one row for all).
- *   d_out           device [n_vocab][out_stride]; every row is written.  With
- *                   accumulate != 0 the sums are added to what is there, in
- *                   32 bits and rounded once, and only rows of ids that
- *                   occur are touched.
+ *   d_out           device [n_vocab][out_stride], overlapping no input; every
+ *                   row is written.  With accumulate != 0 the sums are added
+ *                   to what is there, in 32 bits and rounded once, and only
+ *                   rows of ids that occur are touched.
  * Scratch (stream-ordered): none up to 384 ids.  Beyond, on every call:
  * partial sums of 8 ceil(n / L) dim' bytes, dim' being dim rounded up to 8 and
  * L the positions a warp sums, 32 (0.25 dim' n bytes) where n / 32 of them in
