@@ -228,13 +228,13 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
     if not rows:
         return out
     c = _lib()
-    args = (grammar.vectors.data_ptr(), grammar.n_vocab, grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype],
-            rows, cols, _matrix_stride(tokens, "tokens"),
-            c.vec(lengths, torch.int32, tokens.get_device(), rows, "lengths"),
-            ps, ss, grammar.start_state, out.data_ptr(), _matrix_stride(out, "out"))
+    stride, ostride = _matrix_stride(tokens, "tokens"), _matrix_stride(out, "out")
+    size = c.vec(lengths, torch.int32, tokens.get_device(), rows, "lengths")
     if given is not None:
         _written(out)
-    _call(c.grammar_states, "pp_grammar_states", tokens, stream, *args)
+    _call(c.grammar_states, "pp_grammar_states", tokens, stream, grammar.vectors.data_ptr(), grammar.n_vocab,
+          grammar.n_states, tokens.data_ptr(), ITYPE[tokens.dtype], rows, cols, stride, size, ps, ss,
+          grammar.start_state, out.data_ptr(), ostride)
     return out
 
 
