@@ -130,6 +130,7 @@ def lib() -> ctypes.CDLL:
         L.pp_debug_long_fields.restype = ctypes.c_int
         L.pp_debug_long_fields.argtypes = [ctypes.POINTER(ctypes.c_uint64), ctypes.c_int]
         lm.declare(L)
+        adamw.declare(L)
         _lib = L
     return _lib
 
@@ -609,6 +610,7 @@ def tokenize_host(h_in: torch.Tensor, desc: DfaDesc | None = None, stream=None):
     return tuple(out), st, int(h_in.numel()), int(d2h)
 
 
-from . import lm  # noqa: E402
-from .lm import (Grammar, embed, embed_grad, grammar_states, process_logits,  # noqa: E402,F401
-                 vocab_grammar)
+from . import adamw, lm  # noqa: E402
+from .adamw import AdamWState, adamw_state, adamw_step  # noqa: E402,F401
+from .lm import (Grammar, embed, embed_grad, grammar_states, process_logits, token_probs,  # noqa: E402,F401
+                 verify_drafts, vocab_grammar)

@@ -1,0 +1,400 @@
+// pp_adamw: one AdamW step over many tensors, states in 32 or in 8 bits.
+//
+// A warp takes a tile of 256 consecutive elements of one tensor: parameter,
+// gradient and both states are read once, stepped in registers and written
+// once.  Nothing is read twice and nothing is shared between tiles but the
+// step's constants, so the memory's rate bounds it (28 bytes an element with
+// 32-bit values all through, 16 with 8-bit states).  A tile is also what shares
+// an exponent in 8 bits: the largest exponent is one warp reduction, and the
+// codes come from the registers that the step left.
+//
+// The tensors' addresses are kernel parameters (up to 640 tensors a launch):
+// nothing to copy to the device, so a step is one launch and can be captured.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "pp_internal.h"
+#include "pp_lm.cuh"
+
+namespace {
+
+using ppl::from_f;
+using ppl::to_f;
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int TILE = PP_ADAMW_BLOCK, EACH = TILE / 32;  // elements of a warp and of a lane
+constexpr int BLOCKS = 8;                               // a multiprocessor
+
+struct Item {
+  void* param;
+  const void* grad;
+  uint64_t n;
+  uint64_t first;       // of the state's elements
+  uint32_t tile_begin;  // of the launch's tiles
+  float decay;
+  int32_t param_type, grad_type;
+};
+
+struct Common {
+  void* m;
+  void* v;
+  uint8_t* m_exp;
+  uint8_t* v_exp;
+  float* master;
+  int32_t* counters;  // steps done; blocks that are through with this one
+  const float* lr_at;
+  const float* scale_at;
+  const float* skip_at;
+  float lr, b1, c1, b2, c2, eps;  // c: 1 - b, rounded once
+  float log_b1, log_b2;
+  uint32_t n_items, n_tiles, seed;
+  int32_t nearest, last;
+};
+
+template <int CAP>
+struct Args {
+  Common c;
+  Item item[CAP];
+};
+static_assert(sizeof(Args<640>) < 32764, "kernel parameters");
+
+// A hash of 32 bits: odd multipliers from the fractions of the roots of 2 and
+// 3, between shifts that bring high bits down.
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ x >> 16;
+}
+
+// EACH values of a lane.  In a whole tile at 16-byte addresses a lane's are
+// EACH consecutive ones; otherwise, element by element, those at lane, lane +
+// 32, ... so that a warp's accesses lie side by side.
+template <class T>
+__device__ __forceinline__ void read_whole(const T* p, float* x) {
+  constexpr int N = 16 / sizeof(T);
+#pragma unroll
+  for (int k = 0; k < EACH; k += N) {
+    const ppl::Pack<T, N> q = *reinterpret_cast<const ppl::Pack<T, N>*>(p + k);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[k + i] = to_f(q.v[i]);
+  }
+}
+template <class T>
+__device__ __forceinline__ void write_whole(T* p, const float* x) {
+  constexpr int N = 16 / sizeof(T);
+#pragma unroll
+  for (int k = 0; k < EACH; k += N) {
+    ppl::Pack<T, N> q;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q.v[i] = from_f<T>(x[k + i]);
+    *reinterpret_cast<ppl::Pack<T, N>*>(p + k) = q;
+  }
+}
+template <class T>
+__device__ __forceinline__ void read(const T* p, bool whole, uint32_t lane, uint32_t n, float* x) {
+  if (whole) return read_whole(p + lane * EACH, x);
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) x[k] = lane + k * 32 < n ? to_f(p[lane + k * 32]) : 0.f;
+}
+template <class T>
+__device__ __forceinline__ void write(T* p, bool whole, uint32_t lane, uint32_t n, const float* x) {
+  if (whole) return write_whole(p + lane * EACH, x);
+#pragma unroll
+  for (int k = 0; k < EACH; ++k)
+    if (lane + k * 32 < n) p[lane + k * 32] = from_f<T>(x[k]);
+}
+__device__ __forceinline__ void read_any(const void* p, int type, uint64_t at, bool whole, uint32_t lane, uint32_t n, float* x) {
+  switch (type) {
+    case PP_F32: return read(static_cast<const float*>(p) + at, whole, lane, n, x);
+    case PP_F16: return read(static_cast<const __half*>(p) + at, whole, lane, n, x);
+    default: return read(static_cast<const __nv_bfloat16*>(p) + at, whole, lane, n, x);
+  }
+}
+__device__ __forceinline__ void write_any(void* p, int type, uint64_t at, bool whole, uint32_t lane, uint32_t n, const float* x) {
+  switch (type) {
+    case PP_F32: return write(static_cast<float*>(p) + at, whole, lane, n, x);
+    case PP_F16: return write(static_cast<__half*>(p) + at, whole, lane, n, x);
+    default: return write(static_cast<__nv_bfloat16*>(p) + at, whole, lane, n, x);
+  }
+}
+
+// ------------------------------------------------------------ 8-bit states
+// A tile's values share the exponent E (a float's exponent field) of their
+// largest magnitude.  A code is the top of the float whose exponent field is
+// shifted so that E becomes TOP: 4 bits of exponent and a sign for the mean
+// (TOP 14), 5 for the square (TOP 30, no sign), 3 of mantissa; what underflows
+// the shifted field is a subnormal float and so a subnormal code.  A value
+// that rounds up from the largest still has a code.
+constexpr int TOP_M = 14, TOP_V = 30;
+__device__ __forceinline__ float pow2(int field) { return __int_as_float(field << 23); }
+
+template <int TOP>
+__device__ __forceinline__ float decode(uint32_t code, float scale) {
+  const float x = __uint_as_float((TOP == TOP_M ? code & 127 : code) << 20) * pow2(254 - TOP) * scale;
+  return TOP == TOP_M && code > 127 ? -x : x;
+}
+__device__ __forceinline__ float scale_of(uint32_t e) { return e == 255 ? __int_as_float(0x7FC00000) : pow2(int(e)); }
+
+// A lane's codes, as 8 bytes; the tile's exponent in e.
+template <int TOP>
+__device__ __forceinline__ uint2 encode(const float* x, const uint32_t* random, uint32_t& e) {
+  uint32_t field = 1;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) field = max(field, __float_as_uint(x[k]) << 1 >> 24);
+  field = __reduce_max_sync(~0u, field);
+  e = field < 254 ? field : 255;
+  if (e == 255) return make_uint2(0, 0);
+  const float up = pow2(254 - int(field));
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const float y = fabsf(x[k]) * up * pow2(TOP);
+    uint32_t c = (__float_as_uint(y) + random[k]) >> 20;
+    // a square never rounds to zero: the step divides by its root
+    if (TOP == TOP_V) c = x[k] > 0.f && c == 0 ? 1 : c;
+    else c |= x[k] < 0.f ? 128 : 0;
+    w[k / 4] |= c << (k % 4 * 8);
+  }
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ uint2 read_codes(const uint8_t* p, bool whole, uint32_t lane, uint32_t n) {
+  if (whole) return *reinterpret_cast<const uint2*>(p + lane * EACH);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < EACH; ++k)
+    if (lane + k * 32 < n) w[k / 4] |= uint32_t(p[lane + k * 32]) << (k % 4 * 8);
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void write_codes(uint8_t* p, bool whole, uint32_t lane, uint32_t n, uint2 c) {
+  if (whole) {
+    *reinterpret_cast<uint2*>(p + lane * EACH) = c;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < EACH; ++k)
+    if (lane + k * 32 < n) p[lane + k * 32] = uint8_t((k < 4 ? c.x : c.y) >> (k % 4 * 8));
+}
+template <int TOP>
+__device__ __forceinline__ void decode_all(uint2 c, uint32_t e, float* x) {
+  const float scale = scale_of(e);
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) x[k] = decode<TOP>((k < 4 ? c.x : c.y) >> (k % 4 * 8) & 255, scale);
+}
+
+template <int BITS, int CAP>
+__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Args<CAP> a) {
+  const Common& c = a.c;
+  if (c.skip_at && *c.skip_at != 0.f) return;
+  const uint32_t lane = threadIdx.x % 32;
+  const int step = c.counters[0] + 1;
+  const float lr = c.lr_at ? *c.lr_at : c.lr;
+  const float scale = c.scale_at ? *c.scale_at : 1.f;
+  // 1 - b^t without a difference of nearly equal numbers
+  const float rate = lr / -expm1f(float(step) * c.log_b1);
+  const float root = 1.f / sqrtf(-expm1f(float(step) * c.log_b2));
+  const uint32_t key = mix(mix(c.seed) + uint32_t(step));
+  for (uint32_t tile = blockIdx.x * WARPS + threadIdx.x / 32; tile < c.n_tiles; tile += gridDim.x * WARPS) {
+    uint32_t i = 0;  // the last tensor that begins at or before the tile
+    for (uint32_t size = c.n_items; size > 1;) {
+      const uint32_t half = size / 2;
+      if (a.item[i + half].tile_begin <= tile) i += half;
+      size -= half;
+    }
+    const Item& t = a.item[i];
+    const uint64_t at = uint64_t(tile - t.tile_begin) * TILE;
+    const uint32_t n = uint32_t(t.n - at < TILE ? t.n - at : TILE);
+    const bool whole = n == TILE && reinterpret_cast<uintptr_t>(t.param) % 16 == 0 && reinterpret_cast<uintptr_t>(t.grad) % 16 == 0;
+    const uint64_t s = t.first + at;
+    float p[EACH], g[EACH], m[EACH], v[EACH];
+    read_any(t.grad, t.grad_type, at, whole, lane, n, g);
+    if (c.master) read(c.master + s, whole, lane, n, p);
+    else read_any(t.param, t.param_type, at, whole, lane, n, p);
+    if (BITS == 32) {
+      read(static_cast<const float*>(c.m) + s, whole, lane, n, m);
+      read(static_cast<const float*>(c.v) + s, whole, lane, n, v);
+    } else {
+      decode_all<TOP_M>(read_codes(static_cast<const uint8_t*>(c.m) + s, whole, lane, n), c.m_exp[s / TILE], m);
+      decode_all<TOP_V>(read_codes(static_cast<const uint8_t*>(c.v) + s, whole, lane, n), c.v_exp[s / TILE], v);
+    }
+    const float keep = 1.f - lr * t.decay;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const float x = __fmul_rn(g[k], scale);
+      // each product and sum rounded by itself: the states are the formula's, bit by bit
+      m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(x, c.c1));
+      v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(x, x), c.c2));
+      p[k] = p[k] * keep - rate * m[k] / (sqrtf(v[k]) * root + c.eps);
+    }
+    write_any(t.param, t.param_type, at, whole, lane, n, p);
+    if (c.master) write(c.master + s, whole, lane, n, p);
+    if (BITS == 32) {
+      write(static_cast<float*>(c.m) + s, whole, lane, n, m);
+      write(static_cast<float*>(c.v) + s, whole, lane, n, v);
+    } else {
+      // 32 hashed bits an element, half for each state
+      const uint32_t low = uint32_t(s), high = mix(key + uint32_t(s >> 32));  // a tile does not cross 2^32
+      uint32_t rm[EACH], rv[EACH];
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        if (c.nearest) {
+          rm[k] = rv[k] = 1u << 19;
+        } else {
+          const uint32_t r = mix((low + (whole ? lane * EACH + k : lane + k * 32)) ^ high);
+          rm[k] = r >> 16 << 4;
+          rv[k] = (r & 0xFFFF) << 4;
+        }
+        if (!whole && lane + k * 32 >= n) m[k] = v[k] = 0.f;  // no part of the tile's exponents
+      }
+      uint32_t em, ev;
+      const uint2 cm = encode<TOP_M>(m, rm, em), cv = encode<TOP_V>(v, rv, ev);
+      write_codes(static_cast<uint8_t*>(c.m) + s, whole, lane, n, cm);
+      write_codes(static_cast<uint8_t*>(c.v) + s, whole, lane, n, cv);
+      if (lane == 0) {
+        c.m_exp[s / TILE] = uint8_t(em);
+        c.v_exp[s / TILE] = uint8_t(ev);
+      }
+    }
+  }
+  if (!c.last) return;
+  // the block that is through last counts the step: by then every block has read the count
+  __syncthreads();
+  if (threadIdx.x == 0 && atomicAdd(&c.counters[1], 1) == int(gridDim.x) - 1) {
+    c.counters[1] = 0;
+    c.counters[0] = step;
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(THREADS) values_kernel(const uint8_t* m, const uint8_t* m_exp, const uint8_t* v,
+                                                         const uint8_t* v_exp, uint32_t n_tiles, T* m_out, T* v_out) {
+  const uint32_t lane = threadIdx.x % 32;
+  for (uint32_t tile = blockIdx.x * WARPS + threadIdx.x / 32; tile < n_tiles; tile += gridDim.x * WARPS) {
+    const uint64_t s = uint64_t(tile) * TILE;
+    float x[EACH];
+    if (m_out) {
+      decode_all<TOP_M>(read_codes(m + s, true, lane, TILE), m_exp[tile], x);
+      write(m_out + s, true, lane, TILE, x);
+    }
+    if (v_out) {
+      decode_all<TOP_V>(read_codes(v + s, true, lane, TILE), v_exp[tile], x);
+      write(v_out + s, true, lane, TILE, x);
+    }
+  }
+}
+
+cudaError_t grid_for(uint64_t tiles, unsigned* grid) {
+  int sms;
+  const cudaError_t e = ppi::sm_count(&sms);
+  *grid = unsigned(std::min<uint64_t>(std::max<uint64_t>((tiles + WARPS - 1) / WARPS, 1), uint64_t(sms) * BLOCKS));
+  return e;
+}
+
+template <int CAP>
+cudaError_t launch(const Common& c, const Item* items, int bits, cudaStream_t stream) {
+  Args<CAP> a;
+  a.c = c;
+  std::memcpy(a.item, items, c.n_items * sizeof(Item));
+  unsigned grid;
+  const cudaError_t e = grid_for(c.n_tiles, &grid);
+  if (e != cudaSuccess) return e;
+  if (bits == 32) adamw_kernel<32, CAP><<<grid, THREADS, 0, stream>>>(a);
+  else adamw_kernel<8, CAP><<<grid, THREADS, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+bool state_ok(const pp_adamw_state* s) {
+  if (!s || (s->bits != 32 && s->bits != 8)) return false;
+  if (s->n % TILE != 0) return false;
+  if (s->n && (!s->d_exp_avg || !s->d_exp_avg_sq)) return false;
+  if (!ppl::aligned(s->d_exp_avg, 16) || !ppl::aligned(s->d_exp_avg_sq, 16)) return false;
+  return s->bits == 32 || !s->n || (s->d_exp_avg_exponent && s->d_exp_avg_sq_exponent);
+}
+
+}  // namespace
+
+extern "C" pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, const pp_adamw_state* state,
+                          const pp_adamw_opts* o, cudaStream_t stream) {
+  if (!state_ok(state) || !o || (n_tensors && !tensors)) return PP_EINVAL;
+  if (!state->d_counters || !ppl::aligned(state->d_counters, 4) || !ppl::aligned(state->d_master, 16)) return PP_EINVAL;
+  if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) || !(o->eps >= 0) || !std::isfinite(o->eps)) return PP_EINVAL;
+  if (!o->d_lr && !(o->lr >= 0 && std::isfinite(o->lr))) return PP_EINVAL;
+  if (!ppl::aligned(o->d_lr, 4) || !ppl::aligned(o->d_grad_scale, 4) || !ppl::aligned(o->d_skip, 4)) return PP_EINVAL;
+  if (state->n / TILE >= ppl::MAX_DIM) return PP_ETOOLARGE;
+  for (size_t i = 0; i < n_tensors; ++i) {
+    const pp_adamw_tensor& t = tensors[i];
+    if (!ppl::ftype_ok(t.param_type) || !ppl::ftype_ok(t.grad_type) || !std::isfinite(t.weight_decay)) return PP_EINVAL;
+    if (t.first % TILE != 0 || t.first > state->n || t.n > state->n - t.first) return PP_EINVAL;
+    if (t.n && (!t.d_param || !t.d_grad || !ppl::aligned(t.d_param, ppl::fsize(t.param_type)) ||
+                !ppl::aligned(t.d_grad, ppl::fsize(t.grad_type))))
+      return PP_EINVAL;
+  }
+  Common c;
+  std::memset(&c, 0, sizeof c);
+  c.m = state->d_exp_avg;
+  c.v = state->d_exp_avg_sq;
+  c.m_exp = state->d_exp_avg_exponent;
+  c.v_exp = state->d_exp_avg_sq_exponent;
+  c.master = state->d_master;
+  c.counters = state->d_counters;
+  c.lr_at = o->d_lr;
+  c.scale_at = o->d_grad_scale;
+  c.skip_at = o->d_skip;
+  c.lr = float(o->lr);
+  c.b1 = float(o->beta1);
+  c.c1 = float(1 - o->beta1);
+  c.b2 = float(o->beta2);
+  c.c2 = float(1 - o->beta2);
+  c.eps = float(o->eps);
+  c.log_b1 = float(std::log(o->beta1));
+  c.log_b2 = float(std::log(o->beta2));
+  c.seed = state->seed;
+  c.nearest = state->nearest;
+  constexpr size_t MOST = 640;
+  Item items[MOST];
+  size_t i = 0;
+  do {  // once also without tensors: the step counts
+    uint64_t tiles = 0;
+    uint32_t n = 0;
+    for (; i < n_tensors && n < MOST; ++i) {
+      const pp_adamw_tensor& t = tensors[i];
+      if (!t.n) continue;
+      items[n++] = {t.d_param, t.d_grad, t.n, t.first, uint32_t(tiles), t.weight_decay, t.param_type, t.grad_type};
+      tiles += (t.n + TILE - 1) / TILE;
+      if (tiles >= ppl::MAX_DIM) return PP_ETOOLARGE;  // only where tensors share state
+    }
+    c.n_items = n;
+    c.n_tiles = uint32_t(tiles);
+    c.last = i == n_tensors;
+    const cudaError_t e = n <= 16 ? launch<16>(c, items, state->bits, stream)
+                          : n <= 128 ? launch<128>(c, items, state->bits, stream)
+                                     : launch<MOST>(c, items, state->bits, stream);
+    if (e != cudaSuccess) return ppl::rc_of(e);
+  } while (i < n_tensors);
+  return PP_OK;
+}
+
+extern "C" pp_rc pp_adamw_values(const pp_adamw_state* state, pp_ftype type, void* d_exp_avg, void* d_exp_avg_sq,
+                                 cudaStream_t stream) {
+  if (!state_ok(state) || state->bits != 8 || !ppl::ftype_ok(type)) return PP_EINVAL;
+  if (!ppl::aligned(d_exp_avg, 16) || !ppl::aligned(d_exp_avg_sq, 16)) return PP_EINVAL;
+  if (state->n / TILE >= ppl::MAX_DIM) return PP_ETOOLARGE;
+  if (!state->n || (!d_exp_avg && !d_exp_avg_sq)) return PP_OK;
+  const uint32_t tiles = uint32_t(state->n / TILE);
+  unsigned grid;
+  const cudaError_t e = grid_for(tiles, &grid);
+  if (e != cudaSuccess) return ppl::rc_of(e);
+  const uint8_t* m = static_cast<const uint8_t*>(state->d_exp_avg);
+  const uint8_t* v = static_cast<const uint8_t*>(state->d_exp_avg_sq);
+  auto go = [&](auto kernel, auto* mo, auto* vo) {
+    kernel<<<grid, THREADS, 0, stream>>>(m, state->d_exp_avg_exponent, v, state->d_exp_avg_sq_exponent, tiles, mo, vo);
+  };
+  switch (type) {
+    case PP_F32: go(values_kernel<float>, static_cast<float*>(d_exp_avg), static_cast<float*>(d_exp_avg_sq)); break;
+    case PP_F16: go(values_kernel<__half>, static_cast<__half*>(d_exp_avg), static_cast<__half*>(d_exp_avg_sq)); break;
+    default: go(values_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(d_exp_avg), static_cast<__nv_bfloat16*>(d_exp_avg_sq)); break;
+  }
+  return ppl::rc_of(cudaGetLastError());
+}

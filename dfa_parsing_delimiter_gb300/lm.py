@@ -3,6 +3,8 @@
   pp_vocab_grammar / vocab_grammar    a vocabulary under a DFA -> Grammar
   pp_grammar_states / grammar_states  the DFA's state along token sequences
   pp_logits / process_logits          penalties, biases and the grammar's mask
+  pp_token_probs / token_probs        logits as probabilities: temperature, top-k
+  pp_verify_drafts / verify_drafts    drafted tokens against them; the next token
   pp_embed / embed                    rows of a table by id
   pp_embed_grad / embed_grad          the gradient for the table (both differentiable)
 
@@ -48,6 +50,12 @@ class LogitOpts(ctypes.Structure):
                 ("n_states", ctypes.c_int32), ("history_type", ctypes.c_int32)]
 
 
+class DraftOpts(ctypes.Structure):
+    """pp_draft_opts."""
+    _fields_ = [("d_probs", _vp), ("d_probs_row", _vp), ("probs_rows", _sz), ("probs_stride", _sz),
+                ("d_target_row", _vp), ("d_lengths", _vp)]
+
+
 _NO_HISTORY, _NO_BIAS, _NO_GRAMMAR = (0,) * 10, (0,) * 4, (0,) * 5
 
 
@@ -64,6 +72,9 @@ def declare(L: ctypes.CDLL) -> None:
         "pp_embed_grad_noalloc": [_vp, _int, _sz, _sz, _vp, _int, _sz, _sz, _sz, _f32, _i64, _int, _vp,
                                   _int, _sz, _vp, _sz, _vp],
         "pp_embed_grad_scratch": [_sz, _sz, _sz],
+        "pp_token_probs": [_vp, _int, _sz, _sz, _sz, _vp, _vp, _vp, _sz, _vp],
+        "pp_verify_drafts": [_vp, _int, _sz, _sz, _sz, _vp, _int, _sz, _sz, _sz, _vp, _sz, _vp,
+                             _vp, _vp, _sz, _vp, _vp],
     }
     for name, args in sigs.items():
         getattr(L, name).restype = _sz if name == "pp_embed_grad_scratch" else _int
@@ -87,7 +98,9 @@ def _load():
     bind = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(bind)
     bind.init(*[ctypes.cast(getattr(L, "pp_" + name), _vp).value
-                for name in ("vocab_grammar", "grammar_states", "logits", "embed", "embed_grad_noalloc", "embed_grad_scratch")])
+                for name in ("vocab_grammar", "grammar_states", "logits", "embed", "embed_grad_noalloc", "embed_grad_scratch",
+                              "token_probs", "verify_drafts", "adamw")])
+    bind.types(*FTYPE)  # in the order of their numbers
     _c = bind
     return bind
 
@@ -241,12 +254,13 @@ def grammar_states(grammar: Grammar, tokens: torch.Tensor, start=None, lengths=N
 # ------------------------------------------------------------------ logits
 class _Underived(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, arguments, *followed):
-        return process_logits(*arguments)  # autograd follows nothing in here
+    def forward(ctx, call, arguments, *followed):
+        ctx.what = call.__name__
+        return call(*arguments)  # autograd follows nothing in here
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("process_logits has no derivative: detach its arguments")
+        raise RuntimeError(f"{ctx.what} has no derivative: detach its arguments")
 
     jvp = backward
 
@@ -270,8 +284,8 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
         followed = [t for t in values if t is not None and _followed(t)]
         if followed:
             _need(out is None, "out: not for values that require a gradient")
-            return _Underived.apply((logits, history, history_len, prompt_len, history_row, repetition, presence,
-                                     frequency, bias, grammar, states, None, stream), *followed)
+            return _Underived.apply(process_logits, (logits, history, history_len, prompt_len, history_row, repetition, presence,
+                                                     frequency, bias, grammar, states, None, stream), *followed)
     _need(logits.dtype in FTYPE and logits.dim() == 2, "logits: want 2 dimensions of float32, float16 or bfloat16")
     rows, vocab = logits.shape
     dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
@@ -322,6 +336,90 @@ def process_logits(logits: torch.Tensor, history=None, history_len=None, prompt_
         _call(c.logits, "pp_logits", logits, stream, logits.data_ptr(), FTYPE[logits.dtype], rows, vocab,
               stride, *hist, *lists, *mask, itype, out.data_ptr(), ostride)
     return out
+
+
+# ------------------------------------------------------------------ tokens
+def token_probs(logits: torch.Tensor, temperature=None, top_k=None, out=None, stream=None) -> torch.Tensor:
+    """pp_token_probs of [rows, n_vocab] logits: float32 probabilities.
+    temperature: float32 [rows] (not above 0: all at the largest logit);
+    top_k: int32 [rows], how many of the most likely tokens stay (below 1:
+    all).  `out` may be float32 logits themselves.  There is no derivative: a
+    result of values that require a gradient raises RuntimeError when it is
+    differentiated (and such values take no `out`)."""
+    if forward_ad._current_level >= 0 or logits.requires_grad or (temperature is not None and temperature.requires_grad):
+        followed = [t for t in (logits, temperature) if t is not None and _followed(t)]
+        if followed:
+            _need(out is None, "out: not for values that require a gradient")
+            return _Underived.apply(token_probs, (logits, temperature, top_k, None, stream), *followed)
+    _need(logits.dtype in FTYPE and logits.dim() == 2, "logits: want 2 dimensions of float32, float16 or bfloat16")
+    rows, vocab = logits.shape
+    dev, c = logits.get_device(), _lib()
+    given = out
+    if out is None:
+        out = _new((rows, vocab), torch.float32, logits, stream)
+    else:
+        _on(out, logits, "out", (torch.float32,), 2)
+        _need(out.shape == logits.shape, "out: want the shape of the logits")
+    t = c.vec(temperature, torch.float32, dev, rows, "temperature")
+    k = c.vec(top_k, torch.int32, dev, rows, "top_k")
+    if rows and vocab:
+        stride, ostride = _matrix_stride(logits, "logits"), _matrix_stride(out, "out")
+        if given is not None:
+            _written(out)
+        _call(c.token_probs, "pp_token_probs", logits, stream, logits.data_ptr(), FTYPE[logits.dtype], rows, vocab,
+              stride, t, k, out.data_ptr(), ostride)
+    return out
+
+
+def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, accept: torch.Tensor, sample: torch.Tensor,
+                  draft_probs=None, lengths=None, target_row=None, draft_row=None, out=None,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """pp_verify_drafts: (tokens int32 [n, k + 1], counts int32 [n]), the
+    accepted ones of [n, k] drafted tokens and the one that follows them, then
+    -1; without drafts (k or a length of 0) one drawn token.  target: [rows,
+    n_vocab] probabilities, of which request r has k + 1 rows from
+    target_row[r] on (default: r * (k + 1)); draft_probs: the rows that its
+    drafts were drawn from, k from draft_row[r] on (default: r * k), or None
+    for drafts without a choice; lengths: int32 [n], the drafts of each request
+    that count; accept: float32 [n, k] and sample: float32 [n], random numbers
+    in [0, 1).  out: (tokens, counts) to write to."""
+    _need(target.dtype in FTYPE and target.dim() == 2 and target.size(1) > 0,
+          "target: want 2 dimensions of float32, float16 or bfloat16, and a token at least")
+    _on(drafts, target, "drafts", ITYPE, 2)
+    _on(accept, target, "accept", (torch.float32,), 2)
+    n, k = drafts.shape
+    _need(accept.shape == drafts.shape, "accept: want a number for each draft")
+    dev, i32, c = target.get_device(), torch.int32, _lib()
+    rows, vocab = target.shape
+    _need(target_row is not None or rows >= n * (k + 1), "target: want a row for each draft and one more a request")
+    probs = (0, 0, 0, 0)
+    if draft_probs is not None:
+        _on(draft_probs, target, "draft_probs", (target.dtype,), 2)
+        _need(draft_probs.size(1) == vocab, "draft_probs: want the target's vocabulary")
+        _need(draft_row is not None or draft_probs.size(0) >= n * k, "draft_probs: want a row for each draft")
+        # rows of no tokens have no address, and are still not those of sure drafts
+        probs = (draft_probs.data_ptr() or target.data_ptr(), c.vec(draft_row, i32, dev, n, "draft_row"), draft_probs.size(0),
+                 _matrix_stride(draft_probs, "draft_probs"))
+    s = c.vec(sample, torch.float32, dev, n, "sample")
+    first, size = c.vec(target_row, i32, dev, n, "target_row"), c.vec(lengths, i32, dev, n, "lengths")
+    if out is None:
+        tokens, counts = _new((n, k + 1), i32, target, stream), _new((n,), i32, target, stream)
+    else:
+        tokens, counts = out
+        _on(tokens, target, "out", (i32,), 2)
+        _on(counts, target, "out", (i32,), 1)
+        _need(tokens.shape == (n, k + 1) and counts.shape == (n,) and counts.is_contiguous(),
+              "out: want tokens, one column more than drafts, and a count for each request")
+    if n:
+        at = _matrix_stride(tokens, "out")
+        if out is not None:
+            _written(tokens)
+            _written(counts)
+        _call(c.verify_drafts, "pp_verify_drafts", target, stream, target.data_ptr(), FTYPE[target.dtype], rows, vocab,
+              _matrix_stride(target, "target"), drafts.data_ptr(), ITYPE[drafts.dtype], n, k, _matrix_stride(drafts, "drafts"),
+              accept.data_ptr(), _matrix_stride(accept, "accept"), s, *probs, first, size, tokens.data_ptr(), at,
+              counts.data_ptr())
+    return tokens, counts
 
 
 # ------------------------------------------------------------------ embedding

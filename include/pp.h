@@ -537,8 +537,9 @@ pp_rc pp_debug_long_fields(uint64_t* out, int reset);
 /* ------------------------------------------------------ language models
  * The same DFAs at the two ends of a language model: what it answers with
  * is held to a pp_dfa_desc while it is sampled (pp_vocab_grammar,
- * pp_grammar_states, pp_logits), and the id columns that pp_parse writes, or
- * token ids, become vectors (pp_embed, pp_embed_grad).  The conventions at
+ * pp_grammar_states, pp_logits) and drawn from (pp_token_probs,
+ * pp_verify_drafts), and the id columns that pp_parse writes, or token ids,
+ * become vectors (pp_embed, pp_embed_grad) whose table is trained (pp_adamw).  The conventions at
  * the top of this file hold, except that these entry points have no
  * pp_status: every value of every input has a defined result, stated below.
  * They can be captured into graphs; make the first call of each on a device,
@@ -723,6 +724,154 @@ pp_rc pp_embed_grad_noalloc(const void* d_ids, pp_itype id_type, size_t id_strid
                             cudaStream_t stream);
 /* Bytes of scratch that pp_embed_grad_noalloc needs (0: none).  Host only. */
 size_t pp_embed_grad_scratch(size_t n, size_t n_vocab, size_t dim);
+
+/*
+ * pp_token_probs — logits as probabilities, by a temperature and cut to each
+ * row's most likely tokens.  For every row r:
+ *   kept  = the top_k[r] largest logits, of equal ones those of the lowest
+ *           tokens; all of them if top_k[r] is below 1 or above n_vocab.  -infinity
+ *           and NaN are never kept.
+ *   e[v]  = exp((in[r][v] - max) / temperature[r]) where kept, 1 for every logit
+ *           equal to the largest (infinity too), 0 elsewhere
+ *   out   = e / sum(e)
+ * A temperature that is not above 0 gives 1 to the lowest token of the largest
+ * logit.  A row in which nothing is above -infinity (a grammar state that allows
+ * nothing) is all 0.  Arithmetic in 32 bits; which tokens are kept is exact, and the
+ * same inputs give the same bits.
+ *   d_logits        device [n_rows][logits_stride], n_vocab values a row.
+ *   d_temperature   device float[n_rows], or NULL: 1.
+ *   d_top_k         device int32[n_rows], or NULL: all.
+ *   d_probs         device float[n_rows][probs_stride]; may be d_logits of type
+ *                   PP_F32 (with the same stride), but not overlap it otherwise.
+ * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n_vocab of 2^30 or n_rows
+ * of 2^28 - 8192 or more, PP_ECUDA on CUDA errors.  No scratch.
+ */
+pp_rc pp_token_probs(const void* d_logits, pp_ftype type, size_t n_rows, size_t n_vocab,
+                     size_t logits_stride, const float* d_temperature, const int32_t* d_top_k,
+                     float* d_probs, size_t probs_stride, cudaStream_t stream);
+
+/* pp_verify_drafts options; every pointer may be NULL (device memory). */
+typedef struct {
+  /* the draft's own probabilities: row probs_row[r] + i (without a list
+   * r * n_drafts + i) of d_probs is what draft i of request r was drawn from.
+   * NULL: every draft was sure (probability 1). */
+  const void* d_probs;
+  const int32_t* d_probs_row;
+  size_t probs_rows, probs_stride;
+  const int32_t* d_target_row; /* NULL: r * (n_drafts + 1) */
+  const int32_t* d_lengths;    /* drafts of each request, cut to 0..n_drafts; NULL: n_drafts */
+} pp_draft_opts;
+
+/*
+ * pp_verify_drafts — drafted tokens against the target's probabilities, and the
+ * token that follows the accepted ones; without drafts (n_drafts or a length of
+ * 0) it draws one token.  Request r has drafts d[0 .. n - 1], the target's
+ * probabilities p[i] (row target_row[r] + i; p[n] is for the token after them)
+ * and the draft's q[i]:
+ *   draft i is accepted if accept[r][i] * q[i][d[i]] < p[i][d[i]], exactly; not if
+ *   accept[r][i] is NaN or negative, the token is outside the vocabulary or one
+ *   of the two rows outside its array.
+ *   j = the first draft that is not accepted, or n.
+ *   weights w[v] = P(v) if j = n, else max(P(v) - Q(v), 0), and P(v) if all of
+ *   those are 0; P and Q are p[j] and q[j] in whole units of 2^-u, rounded down,
+ *   u = 62 - ceil(log2(n_vocab)); without d_probs Q is P at d[j] and 0 elsewhere.
+ *   A row outside its array is all 0.  Probabilities outside [0, 1] are cut
+ *   to it, NaN counts as 0.
+ *   token = the lowest v with w[0] + .. + w[v] > floor(W * S / 2^31), W the sum of
+ *   all weights and S = floor(sample[r] * 2^31), cut to 0 .. 2^31 - 1 (NaN: 0).
+ *   tokens[r] = d[0 .. j - 1], token, and -1 up to n_drafts + 1 tokens;
+ *   counts[r] = j + 1.  If W is 0 there is no token: -1, and counts[r] = j.
+ * All in integers: the same inputs give the same tokens.
+ *   d_target        device [target_rows][target_stride], n_vocab values a row.
+ *   d_drafts        device [n_requests][drafts_stride], n_drafts a row.
+ *   d_accept        device float[n_requests][accept_stride], in [0, 1).
+ *   d_sample        device float[n_requests], in [0, 1).
+ *   d_tokens        device int32[n_requests][tokens_stride], n_drafts + 1 a row.
+ *   d_counts        device int32[n_requests].  Outputs overlap no input.
+ * Returns PP_EINVAL for bad arguments, PP_ETOOLARGE for n_vocab of 2^30, n_drafts of
+ * 2^24, n_requests of 2^28 - 8192 or rows of 2^31 - 65536 or more, PP_ECUDA on
+ * CUDA errors.  No scratch.
+ */
+pp_rc pp_verify_drafts(const void* d_target, pp_ftype type, size_t target_rows, size_t n_vocab,
+                       size_t target_stride, const void* d_drafts, pp_itype draft_type,
+                       size_t n_requests, size_t n_drafts, size_t drafts_stride,
+                       const float* d_accept, size_t accept_stride, const float* d_sample,
+                       const pp_draft_opts* opts, int32_t* d_tokens, size_t tokens_stride,
+                       int32_t* d_counts, cudaStream_t stream);
+
+/* Elements that share an exponent in pp_adamw's 8-bit states, and the multiple at
+ * which each tensor's state begins. */
+#define PP_ADAMW_BLOCK 256
+
+/* One tensor of a pp_adamw call (device memory, contiguous). */
+typedef struct {
+  void* d_param;
+  const void* d_grad;
+  uint64_t n;     /* elements */
+  uint64_t first; /* its place in the state, a multiple of PP_ADAMW_BLOCK */
+  float weight_decay;
+  int32_t param_type, grad_type; /* pp_ftype */
+} pp_adamw_tensor;
+
+/* The optimiser's state over all tensors: flat arrays of n elements (device), of
+ * which each tensor has as many as it has elements, from its place on.
+ *   bits 32   float each.
+ *   bits 8    a byte each, and a byte per PP_ADAMW_BLOCK elements: E, the
+ *             exponent field of the block's largest magnitude as a float, at least
+ *             1.  A code's value is that of the float with the code's low 7 bits (of
+ *             exp_avg, whose top bit is the sign; 4 bits of exponent) or 8 bits (of
+ *             exp_avg_sq; 5 bits) above 20 zeros, times 2^113 (exp_avg) or 2^97
+ *             (exp_avg_sq), times 2^(E - 127).  E = 255: a value was not finite (or
+ *             2^127 or more); the whole block is NaN.
+ * All zeros is the state of the first step, for either. */
+typedef struct {
+  void* d_exp_avg;
+  void* d_exp_avg_sq;
+  uint8_t* d_exp_avg_exponent;    /* bits 8: n / PP_ADAMW_BLOCK */
+  uint8_t* d_exp_avg_sq_exponent;
+  float* d_master;     /* 32-bit copies of the parameters, n elements, or NULL */
+  int32_t* d_counters; /* [2]: steps done; 0 (of the call's own, 0 again after it) */
+  uint64_t n;          /* a multiple of PP_ADAMW_BLOCK */
+  int32_t bits;
+  uint32_t seed;   /* of the 8-bit states' rounding */
+  int32_t nearest; /* != 0: they are rounded to nearest instead */
+} pp_adamw_state;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  const float* d_lr;         /* instead of lr, or NULL */
+  const float* d_grad_scale; /* NULL: 1 */
+  const float* d_skip;       /* not 0: the call changes nothing; NULL: 0 */
+} pp_adamw_opts;
+
+/*
+ * pp_adamw — one AdamW step over many tensors in one launch (640 tensors; more
+ * launches beyond).  With t = steps done + 1, in 32 bits, for every element:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g g          (each product and sum rounded)
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * and t becomes the steps done.  p is read from d_master and written to it where
+ * there is one, and rounded once to the parameter's type.  8-bit states are
+ * rounded up or down with chances by which they are right on average: 16 bits of a
+ * hash of the seed, t and the element's place, for each of the two, are added
+ * below a code's last bit.  (To nearest, a beta2 of 0.999 would never move v:
+ * its steps are smaller than half of any code's.)  v above 0 is not rounded to 0.
+ *   tensors         host, read before the call returns; the tensors' parameters and
+ *                   states must not overlap, nor their gradients.
+ *   state, opts     host; see above.
+ * Returns PP_EINVAL for bad arguments (lr and eps below 0 or not finite, a beta
+ * outside [0, 1), states off 16 bytes), PP_ETOOLARGE for a state of 2^39 - 2^24
+ * elements or more, PP_ECUDA on CUDA errors.  No scratch.
+ */
+pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, const pp_adamw_state* state,
+               const pp_adamw_opts* opts, cudaStream_t stream);
+
+/* pp_adamw_values — the values that 8-bit states stand for: n elements each of
+ * `type` (exact in PP_F32 and, where they are in its range, PP_BF16), at 16-byte addresses; either
+ * may be NULL.  Returns PP_EINVAL for bad arguments, PP_ECUDA on CUDA errors. */
+pp_rc pp_adamw_values(const pp_adamw_state* state, pp_ftype type, void* d_exp_avg,
+                      void* d_exp_avg_sq, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
