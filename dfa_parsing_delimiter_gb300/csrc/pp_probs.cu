@@ -56,9 +56,12 @@ __device__ __forceinline__ uint32_t remote_u(const uint32_t* p, uint32_t rank) {
   return v;
 }
 
-// The exponential of (f - top) / temperature, f at most top; c: log2(e) over
-// the temperature.  No difference of infinities, no product of zero and one.
-__device__ __forceinline__ float share(float f, float top, float c) { return f == top ? 1.f : exp2f(fmaxf(f - top, -3.402823466e38f) * c); }
+// The exponential of (f - top) / temperature, f at most top; c: 2 log2(e) over
+// the temperature.  Halves, since the difference of two floats may not be one;
+// an infinite difference gives 0, under an infinite temperature too (-200: 0).
+__device__ __forceinline__ float share(float f, float top, float c) {
+  return f == top ? 1.f : exp2f(fmaxf((f * 0.5f - top * 0.5f) * c, -200.f));
+}
 
 struct Shared {
   float part_max, part_sum;
@@ -135,8 +138,8 @@ __global__ void __launch_bounds__(THREADS) probs_kernel(const ProbArgs a) {
   const T* x = a.resident ? buf - from : in - shift;  // by place
   auto value = [&](uint32_t j) { return fmaxf(to_f(x[j]), -INFINITY); };  // NaN: -infinity
   const float t = a.temperature ? a.temperature[r] : 1.f;
-  const bool greedy = !(t > 0.f);
-  const float c = 1.44269504f / t;
+  const bool greedy = !(t > 0x1p-125f);  // below, c is not a float
+  const float c = 2.88539008f / t;
   // ---- the k-th largest
   uint32_t least = 0, last = ~0u;  // keys above `least` are kept, and those equal to it at places up to `last`
   const int32_t k = a.top_k ? a.top_k[r] : 0;

@@ -734,8 +734,8 @@ size_t pp_embed_grad_scratch(size_t n, size_t n_vocab, size_t dim);
  *   e[v]  = exp((in[r][v] - max) / temperature[r]) where kept, 1 for every logit
  *           equal to the largest (infinity too), 0 elsewhere
  *   out   = e / sum(e)
- * A temperature that is not above 0 gives 1 to the lowest token of the largest
- * logit.  A row in which nothing is above -infinity (a grammar state that allows
+ * A temperature that is not above 2^-125 (0, negative, NaN) gives 1 to the lowest
+ * token of the largest logit.  A row in which nothing is above -infinity (a grammar state that allows
  * nothing) is all 0.  Arithmetic in 32 bits; which tokens are kept is exact, and the
  * same inputs give the same bits.
  *   d_logits        device [n_rows][logits_stride], n_vocab values a row.
