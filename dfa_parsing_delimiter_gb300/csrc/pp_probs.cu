@@ -13,16 +13,19 @@
 // way among their places.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "pp_internal.h"
 #include "pp_lm.cuh"
 
 namespace {
 
+using ppl::from_f;
 using ppl::to_f;
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int CLUSTER = 8;
+constexpr int NV_MOST = 9;  // vectors of a thread
 constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // bytes of a block's part
 
 struct ProbArgs {
@@ -63,6 +66,7 @@ __device__ __forceinline__ float share(float f, float top, float c) {
   return f == top ? 1.f : exp2f(fmaxf((f * 0.5f - top * 0.5f) * c, -200.f));
 }
 
+// ------------------------------------------------------------ rows of any length
 struct Shared {
   float part_max, part_sum;
   uint32_t part_first;  // the first token with part_max
@@ -105,7 +109,7 @@ __device__ __forceinline__ void digit_of(Shared& sh, int pass, uint32_t blocks, 
 }
 
 template <class T>
-__global__ void __launch_bounds__(THREADS) probs_kernel(const ProbArgs a) {
+__global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ Shared sh;
   constexpr int VEC = 16 / sizeof(T);
@@ -231,36 +235,484 @@ __global__ void __launch_bounds__(THREADS) probs_kernel(const ProbArgs a) {
   }
 }
 
+// ------------------------------------------------------------ rows in registers
+// A block's part of a row stays in its threads' registers, NV vectors of 16
+// bytes each.
+constexpr int ENTRIES = 8;  // listed candidates a thread
+
+template <int THREADS>
+struct Fast {
+  static constexpr int WARPS = THREADS / 32, LIST = THREADS * ENTRIES;
+  // of every block of the cluster, written by it
+  float part_max[CLUSTER], part_sum[CLUSTER], part_bound[CLUSTER];
+  uint32_t part_first[CLUSTER], part_n[CLUSTER];
+  float wf[2][WARPS];
+  uint32_t wu[WARPS];
+  uint32_t bin, above, in_bin;
+  uint32_t hist[256];
+  float value[LIST];
+  uint32_t place[LIST];
+};
+
+__device__ __forceinline__ uint32_t there(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void put(uint32_t a, float x) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory"); }
+__device__ __forceinline__ void put(uint32_t a, uint32_t x) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d; d /= 2) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+  return x;
+}
+__device__ __forceinline__ float warp_add(float x) {
+#pragma unroll
+  for (int d = 16; d; d /= 2) x += __shfl_xor_sync(~0u, x, d);
+  return x;
+}
+__device__ __forceinline__ float float_of(uint32_t key) { return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
+
+// The digit (a warp's work) that the want-th element from the largest digit
+// down has, how many have larger ones and how many it.
+template <class S, class F>
+__device__ __forceinline__ void find_digit(S& sh, uint32_t want, F&& count) {
+  const uint32_t lane = threadIdx.x;
+  uint32_t c[8], sum = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum += c[k] = count(255 - 8 * lane - k);
+  uint32_t run = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint32_t y = __shfl_up_sync(~0u, run, d);
+    if (lane >= uint32_t(d)) run += y;
+  }
+  run -= sum;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (run < want && want <= run + c[k]) {
+      sh.bin = 255 - 8 * lane - k;
+      sh.above = run;
+      sh.in_bin = c[k];
+    }
+    run += c[k];
+  }
+}
+
+// A digit of the want-th largest of n entries; digit_at gives an entry's, or -1
+// for one that is out of question.
+template <int THREADS, class F>
+__device__ __forceinline__ void next_digit(Fast<THREADS>& sh, uint32_t n, uint32_t want, F&& digit_at) {
+  for (uint32_t i = threadIdx.x; i < 256; i += THREADS) sh.hist[i] = 0;
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
+    const int d = digit_at(i);
+    if (d >= 0) atomicAdd(&sh.hist[d], 1);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) find_digit(sh, want, [&](uint32_t d) { return sh.hist[d]; });
+  __syncthreads();
+}
+
+// A thread's vectors of a block's part of a row.  Places count from the 16-byte
+// boundary at or before the row's start; what is outside the row is -infinity.
+template <class T, int THREADS, int NV>
+struct Part {
+  static constexpr int VEC = 16 / sizeof(T);
+  // a key's lowest bits, which all values of a sign share
+  static constexpr int LOW = sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 13 : 16;
+  using Vec = ppl::Pack<T, VEC>;
+  Vec x[NV];
+  uint32_t begin;          // place of the first vector
+  uint32_t n;              // vectors
+  uint32_t shift, all;     // the row's first place, and the one after its last
+
+  __device__ __forceinline__ uint32_t at(int i) const { return begin + i * THREADS * VEC; }
+
+  __device__ __forceinline__ void load(const T* in, uint32_t from, uint32_t part, uint32_t n_vocab) {
+    shift = uint32_t(reinterpret_cast<uintptr_t>(in) / sizeof(T) % VEC);
+    all = n_vocab + shift;
+    begin = from + threadIdx.x * VEC;
+    const uint32_t to = min(from + part, all);
+    n = begin < to ? (to - begin + THREADS * VEC - 1) / (THREADS * VEC) : 0;
+    const T none = from_f<T>(-INFINITY);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i < n && at(i) >= shift && at(i) + VEC <= all) {
+        x[i] = *reinterpret_cast<const Vec*>(in - shift + at(i));
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) x[i].v[k] = none;
+      }
+    }
+    // the incomplete vectors, where the row begins and ends
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i < n && (at(i) < shift || at(i) + VEC > all)) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+          if (at(i) + k >= shift && at(i) + k < all) x[i].v[k] = in[at(i) + k - shift];
+      }
+  }
+  // What was computed from the values is not kept for the next pass over them:
+  // in 32 bits they would not fit the registers.
+  __device__ __forceinline__ void forget() {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+        asm volatile("" : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]));
+      }
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F&& f) {
+    forget();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) f(to_f(x[i].v[k]), at(i) + k);
+  }
+  // f(i, p) fills the VEC probabilities p of vector i.
+  template <class F>
+  __device__ __forceinline__ void write(float* out, F&& f) {
+    forget();
+    // the inputs' and the outputs' boundaries agree where their strides do
+    const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i >= n) break;
+      float p[VEC];
+      f(i, p);
+      float* to = out + int64_t(at(i)) - shift;
+      if (wide && at(i) >= shift && at(i) + VEC <= all) {
+        if constexpr (VEC == 8)
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]), "f"(p[4]),
+                       "f"(p[5]), "f"(p[6]), "f"(p[7]) : "memory");
+        else
+          *reinterpret_cast<float4*>(to) = make_float4(p[0], p[1], p[2], p[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+          if (at(i) + k >= shift && at(i) + k < all) to[k] = p[k];
+      }
+    }
+  }
+};
+
+// What is kept: keys above `least`, and those equal to it at places up to `last`.
+struct Cut {
+  uint32_t least, last;
+};
+
+// The cut of any length: digits counted over all values of the cluster, those of
+// this block at places from .. to - 1 of x.
+template <class T, int LOW, int THREADS>
+__device__ __noinline__ Cut cut_of_all(const T* x, uint32_t from, uint32_t to, uint32_t all, Fast<THREADS>& sh, uint32_t blocks, uint32_t want) {
+  Cut cut = {0, ~0u};
+  uint32_t place = 0;
+  const int place_bits = 32 - __clz(all);
+  for (int side = 0; side < 2; ++side) {  // the values, then the places of those that tie
+    for (int bits = side ? place_bits : 32 - LOW; bits > 0;) {
+      const int at = max(bits - 8, 0);
+      const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
+      for (uint32_t i = threadIdx.x; i < 256; i += THREADS) sh.hist[i] = 0;
+      __syncthreads();
+      for (uint32_t j = from + threadIdx.x; j < to; j += THREADS) {
+        uint32_t q = key_of(fmaxf(to_f(x[j]), -INFINITY)) >> LOW;
+        if (side) {
+          if (q != cut.least) continue;
+          q = ~j & ~(~0u << place_bits);
+        }
+        if ((q & mask) == (side ? place : cut.least)) atomicAdd(&sh.hist[q >> at & low], 1);
+      }
+      ppl::cluster_sync();  // every block's counts are there
+      if (threadIdx.x < 32) find_digit(sh, want, [&](uint32_t d) {
+        uint32_t n = 0;
+        for (uint32_t b = 0; b < blocks; ++b) n += remote_u(&sh.hist[d], b);
+        return n;
+      });
+      ppl::cluster_sync();  // and read
+      (side ? place : cut.least) |= sh.bin << at;
+      want -= sh.above;
+      bits = at;
+      if (want != sh.in_bin) continue;
+      if (!side) return cut;  // all that agree so far
+      break;
+    }
+  }
+  cut.last = ~place & ~(~0u << place_bits);
+  return cut;
+}
+
+// The cut and 1 / the sum of the kept exponentials, where the cluster's lists have room
+// for what reaches a bound that at least top_k values reach; false where not.
+template <class P, int THREADS>
+__device__ __forceinline__ bool cut_of_lists(P& part, Fast<THREADS>& sh, uint32_t rank, uint32_t blocks, uint32_t top_k, float m,
+                                             uint32_t thread_key, float c, Cut& cut, float& top, float& factor) {
+  constexpr int WARPS = THREADS / 32, LIST = Fast<THREADS>::LIST, LOW = P::LOW;
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint32_t k_part = (top_k + blocks - 1) / blocks;
+  if (k_part > THREADS) return false;
+  // Each block's k_part-th largest of its threads' maxima (its upper half's bits): at least
+  // k_part of its values reach that, so top_k of the row reach the least of them.
+  uint32_t bound = 0;
+  for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
+    if (__syncthreads_count(thread_key >= (bound | bit)) >= int(k_part)) bound |= bit;
+  if (threadIdx.x < blocks) {
+    put(there(&sh.part_max[rank], threadIdx.x), m);
+    put(there(&sh.part_bound[rank], threadIdx.x), bound > KEY_LOST ? float_of(bound) : -3.402823466e38f);
+  }
+  ppl::cluster_sync();
+  float reach = INFINITY;
+  top = -INFINITY;
+  for (uint32_t b = 0; b < blocks; ++b) {
+    top = fmaxf(top, sh.part_max[b]);
+    reach = fminf(reach, sh.part_bound[b]);
+  }
+  // the candidates in the order of threads, into every block's lists
+  uint32_t n = 0;
+  part.each([&](float f, uint32_t) { n += f >= reach; });
+  uint32_t run = n;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint32_t y = __shfl_up_sync(~0u, run, d);
+    if (lane >= uint32_t(d)) run += y;
+  }
+  if (lane == 31) sh.wu[warp] = run;
+  __syncthreads();
+  uint32_t before = 0, mine = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const uint32_t y = sh.wu[w];
+    if (w < int(warp)) before += y;
+    mine += y;
+  }
+  const uint32_t seg = LIST / blocks;
+  if (n && mine <= seg) {
+    uint32_t to = rank * seg + before + run - n;
+    part.each([&](float f, uint32_t j) {
+      if (f >= reach) {
+        for (uint32_t b = 0; b < blocks; ++b) {
+          put(there(&sh.value[to], b), f);
+          put(there(&sh.place[to], b), j);
+        }
+        ++to;
+      }
+    });
+  }
+  if (threadIdx.x < blocks) put(there(&sh.part_n[rank], threadIdx.x), mine);
+  ppl::cluster_sync();
+  uint32_t total = 0;
+  for (uint32_t b = 0; b < blocks; ++b) {
+    if (sh.part_n[b] > seg) return false;
+    total += sh.part_n[b];
+  }
+  // every block finds the same from here on
+  auto listed = [&](uint32_t i) { return i % seg < sh.part_n[i / seg]; };
+  auto key = [&](uint32_t i) { return key_of(sh.value[i]) >> LOW; };
+  const uint32_t hi = key_of(top) >> LOW, lo = key_of(reach) >> LOW;
+  cut.least = lo;  // all candidates
+  if (total > top_k) {
+    uint32_t want = top_k, in_bin = total;
+    int bits = 32 - __clz(hi ^ lo);  // below those that all candidates share
+    uint32_t known = bits == 32 ? 0 : hi >> bits << bits;
+    while (bits > 0 && want < in_bin) {
+      const int at = max(bits - 8, 0);
+      const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
+      next_digit<THREADS>(sh, LIST, want, [&](uint32_t i) {
+        if (!listed(i)) return -1;
+        const uint32_t q = key(i);
+        return (q & mask) == known ? int(q >> at & low) : -1;
+      });
+      known |= sh.bin << at;
+      want -= sh.above;
+      in_bin = sh.in_bin;
+      bits = at;
+    }
+    cut.least = known;
+    if (want < in_bin) {  // of those that tie the lowest places
+      const int place_bits = 32 - __clz(part.all);
+      uint32_t place = 0;
+      for (bits = place_bits; bits > 0;) {
+        const int at = max(bits - 8, 0);
+        const uint32_t mask = ~0u << bits, low = (1u << (bits - at)) - 1;
+        next_digit<THREADS>(sh, LIST, want, [&](uint32_t i) {
+          if (!listed(i) || key(i) != cut.least) return -1;
+          const uint32_t q = ~sh.place[i] & ~(~0u << place_bits);
+          return (q & mask) == place ? int(q >> at & low) : -1;
+        });
+        place |= sh.bin << at;
+        want -= sh.above;
+        bits = at;
+      }
+      cut.last = ~place & ~(~0u << place_bits);
+    }
+  }
+  float s = 0.f;
+  for (uint32_t i = threadIdx.x; i < LIST; i += THREADS)
+    if (listed(i)) {
+      const uint32_t q = key(i);
+      if (q > cut.least || (q == cut.least && sh.place[i] <= cut.last)) s += share(sh.value[i], top, c);
+    }
+  s = warp_add(s);
+  if (lane == 0) sh.wf[1][warp] = s;
+  __syncthreads();
+  s = warp_add(lane < WARPS ? sh.wf[1][lane] : 0.f);
+  factor = s > 0.f ? 1.f / s : 0.f;
+  return true;
+}
+
+template <class T, int THREADS, int NV, bool CUT>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const ProbArgs a) {
+  ppl::cluster_arrive();
+  constexpr int VEC = 16 / sizeof(T), WARPS = THREADS / 32;
+  using P = Part<T, THREADS, NV>;
+  __shared__ Fast<THREADS> sh;
+  const uint32_t rank = blockIdx.x % a.blocks, r = blockIdx.x / a.blocks;
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  float* out = a.out + r * a.out_stride;
+  const float t = a.temperature ? a.temperature[r] : 1.f;
+  const int32_t top_k = CUT ? a.top_k[r] : 0;
+  const T* in = static_cast<const T*>(a.in) + r * a.in_stride;
+  P part;
+  part.load(in, rank * a.part, a.part, a.n_vocab);
+  const bool greedy = !(t > 0x1p-125f);  // below, c is not a float
+  const float c = 2.88539008f / t;
+  float m = -INFINITY;
+  part.each([&](float f, uint32_t) { m = fmaxf(m, f); });
+  const uint32_t thread_key = key_of(m);
+  m = warp_max(m);
+  if (lane == 0) sh.wf[0][warp] = m;
+  __syncthreads();
+  m = warp_max(sh.wf[0][lane % WARPS]);
+  ppl::cluster_wait();  // every block has started
+  const bool some = CUT && top_k > 0 && uint32_t(top_k) < a.n_vocab && !greedy;
+  Cut cut = {0, ~0u};
+  float top, factor;
+  auto kept = [&](float f, uint32_t j) {
+    const uint32_t q = key_of(f) >> P::LOW;
+    return f > -INFINITY && (q > cut.least || (q == cut.least && j <= cut.last));
+  };
+  if (some) {
+    if (cut_of_lists(part, sh, rank, a.blocks, uint32_t(top_k), m, thread_key, c, cut, top, factor)) {
+      const uint32_t least = cut.least << P::LOW;
+      const float reach = least > KEY_LOST ? float_of(least) : -3.402823466e38f;
+      part.write(out, [&](int i, float* p) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const float f = to_f(part.x[i].v[k]);
+          p[k] = f >= reach && kept(f, part.at(i) + k) ? share(f, top, c) * factor : 0.f;
+        }
+      });
+      return;
+    }
+    cut = cut_of_all<T, P::LOW, THREADS>(in - part.shift, max(rank * a.part, part.shift), min(rank * a.part + a.part, part.all), part.all, sh,
+                                         a.blocks, uint32_t(top_k));
+  }
+  // ---- the sum relative to the block's largest value, and the first place that has it
+  const bool endless = m == INFINITY;
+  auto ex = [&](float f, uint32_t j) {
+    const float e = endless ? (f == m ? 1.f : 0.f) : exp2f(fmaxf(fmaf(f, 0.5f, -0.5f * m) * c, -200.f));
+    return !some || kept(f, j) ? e : 0.f;
+  };
+  float s = 0.f;
+  uint32_t first = ~0u;
+  if (greedy) part.each([&](float f, uint32_t j) { first = f == m ? min(first, j) : first; });
+  else part.each([&](float f, uint32_t j) { s += ex(f, j); });
+  s = warp_add(s);
+  first = __reduce_min_sync(~0u, first);
+  if (lane == 0) sh.wf[1][warp] = s, sh.wu[warp] = first;
+  __syncthreads();
+  if (warp == 0) {
+    s = warp_add(lane < WARPS ? sh.wf[1][lane] : 0.f);
+    first = __reduce_min_sync(~0u, lane < WARPS ? sh.wu[lane] : ~0u);
+    if (lane < a.blocks) {
+      put(there(&sh.part_max[rank], lane), m);
+      put(there(&sh.part_sum[rank], lane), s);
+      put(there(&sh.part_first[rank], lane), first);
+    }
+  }
+  ppl::cluster_sync();
+  top = -INFINITY;
+  for (uint32_t b = 0; b < a.blocks; ++b) top = fmaxf(top, sh.part_max[b]);
+  float total = 0.f;
+  uint32_t best = ~0u;
+  for (uint32_t b = 0; b < a.blocks; ++b) {
+    total += sh.part_sum[b] * share(sh.part_max[b], top, c);
+    if (sh.part_max[b] == top) best = min(best, sh.part_first[b]);
+  }
+  if (greedy) {
+    if (!(top > -INFINITY)) best = ~0u;
+    part.write(out, [&](int i, float* p) {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) p[k] = part.at(i) + k == best ? 1.f : 0.f;
+    });
+    return;
+  }
+  factor = total > 0.f ? share(m, top, c) / total : 0.f;
+  part.write(out, [&](int i, float* p) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) p[k] = ex(to_f(part.x[i].v[k]), part.at(i) + k) * factor;
+  });
+}
+
+template <class K>
+cudaError_t launch_as(K kernel, const ProbArgs& a, uint64_t n_rows, int threads, uint32_t smem, cudaStream_t stream) {
+  cudaLaunchAttribute at;
+  std::memset(&at, 0, sizeof at);
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = a.blocks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(n_rows * a.blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <class T, int THREADS_, bool CUT>
+cudaError_t launch_fast(const ProbArgs& a, uint64_t n_rows, uint32_t vectors, cudaStream_t stream) {
+  const uint32_t nv = (vectors + THREADS_ - 1) / THREADS_;
+  if (nv <= 2) return launch_as(probs_kernel<T, THREADS_, 2, CUT>, a, n_rows, THREADS_, 0, stream);
+  if constexpr (THREADS_ > 128)
+    if (nv <= 5) return launch_as(probs_kernel<T, THREADS_, 5, CUT>, a, n_rows, THREADS_, 0, stream);
+  return launch_as(probs_kernel<T, THREADS_, NV_MOST, CUT>, a, n_rows, THREADS_, 0, stream);
+}
+
 template <class T>
 cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
+  constexpr uint32_t VEC = 16 / sizeof(T);
+  const uint32_t vectors = (a.n_vocab + 2 * VEC - 2) / VEC;  // at any alignment
+  uint32_t blocks = 1;
+  if (vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256)) {
+    a.blocks = 1;
+    a.part = vectors * VEC;
+    return a.top_k ? launch_fast<T, 128, true>(a, n_rows, vectors, stream) : launch_fast<T, 128, false>(a, n_rows, vectors, stream);
+  }
+  while (blocks < CLUSTER && (vectors > 512 * NV_MOST * blocks || (n_rows * blocks < 304 && vectors >= blocks * 2 * 512))) blocks *= 2;
+  const uint32_t each = (vectors + blocks - 1) / blocks;
+  if (each <= 512 * NV_MOST) {
+    a.blocks = blocks;
+    a.part = each * VEC;
+    return a.top_k ? launch_fast<T, 512, true>(a, n_rows, each, stream) : launch_fast<T, 512, false>(a, n_rows, each, stream);
+  }
   static ppi::DeviceOnce once;
   int dev;
   cudaError_t e = ppi::current_device(&dev);
   if (e != cudaSuccess) return e;
   e = once.run(dev, [&](int) {
-    return cudaFuncSetAttribute(probs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(RESIDENT_MOST));
+    return cudaFuncSetAttribute(long_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(RESIDENT_MOST));
   });
   if (e != cudaSuccess) return e;
-  constexpr uint32_t VEC = 16 / sizeof(T);
-  const uint32_t n = a.n_vocab + VEC - 1;
-  uint32_t blocks = 1;
-  while (blocks < CLUSTER && ((n / blocks) * sizeof(T) > 65536 || (n_rows * blocks < 304 && n / (blocks * 2) >= 2048))) blocks *= 2;
-  a.blocks = blocks;
-  a.part = ((n + blocks - 1) / blocks + VEC - 1) / VEC * VEC;
+  a.blocks = CLUSTER;
+  a.part = each * VEC;
   a.resident = a.part * sizeof(T) <= RESIDENT_MOST;
-  cudaLaunchAttribute at;
-  std::memset(&at, 0, sizeof at);
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = blocks;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(n_rows * blocks));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = a.resident ? a.part * sizeof(T) : 0;
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, probs_kernel<T>, static_cast<const ProbArgs>(a));
+  return launch_as(long_kernel<T>, a, n_rows, THREADS, a.resident ? a.part * sizeof(T) : 0, stream);
 }
 
 }  // namespace
