@@ -250,8 +250,7 @@ struct Fast {
   uint32_t wu[WARPS];
   uint32_t bin, above, in_bin;
   uint32_t hist[256];
-  float value[LIST];
-  uint32_t place[LIST];
+  uint2 list[LIST];  // candidates' values and places, a segment of each block's
 };
 
 __device__ __forceinline__ uint32_t there(const void* p, uint32_t rank) {
@@ -300,16 +299,13 @@ __device__ __forceinline__ void find_digit(S& sh, uint32_t want, F&& count) {
   }
 }
 
-// A digit of the want-th largest of n entries; digit_at gives an entry's, or -1
-// for one that is out of question.
+// A digit of the want-th largest of the threads' entries; count(add) calls add
+// with the digit of each of the thread's that are in question.
 template <int THREADS, class F>
-__device__ __forceinline__ void next_digit(Fast<THREADS>& sh, uint32_t n, uint32_t want, F&& digit_at) {
+__device__ __forceinline__ void next_digit(Fast<THREADS>& sh, uint32_t want, F&& count) {
   for (uint32_t i = threadIdx.x; i < 256; i += THREADS) sh.hist[i] = 0;
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
-    const int d = digit_at(i);
-    if (d >= 0) atomicAdd(&sh.hist[d], 1);
-  }
+  count([&](uint32_t digit) { atomicAdd(&sh.hist[digit], 1); });
   __syncthreads();
   if (threadIdx.x < 32) find_digit(sh, want, [&](uint32_t d) { return sh.hist[d]; });
   __syncthreads();
@@ -373,6 +369,13 @@ struct Part {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) f(to_f(x[i].v[k]), at(i) + k);
+  }
+  template <class F>
+  __device__ __forceinline__ void change(F&& f) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) x[i].v[k] = from_f<T>(f(to_f(x[i].v[k]), at(i) + k));
   }
   // f(i, p) fills the VEC probabilities p of vector i.
   template <class F>
@@ -446,11 +449,11 @@ __device__ __noinline__ Cut cut_of_all(const T* x, uint32_t from, uint32_t to, u
   return cut;
 }
 
-// The cut and 1 / the sum of the kept exponentials, where the cluster's lists have room
-// for what reaches a bound that at least top_k values reach; false where not.
+// The probabilities of a cut row, where the cluster's lists have room for what
+// reaches a bound that at least top_k values reach; false where not.
 template <class P, int THREADS>
-__device__ __forceinline__ bool cut_of_lists(P& part, Fast<THREADS>& sh, uint32_t rank, uint32_t blocks, uint32_t top_k, float m,
-                                             uint32_t thread_key, float c, Cut& cut, float& top, float& factor) {
+__device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t rank, uint32_t blocks, uint32_t top_k, float m,
+                                          uint32_t thread_key, float c, float* out) {
   constexpr int WARPS = THREADS / 32, LIST = Fast<THREADS>::LIST, LOW = P::LOW;
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const uint32_t k_part = (top_k + blocks - 1) / blocks;
@@ -465,8 +468,7 @@ __device__ __forceinline__ bool cut_of_lists(P& part, Fast<THREADS>& sh, uint32_
     put(there(&sh.part_bound[rank], threadIdx.x), bound > KEY_LOST ? float_of(bound) : -3.402823466e38f);
   }
   ppl::cluster_sync();
-  float reach = INFINITY;
-  top = -INFINITY;
+  float reach = INFINITY, top = -INFINITY;
   for (uint32_t b = 0; b < blocks; ++b) {
     top = fmaxf(top, sh.part_max[b]);
     reach = fminf(reach, sh.part_bound[b]);
@@ -491,29 +493,53 @@ __device__ __forceinline__ bool cut_of_lists(P& part, Fast<THREADS>& sh, uint32_
   }
   const uint32_t seg = LIST / blocks;
   if (n && mine <= seg) {
-    uint32_t to = rank * seg + before + run - n;
+    uint32_t to = uint32_t(__cvta_generic_to_shared(&sh.list[rank * seg + before + run - n]));
     part.each([&](float f, uint32_t j) {
       if (f >= reach) {
         for (uint32_t b = 0; b < blocks; ++b) {
-          put(there(&sh.value[to], b), f);
-          put(there(&sh.place[to], b), j);
+          uint32_t a;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(to), "r"(b));
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(__float_as_uint(f)), "r"(j) : "memory");
         }
-        ++to;
+        to += 8;
       }
     });
   }
   if (threadIdx.x < blocks) put(there(&sh.part_n[rank], threadIdx.x), mine);
   ppl::cluster_sync();
-  uint32_t total = 0;
+  uint32_t total = 0, own = 0;
   for (uint32_t b = 0; b < blocks; ++b) {
     if (sh.part_n[b] > seg) return false;
+    if (b < rank) own += sh.part_n[b];
     total += sh.part_n[b];
   }
-  // every block finds the same from here on
-  auto listed = [&](uint32_t i) { return i % seg < sh.part_n[i / seg]; };
-  auto key = [&](uint32_t i) { return key_of(sh.value[i]) >> LOW; };
+  // Zeros everywhere: the few others are written over them once they are known.
+  part.write(out, [&](int, float* p) {
+#pragma unroll
+    for (int k = 0; k < P::VEC; ++k) p[k] = 0.f;
+  });
+  // every block finds the same from here on; this thread's entries
+  float value[ENTRIES];
+  uint32_t key[ENTRIES], place[ENTRIES];
+  int entries = 0;
+#pragma unroll
+  for (int e = 0; e < ENTRIES; ++e) {
+    uint32_t i = threadIdx.x + e * THREADS, at = 0;
+    if (i < total) {
+      for (uint32_t b = 0; b < blocks; ++b, at += seg) {
+        const uint32_t here = sh.part_n[b];
+        if (i < here) break;
+        i -= here;
+      }
+      const uint2 q = sh.list[at + i];
+      value[e] = __uint_as_float(q.x);
+      place[e] = q.y;
+      key[e] = key_of(value[e]) >> LOW;
+      ++entries;
+    }
+  }
   const uint32_t hi = key_of(top) >> LOW, lo = key_of(reach) >> LOW;
-  cut.least = lo;  // all candidates
+  Cut cut = {lo, ~0u};  // all candidates
   if (total > top_k) {
     uint32_t want = top_k, in_bin = total;
     int bits = 32 - __clz(hi ^ lo);  // below those that all candidates share
@@ -521,10 +547,10 @@ __device__ __forceinline__ bool cut_of_lists(P& part, Fast<THREADS>& sh, uint32_
     while (bits > 0 && want < in_bin) {
       const int at = max(bits - 8, 0);
       const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
-      next_digit<THREADS>(sh, LIST, want, [&](uint32_t i) {
-        if (!listed(i)) return -1;
-        const uint32_t q = key(i);
-        return (q & mask) == known ? int(q >> at & low) : -1;
+      next_digit<THREADS>(sh, want, [&](auto&& add) {
+#pragma unroll
+        for (int e = 0; e < ENTRIES; ++e)
+          if (e < entries && (key[e] & mask) == known) add(key[e] >> at & low);
       });
       known |= sh.bin << at;
       want -= sh.above;
@@ -534,33 +560,39 @@ __device__ __forceinline__ bool cut_of_lists(P& part, Fast<THREADS>& sh, uint32_
     cut.least = known;
     if (want < in_bin) {  // of those that tie the lowest places
       const int place_bits = 32 - __clz(part.all);
-      uint32_t place = 0;
-      for (bits = place_bits; bits > 0;) {
+      const uint32_t inside = ~(~0u << place_bits);
+      uint32_t found = 0;
+      for (bits = place_bits; bits > 0 && want < in_bin;) {
         const int at = max(bits - 8, 0);
         const uint32_t mask = ~0u << bits, low = (1u << (bits - at)) - 1;
-        next_digit<THREADS>(sh, LIST, want, [&](uint32_t i) {
-          if (!listed(i) || key(i) != cut.least) return -1;
-          const uint32_t q = ~sh.place[i] & ~(~0u << place_bits);
-          return (q & mask) == place ? int(q >> at & low) : -1;
+        next_digit<THREADS>(sh, want, [&](auto&& add) {
+#pragma unroll
+          for (int e = 0; e < ENTRIES; ++e) {
+            const uint32_t q = ~place[e] & inside;
+            if (e < entries && key[e] == cut.least && (q & mask) == found) add(q >> at & low);
+          }
         });
-        place |= sh.bin << at;
+        found |= sh.bin << at;
         want -= sh.above;
+        in_bin = sh.in_bin;
         bits = at;
       }
-      cut.last = ~place & ~(~0u << place_bits);
+      cut.last = ~found & inside;
     }
   }
   float s = 0.f;
-  for (uint32_t i = threadIdx.x; i < LIST; i += THREADS)
-    if (listed(i)) {
-      const uint32_t q = key(i);
-      if (q > cut.least || (q == cut.least && sh.place[i] <= cut.last)) s += share(sh.value[i], top, c);
-    }
+#pragma unroll
+  for (int e = 0; e < ENTRIES; ++e)
+    if (e < entries && (key[e] > cut.least || (key[e] == cut.least && place[e] <= cut.last))) s += share(value[e], top, c);
   s = warp_add(s);
   if (lane == 0) sh.wf[1][warp] = s;
   __syncthreads();
   s = warp_add(lane < WARPS ? sh.wf[1][lane] : 0.f);
-  factor = s > 0.f ? 1.f / s : 0.f;
+  const float factor = s > 0.f ? 1.f / s : 0.f;
+#pragma unroll
+  for (int e = 0; e < ENTRIES; ++e)  // after the zeros: there were barriers since
+    if (e < entries && threadIdx.x + e * THREADS - own < mine && (key[e] > cut.least || (key[e] == cut.least && place[e] <= cut.last)))
+      out[int64_t(place[e]) - part.shift] = share(value[e], top, c) * factor;
   return true;
 }
 
@@ -590,37 +622,37 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
   ppl::cluster_wait();  // every block has started
   const bool some = CUT && top_k > 0 && uint32_t(top_k) < a.n_vocab && !greedy;
   Cut cut = {0, ~0u};
-  float top, factor;
   auto kept = [&](float f, uint32_t j) {
     const uint32_t q = key_of(f) >> P::LOW;
     return f > -INFINITY && (q > cut.least || (q == cut.least && j <= cut.last));
   };
   if (some) {
-    if (cut_of_lists(part, sh, rank, a.blocks, uint32_t(top_k), m, thread_key, c, cut, top, factor)) {
-      const uint32_t least = cut.least << P::LOW;
-      const float reach = least > KEY_LOST ? float_of(least) : -3.402823466e38f;
-      part.write(out, [&](int i, float* p) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float f = to_f(part.x[i].v[k]);
-          p[k] = f >= reach && kept(f, part.at(i) + k) ? share(f, top, c) * factor : 0.f;
-        }
-      });
-      return;
-    }
+    if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, thread_key, c, out)) return;
     cut = cut_of_all<T, P::LOW, THREADS>(in - part.shift, max(rank * a.part, part.shift), min(rank * a.part + a.part, part.all), part.all, sh,
                                          a.blocks, uint32_t(top_k));
+    part.load(in, rank * a.part, a.part, a.n_vocab);  // again, rather than kept in registers meanwhile
   }
   // ---- the sum relative to the block's largest value, and the first place that has it
+  // 2^64 times share(f, m, c), which no exponential within a float's range of 1 leaves
   const bool endless = m == INFINITY;
   auto ex = [&](float f, uint32_t j) {
-    const float e = endless ? (f == m ? 1.f : 0.f) : exp2f(fmaxf(fmaf(f, 0.5f, -0.5f * m) * c, -200.f));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaxf(fmaf(fmaf(f, 0.5f, -0.5f * m), c, 64.f), -200.f)));
+    if (endless) e = f == m ? 0x1p64f : 0.f;
     return !some || kept(f, j) ? e : 0.f;
   };
   float s = 0.f;
   uint32_t first = ~0u;
   if (greedy) part.each([&](float f, uint32_t j) { first = f == m ? min(first, j) : first; });
-  else part.each([&](float f, uint32_t j) { s += ex(f, j); });
+  else if constexpr (sizeof(T) == 4) {  // in the values' place
+    part.change([&](float f, uint32_t j) {
+      const float e = ex(f, j);
+      s += e;
+      return e;
+    });
+  } else {
+    part.each([&](float f, uint32_t j) { s += ex(f, j); });
+  }
   s = warp_add(s);
   first = __reduce_min_sync(~0u, first);
   if (lane == 0) sh.wf[1][warp] = s, sh.wu[warp] = first;
@@ -635,7 +667,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
     }
   }
   ppl::cluster_sync();
-  top = -INFINITY;
+  float top = -INFINITY;
   for (uint32_t b = 0; b < a.blocks; ++b) top = fmaxf(top, sh.part_max[b]);
   float total = 0.f;
   uint32_t best = ~0u;
@@ -651,10 +683,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
     });
     return;
   }
-  factor = total > 0.f ? share(m, top, c) / total : 0.f;
+  const float factor = total > 0.f ? share(m, top, c) / total : 0.f;
   part.write(out, [&](int i, float* p) {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) p[k] = ex(to_f(part.x[i].v[k]), part.at(i) + k) * factor;
+    for (int k = 0; k < VEC; ++k) {
+      const float f = to_f(part.x[i].v[k]);
+      p[k] = (sizeof(T) == 4 ? f : ex(f, part.at(i) + k)) * factor;
+    }
   });
 }
 
