@@ -25,6 +25,7 @@ using ppl::to_f;
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int CLUSTER = 8;
+constexpr int MID = 512;
 constexpr int NV_MOST = 9;  // vectors of a thread
 constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // bytes of a block's part
 
@@ -238,19 +239,21 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
 // ------------------------------------------------------------ rows in registers
 // A block's part of a row stays in its threads' registers, NV vectors of 16
 // bytes each.
-constexpr int ENTRIES = 8;  // listed candidates a thread
+constexpr int ENTRIES = 4;  // listed candidates a thread
 
 template <int THREADS>
 struct Fast {
   static constexpr int WARPS = THREADS / 32, LIST = THREADS * ENTRIES;
   // of every block of the cluster, written by it
+  unsigned long long sums[WARPS];
   float part_max[CLUSTER], part_sum[CLUSTER], part_bound[CLUSTER];
   uint32_t part_first[CLUSTER], part_n[CLUSTER];
   float wf[2][WARPS];
   uint32_t wu[WARPS];
   uint32_t bin, above, in_bin;
   uint32_t hist[256];
-  uint2 list[LIST];  // candidates' values and places, a segment of each block's
+  uint32_t listed;
+  uint2 list[LIST];  // the block's candidates: values and places
 };
 
 __device__ __forceinline__ uint32_t there(const void* p, uint32_t rank) {
@@ -449,99 +452,81 @@ __device__ __noinline__ Cut cut_of_all(const T* x, uint32_t from, uint32_t to, u
   return cut;
 }
 
-// The probabilities of a cut row, where the cluster's lists have room for what
+// The probabilities of a cut row, where the blocks' lists have room for what
 // reaches a bound that at least top_k values reach; false where not.
 template <class P, int THREADS>
 __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t rank, uint32_t blocks, uint32_t top_k, float m,
-                                          uint32_t thread_key, float c, float* out) {
-  constexpr int WARPS = THREADS / 32, LIST = Fast<THREADS>::LIST, LOW = P::LOW;
-  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+                                          float thread_max, float c, float* out) {
+  constexpr int LIST = Fast<THREADS>::LIST, LOW = P::LOW;
   const uint32_t k_part = (top_k + blocks - 1) / blocks;
   if (k_part > THREADS) return false;
-  // Each block's k_part-th largest of its threads' maxima (its upper half's bits): at least
+  // Each block's k_part-th largest of its threads' maxima (its key's upper half): at least
   // k_part of its values reach that, so top_k of the row reach the least of them.
-  uint32_t bound = 0;
-  for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
-    if (__syncthreads_count(thread_key >= (bound | bit)) >= int(k_part)) bound |= bit;
+  uint32_t bound = 0, want = k_part;
+  for (int at = 24; at >= 16; at -= 8) {
+    const uint32_t key = key_of(thread_max);
+    next_digit<THREADS>(sh, want, [&](auto&& add) {
+      if (at == 24 || key >> 24 == bound >> 24) add(key >> at & 255);
+    });
+    bound |= sh.bin << at;
+    want -= sh.above;
+  }
   if (threadIdx.x < blocks) {
     put(there(&sh.part_max[rank], threadIdx.x), m);
     put(there(&sh.part_bound[rank], threadIdx.x), bound > KEY_LOST ? float_of(bound) : -3.402823466e38f);
   }
+  if (threadIdx.x == 0) sh.listed = 0;
   ppl::cluster_sync();
   float reach = INFINITY, top = -INFINITY;
   for (uint32_t b = 0; b < blocks; ++b) {
     top = fmaxf(top, sh.part_max[b]);
     reach = fminf(reach, sh.part_bound[b]);
   }
-  // the candidates in the order of threads, into every block's lists
-  uint32_t n = 0;
-  part.each([&](float f, uint32_t) { n += f >= reach; });
-  uint32_t run = n;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const uint32_t y = __shfl_up_sync(~0u, run, d);
-    if (lane >= uint32_t(d)) run += y;
-  }
-  if (lane == 31) sh.wu[warp] = run;
-  __syncthreads();
-  uint32_t before = 0, mine = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const uint32_t y = sh.wu[w];
-    if (w < int(warp)) before += y;
-    mine += y;
-  }
-  const uint32_t seg = LIST / blocks;
-  if (n && mine <= seg) {
-    uint32_t to = uint32_t(__cvta_generic_to_shared(&sh.list[rank * seg + before + run - n]));
+  // the candidates, in any order
+  if (thread_max >= reach)
     part.each([&](float f, uint32_t j) {
       if (f >= reach) {
-        for (uint32_t b = 0; b < blocks; ++b) {
-          uint32_t a;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(to), "r"(b));
-          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(__float_as_uint(f)), "r"(j) : "memory");
-        }
-        to += 8;
+        const uint32_t at = atomicAdd(&sh.listed, 1);
+        if (at < LIST) sh.list[at] = make_uint2(__float_as_uint(f), j);
       }
     });
-  }
+  __syncthreads();
+  const uint32_t mine = sh.listed;
   if (threadIdx.x < blocks) put(there(&sh.part_n[rank], threadIdx.x), mine);
   ppl::cluster_sync();
   uint32_t total = 0, own = 0;
   for (uint32_t b = 0; b < blocks; ++b) {
-    if (sh.part_n[b] > seg) return false;
     if (b < rank) own += sh.part_n[b];
     total += sh.part_n[b];
   }
+  if (total > LIST) return false;
+  // This thread's entries of all the blocks' lists.  Every block finds the same in them.
+  float value[ENTRIES];
+  uint32_t place[ENTRIES];
+  int entries = 0;
+#pragma unroll
+  for (int e = 0; e < ENTRIES; ++e) {
+    uint32_t i = threadIdx.x + e * THREADS, b = 0;
+    if (i < total) {
+      for (uint32_t n; i >= (n = sh.part_n[b]); ++b) i -= n;
+      uint32_t v;
+      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v), "=r"(place[e]) : "r"(there(&sh.list[i], b)) : "memory");
+      value[e] = __uint_as_float(v);
+      ++entries;
+    }
+  }
+  ppl::cluster_arrive_release();  // this block has read what it needs of the others
   // Zeros everywhere: the few others are written over them once they are known.
   part.write(out, [&](int, float* p) {
 #pragma unroll
     for (int k = 0; k < P::VEC; ++k) p[k] = 0.f;
   });
-  // every block finds the same from here on; this thread's entries
-  float value[ENTRIES];
-  uint32_t key[ENTRIES], place[ENTRIES];
-  int entries = 0;
-#pragma unroll
-  for (int e = 0; e < ENTRIES; ++e) {
-    uint32_t i = threadIdx.x + e * THREADS, at = 0;
-    if (i < total) {
-      for (uint32_t b = 0; b < blocks; ++b, at += seg) {
-        const uint32_t here = sh.part_n[b];
-        if (i < here) break;
-        i -= here;
-      }
-      const uint2 q = sh.list[at + i];
-      value[e] = __uint_as_float(q.x);
-      place[e] = q.y;
-      key[e] = key_of(value[e]) >> LOW;
-      ++entries;
-    }
-  }
+  auto key = [&](int e) { return key_of(value[e]) >> LOW; };
   const uint32_t hi = key_of(top) >> LOW, lo = key_of(reach) >> LOW;
   Cut cut = {lo, ~0u};  // all candidates
   if (total > top_k) {
-    uint32_t want = top_k, in_bin = total;
+    uint32_t in_bin = total;
+    want = top_k;
     int bits = 32 - __clz(hi ^ lo);  // below those that all candidates share
     uint32_t known = bits == 32 ? 0 : hi >> bits << bits;
     while (bits > 0 && want < in_bin) {
@@ -550,7 +535,7 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
       next_digit<THREADS>(sh, want, [&](auto&& add) {
 #pragma unroll
         for (int e = 0; e < ENTRIES; ++e)
-          if (e < entries && (key[e] & mask) == known) add(key[e] >> at & low);
+          if (e < entries && (key(e) & mask) == known) add(key(e) >> at & low);
       });
       known |= sh.bin << at;
       want -= sh.above;
@@ -569,7 +554,7 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
 #pragma unroll
           for (int e = 0; e < ENTRIES; ++e) {
             const uint32_t q = ~place[e] & inside;
-            if (e < entries && key[e] == cut.least && (q & mask) == found) add(q >> at & low);
+            if (e < entries && key(e) == cut.least && (q & mask) == found) add(q >> at & low);
           }
         });
         found |= sh.bin << at;
@@ -580,19 +565,29 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
       cut.last = ~found & inside;
     }
   }
-  float s = 0.f;
+  // The lists' order is not the same each time, so the sum is one of whole numbers: units
+  // of 2^-44, of exponentials up to 1 of which one is.
+  float p[ENTRIES];
+  unsigned long long s = 0;
 #pragma unroll
-  for (int e = 0; e < ENTRIES; ++e)
-    if (e < entries && (key[e] > cut.least || (key[e] == cut.least && place[e] <= cut.last))) s += share(value[e], top, c);
-  s = warp_add(s);
-  if (lane == 0) sh.wf[1][warp] = s;
+  for (int e = 0; e < ENTRIES; ++e) {
+    p[e] = e < entries && (key(e) > cut.least || (key(e) == cut.least && place[e] <= cut.last)) ? share(value[e], top, c) : 0.f;
+    const float high = p[e] * 0x1p22f;
+    const uint32_t whole = __float2uint_rz(high);
+    s += (uint64_t(whole) << 22) + __float2uint_rz((high - float(whole)) * 0x1p22f);
+  }
+#pragma unroll
+  for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
+  if (threadIdx.x % 32 == 0) sh.sums[threadIdx.x / 32] = s;
   __syncthreads();
-  s = warp_add(lane < WARPS ? sh.wf[1][lane] : 0.f);
-  const float factor = s > 0.f ? 1.f / s : 0.f;
+  s = sh.sums[threadIdx.x % (THREADS / 32)];
+#pragma unroll
+  for (int d = THREADS / 64; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
+  const float factor = s ? 1.f / (float(uint32_t(s >> 22)) * 0x1p-22f + float(uint32_t(s) & 0x3FFFFF) * 0x1p-44f) : 0.f;
 #pragma unroll
   for (int e = 0; e < ENTRIES; ++e)  // after the zeros: there were barriers since
-    if (e < entries && threadIdx.x + e * THREADS - own < mine && (key[e] > cut.least || (key[e] == cut.least && place[e] <= cut.last)))
-      out[int64_t(place[e]) - part.shift] = share(value[e], top, c) * factor;
+    if (e < entries && threadIdx.x + e * THREADS - own < mine && p[e] > 0.f) out[int64_t(place[e]) - part.shift] = p[e] * factor;
+  ppl::cluster_wait();
   return true;
 }
 
@@ -614,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
   const float c = 2.88539008f / t;
   float m = -INFINITY;
   part.each([&](float f, uint32_t) { m = fmaxf(m, f); });
-  const uint32_t thread_key = key_of(m);
+  const float thread_max = m;
   m = warp_max(m);
   if (lane == 0) sh.wf[0][warp] = m;
   __syncthreads();
@@ -627,7 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
     return f > -INFINITY && (q > cut.least || (q == cut.least && j <= cut.last));
   };
   if (some) {
-    if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, thread_key, c, out)) return;
+    if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, thread_max, c, out)) return;
     cut = cut_of_all<T, P::LOW, THREADS>(in - part.shift, max(rank * a.part, part.shift), min(rank * a.part + a.part, part.all), part.all, sh,
                                          a.blocks, uint32_t(top_k));
     part.load(in, rank * a.part, a.part, a.n_vocab);  // again, rather than kept in registers meanwhile
@@ -727,11 +722,18 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
   if (vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256)) {
     a.blocks = 1;
     a.part = vectors * VEC;
-    return a.top_k ? launch_fast<T, 128, true>(a, n_rows, vectors, stream) : launch_fast<T, 128, false>(a, n_rows, vectors, stream);
+    return a.top_k ? launch_fast<T, 256, true>(a, n_rows, vectors, stream) : launch_fast<T, 128, false>(a, n_rows, vectors, stream);
   }
-  while (blocks < CLUSTER && (vectors > 512 * NV_MOST * blocks || (n_rows * blocks < 304 && vectors >= blocks * 2 * 512))) blocks *= 2;
+  if (vectors <= MID * NV_MOST * CLUSTER) {
+    while (blocks < CLUSTER && (vectors > MID * NV_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
+    const uint32_t each = (vectors + blocks - 1) / blocks;
+    a.blocks = blocks;
+    a.part = each * VEC;
+    return a.top_k ? launch_fast<T, MID, true>(a, n_rows, each, stream) : launch_fast<T, MID, false>(a, n_rows, each, stream);
+  }
+  blocks = CLUSTER;
   const uint32_t each = (vectors + blocks - 1) / blocks;
-  if (each <= 512 * NV_MOST) {
+  if (MID < 512 && each <= 512 * NV_MOST) {
     a.blocks = blocks;
     a.part = each * VEC;
     return a.top_k ? launch_fast<T, 512, true>(a, n_rows, each, stream) : launch_fast<T, 512, false>(a, n_rows, each, stream);
