@@ -239,11 +239,11 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
 // ------------------------------------------------------------ rows in registers
 // A block's part of a row stays in its threads' registers, NV vectors of 16
 // bytes each.
-constexpr int ENTRIES = 4;  // listed candidates a thread
+constexpr int entries_of(int threads) { return threads > 128 ? 4 : 8; }  // listed candidates a thread
 
 template <int THREADS>
 struct Fast {
-  static constexpr int WARPS = THREADS / 32, LIST = THREADS * ENTRIES;
+  static constexpr int WARPS = THREADS / 32, ENTRIES = entries_of(THREADS), LIST = THREADS * ENTRIES;
   // of every block of the cluster, written by it
   unsigned long long sums[WARPS];
   float part_max[CLUSTER], part_sum[CLUSTER], part_bound[CLUSTER];
@@ -318,7 +318,7 @@ __device__ __forceinline__ void next_digit(Fast<THREADS>& sh, uint32_t want, F&&
 // boundary at or before the row's start; what is outside the row is -infinity.
 template <class T, int THREADS, int NV>
 struct Part {
-  static constexpr int VEC = 16 / sizeof(T);
+  static constexpr int VEC = 16 / sizeof(T), N = NV;
   // a key's lowest bits, which all values of a sign share
   static constexpr int LOW = sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 13 : 16;
   using Vec = ppl::Pack<T, VEC>;
@@ -338,21 +338,23 @@ struct Part {
     const T none = from_f<T>(-INFINITY);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i < n && at(i) >= shift && at(i) + VEC <= all) {
-        x[i] = *reinterpret_cast<const Vec*>(in - shift + at(i));
-      } else {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) x[i].v[k] = none;
-      }
+      for (int k = 0; k < VEC; ++k) x[i].v[k] = none;
+      if (i < n && at(i) >= shift && at(i) + VEC <= all) x[i] = *reinterpret_cast<const Vec*>(in - shift + at(i));
     }
     // the incomplete vectors, where the row begins and ends
+    const uint32_t last = all / VEC * VEC;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i < n && (at(i) < shift || at(i) + VEC > all)) {
+    for (int side = 0; side < 2; ++side) {
+      const uint32_t j = side ? last : 0;
+      if (j < begin || j >= to || (j - begin) % (THREADS * VEC) != 0 || (side ? last == 0 || last == all : shift == 0 && all >= VEC)) continue;
+      Vec edge;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          if (at(i) + k >= shift && at(i) + k < all) x[i].v[k] = in[at(i) + k - shift];
-      }
+      for (int k = 0; k < VEC; ++k) edge.v[k] = j + k >= shift && j + k < all ? in[int64_t(j) + k - shift] : none;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (at(i) == j) x[i] = edge;
+    }
   }
   // What was computed from the values is not kept for the next pass over them:
   // in 32 bits they would not fit the registers.
@@ -412,61 +414,75 @@ struct Cut {
   uint32_t least, last;
 };
 
-// The cut of any length: digits counted over all values of the cluster, those of
-// this block at places from .. to - 1 of x.
-template <class T, int LOW, int THREADS>
-__device__ __noinline__ Cut cut_of_all(const T* x, uint32_t from, uint32_t to, uint32_t all, Fast<THREADS>& sh, uint32_t blocks, uint32_t want) {
+// The cut of any length: digits counted over all values of the cluster.  A
+// function of its own, since its registers would crowd out the values elsewhere.
+template <class T, int THREADS, int NV>
+__device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size, uint32_t n_vocab, Fast<THREADS>& sh, uint32_t blocks,
+                                       uint32_t want) {
+  using P = Part<T, THREADS, NV>;
+  P part;
+  part.load(in, from, size, n_vocab);
   Cut cut = {0, ~0u};
-  uint32_t place = 0;
-  const int place_bits = 32 - __clz(all);
-  for (int side = 0; side < 2; ++side) {  // the values, then the places of those that tie
-    for (int bits = side ? place_bits : 32 - LOW; bits > 0;) {
-      const int at = max(bits - 8, 0);
-      const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
-      for (uint32_t i = threadIdx.x; i < 256; i += THREADS) sh.hist[i] = 0;
-      __syncthreads();
-      for (uint32_t j = from + threadIdx.x; j < to; j += THREADS) {
-        uint32_t q = key_of(fmaxf(to_f(x[j]), -INFINITY)) >> LOW;
-        if (side) {
-          if (q != cut.least) continue;
-          q = ~j & ~(~0u << place_bits);
-        }
-        if ((q & mask) == (side ? place : cut.least)) atomicAdd(&sh.hist[q >> at & low], 1);
-      }
-      ppl::cluster_sync();  // every block's counts are there
-      if (threadIdx.x < 32) find_digit(sh, want, [&](uint32_t d) {
-        uint32_t n = 0;
-        for (uint32_t b = 0; b < blocks; ++b) n += remote_u(&sh.hist[d], b);
-        return n;
-      });
-      ppl::cluster_sync();  // and read
-      (side ? place : cut.least) |= sh.bin << at;
-      want -= sh.above;
-      bits = at;
-      if (want != sh.in_bin) continue;
-      if (!side) return cut;  // all that agree so far
-      break;
+  const int place_bits = 32 - __clz(part.all);
+  // side 0: the values; side 1: the places of those that tie, where not all are kept
+  uint32_t found = 0;
+  int bits = 32 - P::LOW, side = 0;
+  while (true) {
+    const int at = max(bits - 8, 0);
+    const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
+    for (uint32_t i = threadIdx.x; i < 256; i += THREADS) sh.hist[i] = 0;
+    __syncthreads();
+    part.each([&](float f, uint32_t j) {
+      uint32_t q = key_of(fmaxf(f, -INFINITY)) >> P::LOW;
+      bool in = !side || q == cut.least;
+      if (side) q = ~j & ~(~0u << place_bits);
+      in = in && (q & mask) == found;
+      if (in) atomicAdd(&sh.hist[q >> at & low], 1);
+    });
+    ppl::cluster_sync();  // every block's counts are there
+    if (threadIdx.x < 32) find_digit(sh, want, [&](uint32_t d) {
+      uint32_t n = 0;
+      for (uint32_t b = 0; b < blocks; ++b) n += remote_u(&sh.hist[d], b);
+      return n;
+    });
+    ppl::cluster_sync();  // and read
+    found |= sh.bin << at;
+    want -= sh.above;
+    bits = at;
+    const bool whole = want == sh.in_bin;  // all that agree so far are kept
+    if (!whole && bits > 0) continue;
+    if (side) {
+      cut.last = ~found & ~(~0u << place_bits);
+      return cut;
     }
+    cut.least = found;
+    if (whole) return cut;
+    side = 1;
+    found = 0;
+    bits = place_bits;
   }
-  cut.last = ~place & ~(~0u << place_bits);
-  return cut;
 }
 
 // The probabilities of a cut row, where the blocks' lists have room for what
 // reaches a bound that at least top_k values reach; false where not.
-template <class P, int THREADS>
+template <class P, int THREADS, int G, class T>
 __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t rank, uint32_t blocks, uint32_t top_k, float m,
-                                          float thread_max, float c, float* out) {
-  constexpr int LIST = Fast<THREADS>::LIST, LOW = P::LOW;
+                                          const float (&maxima)[G], float c, const T* in, float* out) {
+  constexpr int LIST = Fast<THREADS>::LIST, ENTRIES = Fast<THREADS>::ENTRIES, LOW = P::LOW;
   const uint32_t k_part = (top_k + blocks - 1) / blocks;
-  if (k_part > THREADS) return false;
-  // Each block's k_part-th largest of its threads' maxima (its key's upper half): at least
-  // k_part of its values reach that, so top_k of the row reach the least of them.
+  const bool every = part.all <= LIST;  // the lists have room for the row
+  if (k_part > THREADS * G && !every) return false;
+  // Each block's k_part-th largest of its threads' (or vectors') maxima (its key's upper half): at least
+  // k_part of its values reach that, so top_k of the row reach the least of them.  A block
+  // with fewer than that finds -infinity.
   uint32_t bound = 0, want = k_part;
-  for (int at = 24; at >= 16; at -= 8) {
-    const uint32_t key = key_of(thread_max);
+  for (int at = 24; at >= 16 && !every; at -= 8) {
     next_digit<THREADS>(sh, want, [&](auto&& add) {
-      if (at == 24 || key >> 24 == bound >> 24) add(key >> at & 255);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const uint32_t key = key_of(maxima[i]);
+        if (at == 24 || key >> 24 == bound >> 24) add(key >> at & 255);
+      }
     });
     bound |= sh.bin << at;
     want -= sh.above;
@@ -483,13 +499,22 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
     reach = fminf(reach, sh.part_bound[b]);
   }
   // the candidates, in any order
-  if (thread_max >= reach)
-    part.each([&](float f, uint32_t j) {
-      if (f >= reach) {
-        const uint32_t at = atomicAdd(&sh.listed, 1);
-        if (at < LIST) sh.list[at] = make_uint2(__float_as_uint(f), j);
-      }
-    });
+  // and few, so only marked here; a branch for each value is a kernel of code
+  constexpr int WORDS = (P::N * P::VEC + 31) / 32;
+  uint32_t marks[WORDS] = {};
+  part.forget();
+#pragma unroll
+  for (int i = 0; i < P::N; ++i)
+#pragma unroll
+    for (int k = 0; k < P::VEC; ++k)
+      if (to_f(part.x[i].v[k]) >= reach) marks[(i * P::VEC + k) / 32] |= 1u << (i * P::VEC + k) % 32;
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w)
+    for (; marks[w]; marks[w] &= marks[w] - 1) {
+      const int e = w * 32 + __ffs(marks[w]) - 1;
+      const uint32_t j = part.at(e / P::VEC) + e % P::VEC, at = atomicAdd(&sh.listed, 1);
+      if (at < LIST) sh.list[at] = make_uint2(__float_as_uint(to_f(in[int64_t(j) - part.shift])), j);
+    }
   __syncthreads();
   const uint32_t mine = sh.listed;
   if (threadIdx.x < blocks) put(there(&sh.part_n[rank], threadIdx.x), mine);
@@ -607,9 +632,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
   part.load(in, rank * a.part, a.part, a.n_vocab);
   const bool greedy = !(t > 0x1p-125f);  // below, c is not a float
   const float c = 2.88539008f / t;
-  float m = -INFINITY;
-  part.each([&](float f, uint32_t) { m = fmaxf(m, f); });
-  const float thread_max = m;
+  constexpr int G = THREADS > 128 ? 1 : NV;  // maxima a thread: more where there are few threads
+  float m = -INFINITY, maxima[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) maxima[i] = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) maxima[i % G] = fmaxf(maxima[i % G], to_f(part.x[i].v[k]));
+#pragma unroll
+  for (int i = 0; i < G; ++i) m = fmaxf(m, maxima[i]);
   m = warp_max(m);
   if (lane == 0) sh.wf[0][warp] = m;
   __syncthreads();
@@ -622,9 +654,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
     return f > -INFINITY && (q > cut.least || (q == cut.least && j <= cut.last));
   };
   if (some) {
-    if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, thread_max, c, out)) return;
-    cut = cut_of_all<T, P::LOW, THREADS>(in - part.shift, max(rank * a.part, part.shift), min(rank * a.part + a.part, part.all), part.all, sh,
-                                         a.blocks, uint32_t(top_k));
+    if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, maxima, c, in, out)) return;
+    cut = cut_of_all<T, THREADS, NV>(in, rank * a.part, a.part, a.n_vocab, sh, a.blocks, uint32_t(top_k));
     part.load(in, rank * a.part, a.part, a.n_vocab);  // again, rather than kept in registers meanwhile
   }
   // ---- the sum relative to the block's largest value, and the first place that has it
@@ -709,8 +740,7 @@ template <class T, int THREADS_, bool CUT>
 cudaError_t launch_fast(const ProbArgs& a, uint64_t n_rows, uint32_t vectors, cudaStream_t stream) {
   const uint32_t nv = (vectors + THREADS_ - 1) / THREADS_;
   if (nv <= 2) return launch_as(probs_kernel<T, THREADS_, 2, CUT>, a, n_rows, THREADS_, 0, stream);
-  if constexpr (THREADS_ > 128)
-    if (nv <= 5) return launch_as(probs_kernel<T, THREADS_, 5, CUT>, a, n_rows, THREADS_, 0, stream);
+  if (nv <= 5) return launch_as(probs_kernel<T, THREADS_, 5, CUT>, a, n_rows, THREADS_, 0, stream);
   return launch_as(probs_kernel<T, THREADS_, NV_MOST, CUT>, a, n_rows, THREADS_, 0, stream);
 }
 
@@ -719,11 +749,10 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
   constexpr uint32_t VEC = 16 / sizeof(T);
   const uint32_t vectors = (a.n_vocab + 2 * VEC - 2) / VEC;  // at any alignment
   uint32_t blocks = 1;
-  if (vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256)) {
-    a.blocks = 1;
-    a.part = vectors * VEC;
-    return a.top_k ? launch_fast<T, 256, true>(a, n_rows, vectors, stream) : launch_fast<T, 128, false>(a, n_rows, vectors, stream);
-  }
+  a.blocks = 1;
+  a.part = vectors * VEC;
+  if (vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256))
+    return a.top_k ? launch_fast<T, 128, true>(a, n_rows, vectors, stream) : launch_fast<T, 128, false>(a, n_rows, vectors, stream);
   if (vectors <= MID * NV_MOST * CLUSTER) {
     while (blocks < CLUSTER && (vectors > MID * NV_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
     const uint32_t each = (vectors + blocks - 1) / blocks;
