@@ -15,6 +15,7 @@
 // itself, sums its part of the row, a segment a warp, and gives the sum to the
 // other blocks; the warp whose segment holds the drawn sum reads it again.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "pp_internal.h"
@@ -43,12 +44,13 @@ struct VerifyArgs {
   uint32_t target_rows, probs_rows, n_drafts, n_vocab;
   uint32_t blocks, part;  // blocks of a cluster, tokens of a block
   int32_t draft_type;
-  float unit;  // 2^unit_bits
+  int32_t unit_bits;
+  float scale;
 };
 
 // A probability's float: NaN counts as 0, values outside [0, 1] are cut.
 template <class T>
-__device__ __forceinline__ float prob(const T* p) { return fminf(fmaxf(to_f(*p), 0.f), 1.f); }
+__device__ __forceinline__ float prob(const T* p) { return __saturatef(to_f(*p)); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -56,49 +58,122 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
-// What token v of the row weighs.  SURE: the draft's probability is all at one
-// token.  left: the draft's part is taken off.
-template <class T, bool SURE>
-__device__ __forceinline__ uint64_t weight(const T* p, const T* q, uint32_t v, uint32_t gone, float unit) {
-  const uint64_t a = __float2ull_rz(prob(p + v) * unit);
-  if (SURE) return v == gone ? 0 : a;
-  const uint64_t b = q ? __float2ull_rz(prob(q + v) * unit) : 0;
-  return a > b ? a - b : 0;
-}
-
-// The sum of this warp's segment.
-template <class T, bool SURE>
-__device__ __forceinline__ uint64_t segment_sum(const T* p, const T* q, uint32_t lo, uint32_t hi, uint32_t gone, float unit) {
-  uint64_t s = 0;
-  uint32_t v = lo + threadIdx.x % 32;
-  for (; v + (UNROLL - 1) * 32 < hi; v += UNROLL * 32) {
+// A probability in units, in PARTS digits of base 2^23.  Conversions to 64 bits
+// run at 2 a clock and multiprocessor here, so there are none: 2^23 is added, rounding
+// down, to what the digit is the whole part of, which leaves the digit in the low bits.
+// The rest is exact, and so is its product with 2^23.
+template <int PARTS>
+struct Units {
+  uint32_t digit[PARTS];  // each plus the bits of 2^23
+  __device__ __forceinline__ Units(float p, float scale) {  // scale: 2^(unit_bits - 23 (PARTS - 1))
+    constexpr float BASE = 8388608.f;
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) s += weight<T, SURE>(p, q, v + k * 32, gone, unit);
-  }
-  for (; v < hi; v += 32) s += weight<T, SURE>(p, q, v, gone, unit);
-  return warp_sum(s);
-}
-
-// The lowest token of the segment at which the running sum passes t.
-template <class T, bool SURE>
-__device__ __forceinline__ uint32_t segment_pick(const T* p, const T* q, uint32_t lo, uint32_t hi, uint32_t gone, float unit, uint64_t t) {
-  const uint32_t lane = threadIdx.x % 32;
-  for (uint32_t at = lo; at < hi; at += 32) {
-    const uint32_t v = at + lane;
-    uint64_t x = v < hi ? weight<T, SURE>(p, q, v, gone, unit) : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const uint64_t y = __shfl_up_sync(~0u, x, d);
-      if (lane >= d) x += y;
+    for (int k = 0; k < PARTS; ++k) {
+      const float up = __fmaf_rd(p, scale, BASE);
+      digit[k] = __float_as_uint(up);
+      if (k + 1 < PARTS) {
+        p = fmaf(p, scale, BASE - up);
+        scale = BASE;
+      }
     }
-    const uint32_t past = __ballot_sync(~0u, x > t);
-    if (past) return at + __ffs(past) - 1;
-    t -= __shfl_sync(~0u, x, 31);
   }
-  return lo;  // not reached: the segment's sum is above t
-}
+};
 
-template <class T, bool SURE>
+// A sum of such numbers, less others of as many: the bits of 2^23 cancel.
+template <int PARTS>
+struct Sum {
+  int32_t digit[PARTS];
+  __device__ __forceinline__ Sum() {
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) digit[k] = 0;
+  }
+  __device__ __forceinline__ void add(const Units<PARTS>& a, const Units<PARTS>& b) {
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) digit[k] += int32_t(a.digit[k] - b.digit[k]);
+  }
+  __device__ __forceinline__ uint64_t value() const {
+    int64_t v = 0;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) v = v * (1 << 23) + digit[k];
+    return uint64_t(v);
+  }
+};
+
+// Tokens lo .. hi - 1 of a row: what token v weighs is P less Q where P is more.
+// LESS: there is a q.  A token `gone` weighs nothing.
+template <class T, int PARTS, bool LESS>
+struct Segment {
+  const T* p;
+  const T* q;
+  uint32_t lo, hi, gone;
+  float scale;
+
+  __device__ __forceinline__ void add(Sum<PARTS>& s, float a, float b) const {
+    const Units<PARTS> x(a, scale), y(LESS ? b : 0.f, scale);
+    // P is more than Q only where p is more than q
+    if (!LESS || a > b) s.add(x, y);
+  }
+  __device__ __forceinline__ uint64_t weight(uint32_t v) const {
+    Sum<PARTS> s;
+    if (v < hi && v != gone) add(s, prob(p + v), LESS ? prob(q + v) : 0.f);
+    return s.value();
+  }
+  __device__ __forceinline__ uint64_t sum() const {
+    const uint32_t lane = threadIdx.x % 32;
+    uint64_t total = 0;
+    uint32_t v = lo + lane;
+    const uint32_t whole = hi > lo ? (hi - lo) / (UNROLL * 32) : 0;
+    for (uint32_t k = 0; k < whole; ++k, v += UNROLL * 32) {
+      float a[UNROLL], b[UNROLL];
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) a[i] = prob(p + v + i * 32);
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) b[i] = LESS ? prob(q + v + i * 32) : 0.f;
+      Sum<PARTS> s;  // digits below 2^23, UNROLL of them: no overflow
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) add(s, a[i], b[i]);
+      total += s.value();
+    }
+    for (; v < hi; v += 32) {
+      Sum<PARTS> s;
+      add(s, prob(p + v), LESS ? prob(q + v) : 0.f);
+      total += s.value();
+    }
+    total = warp_sum(total);
+    if (gone >= lo && gone < hi) {
+      Sum<PARTS> s;
+      add(s, prob(p + gone), LESS ? prob(q + gone) : 0.f);
+      total -= s.value();
+    }
+    return total;
+  }
+  // The lowest token at which the running sum passes t, less than the whole.
+  __device__ __forceinline__ uint32_t pick(uint64_t t) const {
+    const uint32_t lane = threadIdx.x % 32;
+    for (uint32_t at = lo; at < hi; at += 32 * UNROLL) {
+      // the sums of UNROLL times 32 tokens, loads and scans side by side
+      uint64_t x[UNROLL];
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) x[i] = weight(at + i * 32 + lane);
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2)
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+          const uint64_t y = __shfl_up_sync(~0u, x[i], d);
+          if (lane >= uint32_t(d)) x[i] += y;
+        }
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) {
+        const uint32_t past = __ballot_sync(~0u, x[i] > t);
+        if (past) return at + i * 32 + __ffs(past) - 1;
+        t -= __shfl_sync(~0u, x[i], 31);
+      }
+    }
+    return lo;  // not reached
+  }
+};
+
+template <class T, bool SURE, int PARTS>
 __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
   ppl::cluster_arrive();
   __shared__ uint64_t totals[2][CLUSTER];  // of the blocks, twice: by what the draft left, and by the target
@@ -155,8 +230,10 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
   const uint32_t each = (a.part + WARPS * 32 - 1) / (WARPS * 32) * 32;
   const uint32_t lo = min(begin + warp * each, end), hi = min(lo + each, end);
   uint64_t total = 0, before = 0, mine = 0;  // of all blocks, of those before this one, this block's
+  const Segment<T, PARTS, true> less = {p, q, lo, hi, gone, a.scale};
   for (int round = 0; round < 2; ++round) {
-    const uint64_t s = p ? segment_sum<T, SURE>(p, q, lo, hi, gone, a.unit) : 0;
+    uint64_t s = 0;
+    if (p) s = round || SURE || !q ? Segment<T, PARTS, false>{p, nullptr, lo, hi, round ? ~0u : gone, a.scale}.sum() : less.sum();
     if (lane == 0) sums[warp] = s;
     __syncthreads();
     if (round == 0) ppl::cluster_wait();
@@ -198,7 +275,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
     const uint64_t s = sums[k];
     if (t < s) {
       if (int(warp) == k) {
-        const uint32_t v = segment_pick<T, SURE>(p, q, lo, hi, gone, a.unit, t);
+        const uint32_t v = SURE || !q ? Segment<T, PARTS, false>{p, nullptr, lo, hi, gone, a.scale}.pick(t) : less.pick(t);
         if (lane == 0) out[j] = int32_t(v);
       }
       return;
@@ -207,7 +284,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
   }
 }
 
-template <class T, bool SURE>
+template <class T, bool SURE, int PARTS>
 cudaError_t launch(VerifyArgs& a, uint64_t n_requests, cudaStream_t stream) {
   // as many blocks a request as fill 152 multiprocessors four times, none of
   // fewer than 2048 tokens
@@ -226,12 +303,18 @@ cudaError_t launch(VerifyArgs& a, uint64_t n_requests, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T, SURE>, static_cast<const VerifyArgs>(a));
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, SURE, PARTS>, static_cast<const VerifyArgs>(a));
 }
 
 template <class T>
 cudaError_t launch_type(VerifyArgs& a, uint64_t n, cudaStream_t stream) {
-  return a.probs ? launch<T, false>(a, n, stream) : launch<T, true>(a, n, stream);
+  // the highest of PARTS digits is at most 2^23
+  if (a.unit_bits <= 46) {
+    a.scale = std::ldexp(1.f, a.unit_bits - 23);
+    return a.probs ? launch<T, false, 2>(a, n, stream) : launch<T, true, 2>(a, n, stream);
+  }
+  a.scale = std::ldexp(1.f, a.unit_bits - 46);
+  return a.probs ? launch<T, false, 3>(a, n, stream) : launch<T, true, 3>(a, n, stream);
 }
 
 }  // namespace
@@ -282,9 +365,8 @@ extern "C" pp_rc pp_verify_drafts(const void* d_target, pp_ftype type, size_t ta
   a.n_vocab = uint32_t(n_vocab);
   a.draft_type = draft_type;
   // n_vocab probabilities of at most 1 sum to less than 2^62 units
-  int bits = 62;
-  for (size_t v = n_vocab - 1; v; v >>= 1) --bits;
-  a.unit = float(uint64_t(1) << bits);
+  a.unit_bits = 62;
+  for (size_t v = n_vocab - 1; v; v >>= 1) --a.unit_bits;
   cudaError_t e;
   switch (type) {
     case PP_F32: e = launch_type<float>(a, n_requests, stream); break;
