@@ -25,9 +25,10 @@ namespace {
 
 using ppl::to_f;
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int THREADS = 256, RESIDENT = 6, WARPS = THREADS / 32;
 constexpr int CLUSTER = 8;  // blocks at most
 constexpr int UNROLL = 8;
+constexpr int FEW = 8;  // tokens of a thread that looks for one
 
 struct VerifyArgs {
   const void* target;
@@ -147,34 +148,50 @@ struct Segment {
     }
     return total;
   }
-  // The lowest token at which the running sum passes t, less than the whole.
-  __device__ __forceinline__ uint32_t pick(uint64_t t) const {
-    const uint32_t lane = threadIdx.x % 32;
-    for (uint32_t at = lo; at < hi; at += 32 * UNROLL) {
-      // the sums of UNROLL times 32 tokens, loads and scans side by side
-      uint64_t x[UNROLL];
+  // The lowest token at which the running sum passes t, less than the whole, goes to *out.  All threads of the
+  // block, each with a few tokens one behind the other, so that one scan over the threads does.
+  __device__ __forceinline__ void pick(uint64_t t, uint64_t (&sums)[WARPS], int32_t* out) const {
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (uint32_t at = lo; at < hi; at += THREADS * FEW) {
+      const uint32_t v = at + threadIdx.x * FEW;
+      uint64_t w[FEW], x = 0;
 #pragma unroll
-      for (int i = 0; i < UNROLL; ++i) x[i] = weight(at + i * 32 + lane);
+      for (int i = 0; i < FEW; ++i) x += w[i] = weight(v + i);
+      uint64_t run = x;
 #pragma unroll
-      for (int d = 1; d < 32; d *= 2)
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-          const uint64_t y = __shfl_up_sync(~0u, x[i], d);
-          if (lane >= uint32_t(d)) x[i] += y;
-        }
-#pragma unroll
-      for (int i = 0; i < UNROLL; ++i) {
-        const uint32_t past = __ballot_sync(~0u, x[i] > t);
-        if (past) return at + i * 32 + __ffs(past) - 1;
-        t -= __shfl_sync(~0u, x[i], 31);
+      for (int d = 1; d < 32; d *= 2) {
+        const uint64_t y = __shfl_up_sync(~0u, run, d);
+        if (lane >= uint32_t(d)) run += y;
       }
+      __syncthreads();  // all are done with what was in sums
+      if (lane == 31) sums[warp] = run;
+      __syncthreads();
+      uint64_t before = run - x, all = 0;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        if (k < int(warp)) before += sums[k];
+        all += sums[k];
+      }
+      if (t >= before && t - before < x) {
+        t -= before;
+        uint32_t k = 0;
+#pragma unroll
+        for (int i = 0; i < FEW; ++i) {  // the first whose running sum passes t
+          const bool over = t < w[i];
+          if (over) break;
+          t -= w[i];
+          ++k;
+        }
+        *out = int32_t(v + k);
+      }
+      if (t < all) return;  // for the thread that has just written, too: t is less than x then
+      t -= all;
     }
-    return lo;  // not reached
   }
 };
 
 template <class T, bool SURE, int PARTS>
-__global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(THREADS, RESIDENT) verify_kernel(const VerifyArgs a) {
   ppl::cluster_arrive();
   __shared__ uint64_t totals[2][CLUSTER];  // of the blocks, twice: by what the draft left, and by the target
   __shared__ uint64_t sums[WARPS];
@@ -183,41 +200,52 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const T* target = static_cast<const T*>(a.target);
   const T* probs = static_cast<const T*>(a.probs);
+  auto draft = [&](int i) { return ppl::load_id(a.drafts, a.draft_type, r * a.drafts_stride + i); };
+  // what does not hang on one another is loaded at once
+  const int most = int(a.n_drafts);
+  const float u_sample = a.sample[r];
+  int64_t d = -1;
+  float u = 0.f;
+  if (warp == 0 && int(lane) < most) {
+    d = draft(lane);
+    u = a.accept[r * a.accept_stride + lane];
+  }
   const int64_t first = a.target_row ? int64_t(a.target_row[r]) : int64_t(r) * (a.n_drafts + 1);
   const int64_t qfirst = SURE ? 0 : a.probs_row ? int64_t(a.probs_row[r]) : int64_t(r) * a.n_drafts;
-  int n = int(a.n_drafts);
-  if (a.lengths) n = max(0, min(n, a.lengths[r]));
+  const int n = a.lengths ? max(0, min(most, a.lengths[r])) : most;
   auto row = [&](int64_t i) -> const T* { return i >= 0 && i < int64_t(a.target_rows) ? target + uint64_t(i) * a.target_stride : nullptr; };
   auto qrow = [&](int64_t i) -> const T* { return i >= 0 && i < int64_t(a.probs_rows) ? probs + uint64_t(i) * a.probs_stride : nullptr; };
-  auto draft = [&](int i) { return ppl::load_id(a.drafts, a.draft_type, r * a.drafts_stride + i); };
   if (warp == 0) {
     int accepted = n;
+    int64_t token = -1;  // the draft that is not accepted
     for (int i0 = 0; i0 < n; i0 += 32) {
       const int i = i0 + int(lane);
       bool bad = false;
       if (i < n) {
-        const int64_t d = draft(i);
-        const float u = a.accept[r * a.accept_stride + i];
+        if (i0) {
+          d = draft(i);
+          u = a.accept[r * a.accept_stride + i];
+        }
         const T* p = row(first + i);
         const T* q = SURE ? nullptr : qrow(qfirst + i);
         bad = true;
         if (d >= 0 && d < int64_t(a.n_vocab) && p && (SURE || q)) {
           // 24 bits by 24 bits: the product is exact
-          const double share = SURE ? double(u) : double(u) * double(prob(q + d));
-          bad = !(u >= 0.f && share < double(prob(p + d)));
+          const float pd = prob(p + d), qd = SURE ? 1.f : prob(q + d);
+          bad = !(u >= 0.f && double(u) * double(qd) < double(pd));
         }
       }
       const uint32_t some = __ballot_sync(~0u, bad);
       if (some) {
         accepted = i0 + __ffs(some) - 1;
+        token = __shfl_sync(~0u, d, __ffs(some) - 1);
         break;
       }
     }
     if (lane == 0) {
       s_accepted = accepted;
       s_rejected = accepted < n;
-      const int64_t d = accepted < n ? draft(accepted) : -1;
-      s_token = d >= 0 && d < int64_t(a.n_vocab) ? uint32_t(d) : ~0u;
+      s_token = token >= 0 && token < int64_t(a.n_vocab) ? uint32_t(token) : ~0u;
     }
   }
   __syncthreads();
@@ -266,22 +294,15 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
   }
   if (!total) return;
   // the random number in units of 2^-31 of the total
-  const float u = a.sample[r];
-  const uint32_t w = u > 0.f ? (u < 1.f ? uint32_t(u * 2147483648.f) : 0x7FFFFFFFu) : 0;
+  const uint32_t w = u_sample > 0.f ? (u_sample < 1.f ? uint32_t(u_sample * 2147483648.f) : 0x7FFFFFFFu) : 0;
   uint64_t t = __umul64hi(total, w) << 33 | (total * w) >> 31;
   if (t < before || t - before >= mine) return;
   t -= before;
-  for (int k = 0; k < WARPS; ++k) {  // which warp's segment
-    const uint64_t s = sums[k];
-    if (t < s) {
-      if (int(warp) == k) {
-        const uint32_t v = SURE || !q ? Segment<T, PARTS, false>{p, nullptr, lo, hi, gone, a.scale}.pick(t) : less.pick(t);
-        if (lane == 0) out[j] = int32_t(v);
-      }
-      return;
-    }
-    t -= s;
-  }
+  uint32_t k = 0;  // which warp's segment
+  for (; t >= sums[k]; ++k) t -= sums[k];
+  const uint32_t from = min(begin + k * each, end), to = min(from + each, end);
+  if (SURE || !q) Segment<T, PARTS, false>{p, nullptr, from, to, gone, a.scale}.pick(t, sums, out + j);
+  else Segment<T, PARTS, true>{p, q, from, to, gone, a.scale}.pick(t, sums, out + j);
 }
 
 template <class T, bool SURE, int PARTS>
@@ -289,7 +310,7 @@ cudaError_t launch(VerifyArgs& a, uint64_t n_requests, cudaStream_t stream) {
   // as many blocks a request as fill 152 multiprocessors four times, none of
   // fewer than 2048 tokens
   uint32_t blocks = 1;
-  while (blocks < CLUSTER && n_requests * blocks < 608 && a.n_vocab / (blocks * 2) >= 2048) blocks *= 2;
+  while (blocks < CLUSTER && n_requests * blocks < 2432 && a.n_vocab / (blocks * 2) >= 2048) blocks *= 2;
   a.blocks = blocks;
   a.part = ((a.n_vocab + blocks - 1) / blocks + 31) / 32 * 32;
   cudaLaunchAttribute at;
