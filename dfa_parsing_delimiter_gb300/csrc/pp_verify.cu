@@ -25,9 +25,9 @@ namespace {
 
 using ppl::to_f;
 
-constexpr int THREADS = 256, RESIDENT = 6, WARPS = THREADS / 32;
+constexpr int THREADS = 256, RESIDENT = 4, WARPS = THREADS / 32;
 constexpr int CLUSTER = 8;  // blocks at most
-constexpr int UNROLL = 8;
+constexpr int UNROLL = 16;  // loads of each row that a thread has on their way
 constexpr int FEW = 8;  // tokens of a thread that looks for one
 
 struct VerifyArgs {
@@ -123,23 +123,20 @@ struct Segment {
     const uint32_t lane = threadIdx.x % 32;
     uint64_t total = 0;
     uint32_t v = lo + lane;
-    const uint32_t whole = hi > lo ? (hi - lo) / (UNROLL * 32) : 0;
-    for (uint32_t k = 0; k < whole; ++k, v += UNROLL * 32) {
+    auto batch = [&](bool whole) {
       float a[UNROLL], b[UNROLL];
 #pragma unroll
-      for (int i = 0; i < UNROLL; ++i) a[i] = prob(p + v + i * 32);
+      for (int i = 0; i < UNROLL; ++i) a[i] = whole || v + i * 32 < hi ? prob(p + v + i * 32) : 0.f;
 #pragma unroll
-      for (int i = 0; i < UNROLL; ++i) b[i] = LESS ? prob(q + v + i * 32) : 0.f;
+      for (int i = 0; i < UNROLL; ++i) b[i] = LESS && (whole || v + i * 32 < hi) ? prob(q + v + i * 32) : 0.f;
       Sum<PARTS> s;  // digits below 2^23, UNROLL of them: no overflow
 #pragma unroll
       for (int i = 0; i < UNROLL; ++i) add(s, a[i], b[i]);
       total += s.value();
-    }
-    for (; v < hi; v += 32) {
-      Sum<PARTS> s;
-      add(s, prob(p + v), LESS ? prob(q + v) : 0.f);
-      total += s.value();
-    }
+    };
+    const uint32_t whole = hi > lo ? (hi - lo) / (UNROLL * 32) : 0;
+    for (uint32_t k = 0; k < whole; ++k, v += UNROLL * 32) batch(true);
+    if (v - lane < hi) batch(false);
     total = warp_sum(total);
     if (gone >= lo && gone < hi) {
       Sum<PARTS> s;
@@ -307,10 +304,12 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) verify_kernel(const VerifyA
 
 template <class T, bool SURE, int PARTS>
 cudaError_t launch(VerifyArgs& a, uint64_t n_requests, cudaStream_t stream) {
-  // as many blocks a request as fill 152 multiprocessors four times, none of
-  // fewer than 2048 tokens
+  // a block for each half of 152 multiprocessors' room at least, if with only 2048 tokens
+  // each; beyond that as long as a block has 16384 tokens, for its steps cost it as
+  // much time as some thousands of them (256 x 50001: two blocks a request 16 us, four 18;
+  // 512 x 131075: four 75 us, two 98)
   uint32_t blocks = 1;
-  while (blocks < CLUSTER && n_requests * blocks < 2432 && a.n_vocab / (blocks * 2) >= 2048) blocks *= 2;
+  while (blocks < CLUSTER && n_requests * blocks < 1025 && a.n_vocab / (blocks * 2) >= (n_requests * blocks < 304 ? 2048 : 16384)) blocks *= 2;
   a.blocks = blocks;
   a.part = ((a.n_vocab + blocks - 1) / blocks + 31) / 32 * 32;
   cudaLaunchAttribute at;
