@@ -24,7 +24,7 @@ using ppl::to_f;
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int TILE = PP_ADAMW_BLOCK, EACH = TILE / 32;  // elements of a warp and of a lane
-constexpr int BLOCKS = 8;                               // a multiprocessor
+constexpr int RESIDENT = 4, BLOCKS = 8;                               // a multiprocessor
 
 struct Item {
   void* param;
@@ -48,8 +48,9 @@ struct Common {
   const float* skip_at;
   float lr, b1, c1, b2, c2, eps;  // c: 1 - b, rounded once
   float log_b1, log_b2;
-  uint32_t n_items, n_tiles, seed;
+  uint32_t n_items, n_tiles, chunk, seed;
   int32_t nearest, last;
+  int32_t wide;  // the states lie at 32-byte addresses
 };
 
 template <int CAP>
@@ -69,29 +70,29 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ x >> 16;
 }
 
-// EACH values of a lane.  In a whole tile at 16-byte addresses a lane's are
+// EACH values of a lane.  In a whole tile at 32-byte addresses a lane's are
 // EACH consecutive ones; otherwise, element by element, those at lane, lane +
 // 32, ... so that a warp's accesses lie side by side.
+__device__ __forceinline__ void read_whole(const float* p, float* x) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void write_whole(float* p, const float* x) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]),
+               "f"(x[5]), "f"(x[6]), "f"(x[7]) : "memory");
+}
 template <class T>
 __device__ __forceinline__ void read_whole(const T* p, float* x) {
-  constexpr int N = 16 / sizeof(T);
+  const ppl::Pack<T, EACH> q = *reinterpret_cast<const ppl::Pack<T, EACH>*>(p);
 #pragma unroll
-  for (int k = 0; k < EACH; k += N) {
-    const ppl::Pack<T, N> q = *reinterpret_cast<const ppl::Pack<T, N>*>(p + k);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[k + i] = to_f(q.v[i]);
-  }
+  for (int i = 0; i < EACH; ++i) x[i] = to_f(q.v[i]);
 }
 template <class T>
 __device__ __forceinline__ void write_whole(T* p, const float* x) {
-  constexpr int N = 16 / sizeof(T);
+  ppl::Pack<T, EACH> q;
 #pragma unroll
-  for (int k = 0; k < EACH; k += N) {
-    ppl::Pack<T, N> q;
-#pragma unroll
-    for (int i = 0; i < N; ++i) q.v[i] = from_f<T>(x[k + i]);
-    *reinterpret_cast<ppl::Pack<T, N>*>(p + k) = q;
-  }
+  for (int i = 0; i < EACH; ++i) q.v[i] = from_f<T>(x[i]);
+  *reinterpret_cast<ppl::Pack<T, EACH>*>(p) = q;
 }
 template <class T>
 __device__ __forceinline__ void read(const T* p, bool whole, uint32_t lane, uint32_t n, float* x) {
@@ -128,35 +129,67 @@ __device__ __forceinline__ void write_any(void* p, int type, uint64_t at, bool w
 // (TOP 14), 5 for the square (TOP 30, no sign), 3 of mantissa; what underflows
 // the shifted field is a subnormal float and so a subnormal code.  A value
 // that rounds up from the largest still has a code.
+//
+// The shift is a product with a power of two.  One that is not a float (E above
+// TOP + 126, values of 2^(TOP - 1) and more) is split into two, which is rare enough
+// for loops of its own.
 constexpr int TOP_M = 14, TOP_V = 30;
 __device__ __forceinline__ float pow2(int field) { return __int_as_float(field << 23); }
+__device__ __forceinline__ uint32_t byte_of(uint2 c, int k) { return __byte_perm(k < 4 ? c.x : c.y, 0, 0x4440 | (k & 3)); }
 
 template <int TOP>
-__device__ __forceinline__ float decode(uint32_t code, float scale) {
-  const float x = __uint_as_float((TOP == TOP_M ? code & 127 : code) << 20) * pow2(254 - TOP) * scale;
-  return TOP == TOP_M && code > 127 ? -x : x;
-}
-__device__ __forceinline__ float scale_of(uint32_t e) { return e == 255 ? __int_as_float(0x7FC00000) : pow2(int(e)); }
-
-// A lane's codes, as 8 bytes; the tile's exponent in e.
-template <int TOP>
-__device__ __forceinline__ uint2 encode(const float* x, const uint32_t* random, uint32_t& e) {
-  uint32_t field = 1;
-#pragma unroll
-  for (int k = 0; k < EACH; ++k) field = max(field, __float_as_uint(x[k]) << 1 >> 24);
-  field = __reduce_max_sync(~0u, field);
-  e = field < 254 ? field : 255;
-  if (e == 255) return make_uint2(0, 0);
-  const float up = pow2(254 - int(field));
-  uint32_t w[2] = {0, 0};
+__device__ __forceinline__ void decode_all(uint2 c, uint32_t e, float* x) {
+  constexpr int MOST = TOP + 127;  // 2^(E - TOP) is a float up to here
+  const float scale = e == 255 ? __int_as_float(0x7FC00000) : e ? pow2(min(int(e), MOST) + 127 - TOP) : 0.f;
 #pragma unroll
   for (int k = 0; k < EACH; ++k) {
-    const float y = fabsf(x[k]) * up * pow2(TOP);
-    uint32_t c = (__float_as_uint(y) + random[k]) >> 20;
-    // a square never rounds to zero: the step divides by its root
-    if (TOP == TOP_V) c = x[k] > 0.f && c == 0 ? 1 : c;
-    else c |= x[k] < 0.f ? 128 : 0;
-    w[k / 4] |= c << (k % 4 * 8);
+    uint32_t bits;
+    if (TOP == TOP_M) {  // the code in the highest byte, its sign kept by the shift
+      const uint32_t high = __byte_perm(k < 4 ? c.x : c.y, 0, 0x0444 | (k & 3) << 12);
+      bits = uint32_t(int32_t(high) >> 4) & 0x87F00000u;
+    } else {
+      bits = byte_of(c, k) << 20;
+    }
+    x[k] = __uint_as_float(bits) * scale;
+  }
+  if (e > MOST && e != 255) {
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) x[k] *= pow2(int(e) - MOST + 127);
+  }
+}
+
+// A lane's codes, as 8 bytes; the tile's exponent in e.  x is lost.  random: 16
+// bits for each, or half a step.
+template <int TOP>
+__device__ __forceinline__ uint2 encode(float* x, const uint32_t* random, uint32_t& e) {
+  constexpr int MOST = TOP + 126;  // 2^(TOP - E) is a float up to here
+  uint32_t most = 0;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) most = max(most, TOP == TOP_M ? __float_as_uint(x[k]) * 2 : __float_as_uint(x[k]));
+  most = __reduce_max_sync(~0u, most);
+  const int field = max(int(TOP == TOP_M ? most >> 24 : most >> 23 & 255), 1);
+  e = field < 254 ? field : 255;
+  if (e == 255) return make_uint2(0, 0);
+  if (field > MOST) {
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) x[k] *= pow2(127 + MOST - field);
+  }
+  const float scale = pow2(127 + TOP - min(field, MOST));
+  // A multiply-add where an addition and a shift would do: logic runs at half the rate.
+  uint32_t y[EACH], t[EACH];
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    y[k] = __float_as_uint(x[k] * scale);
+    t[k] = random[k] * 16 + y[k];
+    if (TOP == TOP_V && x[k] > 0.f) t[k] = max(t[k], 1u << 20);  // a square never rounds to zero: the step divides by its root
+    t[k] *= 16;  // the code in the highest byte
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    w[k] = __byte_perm(__byte_perm(t[4 * k], t[4 * k + 1], 0x0073), __byte_perm(t[4 * k + 2], t[4 * k + 3], 0x0073), 0x5410);
+    if (TOP == TOP_M)  // seven bits; the eighth is the sign
+      w[k] |= 0x80808080u & __byte_perm(__byte_perm(y[4 * k], y[4 * k + 1], 0x0073), __byte_perm(y[4 * k + 2], y[4 * k + 3], 0x0073), 0x5410);
   }
   return make_uint2(w[0], w[1]);
 }
@@ -177,15 +210,17 @@ __device__ __forceinline__ void write_codes(uint8_t* p, bool whole, uint32_t lan
   for (int k = 0; k < EACH; ++k)
     if (lane + k * 32 < n) p[lane + k * 32] = uint8_t((k < 4 ? c.x : c.y) >> (k % 4 * 8));
 }
-template <int TOP>
-__device__ __forceinline__ void decode_all(uint2 c, uint32_t e, float* x) {
-  const float scale = scale_of(e);
-#pragma unroll
-  for (int k = 0; k < EACH; ++k) x[k] = decode<TOP>((k < 4 ? c.x : c.y) >> (k % 4 * 8) & 255, scale);
+
+// The square root and the quotient of the step are each within 2^-22 of their
+// values, as is the rate: what a parameter changes by is exact to 22 bits or so.
+__device__ __forceinline__ float root_of(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int BITS, int CAP>
-__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Args<CAP> a) {
+__global__ void __launch_bounds__(THREADS, RESIDENT) adamw_kernel(const __grid_constant__ Args<CAP> a) {
   const Common& c = a.c;
   if (c.skip_at && *c.skip_at != 0.f) return;
   const uint32_t lane = threadIdx.x % 32;
@@ -196,17 +231,21 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
   const float rate = lr / -expm1f(float(step) * c.log_b1);
   const float root = 1.f / sqrtf(-expm1f(float(step) * c.log_b2));
   const uint32_t key = mix(mix(c.seed) + uint32_t(step));
-  for (uint32_t tile = blockIdx.x * WARPS + threadIdx.x / 32; tile < c.n_tiles; tile += gridDim.x * WARPS) {
-    uint32_t i = 0;  // the last tensor that begins at or before the tile
-    for (uint32_t size = c.n_items; size > 1;) {
-      const uint32_t half = size / 2;
-      if (a.item[i + half].tile_begin <= tile) i += half;
-      size -= half;
-    }
+  // a block takes c.chunk tiles a turn, for which a tensor is looked up once
+  for (uint32_t chunk = blockIdx.x * c.chunk; chunk < c.n_tiles; chunk += gridDim.x * c.chunk) {
+   uint32_t i = 0;  // the last tensor that begins at or before the chunk
+   for (uint32_t size = c.n_items; size > 1;) {
+     const uint32_t half = size / 2;
+     if (a.item[i + half].tile_begin <= chunk) i += half;
+     size -= half;
+   }
+   const uint32_t stop = min(chunk + c.chunk, c.n_tiles);
+   for (uint32_t tile = chunk + threadIdx.x / 32; tile < stop; tile += WARPS) {
+    while (i + 1 < c.n_items && a.item[i + 1].tile_begin <= tile) ++i;
     const Item& t = a.item[i];
     const uint64_t at = uint64_t(tile - t.tile_begin) * TILE;
     const uint32_t n = uint32_t(t.n - at < TILE ? t.n - at : TILE);
-    const bool whole = n == TILE && reinterpret_cast<uintptr_t>(t.param) % 16 == 0 && reinterpret_cast<uintptr_t>(t.grad) % 16 == 0;
+    const bool whole = n == TILE && c.wide && (reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad)) % 32 == 0;
     const uint64_t s = t.first + at;
     float p[EACH], g[EACH], m[EACH], v[EACH];
     read_any(t.grad, t.grad_type, at, whole, lane, n, g);
@@ -226,7 +265,7 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
       // each product and sum rounded by itself: the states are the formula's, bit by bit
       m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(x, c.c1));
       v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(x, x), c.c2));
-      p[k] = p[k] * keep - rate * m[k] / (sqrtf(v[k]) * root + c.eps);
+      p[k] = p[k] * keep - __fdividef(rate * m[k], root_of(v[k]) * root + c.eps);
     }
     write_any(t.param, t.param_type, at, whole, lane, n, p);
     if (c.master) write(c.master + s, whole, lane, n, p);
@@ -235,16 +274,17 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
       write(static_cast<float*>(c.v) + s, whole, lane, n, v);
     } else {
       // 32 hashed bits an element, half for each state
-      const uint32_t low = uint32_t(s), high = mix(key + uint32_t(s >> 32));  // a tile does not cross 2^32
+      // places differ in other bits within a tile than its first, so they are joined by exclusive or
+      const uint32_t place = (uint32_t(s) | (whole ? lane * EACH : lane)) ^ mix(key + uint32_t(s >> 32));
       uint32_t rm[EACH], rv[EACH];
 #pragma unroll
       for (int k = 0; k < EACH; ++k) {
         if (c.nearest) {
-          rm[k] = rv[k] = 1u << 19;
+          rm[k] = rv[k] = 1u << 15;
         } else {
-          const uint32_t r = mix((low + (whole ? lane * EACH + k : lane + k * 32)) ^ high);
-          rm[k] = r >> 16 << 4;
-          rv[k] = (r & 0xFFFF) << 4;
+          const uint32_t r = mix(place ^ (whole ? k : k * 32));
+          rm[k] = r >> 16;
+          rv[k] = r & 0xFFFF;
         }
         if (!whole && lane + k * 32 >= n) m[k] = v[k] = 0.f;  // no part of the tile's exponents
       }
@@ -257,6 +297,7 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
         c.v_exp[s / TILE] = uint8_t(ev);
       }
     }
+   }
   }
   if (!c.last) return;
   // the block that is through last counts the step: by then every block has read the count
@@ -269,26 +310,26 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
 
 template <class T>
 __global__ void __launch_bounds__(THREADS) values_kernel(const uint8_t* m, const uint8_t* m_exp, const uint8_t* v,
-                                                         const uint8_t* v_exp, uint32_t n_tiles, T* m_out, T* v_out) {
+                                                         const uint8_t* v_exp, uint32_t n_tiles, bool wide, T* m_out, T* v_out) {
   const uint32_t lane = threadIdx.x % 32;
   for (uint32_t tile = blockIdx.x * WARPS + threadIdx.x / 32; tile < n_tiles; tile += gridDim.x * WARPS) {
     const uint64_t s = uint64_t(tile) * TILE;
     float x[EACH];
     if (m_out) {
-      decode_all<TOP_M>(read_codes(m + s, true, lane, TILE), m_exp[tile], x);
-      write(m_out + s, true, lane, TILE, x);
+      decode_all<TOP_M>(read_codes(m + s, wide, lane, TILE), m_exp[tile], x);
+      write(m_out + s, wide, lane, TILE, x);
     }
     if (v_out) {
-      decode_all<TOP_V>(read_codes(v + s, true, lane, TILE), v_exp[tile], x);
-      write(v_out + s, true, lane, TILE, x);
+      decode_all<TOP_V>(read_codes(v + s, wide, lane, TILE), v_exp[tile], x);
+      write(v_out + s, wide, lane, TILE, x);
     }
   }
 }
 
-cudaError_t grid_for(uint64_t tiles, unsigned* grid) {
+cudaError_t grid_for(uint64_t tiles, uint32_t each, unsigned* grid) {
   int sms;
   const cudaError_t e = ppi::sm_count(&sms);
-  *grid = unsigned(std::min<uint64_t>(std::max<uint64_t>((tiles + WARPS - 1) / WARPS, 1), uint64_t(sms) * BLOCKS));
+  *grid = unsigned(std::min<uint64_t>(std::max<uint64_t>((tiles + each - 1) / each, 1), uint64_t(sms) * BLOCKS));
   return e;
 }
 
@@ -298,7 +339,7 @@ cudaError_t launch(const Common& c, const Item* items, int bits, cudaStream_t st
   a.c = c;
   std::memcpy(a.item, items, c.n_items * sizeof(Item));
   unsigned grid;
-  const cudaError_t e = grid_for(c.n_tiles, &grid);
+  const cudaError_t e = grid_for(c.n_tiles, c.chunk, &grid);
   if (e != cudaSuccess) return e;
   if (bits == 32) adamw_kernel<32, CAP><<<grid, THREADS, 0, stream>>>(a);
   else adamw_kernel<8, CAP><<<grid, THREADS, 0, stream>>>(a);
@@ -352,6 +393,7 @@ extern "C" pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, cons
   c.log_b2 = float(std::log(o->beta2));
   c.seed = state->seed;
   c.nearest = state->nearest;
+  c.wide = ppl::aligned(c.m, 32) && ppl::aligned(c.v, 32) && ppl::aligned(c.master, 32);
   constexpr size_t MOST = 640;
   Item items[MOST];
   size_t i = 0;
@@ -367,6 +409,7 @@ extern "C" pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, cons
     }
     c.n_items = n;
     c.n_tiles = uint32_t(tiles);
+    c.chunk = tiles < 152 * BLOCKS * WARPS * 4 ? WARPS : WARPS * 4;
     c.last = i == n_tensors;
     const cudaError_t e = n <= 16 ? launch<16>(c, items, state->bits, stream)
                           : n <= 128 ? launch<128>(c, items, state->bits, stream)
@@ -384,12 +427,13 @@ extern "C" pp_rc pp_adamw_values(const pp_adamw_state* state, pp_ftype type, voi
   if (!state->n || (!d_exp_avg && !d_exp_avg_sq)) return PP_OK;
   const uint32_t tiles = uint32_t(state->n / TILE);
   unsigned grid;
-  const cudaError_t e = grid_for(tiles, &grid);
+  const cudaError_t e = grid_for(tiles, WARPS, &grid);
   if (e != cudaSuccess) return ppl::rc_of(e);
   const uint8_t* m = static_cast<const uint8_t*>(state->d_exp_avg);
   const uint8_t* v = static_cast<const uint8_t*>(state->d_exp_avg_sq);
+  const bool wide = ppl::aligned(d_exp_avg, 32) && ppl::aligned(d_exp_avg_sq, 32);
   auto go = [&](auto kernel, auto* mo, auto* vo) {
-    kernel<<<grid, THREADS, 0, stream>>>(m, state->d_exp_avg_exponent, v, state->d_exp_avg_sq_exponent, tiles, mo, vo);
+    kernel<<<grid, THREADS, 0, stream>>>(m, state->d_exp_avg_exponent, v, state->d_exp_avg_sq_exponent, tiles, wide, mo, vo);
   };
   switch (type) {
     case PP_F32: go(values_kernel<float>, static_cast<float*>(d_exp_avg), static_cast<float*>(d_exp_avg_sq)); break;
