@@ -94,31 +94,39 @@ __device__ __forceinline__ void write_whole(T* p, const float* x) {
   for (int i = 0; i < EACH; ++i) q.v[i] = from_f<T>(x[i]);
   *reinterpret_cast<ppl::Pack<T, EACH>*>(p) = q;
 }
-template <class T>
-__device__ __forceinline__ void read(const T* p, bool whole, uint32_t lane, uint32_t n, float* x) {
-  if (whole) return read_whole(p + lane * EACH, x);
+template <bool WHOLE, class T>
+__device__ __forceinline__ void read(const T* p, uint32_t lane, uint32_t n, float* x) {
+  if constexpr (WHOLE) {
+    read_whole(p + lane * EACH, x);
+  } else {
 #pragma unroll
-  for (int k = 0; k < EACH; ++k) x[k] = lane + k * 32 < n ? to_f(p[lane + k * 32]) : 0.f;
-}
-template <class T>
-__device__ __forceinline__ void write(T* p, bool whole, uint32_t lane, uint32_t n, const float* x) {
-  if (whole) return write_whole(p + lane * EACH, x);
-#pragma unroll
-  for (int k = 0; k < EACH; ++k)
-    if (lane + k * 32 < n) p[lane + k * 32] = from_f<T>(x[k]);
-}
-__device__ __forceinline__ void read_any(const void* p, int type, uint64_t at, bool whole, uint32_t lane, uint32_t n, float* x) {
-  switch (type) {
-    case PP_F32: return read(static_cast<const float*>(p) + at, whole, lane, n, x);
-    case PP_F16: return read(static_cast<const __half*>(p) + at, whole, lane, n, x);
-    default: return read(static_cast<const __nv_bfloat16*>(p) + at, whole, lane, n, x);
+    for (int k = 0; k < EACH; ++k) x[k] = lane + k * 32 < n ? to_f(p[lane + k * 32]) : 0.f;
   }
 }
-__device__ __forceinline__ void write_any(void* p, int type, uint64_t at, bool whole, uint32_t lane, uint32_t n, const float* x) {
+template <bool WHOLE, class T>
+__device__ __forceinline__ void write(T* p, uint32_t lane, uint32_t n, const float* x) {
+  if constexpr (WHOLE) {
+    write_whole(p + lane * EACH, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < EACH; ++k)
+      if (lane + k * 32 < n) p[lane + k * 32] = from_f<T>(x[k]);
+  }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void read_any(const void* p, int type, uint64_t at, uint32_t lane, uint32_t n, float* x) {
   switch (type) {
-    case PP_F32: return write(static_cast<float*>(p) + at, whole, lane, n, x);
-    case PP_F16: return write(static_cast<__half*>(p) + at, whole, lane, n, x);
-    default: return write(static_cast<__nv_bfloat16*>(p) + at, whole, lane, n, x);
+    case PP_F32: return read<WHOLE>(static_cast<const float*>(p) + at, lane, n, x);
+    case PP_F16: return read<WHOLE>(static_cast<const __half*>(p) + at, lane, n, x);
+    default: return read<WHOLE>(static_cast<const __nv_bfloat16*>(p) + at, lane, n, x);
+  }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void write_any(void* p, int type, uint64_t at, uint32_t lane, uint32_t n, const float* x) {
+  switch (type) {
+    case PP_F32: return write<WHOLE>(static_cast<float*>(p) + at, lane, n, x);
+    case PP_F16: return write<WHOLE>(static_cast<__half*>(p) + at, lane, n, x);
+    default: return write<WHOLE>(static_cast<__nv_bfloat16*>(p) + at, lane, n, x);
   }
 }
 
@@ -159,7 +167,7 @@ __device__ __forceinline__ void decode_all(uint2 c, uint32_t e, float* x) {
 }
 
 // A lane's codes, as 8 bytes; the tile's exponent in e.  x is lost.  random: 16
-// bits for each, or half a step.
+// bits (for the mean the high ones, for the square the low ones) for each, or half a step.
 template <int TOP>
 __device__ __forceinline__ uint2 encode(float* x, const uint32_t* random, uint32_t& e) {
   constexpr int MOST = TOP + 126;  // 2^(TOP - E) is a float up to here
@@ -180,7 +188,7 @@ __device__ __forceinline__ uint2 encode(float* x, const uint32_t* random, uint32
 #pragma unroll
   for (int k = 0; k < EACH; ++k) {
     y[k] = __float_as_uint(x[k] * scale);
-    t[k] = random[k] * 16 + y[k];
+    t[k] = (TOP == TOP_M ? random[k] >> 16 : random[k] & 0xFFFFu) * 16 + y[k];
     if (TOP == TOP_V && x[k] > 0.f) t[k] = max(t[k], 1u << 20);  // a square never rounds to zero: the step divides by its root
     t[k] *= 16;  // the code in the highest byte
   }
@@ -193,22 +201,27 @@ __device__ __forceinline__ uint2 encode(float* x, const uint32_t* random, uint32
   }
   return make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ uint2 read_codes(const uint8_t* p, bool whole, uint32_t lane, uint32_t n) {
-  if (whole) return *reinterpret_cast<const uint2*>(p + lane * EACH);
-  uint32_t w[2] = {0, 0};
+template <bool WHOLE>
+__device__ __forceinline__ uint2 read_codes(const uint8_t* p, uint32_t lane, uint32_t n) {
+  if constexpr (WHOLE) {
+    return *reinterpret_cast<const uint2*>(p + lane * EACH);
+  } else {
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int k = 0; k < EACH; ++k)
-    if (lane + k * 32 < n) w[k / 4] |= uint32_t(p[lane + k * 32]) << (k % 4 * 8);
-  return make_uint2(w[0], w[1]);
-}
-__device__ __forceinline__ void write_codes(uint8_t* p, bool whole, uint32_t lane, uint32_t n, uint2 c) {
-  if (whole) {
-    *reinterpret_cast<uint2*>(p + lane * EACH) = c;
-    return;
+    for (int k = 0; k < EACH; ++k)
+      if (lane + k * 32 < n) w[k / 4] |= uint32_t(p[lane + k * 32]) << (k % 4 * 8);
+    return make_uint2(w[0], w[1]);
   }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void write_codes(uint8_t* p, uint32_t lane, uint32_t n, uint2 c) {
+  if constexpr (WHOLE) {
+    *reinterpret_cast<uint2*>(p + lane * EACH) = c;
+  } else {
 #pragma unroll
-  for (int k = 0; k < EACH; ++k)
-    if (lane + k * 32 < n) p[lane + k * 32] = uint8_t((k < 4 ? c.x : c.y) >> (k % 4 * 8));
+    for (int k = 0; k < EACH; ++k)
+      if (lane + k * 32 < n) p[lane + k * 32] = uint8_t((k < 4 ? c.x : c.y) >> (k % 4 * 8));
+  }
 }
 
 // The square root and the quotient of the step are each within 2^-22 of their
@@ -219,85 +232,109 @@ __device__ __forceinline__ float root_of(float x) {
   return y;
 }
 
+struct Constants {
+  float lr, scale, rate, root;  // root: of 1 / (1 - beta2^t)
+  uint32_t key;
+};
+
+// One tile of n elements, at `at` of its tensor.
+template <int BITS, bool WHOLE>
+__device__ __forceinline__ void step_tile(const Common& c, const Constants& d, const Item& t, uint64_t at, uint32_t n) {
+  const uint32_t lane = threadIdx.x % 32;
+  const uint64_t s = t.first + at;
+  float p[EACH], g[EACH], m[EACH], v[EACH];
+  read_any<WHOLE>(t.grad, t.grad_type, at, lane, n, g);
+  if (BITS == 32) {
+    read<WHOLE>(static_cast<const float*>(c.m) + s, lane, n, m);
+    read<WHOLE>(static_cast<const float*>(c.v) + s, lane, n, v);
+  }
+  uint2 cm, cv;
+  uint32_t em, ev;
+  if (BITS == 8) {
+    cm = read_codes<WHOLE>(static_cast<const uint8_t*>(c.m) + s, lane, n);
+    cv = read_codes<WHOLE>(static_cast<const uint8_t*>(c.v) + s, lane, n);
+    em = c.m_exp[s / TILE];
+    ev = c.v_exp[s / TILE];
+  }
+  if (c.master) read<WHOLE>(c.master + s, lane, n, p);
+  else read_any<WHOLE>(t.param, t.param_type, at, lane, n, p);
+  if (BITS == 8) {
+    decode_all<TOP_M>(cm, em, m);
+    decode_all<TOP_V>(cv, ev, v);
+  }
+  const float keep = 1.f - d.lr * t.decay;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const float x = __fmul_rn(g[k], d.scale);
+    // each product and sum rounded by itself: the states are the formula's, bit by bit
+    m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(x, c.c1));
+    v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(x, x), c.c2));
+    p[k] = p[k] * keep - __fdividef(d.rate * m[k], root_of(v[k]) * d.root + c.eps);
+  }
+  write_any<WHOLE>(t.param, t.param_type, at, lane, n, p);
+  if (c.master) write<WHOLE>(c.master + s, lane, n, p);
+  if (BITS == 32) {
+    write<WHOLE>(static_cast<float*>(c.m) + s, lane, n, m);
+    write<WHOLE>(static_cast<float*>(c.v) + s, lane, n, v);
+    return;
+  }
+  uint32_t random[EACH];
+  if (c.nearest) {
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) random[k] = 0x80008000u;
+  } else {
+    // 32 hashed bits an element, half for each state; within a tile places differ in other bits than its
+    // first, so they are joined by exclusive or
+    const uint32_t place = (uint32_t(s) | (WHOLE ? lane * EACH : lane)) ^ mix(d.key + uint32_t(s >> 32));
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) random[k] = mix(place ^ (WHOLE ? k : k * 32));
+  }
+  if (!WHOLE) {
+#pragma unroll
+    for (int k = 0; k < EACH; ++k)
+      if (lane + k * 32 >= n) m[k] = v[k] = 0.f;  // no part of the tile's exponents
+  }
+  cm = encode<TOP_M>(m, random, em);
+  cv = encode<TOP_V>(v, random, ev);
+  write_codes<WHOLE>(static_cast<uint8_t*>(c.m) + s, lane, n, cm);
+  write_codes<WHOLE>(static_cast<uint8_t*>(c.v) + s, lane, n, cv);
+  if (lane == 0) {
+    c.m_exp[s / TILE] = uint8_t(em);
+    c.v_exp[s / TILE] = uint8_t(ev);
+  }
+}
+
 template <int BITS, int CAP>
 __global__ void __launch_bounds__(THREADS, RESIDENT) adamw_kernel(const __grid_constant__ Args<CAP> a) {
   const Common& c = a.c;
   if (c.skip_at && *c.skip_at != 0.f) return;
-  const uint32_t lane = threadIdx.x % 32;
   const int step = c.counters[0] + 1;
-  const float lr = c.lr_at ? *c.lr_at : c.lr;
-  const float scale = c.scale_at ? *c.scale_at : 1.f;
+  Constants d;
+  d.lr = c.lr_at ? *c.lr_at : c.lr;
+  d.scale = c.scale_at ? *c.scale_at : 1.f;
   // 1 - b^t without a difference of nearly equal numbers
-  const float rate = lr / -expm1f(float(step) * c.log_b1);
-  const float root = 1.f / sqrtf(-expm1f(float(step) * c.log_b2));
-  const uint32_t key = mix(mix(c.seed) + uint32_t(step));
+  d.rate = d.lr / -expm1f(float(step) * c.log_b1);
+  d.root = 1.f / sqrtf(-expm1f(float(step) * c.log_b2));
+  d.key = mix(mix(c.seed) + uint32_t(step));
   // a block takes c.chunk tiles a turn, for which a tensor is looked up once
   for (uint32_t chunk = blockIdx.x * c.chunk; chunk < c.n_tiles; chunk += gridDim.x * c.chunk) {
-   uint32_t i = 0;  // the last tensor that begins at or before the chunk
-   for (uint32_t size = c.n_items; size > 1;) {
-     const uint32_t half = size / 2;
-     if (a.item[i + half].tile_begin <= chunk) i += half;
-     size -= half;
-   }
-   const uint32_t stop = min(chunk + c.chunk, c.n_tiles);
-   for (uint32_t tile = chunk + threadIdx.x / 32; tile < stop; tile += WARPS) {
-    while (i + 1 < c.n_items && a.item[i + 1].tile_begin <= tile) ++i;
-    const Item& t = a.item[i];
-    const uint64_t at = uint64_t(tile - t.tile_begin) * TILE;
-    const uint32_t n = uint32_t(t.n - at < TILE ? t.n - at : TILE);
-    const bool whole = n == TILE && c.wide && (reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad)) % 32 == 0;
-    const uint64_t s = t.first + at;
-    float p[EACH], g[EACH], m[EACH], v[EACH];
-    read_any(t.grad, t.grad_type, at, whole, lane, n, g);
-    if (c.master) read(c.master + s, whole, lane, n, p);
-    else read_any(t.param, t.param_type, at, whole, lane, n, p);
-    if (BITS == 32) {
-      read(static_cast<const float*>(c.m) + s, whole, lane, n, m);
-      read(static_cast<const float*>(c.v) + s, whole, lane, n, v);
-    } else {
-      decode_all<TOP_M>(read_codes(static_cast<const uint8_t*>(c.m) + s, whole, lane, n), c.m_exp[s / TILE], m);
-      decode_all<TOP_V>(read_codes(static_cast<const uint8_t*>(c.v) + s, whole, lane, n), c.v_exp[s / TILE], v);
+    uint32_t i = 0;  // the last tensor that begins at or before the chunk
+    for (uint32_t size = c.n_items; size > 1;) {
+      const uint32_t half = size / 2;
+      if (a.item[i + half].tile_begin <= chunk) i += half;
+      size -= half;
     }
-    const float keep = 1.f - lr * t.decay;
-#pragma unroll
-    for (int k = 0; k < EACH; ++k) {
-      const float x = __fmul_rn(g[k], scale);
-      // each product and sum rounded by itself: the states are the formula's, bit by bit
-      m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(x, c.c1));
-      v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(x, x), c.c2));
-      p[k] = p[k] * keep - __fdividef(rate * m[k], root_of(v[k]) * root + c.eps);
+    const uint32_t stop = min(chunk + c.chunk, c.n_tiles);
+    for (uint32_t tile = chunk + threadIdx.x / 32; tile < stop; tile += WARPS) {
+      while (i + 1 < c.n_items && a.item[i + 1].tile_begin <= tile) ++i;
+      const Item& t = a.item[i];
+      const uint64_t at = uint64_t(tile - t.tile_begin) * TILE;
+      const uint32_t n = uint32_t(t.n - at < TILE ? t.n - at : TILE);
+      if (n == TILE && c.wide && (reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad)) % 32 == 0)
+        step_tile<BITS, true>(c, d, t, at, n);
+      else
+        step_tile<BITS, false>(c, d, t, at, n);
     }
-    write_any(t.param, t.param_type, at, whole, lane, n, p);
-    if (c.master) write(c.master + s, whole, lane, n, p);
-    if (BITS == 32) {
-      write(static_cast<float*>(c.m) + s, whole, lane, n, m);
-      write(static_cast<float*>(c.v) + s, whole, lane, n, v);
-    } else {
-      // 32 hashed bits an element, half for each state
-      // places differ in other bits within a tile than its first, so they are joined by exclusive or
-      const uint32_t place = (uint32_t(s) | (whole ? lane * EACH : lane)) ^ mix(key + uint32_t(s >> 32));
-      uint32_t rm[EACH], rv[EACH];
-#pragma unroll
-      for (int k = 0; k < EACH; ++k) {
-        if (c.nearest) {
-          rm[k] = rv[k] = 1u << 15;
-        } else {
-          const uint32_t r = mix(place ^ (whole ? k : k * 32));
-          rm[k] = r >> 16;
-          rv[k] = r & 0xFFFF;
-        }
-        if (!whole && lane + k * 32 >= n) m[k] = v[k] = 0.f;  // no part of the tile's exponents
-      }
-      uint32_t em, ev;
-      const uint2 cm = encode<TOP_M>(m, rm, em), cv = encode<TOP_V>(v, rv, ev);
-      write_codes(static_cast<uint8_t*>(c.m) + s, whole, lane, n, cm);
-      write_codes(static_cast<uint8_t*>(c.v) + s, whole, lane, n, cv);
-      if (lane == 0) {
-        c.m_exp[s / TILE] = uint8_t(em);
-        c.v_exp[s / TILE] = uint8_t(ev);
-      }
-    }
-   }
   }
   if (!c.last) return;
   // the block that is through last counts the step: by then every block has read the count
@@ -308,20 +345,20 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) adamw_kernel(const __grid_c
   }
 }
 
-template <class T>
+template <class T, bool WHOLE>
 __global__ void __launch_bounds__(THREADS) values_kernel(const uint8_t* m, const uint8_t* m_exp, const uint8_t* v,
-                                                         const uint8_t* v_exp, uint32_t n_tiles, bool wide, T* m_out, T* v_out) {
+                                                         const uint8_t* v_exp, uint32_t n_tiles, T* m_out, T* v_out) {
   const uint32_t lane = threadIdx.x % 32;
   for (uint32_t tile = blockIdx.x * WARPS + threadIdx.x / 32; tile < n_tiles; tile += gridDim.x * WARPS) {
     const uint64_t s = uint64_t(tile) * TILE;
     float x[EACH];
     if (m_out) {
-      decode_all<TOP_M>(read_codes(m + s, wide, lane, TILE), m_exp[tile], x);
-      write(m_out + s, wide, lane, TILE, x);
+      decode_all<TOP_M>(read_codes<WHOLE>(m + s, lane, TILE), m_exp[tile], x);
+      write<WHOLE>(m_out + s, lane, TILE, x);
     }
     if (v_out) {
-      decode_all<TOP_V>(read_codes(v + s, wide, lane, TILE), v_exp[tile], x);
-      write(v_out + s, wide, lane, TILE, x);
+      decode_all<TOP_V>(read_codes<WHOLE>(v + s, lane, TILE), v_exp[tile], x);
+      write<WHOLE>(v_out + s, lane, TILE, x);
     }
   }
 }
@@ -433,12 +470,12 @@ extern "C" pp_rc pp_adamw_values(const pp_adamw_state* state, pp_ftype type, voi
   const uint8_t* v = static_cast<const uint8_t*>(state->d_exp_avg_sq);
   const bool wide = ppl::aligned(d_exp_avg, 32) && ppl::aligned(d_exp_avg_sq, 32);
   auto go = [&](auto kernel, auto* mo, auto* vo) {
-    kernel<<<grid, THREADS, 0, stream>>>(m, state->d_exp_avg_exponent, v, state->d_exp_avg_sq_exponent, tiles, wide, mo, vo);
+    kernel<<<grid, THREADS, 0, stream>>>(m, state->d_exp_avg_exponent, v, state->d_exp_avg_sq_exponent, tiles, mo, vo);
   };
   switch (type) {
-    case PP_F32: go(values_kernel<float>, static_cast<float*>(d_exp_avg), static_cast<float*>(d_exp_avg_sq)); break;
-    case PP_F16: go(values_kernel<__half>, static_cast<__half*>(d_exp_avg), static_cast<__half*>(d_exp_avg_sq)); break;
-    default: go(values_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(d_exp_avg), static_cast<__nv_bfloat16*>(d_exp_avg_sq)); break;
+    case PP_F32: go(wide ? values_kernel<float, true> : values_kernel<float, false>, static_cast<float*>(d_exp_avg), static_cast<float*>(d_exp_avg_sq)); break;
+    case PP_F16: go(wide ? values_kernel<__half, true> : values_kernel<__half, false>, static_cast<__half*>(d_exp_avg), static_cast<__half*>(d_exp_avg_sq)); break;
+    default: go(wide ? values_kernel<__nv_bfloat16, true> : values_kernel<__nv_bfloat16, false>, static_cast<__nv_bfloat16*>(d_exp_avg), static_cast<__nv_bfloat16*>(d_exp_avg_sq)); break;
   }
   return ppl::rc_of(cudaGetLastError());
 }
