@@ -130,6 +130,22 @@ __device__ __forceinline__ void write_any(void* p, int type, uint64_t at, uint32
   }
 }
 
+// Two floats at a time.
+struct Two {
+  unsigned long long v;
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
+  return a;
+}
+
 // ------------------------------------------------------------ 8-bit states
 // A tile's values share the exponent E (a float's exponent field) of their
 // largest magnitude.  A code is the top of the float whose exponent field is
@@ -158,8 +174,10 @@ __device__ __forceinline__ void decode_all(uint2 c, uint32_t e, float* x) {
     } else {
       bits = byte_of(c, k) << 20;
     }
-    x[k] = __uint_as_float(bits) * scale;
+    x[k] = __uint_as_float(bits);
   }
+#pragma unroll
+  for (int k = 0; k < EACH; k += 2) (Two(x[k], x[k + 1]) * Two(scale)).get(x[k], x[k + 1]);
   if (e > MOST && e != 255) {
 #pragma unroll
     for (int k = 0; k < EACH; ++k) x[k] *= pow2(int(e) - MOST + 127);
@@ -186,8 +204,14 @@ __device__ __forceinline__ uint2 encode(float* x, const uint32_t* random, uint32
   // A multiply-add where an addition and a shift would do: logic runs at half the rate.
   uint32_t y[EACH], t[EACH];
 #pragma unroll
+  for (int k = 0; k < EACH; k += 2) {
+    float a, b;
+    (Two(x[k], x[k + 1]) * Two(scale)).get(a, b);
+    y[k] = __float_as_uint(a);
+    y[k + 1] = __float_as_uint(b);
+  }
+#pragma unroll
   for (int k = 0; k < EACH; ++k) {
-    y[k] = __float_as_uint(x[k] * scale);
     t[k] = (TOP == TOP_M ? random[k] >> 16 : random[k] & 0xFFFFu) * 16 + y[k];
     if (TOP == TOP_V && x[k] > 0.f) t[k] = max(t[k], 1u << 20);  // a square never rounds to zero: the step divides by its root
     t[k] *= 16;  // the code in the highest byte
@@ -258,18 +282,38 @@ __device__ __forceinline__ void step_tile(const Common& c, const Constants& d, c
   }
   if (c.master) read<WHOLE>(c.master + s, lane, n, p);
   else read_any<WHOLE>(t.param, t.param_type, at, lane, n, p);
+  if (BITS == 8 && WHOLE && at + (WARPS + 1) * TILE <= t.n) {
+    // the warp's next tile on its way to the cache: registers for it would cost warps
+    constexpr uint32_t NEXT = WARPS * TILE;
+    const uint32_t i = NEXT + lane * EACH;
+    auto fetch = [](const void* q) { asm volatile("prefetch.global.L2 [%0];" ::"l"(q)); };
+    fetch(static_cast<const char*>(t.grad) + (at + i) * (t.grad_type == PP_F32 ? 4 : 2));
+    fetch(c.master ? reinterpret_cast<const char*>(c.master + s + i) : static_cast<const char*>(t.param) + (at + i) * (t.param_type == PP_F32 ? 4 : 2));
+    fetch(static_cast<const uint8_t*>(c.m) + s + i);
+    fetch(static_cast<const uint8_t*>(c.v) + s + i);
+  }
   if (BITS == 8) {
     decode_all<TOP_M>(cm, em, m);
     decode_all<TOP_V>(cv, ev, v);
   }
   const float keep = 1.f - d.lr * t.decay;
 #pragma unroll
-  for (int k = 0; k < EACH; ++k) {
-    const float x = __fmul_rn(g[k], d.scale);
+  for (int k = 0; k < EACH; k += 2) {
+    const Two x = Two(g[k], g[k + 1]) * Two(d.scale);
     // each product and sum rounded by itself: the states are the formula's, bit by bit
-    m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(x, c.c1));
-    v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(x, x), c.c2));
-    p[k] = p[k] * keep - __fdividef(d.rate * m[k], root_of(v[k]) * d.root + c.eps);
+    // (sums by themselves: two packed ones become a fused one)
+    float more[2], above[2], below[2];
+    (Two(m[k], m[k + 1]) * Two(c.b1)).get(m[k], m[k + 1]);
+    (x * Two(c.c1)).get(more[0], more[1]);
+    m[k] = __fadd_rn(m[k], more[0]);
+    m[k + 1] = __fadd_rn(m[k + 1], more[1]);
+    (Two(v[k], v[k + 1]) * Two(c.b2)).get(v[k], v[k + 1]);
+    (x * x * Two(c.c2)).get(more[0], more[1]);
+    v[k] = __fadd_rn(v[k], more[0]);
+    v[k + 1] = __fadd_rn(v[k + 1], more[1]);
+    (Two(m[k], m[k + 1]) * Two(-d.rate)).get(above[0], above[1]);
+    fma2(Two(root_of(v[k]), root_of(v[k + 1])), Two(d.root), Two(c.eps)).get(below[0], below[1]);
+    fma2(Two(p[k], p[k + 1]), Two(keep), Two(__fdividef(above[0], below[0]), __fdividef(above[1], below[1]))).get(p[k], p[k + 1]);
   }
   write_any<WHOLE>(t.param, t.param_type, at, lane, n, p);
   if (c.master) write<WHOLE>(c.master + s, lane, n, p);
@@ -446,7 +490,9 @@ extern "C" pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, cons
     }
     c.n_items = n;
     c.n_tiles = uint32_t(tiles);
-    c.chunk = tiles < 152 * BLOCKS * WARPS * 4 ? WARPS : WARPS * 4;
+    // up to 16 tiles a warp and turn, and eight turns a resident block: the next tile of a turn is
+    // fetched ahead (185M elements, 8 bits: 634 us, and 660 with turns of 4 tiles)
+    c.chunk = uint32_t(std::min<uint64_t>(std::max<uint64_t>(tiles / (152 * RESIDENT * 8 * WARPS), 1), 16)) * WARPS;
     c.last = i == n_tensors;
     const cudaError_t e = n <= 16 ? launch<16>(c, items, state->bits, stream)
                           : n <= 128 ? launch<128>(c, items, state->bits, stream)
