@@ -1,7 +1,8 @@
 /* Argument marshalling of the language-model entry points for Python: a
  * call whose kernel takes two microseconds should not spend fifteen on its
- * arguments.  vec() checks a tensor and gives its address; the others take
- * plain numbers and call libpp, whose functions init() is given (lm.py). */
+ * arguments.  vec() checks a tensor and gives its address; token_probs,
+ * verify_drafts and adamw check the tensors that they take, the others take
+ * plain numbers; all call libpp, whose functions init() is given (lm.py). */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -16,8 +17,8 @@ static __typeof__(&pp_embed_grad_scratch) f_scratch;
 static __typeof__(&pp_token_probs) f_probs;
 static __typeof__(&pp_verify_drafts) f_verify;
 static __typeof__(&pp_adamw) f_adamw;
-static PyObject* ftypes[3];  /* the dtypes of pp_ftype, from types() */
-static PyObject *s_is_leaf, *s_dtype, *s_get_device, *s_numel, *s_is_contiguous, *s_dim, *s_data_ptr;
+static PyObject *ftypes[3], *itypes[4];  /* the dtypes of pp_ftype and pp_itype, from types() */
+static PyObject *s_is_leaf, *s_shape, *s_stride, *s_dtype, *s_get_device, *s_numel, *s_is_contiguous, *s_dim, *s_data_ptr;
 
 /* a method without arguments that gives an integer; -1 and an error set on failure */
 static long long ask(PyObject* t, PyObject* name) {
@@ -58,6 +59,65 @@ static int numbers(PyObject* const* a, Py_ssize_t n, long long* v, Py_ssize_t re
     if (i == real) *x = PyFloat_AsDouble(a[i]);
     else v[i] = PyLong_AsLongLong(a[i]);
   }
+  return !PyErr_Occurred();
+}
+
+static PyObject* bad(const char* what) {
+  PyErr_SetString(PyExc_ValueError, what);
+  return NULL;
+}
+
+/* the place of a tensor's dtype among n, or -1 */
+static int kind(PyObject* t, PyObject** dtypes, int n) {
+  PyObject* dtype = PyObject_GetAttr(t, s_dtype);
+  if (!dtype) return -1;
+  int k = n - 1;
+  while (k >= 0 && dtype != dtypes[k]) --k;
+  Py_DECREF(dtype);
+  return k;
+}
+
+struct matrix {
+  void* p;
+  int type;
+  long long rows, cols, stride;
+};
+
+/* a matrix of one of n dtypes on the device, with contiguous rows; ValueError for anything else */
+static int matrix(PyObject* t, PyObject** dtypes, int n, long long device, const char* name, struct matrix* m) {
+  m->type = kind(t, dtypes, n);
+  if (PyErr_Occurred()) return 0;
+  PyObject *shape = PyObject_GetAttr(t, s_shape), *stride = shape ? PyObject_CallMethodNoArgs(t, s_stride) : NULL;
+  int ok = shape && stride && m->type >= 0 && ask(t, s_get_device) == device && PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 2 &&
+           PyTuple_Check(stride) && PyTuple_GET_SIZE(stride) == 2;
+  if (ok) {
+    m->rows = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
+    m->cols = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
+    m->stride = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 0));
+    m->p = (void*)(uintptr_t)ask(t, s_data_ptr);
+    ok = m->cols <= 1 || m->rows == 0 || PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1)) == 1;
+  }
+  Py_XDECREF(shape);
+  Py_XDECREF(stride);
+  if (!ok && !PyErr_Occurred()) {
+    PyErr_Format(PyExc_ValueError, "%s: want 2 dimensions, the last contiguous, of %S%s on the other tensors' device, got %S", name, dtypes[0],
+                 n > 1 ? " (or another of its kind)" : "", t);
+    return 0;
+  }
+  return !PyErr_Occurred();
+}
+
+/* the address of a contiguous vector of at least n elements, NULL for None; ValueError for anything else */
+static int vector(PyObject* t, PyObject* dtype, long long device, long long n, const char* name, void** p) {
+  *p = NULL;
+  if (t == Py_None) return 1;
+  const int ok = kind(t, &dtype, 1) == 0 && ask(t, s_get_device) == device && ask(t, s_dim) == 1 && ask(t, s_numel) >= n && ask(t, s_is_contiguous) == 1;
+  if (PyErr_Occurred()) return 0;
+  if (!ok) {
+    PyErr_Format(PyExc_ValueError, "%s: want %lld contiguous elements of %S on the other tensors' device", name, n, dtype);
+    return 0;
+  }
+  *p = (void*)(uintptr_t)ask(t, s_data_ptr);
   return !PyErr_Occurred();
 }
 
@@ -109,34 +169,51 @@ static PyObject* embed_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
               v[10], (int)v[11], PTR(12), (pp_ftype)v[13], SIZE(14), PTR(15), SIZE(16), PTR(17)));
 }
 
+/* logits, temperature, top_k, out, stream: a result of the logits' shape */
 static PyObject* token_probs(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  long long v[10];
-  if (!want(n, 10) || !numbers(a, n, v, -1, NULL)) return NULL;
-  CALL(f_probs(PTR(0), (pp_ftype)v[1], SIZE(2), SIZE(3), SIZE(4), PTR(5), PTR(6), PTR(7), SIZE(8), PTR(9)));
+  if (!want(n, 5)) return NULL;
+  const long long device = ask(a[0], s_get_device), stream = PyLong_AsLongLong(a[4]);
+  struct matrix x, p;
+  void *t, *k;
+  if (PyErr_Occurred() || !matrix(a[0], ftypes, 3, device, "logits", &x) || !matrix(a[3], ftypes, 1, device, "out", &p)) return NULL;
+  if (p.rows != x.rows || p.cols != x.cols) return bad("out: want the shape of the logits");
+  if (!vector(a[1], ftypes[0], device, x.rows, "temperature", &t) || !vector(a[2], itypes[2], device, x.rows, "top_k", &k)) return NULL;
+  CALL(f_probs(x.p, (pp_ftype)x.type, x.rows, x.cols, x.stride, t, k, p.p, p.stride, (cudaStream_t)(uintptr_t)stream));
 }
 
-/* pp_verify_drafts' arguments, with the six fields of pp_draft_opts in its place */
+/* target, drafts, accept, sample, draft_probs, lengths, target_row, draft_row, tokens, counts, stream */
 static PyObject* verify_drafts(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  long long v[23];
-  if (!want(n, 23) || !numbers(a, n, v, -1, NULL)) return NULL;
-  const pp_draft_opts o = {PTR(13), PTR(14), SIZE(15), SIZE(16), PTR(17), PTR(18)};
-  CALL(f_verify(PTR(0), (pp_ftype)v[1], SIZE(2), SIZE(3), SIZE(4), PTR(5), (pp_itype)v[6], SIZE(7), SIZE(8), SIZE(9),
-                PTR(10), SIZE(11), PTR(12), &o, PTR(19), SIZE(20), PTR(21), PTR(22)));
-}
-
-/* the pp_ftype of a tensor, or -1 */
-static int ftype(PyObject* t) {
-  PyObject* dtype = PyObject_GetAttr(t, s_dtype);
-  if (!dtype) return -1;
-  int k = 2;
-  while (k >= 0 && dtype != ftypes[k]) --k;
-  Py_DECREF(dtype);
-  return k;
+  if (!want(n, 11)) return NULL;
+  const long long device = ask(a[0], s_get_device), stream = PyLong_AsLongLong(a[10]);
+  struct matrix p, d, u, q = {NULL, 0, 0, 0, 0}, out;
+  void *sample, *lengths, *row, *qrow, *counts;
+  if (PyErr_Occurred() || !matrix(a[0], ftypes, 3, device, "target", &p) || !matrix(a[1], itypes, 4, device, "drafts", &d) ||
+      !matrix(a[2], ftypes, 1, device, "accept", &u) || !matrix(a[8], itypes + 2, 1, device, "out", &out))
+    return NULL;
+  const long long many = d.rows, drafts = d.cols;
+  if (p.cols < 1) return bad("target: want a token at least");
+  if (u.rows != many || u.cols != drafts) return bad("accept: want a number for each draft");
+  if (out.rows != many || out.cols != drafts + 1) return bad("out: want tokens, one column more than drafts, and a count for each request");
+  if (a[6] == Py_None && p.rows < many * (drafts + 1)) return bad("target: want a row for each draft and one more a request");
+  if (a[4] != Py_None) {
+    if (!matrix(a[4], ftypes + p.type, 1, device, "draft_probs", &q)) return NULL;
+    if (q.cols != p.cols) return bad("draft_probs: want the target's vocabulary");
+    if (a[7] == Py_None && q.rows < many * drafts) return bad("draft_probs: want a row for each draft");
+    if (!q.p) q.p = p.p; /* no rows have no address, and are still not those of sure drafts */
+  }
+  if (!vector(a[3], ftypes[0], device, many, "sample", &sample) || !vector(a[5], itypes[2], device, many, "lengths", &lengths) ||
+      !vector(a[6], itypes[2], device, many, "target_row", &row) || !vector(a[7], itypes[2], device, many, "draft_row", &qrow) ||
+      !vector(a[9], itypes[2], device, many, "out's counts", &counts))
+    return NULL;
+  if (!sample && many) return bad("sample: want a number for each request");
+  const pp_draft_opts o = {q.p, qrow, q.rows, q.stride, row, lengths};
+  CALL(f_verify(p.p, (pp_ftype)p.type, p.rows, p.cols, p.stride, d.p, (pp_itype)d.type, many, drafts, d.stride, u.p, u.stride, sample,
+                &o, out.p, out.stride, counts, (cudaStream_t)(uintptr_t)stream));
 }
 
 /* a contiguous floating tensor of n elements on the device: its address and type */
 static int tensor_of(PyObject* t, long long device, unsigned long long n, void** p, int32_t* type) {
-  *type = ftype(t);
+  *type = kind(t, ftypes, 3);
   if (*type < 0) return 0;
   if (ask(t, s_get_device) != device || (unsigned long long)ask(t, s_numel) != n || ask(t, s_is_contiguous) != 1) return 0;
   *p = (void*)(uintptr_t)ask(t, s_data_ptr);
@@ -234,10 +311,11 @@ done:
 }
 
 static PyObject* types(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (!want(n, 3)) return NULL;
-  for (int k = 0; k < 3; ++k) {
+  if (!want(n, 7)) return NULL;
+  for (int k = 0; k < 7; ++k) {
     Py_INCREF(a[k]);
-    Py_XSETREF(ftypes[k], a[k]);
+    if (k < 3) Py_XSETREF(ftypes[k], a[k]);
+    else Py_XSETREF(itypes[k - 3], a[k]);
   }
   Py_RETURN_NONE;
 }
@@ -272,12 +350,14 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "pp_bind", NULL, -1, 
 
 PyMODINIT_FUNC PyInit_pp_bind(void) {
   s_is_leaf = PyUnicode_InternFromString("is_leaf");
+  s_shape = PyUnicode_InternFromString("shape");
+  s_stride = PyUnicode_InternFromString("stride");
   s_dtype = PyUnicode_InternFromString("dtype");
   s_get_device = PyUnicode_InternFromString("get_device");
   s_numel = PyUnicode_InternFromString("numel");
   s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
   s_dim = PyUnicode_InternFromString("dim");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  if (!s_is_leaf || !s_dtype || !s_get_device || !s_numel || !s_is_contiguous || !s_dim || !s_data_ptr) return NULL;
+  if (!s_is_leaf || !s_shape || !s_stride || !s_dtype || !s_get_device || !s_numel || !s_is_contiguous || !s_dim || !s_data_ptr) return NULL;
   return PyModule_Create(&module);
 }

@@ -787,13 +787,13 @@ extern "C" pp_rc pp_token_probs(const void* d_logits, pp_ftype type, size_t n_ro
                                 size_t logits_stride, const float* d_temperature, const int32_t* d_top_k,
                                 float* d_probs, size_t probs_stride, cudaStream_t stream) {
   if (!ppl::ftype_ok(type)) return PP_EINVAL;
-  if (n_rows && n_vocab && (!d_logits || !d_probs)) return PP_EINVAL;
-  if (n_rows > 1 && (probs_stride < n_vocab || (d_logits == d_probs && logits_stride != probs_stride))) return PP_EINVAL;
-  if (d_logits && d_logits == d_probs && type != PP_F32) return PP_EINVAL;
-  if (!ppl::aligned(d_logits, ppl::fsize(type)) || !ppl::aligned(d_probs, 4) || !ppl::aligned(d_temperature, 4) || !ppl::aligned(d_top_k, 4))
-    return PP_EINVAL;
   if (n_rows >= ppl::MAX_DIM / CLUSTER || n_vocab >= (size_t(1) << 30)) return PP_ETOOLARGE;
   if (!n_rows || !n_vocab) return PP_OK;
+  if (!d_logits || !d_probs) return PP_EINVAL;
+  if (n_rows > 1 && (probs_stride < n_vocab || (d_logits == d_probs && logits_stride != probs_stride))) return PP_EINVAL;
+  if (d_logits == d_probs && type != PP_F32) return PP_EINVAL;
+  if (!ppl::aligned(d_logits, ppl::fsize(type)) || !ppl::aligned(d_probs, 4) || !ppl::aligned(d_temperature, 4) || !ppl::aligned(d_top_k, 4))
+    return PP_EINVAL;
   ProbArgs a;
   std::memset(&a, 0, sizeof a);
   a.in = d_logits;

@@ -9,8 +9,8 @@
   pp_embed_grad / embed_grad          the gradient for the table (both differentiable)
 
 Argument marshalling only, as in the rest of the binding: shapes and types
-are checked here (the vectors' in pp_bind, whose calls also take less of the
-time than ctypes'), everything is computed by libpp's kernels on the given
+are checked here (or in pp_bind, whose calls also take less of the time than
+ctypes'), everything is computed by libpp's kernels on the given
 stream (default: the current one).  New outputs belong to that stream; the
 caller orders the use of every tensor on other streams, as with any kernel
 launch.  Result tensors that are given count as written to in place: they may
@@ -100,7 +100,7 @@ def _load():
     bind.init(*[ctypes.cast(getattr(L, "pp_" + name), _vp).value
                 for name in ("vocab_grammar", "grammar_states", "logits", "embed", "embed_grad_noalloc", "embed_grad_scratch",
                               "token_probs", "verify_drafts", "adamw")])
-    bind.types(*FTYPE)  # in the order of their numbers
+    bind.types(*FTYPE, *ITYPE)  # in the order of their numbers
     _c = bind
     return bind
 
@@ -351,23 +351,11 @@ def token_probs(logits: torch.Tensor, temperature=None, top_k=None, out=None, st
         if followed:
             _need(out is None, "out: not for values that require a gradient")
             return _Underived.apply(token_probs, (logits, temperature, top_k, None, stream), *followed)
-    _need(logits.dtype in FTYPE and logits.dim() == 2, "logits: want 2 dimensions of float32, float16 or bfloat16")
-    rows, vocab = logits.shape
-    dev, c = logits.get_device(), _lib()
-    given = out
     if out is None:
-        out = _new((rows, vocab), torch.float32, logits, stream)
+        out = _new(logits.shape, torch.float32, logits, stream)
     else:
-        _on(out, logits, "out", (torch.float32,), 2)
-        _need(out.shape == logits.shape, "out: want the shape of the logits")
-    t = c.vec(temperature, torch.float32, dev, rows, "temperature")
-    k = c.vec(top_k, torch.int32, dev, rows, "top_k")
-    if rows and vocab:
-        stride, ostride = _matrix_stride(logits, "logits"), _matrix_stride(out, "out")
-        if given is not None:
-            _written(out)
-        _call(c.token_probs, "pp_token_probs", logits, stream, logits.data_ptr(), FTYPE[logits.dtype], rows, vocab,
-              stride, t, k, out.data_ptr(), ostride)
+        _written(out)
+    _call(_lib().token_probs, "pp_token_probs", logits, stream, logits, temperature, top_k, out)
     return out
 
 
@@ -383,42 +371,16 @@ def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, accept: torch.Tens
     for drafts without a choice; lengths: int32 [n], the drafts of each request
     that count; accept: float32 [n, k] and sample: float32 [n], random numbers
     in [0, 1).  out: (tokens, counts) to write to."""
-    _need(target.dtype in FTYPE and target.dim() == 2 and target.size(1) > 0,
-          "target: want 2 dimensions of float32, float16 or bfloat16, and a token at least")
-    _on(drafts, target, "drafts", ITYPE, 2)
-    _on(accept, target, "accept", (torch.float32,), 2)
     n, k = drafts.shape
-    _need(accept.shape == drafts.shape, "accept: want a number for each draft")
-    dev, i32, c = target.get_device(), torch.int32, _lib()
-    rows, vocab = target.shape
-    _need(target_row is not None or rows >= n * (k + 1), "target: want a row for each draft and one more a request")
-    probs = (0, 0, 0, 0)
-    if draft_probs is not None:
-        _on(draft_probs, target, "draft_probs", (target.dtype,), 2)
-        _need(draft_probs.size(1) == vocab, "draft_probs: want the target's vocabulary")
-        _need(draft_row is not None or draft_probs.size(0) >= n * k, "draft_probs: want a row for each draft")
-        # rows of no tokens have no address, and are still not those of sure drafts
-        probs = (draft_probs.data_ptr() or target.data_ptr(), c.vec(draft_row, i32, dev, n, "draft_row"), draft_probs.size(0),
-                 _matrix_stride(draft_probs, "draft_probs"))
-    s = c.vec(sample, torch.float32, dev, n, "sample")
-    first, size = c.vec(target_row, i32, dev, n, "target_row"), c.vec(lengths, i32, dev, n, "lengths")
     if out is None:
-        tokens, counts = _new((n, k + 1), i32, target, stream), _new((n,), i32, target, stream)
+        tokens, counts = _new((n, k + 1), torch.int32, target, stream), _new((n,), torch.int32, target, stream)
     else:
         tokens, counts = out
-        _on(tokens, target, "out", (i32,), 2)
-        _on(counts, target, "out", (i32,), 1)
-        _need(tokens.shape == (n, k + 1) and counts.shape == (n,) and counts.is_contiguous(),
-              "out: want tokens, one column more than drafts, and a count for each request")
-    if n:
-        at = _matrix_stride(tokens, "out")
-        if out is not None:
-            _written(tokens)
-            _written(counts)
-        _call(c.verify_drafts, "pp_verify_drafts", target, stream, target.data_ptr(), FTYPE[target.dtype], rows, vocab,
-              _matrix_stride(target, "target"), drafts.data_ptr(), ITYPE[drafts.dtype], n, k, _matrix_stride(drafts, "drafts"),
-              accept.data_ptr(), _matrix_stride(accept, "accept"), s, *probs, first, size, tokens.data_ptr(), at,
-              counts.data_ptr())
+        _need(counts.shape == (n,), "out: want a count for each request")
+        _written(tokens)
+        _written(counts)
+    _call(_lib().verify_drafts, "pp_verify_drafts", target, stream, target, drafts, accept, sample, draft_probs, lengths,
+          target_row, draft_row, tokens, counts)
     return tokens, counts
 
 

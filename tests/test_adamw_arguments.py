@@ -91,6 +91,7 @@ def test_state_refuses_and_lays_out():
         t.values(torch.float64)
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="tensors of the CPU, which no kernel may get")
 def test_binding_refuses_before_the_library(monkeypatch):
     w, b = torch.randn(3, 100), torch.randn(7)
     s = pp.adamw_state([w, b])

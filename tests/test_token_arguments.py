@@ -54,27 +54,36 @@ def test_verify_drafts_arguments():
     assert call(n=0, target=None, drafts=None, tokens=None) == pp.PP_OK
 
 
-def test_binding_refuses_before_the_library():
+@pytest.mark.skipif(torch.cuda.is_available(), reason="tensors of the CPU, which no kernel may get")
+def test_binding_refuses_before_the_library(monkeypatch):
     x, f2, i2 = torch.zeros(2, 9), torch.zeros(2), torch.zeros(2, dtype=torch.int32)
-    for kw in (dict(logits=x.double()), dict(logits=x[0]), dict(out=torch.zeros(2, 8)), dict(out=x.half()),
-               dict(temperature=f2[:1]), dict(temperature=i2), dict(top_k=f2), dict(top_k=i2[:1]), dict(top_k=i2.long()),
-               dict(logits=torch.zeros(9, 2).t()), dict(logits=x.clone().requires_grad_(), out=torch.zeros(2, 9)), dict()):
-        with pytest.raises(ValueError):  # the last: there is no path without a GPU
-            pp.token_probs(**dict(dict(logits=x), **kw))
     target, q = torch.zeros(8, 9), torch.zeros(6, 9)
     drafts, accept, sample = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3), torch.zeros(2)
     tokens, counts = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    good = dict(target=target, drafts=drafts, accept=accept, sample=sample)
+    with pytest.raises(ValueError):  # there is no path without a GPU
+        pp.token_probs(x)
+    with pytest.raises(ValueError):
+        pp.verify_drafts(**good)
+    # past the check that there is one: what pp_bind refuses
+    monkeypatch.setattr(pp.lm, "_call", lambda fn, what, like, stream, *args: fn(*args, 0))
+    for kw in (dict(logits=x.double()), dict(logits=x[0]), dict(logits=x[None]), dict(out=torch.zeros(2, 8)), dict(out=x.half()),
+               dict(out=torch.zeros(9, 2).t()), dict(temperature=f2[:1]), dict(temperature=i2), dict(temperature=x[:, 0]),
+               dict(top_k=f2), dict(top_k=i2[:1]), dict(top_k=i2.long()), dict(logits=torch.zeros(9, 2).t()),
+               dict(logits=x.clone().requires_grad_(), out=torch.zeros(2, 9)), dict(out=torch.zeros(2, 9, requires_grad=True))):
+        with pytest.raises(ValueError):
+            pp.token_probs(**dict(dict(logits=x), **kw))
     for kw in (dict(target=target.double()), dict(target=target[0]), dict(target=target[:7]), dict(target=torch.zeros(8, 0)),
                dict(target=torch.zeros(9, 8).t()), dict(drafts=drafts.float()), dict(drafts=drafts.short()), dict(drafts=drafts[0]),
                dict(drafts=torch.zeros(3, 2, dtype=torch.int32).t()), dict(accept=accept[:, :2]), dict(accept=accept.double()),
-               dict(accept=torch.zeros(3, 2).t()), dict(sample=sample[:1]), dict(sample=sample.double()), dict(draft_probs=q[:5]),
-               dict(draft_probs=q.half()), dict(draft_probs=q[:, :8]), dict(draft_probs=torch.zeros(9, 6).t()),
+               dict(accept=torch.zeros(3, 2).t()), dict(sample=sample[:1]), dict(sample=sample.double()), dict(sample=None),
+               dict(draft_probs=q[:5]), dict(draft_probs=q.half()), dict(draft_probs=q[:, :8]), dict(draft_probs=torch.zeros(9, 6).t()),
                dict(draft_probs=q, draft_row=i2[:1]), dict(draft_probs=q, draft_row=f2), dict(lengths=f2), dict(lengths=i2[:1]),
                dict(target_row=i2.long()), dict(target_row=i2[:1]), dict(out=(tokens[:, :3], counts)), dict(out=(tokens, counts[:1])),
-               dict(out=(tokens.long(), counts)), dict(out=(tokens, counts.long())),
-               dict(out=(torch.zeros(4, 2, dtype=torch.int32).t(), counts)), dict()):
+               dict(out=(tokens.long(), counts)), dict(out=(tokens, counts.long())), dict(out=(tokens, counts[0])),
+               dict(out=(tokens, torch.zeros(4, dtype=torch.int32)[::2])), dict(out=(torch.zeros(4, 2, dtype=torch.int32).t(), counts))):
         with pytest.raises(ValueError):
-            pp.verify_drafts(**dict(dict(target=target, drafts=drafts, accept=accept, sample=sample), **kw))
+            pp.verify_drafts(**dict(good, **kw))
 
 
 def test_cluster_blocks_have_started_before_remote_accesses():
