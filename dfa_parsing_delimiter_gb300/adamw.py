@@ -173,11 +173,14 @@ def adamw_step(params, grads, state: AdamWState, lr=1e-3, betas=(0.9, 0.999), ep
     _need(0.0 <= eps < math.inf, f"eps: want a number from 0 on, got {eps}")
     c = lm._lib()
     scale_at, skip_at = _number(grad_scale, like, "grad_scale"), _number(skip, like, "skip")
-    changed = [p for p, g in zip(params, grads) if g is not None and not p.is_inference()]
     _call(c.adamw, "pp_adamw", like, stream, params, grads, state.sizes, state.first, weight_decay, like.get_device(),
           state.exp_avg.data_ptr(), state.exp_avg_sq.data_ptr(),
           0 if state.bits == 32 else state.exp_avg_exponent.data_ptr(),
           0 if state.bits == 32 else state.exp_avg_sq_exponent.data_ptr(),
           0 if state.master is None else state.master.data_ptr(), like.data_ptr(), state.n, state.bits, state.seed,
           state.nearest, lr, betas[0], betas[1], eps, lr_at, scale_at, skip_at)
-    increment_version(changed)
+    changed = [p for p, g in zip(params, grads) if g is not None]
+    try:
+        increment_version(changed)
+    except RuntimeError:  # there are inference tensors, which have no version
+        increment_version([p for p in changed if not p.is_inference()])
