@@ -23,7 +23,7 @@ namespace {
 using ppl::from_f;
 using ppl::to_f;
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int LONG_THREADS = 512, LONG_WARPS = LONG_THREADS / 32;
 constexpr int CLUSTER = 8;
 constexpr int MID = 512;
 constexpr int NV_MOST = 9;  // vectors of a thread
@@ -35,7 +35,7 @@ struct ProbArgs {
   const float* temperature;
   const int32_t* top_k;
   uint64_t in_stride, out_stride;
-  uint32_t n_vocab, blocks, part;
+  uint32_t n_vocab, n_rows, blocks, part;
   int32_t resident;
 };
 
@@ -71,8 +71,8 @@ __device__ __forceinline__ float share(float f, float top, float c) {
 struct Shared {
   float part_max, part_sum;
   uint32_t part_first;  // the first token with part_max
-  float wmax[WARPS], wsum[WARPS];
-  uint32_t wfirst[WARPS];
+  float wmax[LONG_WARPS], wsum[LONG_WARPS];
+  uint32_t wfirst[LONG_WARPS];
   uint32_t digit, above;
   uint32_t hist[8][256];
 };
@@ -110,7 +110,7 @@ __device__ __forceinline__ void digit_of(Shared& sh, int pass, uint32_t blocks, 
 }
 
 template <class T>
-__global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
+__global__ void __launch_bounds__(LONG_THREADS) long_kernel(const ProbArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ Shared sh;
   constexpr int VEC = 16 / sizeof(T);
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
   const uint32_t lo = max(from, shift);  // this block's: places lo .. to - 1
   T* buf = reinterpret_cast<T*>(raw);
   if (a.resident) {
-    for (uint32_t v = threadIdx.x * VEC; v < a.part; v += THREADS * VEC) {
+    for (uint32_t v = threadIdx.x * VEC; v < a.part; v += LONG_THREADS * VEC) {
       const uint32_t j = from + v;
       if (j >= shift && j + VEC <= all) {
         *reinterpret_cast<uint4*>(buf + v) = *reinterpret_cast<const uint4*>(in - shift + j);
@@ -134,10 +134,10 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
           if (j + k >= shift && j + k < all) buf[v + k] = in[j + k - shift];
       }
     }
-    for (uint32_t i = threadIdx.x; i < 8 * 256; i += THREADS) sh.hist[i / 256][i % 256] = 0;
+    for (uint32_t i = threadIdx.x; i < 8 * 256; i += LONG_THREADS) sh.hist[i / 256][i % 256] = 0;
     __syncthreads();
   } else {
-    for (uint32_t i = threadIdx.x; i < 8 * 256; i += THREADS) sh.hist[i / 256][i % 256] = 0;
+    for (uint32_t i = threadIdx.x; i < 8 * 256; i += LONG_THREADS) sh.hist[i / 256][i % 256] = 0;
     __syncthreads();
   }
   const T* x = a.resident ? buf - from : in - shift;  // by place
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
     uint32_t want = uint32_t(k), known = 0, mask = 0;
     int pass = 0;
     for (int at = 24; at >= 0; at -= 8, ++pass) {
-      for (uint32_t j = lo + threadIdx.x; j < to; j += THREADS) {
+      for (uint32_t j = lo + threadIdx.x; j < to; j += LONG_THREADS) {
         const uint32_t q = key_of(value(j));
         if ((q & mask) == known) atomicAdd(&sh.hist[pass][q >> at & 255], 1);
       }
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
     uint32_t place = 0;
     mask = 0;
     for (int at = 24; at >= 0; at -= 8, ++pass) {
-      for (uint32_t j = lo + threadIdx.x; j < to; j += THREADS)
+      for (uint32_t j = lo + threadIdx.x; j < to; j += LONG_THREADS)
         if (key_of(value(j)) == least) {
           const uint32_t q = ~j;
           if ((q & mask) == place) atomicAdd(&sh.hist[pass][q >> at & 255], 1);
@@ -186,17 +186,17 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
   };
   // ---- the largest value and the sum relative to it
   float m = -INFINITY;
-  for (uint32_t j = lo + threadIdx.x; j < to; j += THREADS) m = fmaxf(m, value(j));
+  for (uint32_t j = lo + threadIdx.x; j < to; j += LONG_THREADS) m = fmaxf(m, value(j));
 #pragma unroll
   for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   if (lane == 0) sh.wmax[warp] = m;
   __syncthreads();
-  m = sh.wmax[lane % WARPS];
+  m = sh.wmax[lane % LONG_WARPS];
 #pragma unroll
   for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   float s = 0.f;
   uint32_t first = ~0u;
-  for (uint32_t j = lo + threadIdx.x; j < to; j += THREADS) {
+  for (uint32_t j = lo + threadIdx.x; j < to; j += LONG_THREADS) {
     const float f = value(j);
     if (greedy) {
       if (f == m) first = min(first, j);
@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
   if (lane == 0) sh.wsum[warp] = s, sh.wfirst[warp] = first;
   __syncthreads();
   if (warp == 0) {
-    s = lane < WARPS ? sh.wsum[lane] : 0.f;
+    s = lane < LONG_WARPS ? sh.wsum[lane] : 0.f;
 #pragma unroll
     for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
-    first = __reduce_min_sync(~0u, lane < WARPS ? sh.wfirst[lane] : ~0u);
+    first = __reduce_min_sync(~0u, lane < LONG_WARPS ? sh.wfirst[lane] : ~0u);
     if (lane == 0) sh.part_max = m, sh.part_sum = s, sh.part_first = first;
   }
   ppl::cluster_sync();
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
   }
   ppl::cluster_sync();  // no block ends before the others have read it
   const float inv = total > 0.f ? 1.f / total : 0.f;
-  for (uint32_t j = lo + threadIdx.x; j < to; j += THREADS) {
+  for (uint32_t j = lo + threadIdx.x; j < to; j += LONG_THREADS) {
     const float f = value(j);
     float p;
     if (greedy) p = j == best && top > -INFINITY ? 1.f : 0.f;
@@ -240,6 +240,26 @@ __global__ void __launch_bounds__(THREADS) long_kernel(const ProbArgs a) {
 // A block's part of a row stays in its threads' registers, NV vectors of 16
 // bytes each.
 constexpr int entries_of(int threads) { return threads > 128 ? 4 : 8; }  // listed candidates a thread
+
+// The THREADS threads of a row: a block, or for short rows one of its groups.
+// Groups that begin together run the same instructions at nearly the same
+// time, which matters here: the code is long and straight, and blocks at other
+// places in it wait for one another's instructions.
+template <int THREADS>
+__device__ __forceinline__ uint32_t tid() { return threadIdx.x % THREADS; }
+template <int THREADS>
+constexpr int GROUPS_OF = THREADS > 128 ? 1 : 4;
+template <int THREADS>
+__device__ __forceinline__ void row_sync() {
+  if constexpr (GROUPS_OF<THREADS> == 1) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / THREADS), "n"(THREADS) : "memory");
+}
+// The same for a row's cluster: groups have none.
+template <int THREADS>
+__device__ __forceinline__ void all_sync() {
+  if constexpr (GROUPS_OF<THREADS> == 1) ppl::cluster_sync();
+  else row_sync<THREADS>();
+}
 
 template <int THREADS>
 struct Fast {
@@ -280,7 +300,7 @@ __device__ __forceinline__ float float_of(uint32_t key) { return __uint_as_float
 // down has, how many have larger ones and how many it.
 template <class S, class F>
 __device__ __forceinline__ void find_digit(S& sh, uint32_t want, F&& count) {
-  const uint32_t lane = threadIdx.x;
+  const uint32_t lane = threadIdx.x % 32;
   uint32_t c[8], sum = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) sum += c[k] = count(255 - 8 * lane - k);
@@ -306,12 +326,12 @@ __device__ __forceinline__ void find_digit(S& sh, uint32_t want, F&& count) {
 // with the digit of each of the thread's that are in question.
 template <int THREADS, class F>
 __device__ __forceinline__ void next_digit(Fast<THREADS>& sh, uint32_t want, F&& count) {
-  for (uint32_t i = threadIdx.x; i < 256; i += THREADS) sh.hist[i] = 0;
-  __syncthreads();
+  for (uint32_t i = tid<THREADS>(); i < 256; i += THREADS) sh.hist[i] = 0;
+  row_sync<THREADS>();
   count([&](uint32_t digit) { atomicAdd(&sh.hist[digit], 1); });
-  __syncthreads();
-  if (threadIdx.x < 32) find_digit(sh, want, [&](uint32_t d) { return sh.hist[d]; });
-  __syncthreads();
+  row_sync<THREADS>();
+  if (tid<THREADS>() < 32) find_digit(sh, want, [&](uint32_t d) { return sh.hist[d]; });
+  row_sync<THREADS>();
 }
 
 // A thread's vectors of a block's part of a row.  Places count from the 16-byte
@@ -332,7 +352,7 @@ struct Part {
   __device__ __forceinline__ void load(const T* in, uint32_t from, uint32_t part, uint32_t n_vocab) {
     shift = uint32_t(reinterpret_cast<uintptr_t>(in) / sizeof(T) % VEC);
     all = n_vocab + shift;
-    begin = from + threadIdx.x * VEC;
+    begin = from + tid<THREADS>() * VEC;
     const uint32_t to = min(from + part, all);
     n = begin < to ? (to - begin + THREADS * VEC - 1) / (THREADS * VEC) : 0;
     const T none = from_f<T>(-INFINITY);
@@ -430,8 +450,8 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
   while (true) {
     const int at = max(bits - 8, 0);
     const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
-    for (uint32_t i = threadIdx.x; i < 256; i += THREADS) sh.hist[i] = 0;
-    __syncthreads();
+    for (uint32_t i = tid<THREADS>(); i < 256; i += THREADS) sh.hist[i] = 0;
+    row_sync<THREADS>();
     part.each([&](float f, uint32_t j) {
       uint32_t q = key_of(fmaxf(f, -INFINITY)) >> P::LOW;
       bool in = !side || q == cut.least;
@@ -439,13 +459,13 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
       in = in && (q & mask) == found;
       if (in) atomicAdd(&sh.hist[q >> at & low], 1);
     });
-    ppl::cluster_sync();  // every block's counts are there
-    if (threadIdx.x < 32) find_digit(sh, want, [&](uint32_t d) {
+    all_sync<THREADS>();  // every block's counts are there
+    if (tid<THREADS>() < 32) find_digit(sh, want, [&](uint32_t d) {
       uint32_t n = 0;
       for (uint32_t b = 0; b < blocks; ++b) n += remote_u(&sh.hist[d], b);
       return n;
     });
-    ppl::cluster_sync();  // and read
+    all_sync<THREADS>();  // and read
     found |= sh.bin << at;
     want -= sh.above;
     bits = at;
@@ -487,12 +507,12 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
     bound |= sh.bin << at;
     want -= sh.above;
   }
-  if (threadIdx.x < blocks) {
-    put(there(&sh.part_max[rank], threadIdx.x), m);
-    put(there(&sh.part_bound[rank], threadIdx.x), bound > KEY_LOST ? float_of(bound) : -3.402823466e38f);
+  if (tid<THREADS>() < blocks) {
+    put(there(&sh.part_max[rank], tid<THREADS>()), m);
+    put(there(&sh.part_bound[rank], tid<THREADS>()), bound > KEY_LOST ? float_of(bound) : -3.402823466e38f);
   }
-  if (threadIdx.x == 0) sh.listed = 0;
-  ppl::cluster_sync();
+  if (tid<THREADS>() == 0) sh.listed = 0;
+  all_sync<THREADS>();
   float reach = INFINITY, top = -INFINITY;
   for (uint32_t b = 0; b < blocks; ++b) {
     top = fmaxf(top, sh.part_max[b]);
@@ -515,10 +535,10 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
       const uint32_t j = part.at(e / P::VEC) + e % P::VEC, at = atomicAdd(&sh.listed, 1);
       if (at < LIST) sh.list[at] = make_uint2(__float_as_uint(to_f(in[int64_t(j) - part.shift])), j);
     }
-  __syncthreads();
+  row_sync<THREADS>();
   const uint32_t mine = sh.listed;
-  if (threadIdx.x < blocks) put(there(&sh.part_n[rank], threadIdx.x), mine);
-  ppl::cluster_sync();
+  if (tid<THREADS>() < blocks) put(there(&sh.part_n[rank], tid<THREADS>()), mine);
+  all_sync<THREADS>();
   uint32_t total = 0, own = 0;
   for (uint32_t b = 0; b < blocks; ++b) {
     if (b < rank) own += sh.part_n[b];
@@ -531,7 +551,7 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
   int entries = 0;
 #pragma unroll
   for (int e = 0; e < ENTRIES; ++e) {
-    uint32_t i = threadIdx.x + e * THREADS, b = 0;
+    uint32_t i = tid<THREADS>() + e * THREADS, b = 0;
     if (i < total) {
       for (uint32_t n; i >= (n = sh.part_n[b]); ++b) i -= n;
       uint32_t v;
@@ -540,7 +560,7 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
       ++entries;
     }
   }
-  ppl::cluster_arrive_release();  // this block has read what it needs of the others
+  if constexpr (GROUPS_OF<THREADS> == 1) ppl::cluster_arrive_release();  // this block has read what it needs of the others
   // Zeros everywhere: the few others are written over them once they are known.
   part.write(out, [&](int, float* p) {
 #pragma unroll
@@ -603,27 +623,31 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
   }
 #pragma unroll
   for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
-  if (threadIdx.x % 32 == 0) sh.sums[threadIdx.x / 32] = s;
-  __syncthreads();
-  s = sh.sums[threadIdx.x % (THREADS / 32)];
+  if (tid<THREADS>() % 32 == 0) sh.sums[tid<THREADS>() / 32] = s;
+  row_sync<THREADS>();
+  s = sh.sums[tid<THREADS>() % (THREADS / 32)];
 #pragma unroll
   for (int d = THREADS / 64; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
   const float factor = s ? 1.f / (float(uint32_t(s >> 22)) * 0x1p-22f + float(uint32_t(s) & 0x3FFFFF) * 0x1p-44f) : 0.f;
 #pragma unroll
   for (int e = 0; e < ENTRIES; ++e)  // after the zeros: there were barriers since
-    if (e < entries && threadIdx.x + e * THREADS - own < mine && p[e] > 0.f) out[int64_t(place[e]) - part.shift] = p[e] * factor;
-  ppl::cluster_wait();
+    if (e < entries && tid<THREADS>() + e * THREADS - own < mine && p[e] > 0.f) out[int64_t(place[e]) - part.shift] = p[e] * factor;
+  if constexpr (GROUPS_OF<THREADS> == 1) ppl::cluster_wait();
   return true;
 }
 
 template <class T, int THREADS, int NV, bool CUT>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const ProbArgs a) {
-  ppl::cluster_arrive();
+__global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS * GROUPS_OF<THREADS>)) probs_kernel(const ProbArgs a) {
+  constexpr int GROUPS = GROUPS_OF<THREADS>;
+  if constexpr (GROUPS == 1) ppl::cluster_arrive();
   constexpr int VEC = 16 / sizeof(T), WARPS = THREADS / 32;
   using P = Part<T, THREADS, NV>;
-  __shared__ Fast<THREADS> sh;
-  const uint32_t rank = blockIdx.x % a.blocks, r = blockIdx.x / a.blocks;
-  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  __shared__ Fast<THREADS> shared[GROUPS];
+  const uint32_t group = threadIdx.x / THREADS;
+  Fast<THREADS>& sh = shared[group];
+  const uint32_t rank = blockIdx.x % a.blocks, r = blockIdx.x / a.blocks * GROUPS + group;
+  if (r >= a.n_rows) return;
+  const uint32_t lane = tid<THREADS>() % 32, warp = tid<THREADS>() / 32;
   float* out = a.out + r * a.out_stride;
   const float t = a.temperature ? a.temperature[r] : 1.f;
   const int32_t top_k = CUT ? a.top_k[r] : 0;
@@ -644,9 +668,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
   for (int i = 0; i < G; ++i) m = fmaxf(m, maxima[i]);
   m = warp_max(m);
   if (lane == 0) sh.wf[0][warp] = m;
-  __syncthreads();
+  row_sync<THREADS>();
   m = warp_max(sh.wf[0][lane % WARPS]);
-  ppl::cluster_wait();  // every block has started
+  if constexpr (GROUPS == 1) ppl::cluster_wait();  // every block has started
   const bool some = CUT && top_k > 0 && uint32_t(top_k) < a.n_vocab && !greedy;
   Cut cut = {0, ~0u};
   auto kept = [&](float f, uint32_t j) {
@@ -682,7 +706,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
   s = warp_add(s);
   first = __reduce_min_sync(~0u, first);
   if (lane == 0) sh.wf[1][warp] = s, sh.wu[warp] = first;
-  __syncthreads();
+  row_sync<THREADS>();
   if (warp == 0) {
     s = warp_add(lane < WARPS ? sh.wf[1][lane] : 0.f);
     first = __reduce_min_sync(~0u, lane < WARPS ? sh.wu[lane] : ~0u);
@@ -692,7 +716,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
       put(there(&sh.part_first[rank], lane), first);
     }
   }
-  ppl::cluster_sync();
+  all_sync<THREADS>();
   float top = -INFINITY;
   for (uint32_t b = 0; b < a.blocks; ++b) top = fmaxf(top, sh.part_max[b]);
   float total = 0.f;
@@ -720,15 +744,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const Pr
 }
 
 template <class K>
-cudaError_t launch_as(K kernel, const ProbArgs& a, uint64_t n_rows, int threads, uint32_t smem, cudaStream_t stream) {
+cudaError_t launch_as(K kernel, const ProbArgs& a, uint64_t n_rows, int threads, uint32_t smem, cudaStream_t stream, int groups = 1) {
   cudaLaunchAttribute at;
   std::memset(&at, 0, sizeof at);
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = a.blocks;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(n_rows * a.blocks));
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = dim3(unsigned((n_rows + groups - 1) / groups * a.blocks));
+  cfg.blockDim = dim3(threads * groups);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &at;
@@ -739,9 +763,9 @@ cudaError_t launch_as(K kernel, const ProbArgs& a, uint64_t n_rows, int threads,
 template <class T, int THREADS_, bool CUT>
 cudaError_t launch_fast(const ProbArgs& a, uint64_t n_rows, uint32_t vectors, cudaStream_t stream) {
   const uint32_t nv = (vectors + THREADS_ - 1) / THREADS_;
-  if (nv <= 2) return launch_as(probs_kernel<T, THREADS_, 2, CUT>, a, n_rows, THREADS_, 0, stream);
-  if (nv <= 5) return launch_as(probs_kernel<T, THREADS_, 5, CUT>, a, n_rows, THREADS_, 0, stream);
-  return launch_as(probs_kernel<T, THREADS_, NV_MOST, CUT>, a, n_rows, THREADS_, 0, stream);
+  if (nv <= 2) return launch_as(probs_kernel<T, THREADS_, 2, CUT>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
+  if (nv <= 5) return launch_as(probs_kernel<T, THREADS_, 5, CUT>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
+  return launch_as(probs_kernel<T, THREADS_, NV_MOST, CUT>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
 }
 
 template <class T>
@@ -778,7 +802,7 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
   a.blocks = CLUSTER;
   a.part = each * VEC;
   a.resident = a.part * sizeof(T) <= RESIDENT_MOST;
-  return launch_as(long_kernel<T>, a, n_rows, THREADS, a.resident ? a.part * sizeof(T) : 0, stream);
+  return launch_as(long_kernel<T>, a, n_rows, LONG_THREADS, a.resident ? a.part * sizeof(T) : 0, stream);
 }
 
 }  // namespace
@@ -803,6 +827,7 @@ extern "C" pp_rc pp_token_probs(const void* d_logits, pp_ftype type, size_t n_ro
   a.in_stride = logits_stride;
   a.out_stride = probs_stride;
   a.n_vocab = uint32_t(n_vocab);
+  a.n_rows = uint32_t(n_rows);
   cudaError_t e;
   switch (type) {
     case PP_F32: e = launch<float>(a, n_rows, stream); break;
