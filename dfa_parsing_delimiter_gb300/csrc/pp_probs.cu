@@ -434,14 +434,158 @@ struct Cut {
   uint32_t least, last;
 };
 
-// The cut of any length: digits counted over all values of the cluster.  A
-// function of its own, since its registers would crowd out the values elsewhere.
+// This thread's entries of all the blocks' lists.  Every block finds the same in them.
+template <int THREADS>
+__device__ __forceinline__ int listed_of(Fast<THREADS>& sh, uint32_t total, float* value, uint32_t* place) {
+  int entries = 0;
+#pragma unroll
+  for (int e = 0; e < Fast<THREADS>::ENTRIES; ++e) {
+    uint32_t i = tid<THREADS>() + e * THREADS, b = 0;
+    if (i < total) {
+      for (uint32_t n; i >= (n = sh.part_n[b]); ++b) i -= n;
+      uint32_t v;
+      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v), "=r"(place[e]) : "r"(there(&sh.list[i], b)) : "memory");
+      value[e] = __uint_as_float(v);
+      ++entries;
+    }
+  }
+  return entries;
+}
+
+// The cut that keeps `want` of the total listed values, all from reach to top.
+template <class P, int THREADS>
+__device__ __forceinline__ Cut cut_among(Fast<THREADS>& sh, const float* value, const uint32_t* place, int entries, uint32_t total,
+                                         uint32_t want, float top, float reach, uint32_t places) {
+  constexpr int ENTRIES = Fast<THREADS>::ENTRIES, LOW = P::LOW;
+  auto key = [&](int e) { return key_of(value[e]) >> LOW; };
+  const uint32_t hi = key_of(top) >> LOW, lo = key_of(reach) >> LOW;
+  Cut cut = {lo, ~0u};  // all candidates
+  if (total > want) {
+    uint32_t in_bin = total;
+    int bits = 32 - __clz(hi ^ lo);  // below those that all candidates share
+    uint32_t known = bits == 32 ? 0 : hi >> bits << bits;
+    while (bits > 0 && want < in_bin) {
+      const int at = max(bits - 8, 0);
+      const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
+      next_digit<THREADS>(sh, want, [&](auto&& add) {
+#pragma unroll
+        for (int e = 0; e < ENTRIES; ++e)
+          if (e < entries && (key(e) & mask) == known) add(key(e) >> at & low);
+      });
+      known |= sh.bin << at;
+      want -= sh.above;
+      in_bin = sh.in_bin;
+      bits = at;
+    }
+    cut.least = known;
+    if (want < in_bin) {  // of those that tie the lowest places
+      const int place_bits = 32 - __clz(places);
+      const uint32_t inside = ~(~0u << place_bits);
+      uint32_t found = 0;
+      for (bits = place_bits; bits > 0 && want < in_bin;) {
+        const int at = max(bits - 8, 0);
+        const uint32_t mask = ~0u << bits, low = (1u << (bits - at)) - 1;
+        next_digit<THREADS>(sh, want, [&](auto&& add) {
+#pragma unroll
+          for (int e = 0; e < ENTRIES; ++e) {
+            const uint32_t q = ~place[e] & inside;
+            if (e < entries && key(e) == cut.least && (q & mask) == found) add(q >> at & low);
+          }
+        });
+        found |= sh.bin << at;
+        want -= sh.above;
+        in_bin = sh.in_bin;
+        bits = at;
+      }
+      cut.last = ~found & inside;
+    }
+  }
+  return cut;
+}
+
+// The cut of any length.  The values from the largest to the least are counted in 256
+// steps of equal height, and those in the step that the cut goes through are listed.
+// Where the lists have no room for them, their digits are counted over all values of
+// the cluster.  A function of its own, since its registers would crowd out the values
+// elsewhere.
 template <class T, int THREADS, int NV>
-__device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size, uint32_t n_vocab, Fast<THREADS>& sh, uint32_t blocks,
-                                       uint32_t want) {
+__device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size, uint32_t n_vocab, Fast<THREADS>& sh, uint32_t rank,
+                                       uint32_t blocks, uint32_t want) {
   using P = Part<T, THREADS, NV>;
+  constexpr int WARPS = THREADS / 32, LIST = Fast<THREADS>::LIST, ENTRIES = Fast<THREADS>::ENTRIES;
+  const uint32_t lane = tid<THREADS>() % 32, warp = tid<THREADS>() / 32;
   P part;
   part.load(in, from, size, n_vocab);
+  float top = -INFINITY, low = INFINITY;
+  part.each([&](float f, uint32_t) {
+    top = fmaxf(top, f);
+    if (f > -INFINITY) low = fminf(low, f);
+  });
+  top = warp_max(top);
+  low = -warp_max(-low);
+  row_sync<THREADS>();  // all are done with what was there
+  if (lane == 0) sh.wf[0][warp] = top, sh.wf[1][warp] = low;
+  if (tid<THREADS>() == 0) sh.listed = 0;
+  for (uint32_t i = tid<THREADS>(); i < 256; i += THREADS) sh.hist[i] = 0;
+  row_sync<THREADS>();
+  top = warp_max(sh.wf[0][lane % WARPS]);
+  low = -warp_max(-sh.wf[1][lane % WARPS]);
+  all_sync<THREADS>();  // nor does another block read this one's from before
+  if (tid<THREADS>() < blocks) {
+    put(there(&sh.part_max[rank], tid<THREADS>()), top);
+    put(there(&sh.part_bound[rank], tid<THREADS>()), low);
+  }
+  all_sync<THREADS>();
+  for (uint32_t b = 0; b < blocks; ++b) {
+    top = fmaxf(top, sh.part_max[b]);
+    low = fminf(low, sh.part_bound[b]);
+  }
+  const float height = 255.f / (top - low);
+  if (height > 0.f && height < INFINITY) {  // not so where all are equal, or too far from one another
+    // steps never rise as values fall, whatever is rounded
+    auto step = [&](float f) { return 255 - min(int((top - f) * height), 255); };
+    part.each([&](float f, uint32_t) {
+      if (f > -INFINITY) atomicAdd(&sh.hist[step(f)], 1);
+    });
+    all_sync<THREADS>();  // every block's counts are there
+    if (tid<THREADS>() == 0) sh.in_bin = 0;
+    row_sync<THREADS>();
+    if (tid<THREADS>() < 32) find_digit(sh, want, [&](uint32_t d) {
+      uint32_t n = 0;
+      for (uint32_t b = 0; b < blocks; ++b) n += remote_u(&sh.hist[d], b);
+      return n;
+    });
+    row_sync<THREADS>();
+    const uint32_t total = sh.in_bin, left = want - sh.above;
+    const int bin = sh.bin;
+    if (total == 0) return {0, ~0u};  // fewer finite values than are to be kept
+    if (total <= LIST) {
+      float reach = top, high = low;
+      part.each([&](float f, uint32_t j) {
+        if (f > -INFINITY && step(f) == bin) {
+          const uint32_t at = atomicAdd(&sh.listed, 1);
+          sh.list[at] = make_uint2(__float_as_uint(f), j);
+        }
+      });
+      row_sync<THREADS>();
+      if (tid<THREADS>() < blocks) put(there(&sh.part_n[rank], tid<THREADS>()), sh.listed);
+      all_sync<THREADS>();
+      float value[ENTRIES];
+      uint32_t place[ENTRIES];
+      const int entries = listed_of(sh, total, value, place);
+#pragma unroll
+      for (int e = 0; e < ENTRIES; ++e)
+        if (e < entries) reach = fminf(reach, value[e]), high = fmaxf(high, value[e]);
+      reach = -warp_max(-reach);
+      high = warp_max(high);
+      if (lane == 0) sh.wf[0][warp] = high, sh.wf[1][warp] = reach;
+      all_sync<THREADS>();  // and every block has read what it needs of the others
+      high = warp_max(sh.wf[0][lane % WARPS]);
+      reach = -warp_max(-sh.wf[1][lane % WARPS]);
+      return cut_among<P>(sh, value, place, entries, total, left, high, reach, part.all);
+    }
+    all_sync<THREADS>();  // the counts are read
+  }
   Cut cut = {0, ~0u};
   const int place_bits = 32 - __clz(part.all);
   // side 0: the values; side 1: the places of those that tie, where not all are kept
@@ -545,71 +689,17 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
     total += sh.part_n[b];
   }
   if (total > LIST) return false;
-  // This thread's entries of all the blocks' lists.  Every block finds the same in them.
   float value[ENTRIES];
   uint32_t place[ENTRIES];
-  int entries = 0;
-#pragma unroll
-  for (int e = 0; e < ENTRIES; ++e) {
-    uint32_t i = tid<THREADS>() + e * THREADS, b = 0;
-    if (i < total) {
-      for (uint32_t n; i >= (n = sh.part_n[b]); ++b) i -= n;
-      uint32_t v;
-      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v), "=r"(place[e]) : "r"(there(&sh.list[i], b)) : "memory");
-      value[e] = __uint_as_float(v);
-      ++entries;
-    }
-  }
+  const int entries = listed_of(sh, total, value, place);
   if constexpr (GROUPS_OF<THREADS> == 1) ppl::cluster_arrive_release();  // this block has read what it needs of the others
   // Zeros everywhere: the few others are written over them once they are known.
   part.write(out, [&](int, float* p) {
 #pragma unroll
     for (int k = 0; k < P::VEC; ++k) p[k] = 0.f;
   });
+  const Cut cut = cut_among<P>(sh, value, place, entries, total, top_k, top, reach, part.all);
   auto key = [&](int e) { return key_of(value[e]) >> LOW; };
-  const uint32_t hi = key_of(top) >> LOW, lo = key_of(reach) >> LOW;
-  Cut cut = {lo, ~0u};  // all candidates
-  if (total > top_k) {
-    uint32_t in_bin = total;
-    want = top_k;
-    int bits = 32 - __clz(hi ^ lo);  // below those that all candidates share
-    uint32_t known = bits == 32 ? 0 : hi >> bits << bits;
-    while (bits > 0 && want < in_bin) {
-      const int at = max(bits - 8, 0);
-      const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
-      next_digit<THREADS>(sh, want, [&](auto&& add) {
-#pragma unroll
-        for (int e = 0; e < ENTRIES; ++e)
-          if (e < entries && (key(e) & mask) == known) add(key(e) >> at & low);
-      });
-      known |= sh.bin << at;
-      want -= sh.above;
-      in_bin = sh.in_bin;
-      bits = at;
-    }
-    cut.least = known;
-    if (want < in_bin) {  // of those that tie the lowest places
-      const int place_bits = 32 - __clz(part.all);
-      const uint32_t inside = ~(~0u << place_bits);
-      uint32_t found = 0;
-      for (bits = place_bits; bits > 0 && want < in_bin;) {
-        const int at = max(bits - 8, 0);
-        const uint32_t mask = ~0u << bits, low = (1u << (bits - at)) - 1;
-        next_digit<THREADS>(sh, want, [&](auto&& add) {
-#pragma unroll
-          for (int e = 0; e < ENTRIES; ++e) {
-            const uint32_t q = ~place[e] & inside;
-            if (e < entries && key(e) == cut.least && (q & mask) == found) add(q >> at & low);
-          }
-        });
-        found |= sh.bin << at;
-        want -= sh.above;
-        in_bin = sh.in_bin;
-        bits = at;
-      }
-      cut.last = ~found & inside;
-    }
-  }
   // The lists' order is not the same each time, so the sum is one of whole numbers: units
   // of 2^-44, of exponentials up to 1 of which one is.
   float p[ENTRIES];
@@ -679,7 +769,7 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS *
   };
   if (some) {
     if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, maxima, c, in, out)) return;
-    cut = cut_of_all<T, THREADS, NV>(in, rank * a.part, a.part, a.n_vocab, sh, a.blocks, uint32_t(top_k));
+    cut = cut_of_all<T, THREADS, NV>(in, rank * a.part, a.part, a.n_vocab, sh, rank, a.blocks, uint32_t(top_k));
     part.load(in, rank * a.part, a.part, a.n_vocab);  // again, rather than kept in registers meanwhile
   }
   // ---- the sum relative to the block's largest value, and the first place that has it
