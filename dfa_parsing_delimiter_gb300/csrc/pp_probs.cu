@@ -25,7 +25,7 @@ using ppl::to_f;
 
 constexpr int LONG_THREADS = 512, LONG_WARPS = LONG_THREADS / 32;
 constexpr int CLUSTER = 8;
-constexpr int MID = 512;
+constexpr int MID = 512, WIDE = 2, NV_PLAIN = 9;
 constexpr int NV_MOST = 9;  // vectors of a thread
 constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // bytes of a block's part
 
@@ -271,7 +271,7 @@ struct Fast {
   float wf[2][WARPS];
   uint32_t wu[WARPS];
   uint32_t bin, above, in_bin;
-  uint32_t hist[256];
+  uint32_t hist[256], all[256];
   uint32_t listed;
   uint2 list[LIST];  // the block's candidates: values and places
 };
@@ -320,6 +320,21 @@ __device__ __forceinline__ void find_digit(S& sh, uint32_t want, F&& count) {
     }
     run += c[k];
   }
+}
+
+// The counts of all the cluster's blocks, in sh.all.  Every block has counted before, and
+// may count again after the next all_sync.
+template <int THREADS>
+__device__ __forceinline__ void add_up(Fast<THREADS>& sh, uint32_t blocks) {
+  for (uint32_t i = tid<THREADS>(); i < 256; i += THREADS) {
+    uint32_t n[CLUSTER];
+#pragma unroll
+    for (uint32_t b = 0; b < CLUSTER; ++b) n[b] = b < blocks ? remote_u(&sh.hist[i], b) : 0;
+#pragma unroll
+    for (uint32_t b = 1; b < CLUSTER; ++b) n[0] += n[b];
+    sh.all[i] = n[0];
+  }
+  row_sync<THREADS>();
 }
 
 // A digit of the want-th largest of the threads' entries; count(add) calls add
@@ -452,6 +467,28 @@ __device__ __forceinline__ int listed_of(Fast<THREADS>& sh, uint32_t total, floa
   return entries;
 }
 
+// The values for which `pick` holds go to the block's list, in any order.  They are few, so
+// they are only marked in the pass over the values, and read again for the list: a
+// branch for each value makes a kernel of code that is not at hand when it is needed.
+template <class P, int THREADS, class T, class F>
+__device__ __forceinline__ void list_where(P& part, Fast<THREADS>& sh, const T* in, F&& pick) {
+  constexpr int WORDS = (P::N * P::VEC + 31) / 32;
+  uint32_t marks[WORDS] = {};
+  part.forget();
+#pragma unroll
+  for (int i = 0; i < P::N; ++i)
+#pragma unroll
+    for (int k = 0; k < P::VEC; ++k)
+      if (pick(to_f(part.x[i].v[k]))) marks[(i * P::VEC + k) / 32] |= 1u << (i * P::VEC + k) % 32;
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w)
+    for (; marks[w]; marks[w] &= marks[w] - 1) {
+      const int e = w * 32 + __ffs(marks[w]) - 1;
+      const uint32_t j = part.at(e / P::VEC) + e % P::VEC, at = atomicAdd(&sh.listed, 1);
+      if (at < Fast<THREADS>::LIST) sh.list[at] = make_uint2(__float_as_uint(to_f(in[int64_t(j) - part.shift])), j);
+    }
+}
+
 // The cut that keeps `want` of the total listed values, all from reach to top.
 template <class P, int THREADS>
 __device__ __forceinline__ Cut cut_among(Fast<THREADS>& sh, const float* value, const uint32_t* place, int entries, uint32_t total,
@@ -550,23 +587,15 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
     all_sync<THREADS>();  // every block's counts are there
     if (tid<THREADS>() == 0) sh.in_bin = 0;
     row_sync<THREADS>();
-    if (tid<THREADS>() < 32) find_digit(sh, want, [&](uint32_t d) {
-      uint32_t n = 0;
-      for (uint32_t b = 0; b < blocks; ++b) n += remote_u(&sh.hist[d], b);
-      return n;
-    });
+    add_up(sh, blocks);
+    if (tid<THREADS>() < 32) find_digit(sh, want, [&](uint32_t d) { return sh.all[d]; });
     row_sync<THREADS>();
     const uint32_t total = sh.in_bin, left = want - sh.above;
     const int bin = sh.bin;
     if (total == 0) return {0, ~0u};  // fewer finite values than are to be kept
     if (total <= LIST) {
       float reach = top, high = low;
-      part.each([&](float f, uint32_t j) {
-        if (f > -INFINITY && step(f) == bin) {
-          const uint32_t at = atomicAdd(&sh.listed, 1);
-          sh.list[at] = make_uint2(__float_as_uint(f), j);
-        }
-      });
+      list_where(part, sh, in, [&](float f) { return f > -INFINITY && step(f) == bin; });
       row_sync<THREADS>();
       if (tid<THREADS>() < blocks) put(there(&sh.part_n[rank], tid<THREADS>()), sh.listed);
       all_sync<THREADS>();
@@ -604,11 +633,8 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
       if (in) atomicAdd(&sh.hist[q >> at & low], 1);
     });
     all_sync<THREADS>();  // every block's counts are there
-    if (tid<THREADS>() < 32) find_digit(sh, want, [&](uint32_t d) {
-      uint32_t n = 0;
-      for (uint32_t b = 0; b < blocks; ++b) n += remote_u(&sh.hist[d], b);
-      return n;
-    });
+    add_up(sh, blocks);
+    if (tid<THREADS>() < 32) find_digit(sh, want, [&](uint32_t d) { return sh.all[d]; });
     all_sync<THREADS>();  // and read
     found |= sh.bin << at;
     want -= sh.above;
@@ -634,8 +660,8 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
                                           const float (&maxima)[G], float c, const T* in, float* out) {
   constexpr int LIST = Fast<THREADS>::LIST, ENTRIES = Fast<THREADS>::ENTRIES, LOW = P::LOW;
   const uint32_t k_part = (top_k + blocks - 1) / blocks;
-  const bool every = part.all <= LIST;  // the lists have room for the row
-  if (k_part > THREADS * G && !every) return false;
+  const bool every = k_part > THREADS * G;  // only where the lists have room for the row
+  if (every && part.all > LIST) return false;
   // Each block's k_part-th largest of its threads' (or vectors') maxima (its key's upper half): at least
   // k_part of its values reach that, so top_k of the row reach the least of them.  A block
   // with fewer than that finds -infinity.
@@ -663,22 +689,7 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
     reach = fminf(reach, sh.part_bound[b]);
   }
   // the candidates, in any order
-  // and few, so only marked here; a branch for each value is a kernel of code
-  constexpr int WORDS = (P::N * P::VEC + 31) / 32;
-  uint32_t marks[WORDS] = {};
-  part.forget();
-#pragma unroll
-  for (int i = 0; i < P::N; ++i)
-#pragma unroll
-    for (int k = 0; k < P::VEC; ++k)
-      if (to_f(part.x[i].v[k]) >= reach) marks[(i * P::VEC + k) / 32] |= 1u << (i * P::VEC + k) % 32;
-#pragma unroll
-  for (int w = 0; w < WORDS; ++w)
-    for (; marks[w]; marks[w] &= marks[w] - 1) {
-      const int e = w * 32 + __ffs(marks[w]) - 1;
-      const uint32_t j = part.at(e / P::VEC) + e % P::VEC, at = atomicAdd(&sh.listed, 1);
-      if (at < LIST) sh.list[at] = make_uint2(__float_as_uint(to_f(in[int64_t(j) - part.shift])), j);
-    }
+  list_where(part, sh, in, [&](float f) { return f >= reach; });
   row_sync<THREADS>();
   const uint32_t mine = sh.listed;
   if (tid<THREADS>() < blocks) put(there(&sh.part_n[rank], tid<THREADS>()), mine);
@@ -727,7 +738,7 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
 }
 
 template <class T, int THREADS, int NV, bool CUT>
-__global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS * GROUPS_OF<THREADS>)) probs_kernel(const ProbArgs a) {
+__global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, THREADS == 512 && NV <= 5 && !CUT ? WIDE : 1024 / (THREADS * GROUPS_OF<THREADS>)) probs_kernel(const ProbArgs a) {
   constexpr int GROUPS = GROUPS_OF<THREADS>;
   if constexpr (GROUPS == 1) ppl::cluster_arrive();
   constexpr int VEC = 16 / sizeof(T), WARPS = THREADS / 32;
@@ -763,16 +774,17 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS *
   if constexpr (GROUPS == 1) ppl::cluster_wait();  // every block has started
   const bool some = CUT && top_k > 0 && uint32_t(top_k) < a.n_vocab && !greedy;
   Cut cut = {0, ~0u};
-  auto kept = [&](float f, uint32_t j) {
-    const uint32_t q = key_of(f) >> P::LOW;
-    return f > -INFINITY && (q > cut.least || (q == cut.least && j <= cut.last));
-  };
   if (some) {
     if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, maxima, c, in, out)) return;
     cut = cut_of_all<T, THREADS, NV>(in, rank * a.part, a.part, a.n_vocab, sh, rank, a.blocks, uint32_t(top_k));
     part.load(in, rank * a.part, a.part, a.n_vocab);  // again, rather than kept in registers meanwhile
   }
   // ---- the sum relative to the block's largest value, and the first place that has it
+  // Kept, in floats: above all that tie, or of those that tie up to the last place.  (KEY_LOST
+  // and what is beyond infinity's key make NaN, which nothing reaches.)
+  const uint32_t tie = cut.least << P::LOW, over = (cut.least + 1) << P::LOW;
+  const float from_tie = tie > KEY_LOST ? float_of(tie) : -3.402823466e38f, from_over = over > KEY_LOST ? float_of(over) : INFINITY;
+  auto kept = [&](float f, uint32_t j) { return f >= from_over || (f >= from_tie && j <= cut.last); };
   // 2^64 times share(f, m, c), which no exponential within a float's range of 1 leaves
   const bool endless = m == INFINITY;
   auto ex = [&](float f, uint32_t j) {
@@ -868,7 +880,7 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
   if (vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256))
     return a.top_k ? launch_fast<T, 128, true>(a, n_rows, vectors, stream) : launch_fast<T, 128, false>(a, n_rows, vectors, stream);
   if (vectors <= MID * NV_MOST * CLUSTER) {
-    while (blocks < CLUSTER && (vectors > MID * NV_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
+    while (blocks < CLUSTER && (vectors > MID * (a.top_k ? NV_MOST : NV_PLAIN) * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
     const uint32_t each = (vectors + blocks - 1) / blocks;
     a.blocks = blocks;
     a.part = each * VEC;
