@@ -358,9 +358,10 @@ struct Part {
   static constexpr int LOW = sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 13 : 16;
   using Vec = ppl::Pack<T, VEC>;
   Vec x[NV];
-  uint32_t begin;          // place of the first vector
-  uint32_t n;              // vectors
-  uint32_t shift, all;     // the row's first place, and the one after its last
+  uint32_t begin;       // place of the first vector
+  int full, whole, n;   // the first whole vector, the one after the last whole one, all with values
+  int slots;            // vectors that some thread has
+  uint32_t shift, all;  // the row's first place, and the one after its last
 
   __device__ __forceinline__ uint32_t at(int i) const { return begin + i * THREADS * VEC; }
 
@@ -369,26 +370,29 @@ struct Part {
     all = n_vocab + shift;
     begin = from + tid<THREADS>() * VEC;
     const uint32_t to = min(from + part, all);
-    n = begin < to ? (to - begin + THREADS * VEC - 1) / (THREADS * VEC) : 0;
+    constexpr uint32_t STEP = THREADS * VEC;
+    slots = from < to ? (to - from + STEP - 1) / STEP : 0;
+    n = begin < to ? (to - begin + STEP - 1) / STEP : 0;
+    full = begin < shift ? 1 : 0;
+    whole = begin + VEC <= to ? (to - VEC - begin) / STEP + 1 : 0;
     const T none = from_f<T>(-INFINITY);
+    const T* p = in + (int64_t(begin) - shift);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) x[i].v[k] = none;
-      if (i < n && at(i) >= shift && at(i) + VEC <= all) x[i] = *reinterpret_cast<const Vec*>(in - shift + at(i));
+      if (i >= full && i < whole) x[i] = *reinterpret_cast<const Vec*>(p + i * int(STEP));
     }
     // the incomplete vectors, where the row begins and ends
-    const uint32_t last = all / VEC * VEC;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const uint32_t j = side ? last : 0;
-      if (j < begin || j >= to || (j - begin) % (THREADS * VEC) != 0 || (side ? last == 0 || last == all : shift == 0 && all >= VEC)) continue;
+#pragma unroll 1
+    for (int e = full ? 0 : whole; e < n; e = e < whole && whole < n ? whole : n) {
+      const uint32_t j = at(e);
       Vec edge;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) edge.v[k] = j + k >= shift && j + k < all ? in[int64_t(j) + k - shift] : none;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (at(i) == j) x[i] = edge;
+        if (i == e) x[i] = edge;
     }
   }
   // What was computed from the values is not kept for the next pass over them:
@@ -407,15 +411,19 @@ struct Part {
     forget();
 #pragma unroll
     for (int i = 0; i < NV; ++i)
+      if (i < slots) {
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) f(to_f(x[i].v[k]), at(i) + k);
+        for (int k = 0; k < VEC; ++k) f(to_f(x[i].v[k]), at(i) + k);
+      }
   }
   template <class F>
   __device__ __forceinline__ void change(F&& f) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
+      if (i < slots) {
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) x[i].v[k] = from_f<T>(f(to_f(x[i].v[k]), at(i) + k));
+        for (int k = 0; k < VEC; ++k) x[i].v[k] = from_f<T>(f(to_f(x[i].v[k]), at(i) + k));
+      }
   }
   // f(i, p) fills the VEC probabilities p of vector i.
   template <class F>
@@ -423,22 +431,23 @@ struct Part {
     forget();
     // the inputs' and the outputs' boundaries agree where their strides do
     const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
+    float* to = out + (int64_t(begin) - shift);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (i >= n) break;
+      constexpr int STEP = THREADS * VEC;
       float p[VEC];
       f(i, p);
-      float* to = out + int64_t(at(i)) - shift;
-      if (wide && at(i) >= shift && at(i) + VEC <= all) {
+      if (wide && i >= full && i < whole) {
         if constexpr (VEC == 8)
-          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]), "f"(p[4]),
-                       "f"(p[5]), "f"(p[6]), "f"(p[7]) : "memory");
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + i * STEP), "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]),
+                       "f"(p[4]), "f"(p[5]), "f"(p[6]), "f"(p[7]) : "memory");
         else
-          *reinterpret_cast<float4*>(to) = make_float4(p[0], p[1], p[2], p[3]);
+          *reinterpret_cast<float4*>(to + i * STEP) = make_float4(p[0], p[1], p[2], p[3]);
       } else {
 #pragma unroll
         for (int k = 0; k < VEC; ++k)
-          if (at(i) + k >= shift && at(i) + k < all) to[k] = p[k];
+          if (at(i) + k >= shift && at(i) + k < all) to[i * STEP + k] = p[k];
       }
     }
   }
@@ -477,6 +486,7 @@ __device__ __forceinline__ void list_where(P& part, Fast<THREADS>& sh, const T* 
   part.forget();
 #pragma unroll
   for (int i = 0; i < P::N; ++i)
+    if (i < part.slots)
 #pragma unroll
     for (int k = 0; k < P::VEC; ++k)
       if (pick(to_f(part.x[i].v[k]))) marks[(i * P::VEC + k) / 32] |= 1u << (i * P::VEC + k) % 32;
@@ -763,8 +773,10 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, THREADS == 512 &&
   for (int i = 0; i < G; ++i) maxima[i] = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
+    if (i < part.slots) {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) maxima[i % G] = fmaxf(maxima[i % G], to_f(part.x[i].v[k]));
+      for (int k = 0; k < VEC; ++k) maxima[i % G] = fmaxf(maxima[i % G], to_f(part.x[i].v[k]));
+    }
 #pragma unroll
   for (int i = 0; i < G; ++i) m = fmaxf(m, maxima[i]);
   m = warp_max(m);
