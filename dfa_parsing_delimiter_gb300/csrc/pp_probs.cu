@@ -25,7 +25,8 @@ using ppl::to_f;
 
 constexpr int LONG_THREADS = 512, LONG_WARPS = LONG_THREADS / 32;
 constexpr int CLUSTER = 8;
-constexpr int MID = 512, WIDE = 2, NV_PLAIN = 9;
+constexpr int MID = 512;                    // threads for a block's part of a longer row
+constexpr uint32_t PART_MOST = 73728;      // bytes of a part without a cut: three blocks a multiprocessor
 constexpr int NV_MOST = 9;  // vectors of a thread
 constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // bytes of a block's part
 
@@ -747,8 +748,8 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
   return true;
 }
 
-template <class T, int THREADS, int NV, bool CUT>
-__global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, THREADS == 512 && NV <= 5 && !CUT ? WIDE : 1024 / (THREADS * GROUPS_OF<THREADS>)) probs_kernel(const ProbArgs a) {
+template <class T, int THREADS, int NV>
+__global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS * GROUPS_OF<THREADS>)) cut_kernel(const ProbArgs a) {
   constexpr int GROUPS = GROUPS_OF<THREADS>;
   if constexpr (GROUPS == 1) ppl::cluster_arrive();
   constexpr int VEC = 16 / sizeof(T), WARPS = THREADS / 32;
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, THREADS == 512 &&
   const uint32_t lane = tid<THREADS>() % 32, warp = tid<THREADS>() / 32;
   float* out = a.out + r * a.out_stride;
   const float t = a.temperature ? a.temperature[r] : 1.f;
-  const int32_t top_k = CUT ? a.top_k[r] : 0;
+  const int32_t top_k = a.top_k[r];
   const T* in = static_cast<const T*>(a.in) + r * a.in_stride;
   P part;
   part.load(in, rank * a.part, a.part, a.n_vocab);
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, THREADS == 512 &&
   row_sync<THREADS>();
   m = warp_max(sh.wf[0][lane % WARPS]);
   if constexpr (GROUPS == 1) ppl::cluster_wait();  // every block has started
-  const bool some = CUT && top_k > 0 && uint32_t(top_k) < a.n_vocab && !greedy;
+  const bool some = top_k > 0 && uint32_t(top_k) < a.n_vocab && !greedy;
   Cut cut = {0, ~0u};
   if (some) {
     if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, maxima, c, in, out)) return;
@@ -857,6 +858,136 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, THREADS == 512 &&
   });
 }
 
+// ------------------------------------------------------------ rows without a cut
+// A block's part of a row lies in shared memory, each thread's vectors where only
+// it reads them: copies, largest value, sum and writing have no barrier between
+// them but for the exchange of the largest values and the sums.  Few registers and
+// short loops: as many blocks at once as hide one another's latencies.
+template <class T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) plain_kernel(const ProbArgs a) {
+  ppl::cluster_arrive();
+  constexpr int VEC = 16 / sizeof(T), WARPS = THREADS / 32;
+  constexpr int STEP = THREADS * VEC;
+  using Vec = ppl::Pack<T, VEC>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ float part_max[CLUSTER], part_sum[CLUSTER], wmax[WARPS], wsum[WARPS];
+  __shared__ uint32_t part_first[CLUSTER], wfirst[WARPS];
+  const uint32_t rank = blockIdx.x % a.blocks, r = blockIdx.x / a.blocks;
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const T* in = static_cast<const T*>(a.in) + r * a.in_stride;
+  float* out = a.out + r * a.out_stride;
+  // places count from the 16-byte boundary at or before the row's start
+  const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(in) / sizeof(T) % VEC);
+  const uint32_t all = a.n_vocab + shift, to = min((rank + 1) * a.part, all), begin = rank * a.part + threadIdx.x * VEC;
+  const int n = begin < to ? (to - begin + STEP - 1) / STEP : 0;  // vectors with values
+  const int full = begin < shift ? 1 : 0;                         // the first whole one
+  const int whole = begin + VEC <= to ? (to - VEC - begin) / STEP + 1 : 0;  // the one after the last whole one
+  Vec* x = reinterpret_cast<Vec*>(raw) + threadIdx.x;
+  {
+    const T* p = in + (int64_t(begin) - shift);
+    uint32_t slot = uint32_t(__cvta_generic_to_shared(x));
+#pragma unroll 4
+    for (int i = full; i < whole; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + i * THREADS * 16), "l"(p + int64_t(i) * STEP) : "memory");
+    // the incomplete vectors, where the row begins and ends
+    for (int e = full ? 0 : whole; e < n; e = e < whole && whole < n ? whole : n) {
+      const uint32_t j = begin + e * STEP;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) x[e * THREADS].v[k] = j + k >= shift && j + k < all ? in[int64_t(j) + k - shift] : from_f<T>(-INFINITY);
+    }
+  }
+  const float t = a.temperature ? a.temperature[r] : 1.f;
+  const bool greedy = !(t > 0x1p-125f);  // below, c is not a float
+  const float c = 2.88539008f / t;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  float m = -INFINITY;
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const Vec v = x[i * THREADS];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) m = fmaxf(m, to_f(v.v[k]));
+  }
+  m = warp_max(m);
+  if (lane == 0) wmax[warp] = m;
+  __syncthreads();
+  m = warp_max(wmax[lane % WARPS]);
+  // 2^64 times share(f, m, c), which no exponential within a float's range of 1 leaves
+  const bool endless = m == INFINITY;
+  const float half = -0.5f * m;
+  auto ex = [&](float f) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaxf(fmaf(fmaf(f, 0.5f, half), c, 64.f), -200.f)));
+    return endless ? (f == m ? 0x1p64f : 0.f) : e;
+  };
+  float s = 0.f;
+  uint32_t first = ~0u;
+  if (greedy) {
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) first = to_f(x[i * THREADS].v[k]) == m ? min(first, begin + i * STEP + k) : first;
+  } else {
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      Vec v = x[i * THREADS];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float e = ex(to_f(v.v[k]));
+        s += e;
+        if constexpr (sizeof(T) == 4) v.v[k] = e;
+      }
+      if constexpr (sizeof(T) == 4) x[i * THREADS] = v;  // in the values' place
+    }
+  }
+  s = warp_add(s);
+  first = __reduce_min_sync(~0u, first);
+  if (lane == 0) wsum[warp] = s, wfirst[warp] = first;
+  __syncthreads();
+  ppl::cluster_wait();  // every block has started
+  if (warp == 0) {
+    s = warp_add(lane < WARPS ? wsum[lane] : 0.f);
+    first = __reduce_min_sync(~0u, lane < WARPS ? wfirst[lane] : ~0u);
+    if (lane < a.blocks) {
+      put(there(&part_max[rank], lane), m);
+      put(there(&part_sum[rank], lane), s);
+      put(there(&part_first[rank], lane), first);
+    }
+  }
+  ppl::cluster_sync();
+  float top = -INFINITY, total = 0.f;
+  uint32_t best = ~0u;
+  for (uint32_t b = 0; b < a.blocks; ++b) top = fmaxf(top, part_max[b]);
+  for (uint32_t b = 0; b < a.blocks; ++b) {
+    total += part_sum[b] * share(part_max[b], top, c);
+    if (part_max[b] == top && top > -INFINITY) best = min(best, part_first[b]);
+  }
+  const float factor = total > 0.f ? share(m, top, c) / total : 0.f;
+  // the inputs' and the outputs' boundaries agree where their strides do
+  const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
+  float* q = out + (int64_t(begin) - shift);
+#pragma unroll 2
+  for (int i = 0; i < n; ++i, q += STEP) {
+    const Vec v = x[i * THREADS];
+    float p[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const float f = to_f(v.v[k]);
+      p[k] = greedy ? (begin + i * STEP + k == best ? 1.f : 0.f) : (sizeof(T) == 4 ? f : ex(f)) * factor;
+    }
+    if (wide && i >= full && i < whole) {
+      if constexpr (VEC == 8)
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]), "f"(p[4]),
+                     "f"(p[5]), "f"(p[6]), "f"(p[7]) : "memory");
+      else
+        *reinterpret_cast<float4*>(q) = make_float4(p[0], p[1], p[2], p[3]);
+    } else {
+      const uint32_t j = begin + i * STEP;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k)
+        if (j + k >= shift && j + k < all) q[k] = p[k];
+    }
+  }
+}
+
 template <class K>
 cudaError_t launch_as(K kernel, const ProbArgs& a, uint64_t n_rows, int threads, uint32_t smem, cudaStream_t stream, int groups = 1) {
   cudaLaunchAttribute at;
@@ -874,49 +1005,58 @@ cudaError_t launch_as(K kernel, const ProbArgs& a, uint64_t n_rows, int threads,
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <class T, int THREADS_, bool CUT>
-cudaError_t launch_fast(const ProbArgs& a, uint64_t n_rows, uint32_t vectors, cudaStream_t stream) {
+template <class T, int THREADS_>
+cudaError_t launch_cut(const ProbArgs& a, uint64_t n_rows, uint32_t vectors, cudaStream_t stream) {
   const uint32_t nv = (vectors + THREADS_ - 1) / THREADS_;
-  if (nv <= 2) return launch_as(probs_kernel<T, THREADS_, 2, CUT>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
-  if (nv <= 5) return launch_as(probs_kernel<T, THREADS_, 5, CUT>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
-  return launch_as(probs_kernel<T, THREADS_, NV_MOST, CUT>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
+  if (nv <= 2) return launch_as(cut_kernel<T, THREADS_, 2>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
+  if (nv <= 5) return launch_as(cut_kernel<T, THREADS_, 5>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
+  return launch_as(cut_kernel<T, THREADS_, NV_MOST>, a, n_rows, THREADS_, 0, stream, GROUPS_OF<THREADS_>);
+}
+
+// A kernel whose parts lie in shared memory.
+template <class K>
+cudaError_t launch_in_shared(K kernel, ppi::DeviceOnce& once, const ProbArgs& a, uint64_t n_rows, int threads, uint32_t smem, cudaStream_t stream) {
+  int dev;
+  cudaError_t e = ppi::current_device(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run(dev, [&](int) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(RESIDENT_MOST)); });
+  if (e != cudaSuccess) return e;
+  return launch_as(kernel, a, n_rows, threads, smem, stream);
 }
 
 template <class T>
 cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
   constexpr uint32_t VEC = 16 / sizeof(T);
+  static ppi::DeviceOnce once[3];
   const uint32_t vectors = (a.n_vocab + 2 * VEC - 2) / VEC;  // at any alignment
+  // short rows, and enough of them: 128 threads each
+  const bool small = vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256);
   uint32_t blocks = 1;
-  a.blocks = 1;
-  a.part = vectors * VEC;
-  if (vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256))
-    return a.top_k ? launch_fast<T, 128, true>(a, n_rows, vectors, stream) : launch_fast<T, 128, false>(a, n_rows, vectors, stream);
-  if (vectors <= MID * NV_MOST * CLUSTER) {
-    while (blocks < CLUSTER && (vectors > MID * (a.top_k ? NV_MOST : NV_PLAIN) * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
+  auto part = [&] {
     const uint32_t each = (vectors + blocks - 1) / blocks;
     a.blocks = blocks;
     a.part = each * VEC;
-    return a.top_k ? launch_fast<T, MID, true>(a, n_rows, each, stream) : launch_fast<T, MID, false>(a, n_rows, each, stream);
+    return each;
+  };
+  if (small) {
+    part();
+    if (a.top_k) return launch_cut<T, 128>(a, n_rows, vectors, stream);
+    return launch_in_shared(plain_kernel<T, 128>, once[0], a, n_rows, 128, vectors * 16, stream);
+  }
+  if (a.top_k) {
+    // a cluster's part in registers, and more blocks while all of them run at once
+    while (blocks < CLUSTER && (vectors > MID * NV_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
+    const uint32_t each = part();
+    if (each <= MID * NV_MOST) return launch_cut<T, MID>(a, n_rows, each, stream);
+  } else {
+    while (blocks < CLUSTER && (vectors * 16 > PART_MOST * blocks || (n_rows * blocks * 2 <= 528 && vectors >= blocks * 2 * MID))) blocks *= 2;
+    const uint32_t each = part();
+    if (each * 16 <= RESIDENT_MOST) return launch_in_shared(plain_kernel<T, MID>, once[1], a, n_rows, MID, each * 16, stream);
   }
   blocks = CLUSTER;
-  const uint32_t each = (vectors + blocks - 1) / blocks;
-  if (MID < 512 && each <= 512 * NV_MOST) {
-    a.blocks = blocks;
-    a.part = each * VEC;
-    return a.top_k ? launch_fast<T, 512, true>(a, n_rows, each, stream) : launch_fast<T, 512, false>(a, n_rows, each, stream);
-  }
-  static ppi::DeviceOnce once;
-  int dev;
-  cudaError_t e = ppi::current_device(&dev);
-  if (e != cudaSuccess) return e;
-  e = once.run(dev, [&](int) {
-    return cudaFuncSetAttribute(long_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(RESIDENT_MOST));
-  });
-  if (e != cudaSuccess) return e;
-  a.blocks = CLUSTER;
-  a.part = each * VEC;
-  a.resident = a.part * sizeof(T) <= RESIDENT_MOST;
-  return launch_as(long_kernel<T>, a, n_rows, LONG_THREADS, a.resident ? a.part * sizeof(T) : 0, stream);
+  const uint32_t each = part();
+  a.resident = each * 16 <= RESIDENT_MOST;
+  return launch_in_shared(long_kernel<T>, once[2], a, n_rows, LONG_THREADS, a.resident ? each * 16 : 0, stream);
 }
 
 }  // namespace

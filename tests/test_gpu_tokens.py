@@ -130,7 +130,7 @@ def test_probs_in_place_and_without_rows():
     assert pp.token_probs(x[:0]).shape == (0, 5003) and pp.token_probs(x[:, :0]).shape == (6, 0)
 
 
-@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 420001), (torch.bfloat16, 900001)])
+@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 200001), (torch.float32, 420001), (torch.float16, 500000), (torch.bfloat16, 900001)])
 def test_probs_of_rows_beyond_shared_memory(dtype, vocab):
     rng = np.random.default_rng(3)
     x = logits(rng, 2, vocab, dtype)
