@@ -459,23 +459,46 @@ struct Cut {
   uint32_t least, last;
 };
 
-// This thread's entries of all the blocks' lists.  Every block finds the same in them.
+// This thread's entries of all the blocks' lists, in which every block finds the same.
+// Those of a row's only block stay in its list.
 template <int THREADS>
-__device__ __forceinline__ int listed_of(Fast<THREADS>& sh, uint32_t total, float* value, uint32_t* place) {
-  int entries = 0;
+struct Entries {
+  static constexpr int MOST = Fast<THREADS>::ENTRIES;
+  static constexpr bool HELD = GROUPS_OF<THREADS> == 1;
+  float value[HELD ? MOST : 1];
+  uint32_t place[HELD ? MOST : 1];
+  int n;
+  const uint2* list;
+  uint32_t total;
+
+  __device__ __forceinline__ Entries(Fast<THREADS>& sh, uint32_t all) : n(0), list(sh.list), total(all) {
+    if constexpr (HELD) {
 #pragma unroll
-  for (int e = 0; e < Fast<THREADS>::ENTRIES; ++e) {
-    uint32_t i = tid<THREADS>() + e * THREADS, b = 0;
-    if (i < total) {
-      for (uint32_t n; i >= (n = sh.part_n[b]); ++b) i -= n;
-      uint32_t v;
-      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v), "=r"(place[e]) : "r"(there(&sh.list[i], b)) : "memory");
-      value[e] = __uint_as_float(v);
-      ++entries;
+      for (int e = 0; e < MOST; ++e) {
+        uint32_t i = tid<THREADS>() + e * THREADS, b = 0;
+        if (i < total) {
+          for (uint32_t m; i >= (m = sh.part_n[b]); ++b) i -= m;
+          uint32_t v;
+          asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v), "=r"(place[e]) : "r"(there(&sh.list[i], b)) : "memory");
+          value[e] = __uint_as_float(v);
+          ++n;
+        }
+      }
     }
   }
-  return entries;
-}
+  // f(value, place, number of the entry)
+  template <class F>
+  __device__ __forceinline__ void each(F&& f) const {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int e = 0; e < MOST; ++e)
+        if (e < n) f(value[e], place[e], tid<THREADS>() + e * THREADS);
+    } else {
+#pragma unroll 1
+      for (uint32_t i = tid<THREADS>(); i < total; i += THREADS) f(__uint_as_float(list[i].x), list[i].y, i);
+    }
+  }
+};
 
 // The values for which `pick` holds go to the block's list, in any order.  They are few, so
 // they are only marked in the pass over the values, and read again for the list: a
@@ -502,53 +525,43 @@ __device__ __forceinline__ void list_where(P& part, Fast<THREADS>& sh, const T* 
 
 // The cut that keeps `want` of the total listed values, all from reach to top.
 template <class P, int THREADS>
-__device__ __forceinline__ Cut cut_among(Fast<THREADS>& sh, const float* value, const uint32_t* place, int entries, uint32_t total,
-                                         uint32_t want, float top, float reach, uint32_t places) {
-  constexpr int ENTRIES = Fast<THREADS>::ENTRIES, LOW = P::LOW;
-  auto key = [&](int e) { return key_of(value[e]) >> LOW; };
+__device__ __forceinline__ Cut cut_among(Fast<THREADS>& sh, const Entries<THREADS>& entries, uint32_t want, float top, float reach, uint32_t places) {
+  constexpr int LOW = P::LOW;
   const uint32_t hi = key_of(top) >> LOW, lo = key_of(reach) >> LOW;
   Cut cut = {lo, ~0u};  // all candidates
-  if (total > want) {
-    uint32_t in_bin = total;
-    int bits = 32 - __clz(hi ^ lo);  // below those that all candidates share
-    uint32_t known = bits == 32 ? 0 : hi >> bits << bits;
-    while (bits > 0 && want < in_bin) {
-      const int at = max(bits - 8, 0);
-      const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
-      next_digit<THREADS>(sh, want, [&](auto&& add) {
-#pragma unroll
-        for (int e = 0; e < ENTRIES; ++e)
-          if (e < entries && (key(e) & mask) == known) add(key(e) >> at & low);
-      });
-      known |= sh.bin << at;
-      want -= sh.above;
-      in_bin = sh.in_bin;
-      bits = at;
-    }
-    cut.least = known;
-    if (want < in_bin) {  // of those that tie the lowest places
-      const int place_bits = 32 - __clz(places);
-      const uint32_t inside = ~(~0u << place_bits);
-      uint32_t found = 0;
-      for (bits = place_bits; bits > 0 && want < in_bin;) {
-        const int at = max(bits - 8, 0);
-        const uint32_t mask = ~0u << bits, low = (1u << (bits - at)) - 1;
-        next_digit<THREADS>(sh, want, [&](auto&& add) {
-#pragma unroll
-          for (int e = 0; e < ENTRIES; ++e) {
-            const uint32_t q = ~place[e] & inside;
-            if (e < entries && key(e) == cut.least && (q & mask) == found) add(q >> at & low);
-          }
-        });
-        found |= sh.bin << at;
-        want -= sh.above;
-        in_bin = sh.in_bin;
-        bits = at;
+  uint32_t in_bin = entries.total;
+  if (in_bin <= want) return cut;
+  // digit by digit below the bits that all candidates share; then, of those that tie, the places
+  int bits = 32 - __clz(hi ^ lo), side = 0;
+  uint32_t found = bits == 32 ? 0 : hi >> bits << bits;
+  const int place_bits = 32 - __clz(places);
+  const uint32_t inside = ~(~0u << place_bits);
+#pragma unroll 1
+  while (true) {
+    if (want == in_bin || bits == 0) {  // all that agree so far are kept, or the last bit is known
+      if (side) {
+        cut.last = ~found & inside;
+        return cut;
       }
-      cut.last = ~found & inside;
+      cut.least = found;
+      if (want == in_bin) return cut;
+      side = 1;
+      found = 0;
+      bits = place_bits;
     }
+    const int at = max(bits - 8, 0);
+    const uint32_t mask = bits == 32 ? 0 : ~0u << bits, low = (1u << (bits - at)) - 1;
+    next_digit<THREADS>(sh, want, [&](auto&& add) {
+      entries.each([&](float f, uint32_t j, uint32_t) {
+        const uint32_t key = key_of(f) >> LOW, q = side ? ~j & inside : key;
+        if ((!side || key == cut.least) && (q & mask) == found) add(q >> at & low);
+      });
+    });
+    found |= sh.bin << at;
+    want -= sh.above;
+    in_bin = sh.in_bin;
+    bits = at;
   }
-  return cut;
 }
 
 // The cut of any length.  The values from the largest to the least are counted in 256
@@ -560,7 +573,7 @@ template <class T, int THREADS, int NV>
 __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size, uint32_t n_vocab, Fast<THREADS>& sh, uint32_t rank,
                                        uint32_t blocks, uint32_t want) {
   using P = Part<T, THREADS, NV>;
-  constexpr int WARPS = THREADS / 32, LIST = Fast<THREADS>::LIST, ENTRIES = Fast<THREADS>::ENTRIES;
+  constexpr int WARPS = THREADS / 32, LIST = Fast<THREADS>::LIST;
   const uint32_t lane = tid<THREADS>() % 32, warp = tid<THREADS>() / 32;
   P part;
   part.load(in, from, size, n_vocab);
@@ -610,19 +623,15 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
       row_sync<THREADS>();
       if (tid<THREADS>() < blocks) put(there(&sh.part_n[rank], tid<THREADS>()), sh.listed);
       all_sync<THREADS>();
-      float value[ENTRIES];
-      uint32_t place[ENTRIES];
-      const int entries = listed_of(sh, total, value, place);
-#pragma unroll
-      for (int e = 0; e < ENTRIES; ++e)
-        if (e < entries) reach = fminf(reach, value[e]), high = fmaxf(high, value[e]);
+      const Entries<THREADS> entries(sh, total);
+      entries.each([&](float f, uint32_t, uint32_t) { reach = fminf(reach, f), high = fmaxf(high, f); });
       reach = -warp_max(-reach);
       high = warp_max(high);
       if (lane == 0) sh.wf[0][warp] = high, sh.wf[1][warp] = reach;
       all_sync<THREADS>();  // and every block has read what it needs of the others
       high = warp_max(sh.wf[0][lane % WARPS]);
       reach = -warp_max(-sh.wf[1][lane % WARPS]);
-      return cut_among<P>(sh, value, place, entries, total, left, high, reach, part.all);
+      return cut_among<P>(sh, entries, left, high, reach, part.all);
     }
     all_sync<THREADS>();  // the counts are read
   }
@@ -669,7 +678,7 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
 template <class P, int THREADS, int G, class T>
 __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t rank, uint32_t blocks, uint32_t top_k, float m,
                                           const float (&maxima)[G], float c, const T* in, float* out) {
-  constexpr int LIST = Fast<THREADS>::LIST, ENTRIES = Fast<THREADS>::ENTRIES, LOW = P::LOW;
+  constexpr int LIST = Fast<THREADS>::LIST, LOW = P::LOW;
   const uint32_t k_part = (top_k + blocks - 1) / blocks;
   const bool every = k_part > THREADS * G;  // only where the lists have room for the row
   if (every && part.all > LIST) return false;
@@ -711,28 +720,27 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
     total += sh.part_n[b];
   }
   if (total > LIST) return false;
-  float value[ENTRIES];
-  uint32_t place[ENTRIES];
-  const int entries = listed_of(sh, total, value, place);
+  const Entries<THREADS> entries(sh, total);
   if constexpr (GROUPS_OF<THREADS> == 1) ppl::cluster_arrive_release();  // this block has read what it needs of the others
   // Zeros everywhere: the few others are written over them once they are known.
   part.write(out, [&](int, float* p) {
 #pragma unroll
     for (int k = 0; k < P::VEC; ++k) p[k] = 0.f;
   });
-  const Cut cut = cut_among<P>(sh, value, place, entries, total, top_k, top, reach, part.all);
-  auto key = [&](int e) { return key_of(value[e]) >> LOW; };
+  const Cut cut = cut_among<P>(sh, entries, top_k, top, reach, part.all);
+  auto kept = [&](float f, uint32_t j) {
+    const uint32_t key = key_of(f) >> LOW;
+    return key > cut.least || (key == cut.least && j <= cut.last);
+  };
   // The lists' order is not the same each time, so the sum is one of whole numbers: units
   // of 2^-44, of exponentials up to 1 of which one is.
-  float p[ENTRIES];
   unsigned long long s = 0;
-#pragma unroll
-  for (int e = 0; e < ENTRIES; ++e) {
-    p[e] = e < entries && (key(e) > cut.least || (key(e) == cut.least && place[e] <= cut.last)) ? share(value[e], top, c) : 0.f;
-    const float high = p[e] * 0x1p22f;
+  entries.each([&](float f, uint32_t j, uint32_t) {
+    if (!kept(f, j)) return;
+    const float high = share(f, top, c) * 0x1p22f;
     const uint32_t whole = __float2uint_rz(high);
     s += (uint64_t(whole) << 22) + __float2uint_rz((high - float(whole)) * 0x1p22f);
-  }
+  });
 #pragma unroll
   for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
   if (tid<THREADS>() % 32 == 0) sh.sums[tid<THREADS>() / 32] = s;
@@ -741,9 +749,9 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
 #pragma unroll
   for (int d = THREADS / 64; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
   const float factor = s ? 1.f / (float(uint32_t(s >> 22)) * 0x1p-22f + float(uint32_t(s) & 0x3FFFFF) * 0x1p-44f) : 0.f;
-#pragma unroll
-  for (int e = 0; e < ENTRIES; ++e)  // after the zeros: there were barriers since
-    if (e < entries && tid<THREADS>() + e * THREADS - own < mine && p[e] > 0.f) out[int64_t(place[e]) - part.shift] = p[e] * factor;
+  entries.each([&](float f, uint32_t j, uint32_t i) {  // over the zeros: there were barriers since
+    if (i - own < mine && kept(f, j)) out[int64_t(j) - part.shift] = share(f, top, c) * factor;
+  });
   if constexpr (GROUPS_OF<THREADS> == 1) ppl::cluster_wait();
   return true;
 }
@@ -1049,7 +1057,7 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
     const uint32_t each = part();
     if (each <= MID * NV_MOST) return launch_cut<T, MID>(a, n_rows, each, stream);
   } else {
-    while (blocks < CLUSTER && (vectors * 16 > PART_MOST * blocks || (n_rows * blocks * 2 <= 528 && vectors >= blocks * 2 * MID))) blocks *= 2;
+    while (blocks < CLUSTER && (vectors * 16 > PART_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
     const uint32_t each = part();
     if (each * 16 <= RESIDENT_MOST) return launch_in_shared(plain_kernel<T, MID>, once[1], a, n_rows, MID, each * 16, stream);
   }
