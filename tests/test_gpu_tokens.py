@@ -382,3 +382,18 @@ def test_a_drafted_answer_keeps_to_the_grammar():
     none = pp.token_probs(pp.process_logits(raw[:1], grammar=g, states=torch.tensor([255], dtype=torch.uint8, device="cuda")))
     t, c = pp.verify_drafts(none, drafts[:1, :0], accept[:1, :0], sample[:1])
     assert t.tolist() == [[-1]] and c.tolist() == [0]
+
+
+@pytest.mark.parametrize("seed,drafted", [(1, 3), (2, 1), (3, 0), (4, 7)])
+def test_the_example_answers_what_parses_however_much_is_drafted(seed, drafted):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "grammar_rows.py")
+    spec = importlib.util.spec_from_file_location("grammar_rows", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    out = example.run(seed=seed, drafted=drafted)
+    assert out["same_states"] and out["said"] > 0 and out["rounds"] <= 48
+    done = [p for p in out["parsed"] if p is not None]
+    assert all(p["error"] & pp.ERR_FATAL == 0 for p in done)
+    assert all(p is not None for p, over in zip(out["parsed"], out["over"]) if over)
