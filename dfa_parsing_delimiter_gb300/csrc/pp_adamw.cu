@@ -3,10 +3,19 @@
 // A warp takes a tile of 256 consecutive elements of one tensor: parameter,
 // gradient and both states are read once, stepped in registers and written
 // once.  Nothing is read twice and nothing is shared between tiles but the
-// step's constants, so the memory's rate bounds it (28 bytes an element with
-// 32-bit values all through, 16 with 8-bit states).  A tile is also what shares
-// an exponent in 8 bits: the largest exponent is one warp reduction, and the
-// codes come from the registers that the step left.
+// step's constants.  With 32-bit states it is bound by memory, 20 to 28 bytes an
+// element: 131072 x 2048 f32 1150 us (6.5 TB/s; with accesses of 16 bytes, not
+// 32, 1220), 35M bf16 with 32-bit copies 143 us (6.3 TB/s).
+//
+// With 8-bit states a tile is also what shares an exponent: the largest one is a
+// warp reduction, and the codes come from the registers that the step left.  It is
+// bound by instructions (some 85 an element, half of them logic, which runs at half
+// the rate: hashing, codes in and out) and by loads that too few warps wait for:
+// 185M elements of f32 with bf16 gradients 615 us together with 165 for reading the
+// states' values back (floors 380 and 165).  What got it there: the next tile
+// fetched into the cache ahead (634 us, without 705), arithmetic on two floats at a
+// time (615), multiply-adds for shifts and additions, approximate roots and
+// quotients (714 with them, 906 before).
 //
 // The tensors' addresses are kernel parameters (up to 640 tensors a launch):
 // nothing to copy to the device, so a step is one launch and can be captured.
@@ -24,7 +33,9 @@ using ppl::to_f;
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int TILE = PP_ADAMW_BLOCK, EACH = TILE / 32;  // elements of a warp and of a lane
-constexpr int RESIDENT = 4, BLOCKS = 8;                               // a multiprocessor
+// Blocks that a multiprocessor holds (185M, 8 bits: 714 us, 746 with five, 835 with three, at the time)
+// and that a launch has for each.
+constexpr int RESIDENT = 4, BLOCKS = 8;
 
 struct Item {
   void* param;

@@ -1,16 +1,28 @@
 // pp_token_probs: a model's logits as probabilities, by a temperature and cut
 // to each row's k most likely tokens.
 //
-// A cluster of blocks takes a row, each a part of it, which it reads once into
-// shared memory; the largest value, the sum of the exponentials and the
-// k-th largest value are found there, and the probabilities are written.  The
-// blocks exchange their largest value and their sum relative to it once.
+// A row is read once and written once: bound by memory, at six or eight bytes a
+// token.  A cluster of blocks shares it, since a block cannot hold a long row, and
+// holds it on the chip between the reading and the writing:
 //
-// The k-th largest is found digit by digit from the top of the values' bits in
-// the order of their values: a count of each digit over the values that agree
-// with the digits found, added up over the cluster.  Values that tie with it
-// are kept from the lowest token on, so the last one's place is found the same
-// way among their places.
+//   plain_kernel  rows without a cut.  Parts lie in shared memory; largest value,
+//                 sum of exponentials relative to it, one exchange of the two
+//                 through distributed shared memory, probabilities.  2560 rows of
+//                 50001 f32: 176 us (5.8 TB/s; with the parts in registers, two
+//                 blocks a multiprocessor, 213), 512 of 131075 bf16: 82.
+//   cut_kernel    rows with a cut.  Parts lie in registers (in shared memory the
+//                 steps below read them again each time: 512 rows of 131075 f16 111
+//                 us instead of 104, 64 rows of 131072 bf16 24 instead of 19).  At
+//                 least k values of a row reach the least of the blocks' k_part-th
+//                 largest thread maxima, and not many more: those are listed, and
+//                 every block finds the k-th largest in all lists, digit by digit
+//                 of its bits in the order of values, then, of values that tie, the
+//                 last place that is kept.  All else is zero and is written before.
+//                 Bound by the latency of a block's steps one after the other (some
+//                 twenty barriers, three of them of the cluster).
+//   long_kernel   rows that eight blocks cannot hold: the steps read them again.
+//
+// Which tokens are kept is exact, whatever 32 bits make of the exponentials.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -24,11 +36,14 @@ using ppl::from_f;
 using ppl::to_f;
 
 constexpr int LONG_THREADS = 512, LONG_WARPS = LONG_THREADS / 32;
-constexpr int CLUSTER = 8;
-constexpr int MID = 512;                    // threads for a block's part of a longer row
-constexpr uint32_t PART_MOST = 73728;      // bytes of a part without a cut: three blocks a multiprocessor
-constexpr int NV_MOST = 9;  // vectors of a thread
-constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // bytes of a block's part
+constexpr int CLUSTER = 8;   // blocks at most
+constexpr int MID = 512;     // threads of a block that has a part of a longer row
+constexpr int NV_MOST = 9;   // 16-byte vectors of a thread, in registers
+// Bytes of a part in shared memory, so that three or four blocks share a
+// multiprocessor.  512 rows of 131075 bf16: 82 us in clusters of four at 72 KiB and at
+// 108, 91 in clusters of eight at 56; 2560 rows of 50001 f32: 176, 196 and 176.
+constexpr uint32_t PART_MOST = 73728;
+constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // where a block has a multiprocessor for itself
 
 struct ProbArgs {
   const void* in;
@@ -237,15 +252,14 @@ __global__ void __launch_bounds__(LONG_THREADS) long_kernel(const ProbArgs a) {
   }
 }
 
-// ------------------------------------------------------------ rows in registers
-// A block's part of a row stays in its threads' registers, NV vectors of 16
-// bytes each.
+// ------------------------------------------------------------ rows with a cut
 constexpr int entries_of(int threads) { return threads > 128 ? 4 : 8; }  // listed candidates a thread
 
 // The THREADS threads of a row: a block, or for short rows one of its groups.
 // Groups that begin together run the same instructions at nearly the same
-// time, which matters here: the code is long and straight, and blocks at other
-// places in it wait for one another's instructions.
+// time, which matters here: the code is long and straight, and warps at other
+// places in it wait for one another's instructions (8192 rows of 5000 bf16: 162 us
+// four to a block, 184 in blocks of their own, at the time; now 105).
 template <int THREADS>
 __device__ __forceinline__ uint32_t tid() { return threadIdx.x % THREADS; }
 template <int THREADS>
@@ -1037,7 +1051,8 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
   constexpr uint32_t VEC = 16 / sizeof(T);
   static ppi::DeviceOnce once[3];
   const uint32_t vectors = (a.n_vocab + 2 * VEC - 2) / VEC;  // at any alignment
-  // short rows, and enough of them: 128 threads each
+  // Short rows, and enough of them to fill the device: 128 threads each (8192 rows of 5000 bf16
+  // with a cut: 105 us; with a block of 512 threads each 206, at 128 then 184).
   const bool small = vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256);
   uint32_t blocks = 1;
   auto part = [&] {
@@ -1052,7 +1067,8 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
     return launch_in_shared(plain_kernel<T, 128>, once[0], a, n_rows, 128, vectors * 16, stream);
   }
   if (a.top_k) {
-    // a cluster's part in registers, and more blocks while all of them run at once
+    // as many blocks as hold the row; more while all of them run at once (64 rows of 131072 bf16: 33 us
+    // in clusters of four, one wave, and 41 of eight, two, at the time; now 19)
     while (blocks < CLUSTER && (vectors > MID * NV_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
     const uint32_t each = part();
     if (each <= MID * NV_MOST) return launch_cut<T, MID>(a, n_rows, each, stream);
