@@ -4,18 +4,18 @@
 // gradient and both states are read once, stepped in registers and written
 // once.  Nothing is read twice and nothing is shared between tiles but the
 // step's constants.  With 32-bit states it is bound by memory, 20 to 28 bytes an
-// element: 131072 x 2048 f32 1150 us (6.5 TB/s; with accesses of 16 bytes, not
-// 32, 1220), 35M bf16 with 32-bit copies 143 us (6.3 TB/s).
+// element: 131072 x 2048 f32 1125 us (6.7 TB/s; with accesses of 16 bytes, not
+// 32, 1220), 35M bf16 with 32-bit copies 142 us (6.3 TB/s).
 //
 // With 8-bit states a tile is also what shares an exponent: the largest one is a
 // warp reduction, and the codes come from the registers that the step left.  It is
 // bound by instructions (some 85 an element, half of them logic, which runs at half
 // the rate: hashing, codes in and out) and by loads that too few warps wait for:
-// 185M elements of f32 with bf16 gradients 615 us together with 165 for reading the
+// 185M elements of f32 with bf16 gradients 597 us together with 165 for reading the
 // states' values back (floors 380 and 165).  What got it there: the next tile
 // fetched into the cache ahead (634 us, without 705), arithmetic on two floats at a
-// time (615), multiply-adds for shifts and additions, approximate roots and
-// quotients (714 with them, 906 before).
+// time (615), roots and quotients that flush (597), multiply-adds for shifts and
+// additions (714 with them and approximate quotients, 906 before).
 //
 // The tensors' addresses are kernel parameters (up to 640 tensors a launch):
 // nothing to copy to the device, so a step is one launch and can be captured.
@@ -260,17 +260,53 @@ __device__ __forceinline__ void write_codes(uint8_t* p, uint32_t lane, uint32_t 
 }
 
 // The square root and the quotient of the step are each within 2^-22 of their
-// values, as is the rate: what a parameter changes by is exact to 22 bits or so.
+// values, as is the rate: what a parameter changes by is exact to 20 bits or so.
+// FLUSH: numbers below 2^-126 count as zero, which takes fewer instructions (185M
+// elements, 8 bits: 597 us, 615 without) and makes no difference to a root of 2^-63
+// beside an eps of 2^-40 or more.
+template <bool FLUSH>
 __device__ __forceinline__ float root_of(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  if constexpr (FLUSH) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  else asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+template <bool FLUSH>
+__device__ __forceinline__ float quotient(float x, float y) {
+  if constexpr (!FLUSH) return __fdividef(x, y);
+  float q;
+  asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(q) : "f"(x), "f"(y));
+  return q;
 }
 
 struct Constants {
   float lr, scale, rate, root;  // root: of 1 / (1 - beta2^t)
   uint32_t key;
+  bool flush;
 };
+
+// A lane's elements, a step on.
+template <bool FLUSH>
+__device__ __forceinline__ void step_values(const Common& c, const Constants& d, float keep, float* p, const float* g, float* m, float* v) {
+#pragma unroll
+  for (int k = 0; k < EACH; k += 2) {
+    const Two x = Two(g[k], g[k + 1]) * Two(d.scale);
+    // each product and sum rounded by itself: the states are the formula's, bit by bit
+    // (sums by themselves: two packed ones become a fused one)
+    float more[2], above[2], below[2];
+    (Two(m[k], m[k + 1]) * Two(c.b1)).get(m[k], m[k + 1]);
+    (x * Two(c.c1)).get(more[0], more[1]);
+    m[k] = __fadd_rn(m[k], more[0]);
+    m[k + 1] = __fadd_rn(m[k + 1], more[1]);
+    (Two(v[k], v[k + 1]) * Two(c.b2)).get(v[k], v[k + 1]);
+    (x * x * Two(c.c2)).get(more[0], more[1]);
+    v[k] = __fadd_rn(v[k], more[0]);
+    v[k + 1] = __fadd_rn(v[k + 1], more[1]);
+    (Two(m[k], m[k + 1]) * Two(-d.rate)).get(above[0], above[1]);
+    fma2(Two(root_of<FLUSH>(v[k]), root_of<FLUSH>(v[k + 1])), Two(d.root), Two(c.eps)).get(below[0], below[1]);
+    fma2(Two(p[k], p[k + 1]), Two(keep), Two(quotient<FLUSH>(above[0], below[0]), quotient<FLUSH>(above[1], below[1]))).get(p[k], p[k + 1]);
+  }
+}
 
 // One tile of n elements, at `at` of its tensor.
 template <int BITS, bool WHOLE>
@@ -308,24 +344,8 @@ __device__ __forceinline__ void step_tile(const Common& c, const Constants& d, c
     decode_all<TOP_V>(cv, ev, v);
   }
   const float keep = 1.f - d.lr * t.decay;
-#pragma unroll
-  for (int k = 0; k < EACH; k += 2) {
-    const Two x = Two(g[k], g[k + 1]) * Two(d.scale);
-    // each product and sum rounded by itself: the states are the formula's, bit by bit
-    // (sums by themselves: two packed ones become a fused one)
-    float more[2], above[2], below[2];
-    (Two(m[k], m[k + 1]) * Two(c.b1)).get(m[k], m[k + 1]);
-    (x * Two(c.c1)).get(more[0], more[1]);
-    m[k] = __fadd_rn(m[k], more[0]);
-    m[k + 1] = __fadd_rn(m[k + 1], more[1]);
-    (Two(v[k], v[k + 1]) * Two(c.b2)).get(v[k], v[k + 1]);
-    (x * x * Two(c.c2)).get(more[0], more[1]);
-    v[k] = __fadd_rn(v[k], more[0]);
-    v[k + 1] = __fadd_rn(v[k + 1], more[1]);
-    (Two(m[k], m[k + 1]) * Two(-d.rate)).get(above[0], above[1]);
-    fma2(Two(root_of(v[k]), root_of(v[k + 1])), Two(d.root), Two(c.eps)).get(below[0], below[1]);
-    fma2(Two(p[k], p[k + 1]), Two(keep), Two(__fdividef(above[0], below[0]), __fdividef(above[1], below[1]))).get(p[k], p[k + 1]);
-  }
+  if (d.flush) step_values<true>(c, d, keep, p, g, m, v);
+  else step_values<false>(c, d, keep, p, g, m, v);
   write_any<WHOLE>(t.param, t.param_type, at, lane, n, p);
   if (c.master) write<WHOLE>(c.master + s, lane, n, p);
   if (BITS == 32) {
@@ -371,6 +391,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) adamw_kernel(const __grid_c
   d.rate = d.lr / -expm1f(float(step) * c.log_b1);
   d.root = 1.f / sqrtf(-expm1f(float(step) * c.log_b2));
   d.key = mix(mix(c.seed) + uint32_t(step));
+  d.flush = c.eps >= 0x1p-40f;
   // a block takes c.chunk tiles a turn, for which a tensor is looked up once
   for (uint32_t chunk = blockIdx.x * c.chunk; chunk < c.n_tiles; chunk += gridDim.x * c.chunk) {
     uint32_t i = 0;  // the last tensor that begins at or before the chunk

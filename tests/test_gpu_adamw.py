@@ -132,6 +132,20 @@ def test_first_step_from_zeros(bits):
     m.step_and_check(betas=(0.5, 0.0), decay=[0.0, 0.1, 0.2, 0.3, 0.4, 0.5, 0.6, 0.7, 0.8])
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 2.0 ** -41, 2.0 ** -40, 1e-3])
+def test_small_and_large_eps(bits, eps):
+    """Also where a square is a subnormal number beside it."""
+    m = Model(14, bits=bits)
+    m.step_and_check(eps=eps)
+    if bits == 32:  # (in 8 bits a block's largest decides)
+        m.state.exp_avg.mul_(1e-16)
+        m.state.exp_avg_sq.mul_(1e-36)
+        for g in m.grads:
+            g.mul_(1e-19)
+        m.step_and_check(eps=eps, lr=1.0)
+
+
 def test_many_steps_done():
     m = Model(4)
     m.state.step.fill_(2 ** 30)
