@@ -161,8 +161,12 @@ def adamw_step(params, grads, state: AdamWState, lr=1e-3, betas=(0.9, 0.999), ep
     one for each.  lr may be, and grad_scale (which the gradients are
     multiplied by) and skip (not 0: nothing changes) are, one float32 on the
     device, which a captured graph reads anew each time."""
+    if not isinstance(params, (list, tuple)):
+        params = list(params)
     if grads is None:
         grads = [p.grad for p in params]
+    elif not isinstance(grads, (list, tuple)):
+        grads = list(grads)
     like = state._counters
     lr_at = 0
     if isinstance(lr, torch.Tensor):

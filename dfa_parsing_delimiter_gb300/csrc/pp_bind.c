@@ -245,7 +245,7 @@ static PyObject* adamw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject* seq[5] = {NULL};
   pp_adamw_tensor* t = NULL;
   PyObject* result = NULL;
-  const int one = PyFloat_Check(a[4]) || PyLong_Check(a[4]);
+  const int one = PyFloat_Check(a[4]) || PyLong_Check(a[4]) || (PyNumber_Check(a[4]) && !PySequence_Check(a[4]));
   for (int k = 0; k < (one ? 4 : 5); ++k)
     if (!(seq[k] = PySequence_Fast(a[k], "want sequences of tensors and numbers"))) goto done;
   const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq[2]);

@@ -346,6 +346,19 @@ def test_streams_and_graphs(bits):
         assert all(torch.equal(x, y) for x, y in zip(m.params, n.params)) and int(m.state.step) == 13
 
 
+def test_parameters_from_an_iterator():
+    """As torch.nn modules give them; and numbers that are no floats of Python's."""
+    model = torch.nn.Sequential(torch.nn.Linear(7, 30), torch.nn.Linear(30, 2)).cuda()
+    other = [p.detach().clone() for p in model.parameters()]
+    a, b = pp.adamw_state(model.parameters()), pp.adamw_state(other)
+    model(torch.ones(3, 7, device="cuda")).square().sum().backward()
+    grads = [p.grad for p in model.parameters()]
+    pp.adamw_step(model.parameters(), None, a, lr=0.1, weight_decay=np.float32(0.25))
+    pp.adamw_step(iter(other), iter(grads), b, lr=np.float64(0.1), weight_decay=(0.25 for _ in grads))
+    assert all(torch.equal(x, y) for x, y in zip(model.parameters(), other))
+    assert [p._version for p in other] == [1] * 4
+
+
 def test_master_copies_add_up_small_steps():
     """Steps of a hundredth of a bfloat16's: without 32-bit copies they are lost."""
     w = torch.ones(1000, dtype=torch.bfloat16, device="cuda")
