@@ -762,7 +762,7 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
   s = sh.sums[tid<THREADS>() % (THREADS / 32)];
 #pragma unroll
   for (int d = THREADS / 64; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
-  const float factor = s ? 1.f / (float(uint32_t(s >> 22)) * 0x1p-22f + float(uint32_t(s) & 0x3FFFFF) * 0x1p-44f) : 0.f;
+  const float factor = s ? 1.f / (float(uint32_t(s >> 32)) * 0x1p-12f + float(uint32_t(s)) * 0x1p-44f) : 0.f;
   entries.each([&](float f, uint32_t j, uint32_t i) {  // over the zeros: there were barriers since
     if (i - own < mine && kept(f, j)) out[int64_t(j) - part.shift] = share(f, top, c) * factor;
   });

@@ -154,6 +154,55 @@ def test_probs_past_32_bit_offsets():
     assert (got[7] > 0).sum() == 100 and (got[7, :100] > 0).all()
 
 
+def kinds_of_rows(rng, vocab):
+    """Rows on which a cut takes each of its ways: values spread, alike, far from one another, few, masked."""
+    x = rng.normal(0, 3, (9, vocab))
+    x[1] = np.round(x[1])  # ties everywhere
+    x[2] = 0.25
+    x[3, vocab // 2] = -60000.0  # one far below, so that the others share a step
+    x[4] = np.where(rng.random(vocab) < 0.97, -np.inf, x[4])
+    x[5, ::2] = np.nan
+    x[6] = np.arange(vocab) % 7 * 1e-3
+    x[7, :3] = np.inf
+    x[8] = np.exp(x[8])
+    return x
+
+
+@pytest.mark.parametrize("dtype", FT)
+@pytest.mark.parametrize("vocab", [1500, 9000, 20011, 70001, 131075])
+def test_probs_of_long_cuts(dtype, vocab):
+    """Cuts of more than the lists of candidates hold, in clusters of one to eight blocks."""
+    x = dev(kinds_of_rows(np.random.default_rng(vocab), vocab), dtype)
+    for k in (129, 600, 1025, 2049, 5000, vocab // 2, vocab - 1):
+        k = np.full(9, k, np.int32)
+        check(pp.token_probs(x, top_k=dev(k)), x, None, k)
+    biggest = torch.finfo(dtype).max
+    x[0, ::3], x[0, 1::3] = biggest, -biggest  # further apart than a float
+    x[8, 5] = biggest
+    k = np.full(9, vocab // 2 + 1, np.int32)
+    check(pp.token_probs(x, top_k=dev(k), temperature=dev(np.full(9, 1e30, np.float32))), x, np.full(9, 1e30), k)
+
+
+@pytest.mark.parametrize("dtype", FT)
+@pytest.mark.parametrize("rows,vocab", [(609, 257), (610, 1027), (611, 4600), (1215, 33)])
+def test_probs_of_many_short_rows(dtype, rows, vocab):
+    """Several rows a block, the last of which has fewer; every length of a cut at once."""
+    rng = np.random.default_rng(rows)
+    kinds = kinds_of_rows(rng, vocab)
+    x = kinds[rng.integers(0, 9, rows)] + 0.0
+    x[::2] = rng.normal(0, 2, x[::2].shape)
+    x = dev(x, dtype)
+    k = rng.integers(0, vocab + 2, rows).astype(np.int32)
+    k[::3] = np.minimum(k[::3], 5)
+    t = rng.uniform(0.2, 3, rows).astype(np.float32)
+    t[::17] = 0
+    check(pp.token_probs(x, temperature=dev(t), top_k=dev(k)), x, t, k)
+    check(pp.token_probs(x, temperature=dev(t)), x, t)
+    again = x.float().clone()
+    want = pp.token_probs(again, top_k=dev(k))
+    assert torch.equal(pp.token_probs(again, top_k=dev(k), out=again), want)
+
+
 def test_probs_has_no_derivative():
     x = torch.randn(2, 50, device="cuda", requires_grad=True)
     y = pp.token_probs(x)
@@ -215,6 +264,16 @@ def test_verify(dtype, n, k, vocab, ragged):
         run(a, target_row=None, draft_row=None, lengths=None)
 
 
+@pytest.mark.parametrize("dtype", FT)
+@pytest.mark.parametrize("vocab", [1, 2, 64, 65, 32768, 32769, 65536, 65537])
+def test_verify_of_the_largest_sums(dtype, vocab):
+    """All weights 1: sums up to 2^62 units, on both sides of where a probability takes another digit."""
+    p = torch.ones(8, vocab, device="cuda", dtype=dtype)
+    sample = np.array([0, 0.25, 0.5, 0.999, 1 - 2.0 ** -24, 2.0 ** -31, 1e-9, 0.75], np.float32)
+    run(dict(target=p, drafts=np.zeros((8, 0), int), accept=np.zeros((8, 0), np.float32), sample=sample))
+    run(dict(target=p, drafts=np.zeros((4, 1), int), accept=np.array([[0.5], [0.99], [0.0], [1.0]], np.float32), sample=sample[:4]))
+
+
 @pytest.mark.parametrize("itype", IT)
 def test_verify_token_types(itype):
     a = drafted(np.random.default_rng(5), 20, 4, 120, True)
@@ -266,6 +325,8 @@ def test_verify_of_bad_tokens_rows_and_numbers():
     q[2::4, 1::2] = -torch.inf
     run(b, target=p, draft_probs=q)
     run(b, target=torch.zeros_like(p))
+    run(b, target=torch.ones_like(p))  # sums of what is no distribution
+    run(a, target=torch.ones_like(p), draft_probs=torch.full_like(q, 1e-3))
     run(b, target=p[:0])
     run(a, draft_probs=a["target"][:96], target=a["target"])  # mostly others' rows
 
