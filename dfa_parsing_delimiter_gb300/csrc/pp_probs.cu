@@ -20,7 +20,8 @@
 //                 last place that is kept.  All else is zero and is written before.
 //                 Bound by the latency of a block's steps one after the other (some
 //                 twenty barriers, three of them of the cluster).
-//   long_kernel   rows that eight blocks cannot hold: the steps read them again.
+//   long_kernel   rows that eight blocks cannot hold: the steps read them again
+//                 (64 rows of 900001 bf16 290 us, with a cut 1100).
 //
 // Which tokens are kept is exact, whatever 32 bits make of the exponentials.
 #include <algorithm>
@@ -38,6 +39,7 @@ using ppl::to_f;
 constexpr int LONG_THREADS = 512, LONG_WARPS = LONG_THREADS / 32;
 constexpr int CLUSTER = 8;   // blocks at most
 constexpr int MID = 512;     // threads of a block that has a part of a longer row
+constexpr int LARGE = 1024;  // and of the longest rows with a cut
 constexpr int NV_MOST = 9;   // 16-byte vectors of a thread, in registers
 // Bytes of a part in shared memory, so that three or four blocks share a
 // multiprocessor.  512 rows of 131075 bf16: 82 us in clusters of four at 72 KiB and at
@@ -440,12 +442,13 @@ struct Part {
         for (int k = 0; k < VEC; ++k) x[i].v[k] = from_f<T>(f(to_f(x[i].v[k]), at(i) + k));
       }
   }
+  // The inputs' and the outputs' boundaries agree where their strides do.
+  __device__ __forceinline__ bool wide(const float* out) const { return (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0; }
   // f(i, p) fills the VEC probabilities p of vector i.
   template <class F>
   __device__ __forceinline__ void write(float* out, F&& f) {
     forget();
-    // the inputs' and the outputs' boundaries agree where their strides do
-    const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
+    const bool wide = this->wide(out);
     float* to = out + (int64_t(begin) - shift);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -691,7 +694,7 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
 // reaches a bound that at least top_k values reach; false where not.
 template <class P, int THREADS, int G, class T>
 __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t rank, uint32_t blocks, uint32_t top_k, float m,
-                                          const float (&maxima)[G], float c, const T* in, float* out) {
+                                          const float (&maxima)[G], float c, const T* in, uint32_t size, float* out) {
   constexpr int LIST = Fast<THREADS>::LIST, LOW = P::LOW;
   const uint32_t k_part = (top_k + blocks - 1) / blocks;
   const bool every = k_part > THREADS * G;  // only where the lists have room for the row
@@ -737,10 +740,16 @@ __device__ __forceinline__ bool write_cut(P& part, Fast<THREADS>& sh, uint32_t r
   const Entries<THREADS> entries(sh, total);
   if constexpr (GROUPS_OF<THREADS> == 1) ppl::cluster_arrive_release();  // this block has read what it needs of the others
   // Zeros everywhere: the few others are written over them once they are known.
-  part.write(out, [&](int, float* p) {
+  if (part.wide(out)) {
+    part.write(out, [&](int, float* p) {
 #pragma unroll
-    for (int k = 0; k < P::VEC; ++k) p[k] = 0.f;
-  });
+      for (int k = 0; k < P::VEC; ++k) p[k] = 0.f;
+    });
+  } else {  // so that a warp's lie side by side (512 rows of 131075 f16: 115 us, and 315 vector by vector)
+    const uint32_t from = part.begin - tid<THREADS>() * P::VEC;
+#pragma unroll 4
+    for (uint32_t j = max(from, part.shift) + tid<THREADS>(); j < min(from + size, part.all); j += THREADS) out[j - part.shift] = 0.f;
+  }
   const Cut cut = cut_among<P>(sh, entries, top_k, top, reach, part.all);
   auto kept = [&](float f, uint32_t j) {
     const uint32_t key = key_of(f) >> LOW;
@@ -810,7 +819,7 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS *
   const bool some = top_k > 0 && uint32_t(top_k) < a.n_vocab && !greedy;
   Cut cut = {0, ~0u};
   if (some) {
-    if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, maxima, c, in, out)) return;
+    if (write_cut(part, sh, rank, a.blocks, uint32_t(top_k), m, maxima, c, in, a.part, out)) return;
     cut = cut_of_all<T, THREADS, NV>(in, rank * a.part, a.part, a.n_vocab, sh, rank, a.blocks, uint32_t(top_k));
     part.load(in, rank * a.part, a.part, a.n_vocab);  // again, rather than kept in registers meanwhile
   }
@@ -985,17 +994,25 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) plain_kernel(const Pr
   const float factor = total > 0.f ? share(m, top, c) / total : 0.f;
   // the inputs' and the outputs' boundaries agree where their strides do
   const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
+  auto probability = [&](float f, uint32_t j) { return greedy ? (j == best ? 1.f : 0.f) : (sizeof(T) == 4 ? f : ex(f)) * factor; };
+  // Elsewhere value by value, so that a warp's lie side by side: 512 rows of 131075 f16 93 us, 82 where the
+  // boundaries agree (226 with the values of a vector one after the other).
+  if (!wide) {
+    const uint32_t from = rank * a.part;
+    const T* y = reinterpret_cast<const T*>(raw);
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t j = max(from, shift) + threadIdx.x; j < to; j += THREADS) out[j - shift] = probability(to_f(y[j - from]), j);
+    return;
+  }
   float* q = out + (int64_t(begin) - shift);
 #pragma unroll 2
   for (int i = 0; i < n; ++i, q += STEP) {
     const Vec v = x[i * THREADS];
     float p[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const float f = to_f(v.v[k]);
-      p[k] = greedy ? (begin + i * STEP + k == best ? 1.f : 0.f) : (sizeof(T) == 4 ? f : ex(f)) * factor;
-    }
-    if (wide && i >= full && i < whole) {
+    for (int k = 0; k < VEC; ++k) p[k] = probability(to_f(v.v[k]), begin + i * STEP + k);
+    if (i >= full && i < whole) {
       if constexpr (VEC == 8)
         asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]), "f"(p[4]),
                      "f"(p[5]), "f"(p[6]), "f"(p[7]) : "memory");
@@ -1072,6 +1089,8 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
     while (blocks < CLUSTER && (vectors > MID * NV_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
     const uint32_t each = part();
     if (each <= MID * NV_MOST) return launch_cut<T, MID>(a, n_rows, each, stream);
+    // a multiprocessor a block (64 rows of 200064 f32, k = 50: 53 us, 185 in long_kernel; of 500000 bf16 77 and 651)
+    if (each <= LARGE * NV_MOST) return launch_as(cut_kernel<T, LARGE, NV_MOST>, a, n_rows, LARGE, 0, stream);
   } else {
     while (blocks < CLUSTER && (vectors * 16 > PART_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
     const uint32_t each = part();

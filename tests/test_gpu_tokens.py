@@ -183,6 +183,38 @@ def test_probs_of_long_cuts(dtype, vocab):
     check(pp.token_probs(x, top_k=dev(k), temperature=dev(np.full(9, 1e30, np.float32))), x, np.full(9, 1e30), k)
 
 
+@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 147461), (torch.float32, 262144), (torch.float16, 294919), (torch.bfloat16, 510007)])
+def test_probs_of_the_longest_cuts(dtype, vocab):
+    """Rows that only eight of the largest blocks hold, at any alignment."""
+    there, _ = placed(9, vocab, dtype, vocab + 3, 1)
+    there.copy_(dev(kinds_of_rows(np.random.default_rng(vocab), vocab), dtype))
+    for k in (1, 50, 1500, 5000, vocab - 1):
+        k = np.full(9, k, np.int32)
+        check(pp.token_probs(there, top_k=dev(k)), there, None, k)
+    t = np.array([0, 0.5, 1, 2, 0, 0.1, 1, 1, 1], np.float32)
+    k = np.array([3, 0, -1, vocab, 0, 7, vocab + 1, 4096, 4097], np.int32)
+    check(pp.token_probs(there, temperature=dev(t), top_k=dev(k)), there, t, k)
+
+
+@pytest.mark.parametrize("dtype", FT)
+@pytest.mark.parametrize("rows,vocab", [(3, 33000), (300, 9001), (2, 131075), (610, 1027), (2, 160000)])
+def test_probs_into_rows_that_lie_otherwise(dtype, rows, vocab):
+    """Results whose 16-byte boundaries are not the logits'."""
+    rng = np.random.default_rng(rows)
+    x = logits(rng, rows, vocab, dtype)
+    k = np.exp(rng.uniform(0, np.log(vocab), rows)).astype(np.int32)
+    t = rng.uniform(0.3, 2.0, rows).astype(np.float32)
+    t[::5] = 0
+    for cut in (None, k):
+        out, whole = placed(rows, vocab, torch.float32, vocab + 5, 3)
+        pp.token_probs(x, temperature=dev(t), top_k=None if cut is None else dev(cut), out=out)
+        assert torch.equal(out, pp.token_probs(x, temperature=dev(t), top_k=None if cut is None else dev(cut)))
+        check(out, x, t, cut)
+        there = torch.zeros_like(whole, dtype=torch.bool)
+        torch.as_strided(there, (rows, vocab), (vocab + 5, 1), 3).fill_(True)
+        assert (whole[~there] == 77).all()
+
+
 @pytest.mark.parametrize("dtype", FT)
 @pytest.mark.parametrize("rows,vocab", [(609, 257), (610, 1027), (611, 4600), (1215, 33)])
 def test_probs_of_many_short_rows(dtype, rows, vocab):
