@@ -125,7 +125,8 @@ def adamw_state(params, bits: int = 32, master: bool = False, seed: int = 0, nea
     bfloat16, contiguous, on one device).  bits: 32, or 8 for a byte a value
     and a shared exponent, rounded by random bits from `seed` or, with
     `nearest`, to nearest.  master: keep 32-bit copies of the parameters, so
-    that steps smaller than a 16-bit parameter's rounding add up."""
+    that steps smaller than a 16-bit parameter's rounding add up.  The state is
+    made on the current stream: steps on another one wait for that first."""
     params = list(params)
     _need(len(params) > 0, "params: want a tensor at least")
     device, spans = params[0].device, []

@@ -406,6 +406,8 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) adamw_kernel(const __grid_c
       const Item& t = a.item[i];
       const uint64_t at = uint64_t(tile - t.tile_begin) * TILE;
       const uint32_t n = uint32_t(t.n - at < TILE ? t.n - at : TILE);
+      // 32 bytes an access, or element by element (67M elements, 32-bit states: f32 287 and 286 us, bf16 229
+      // and 243; 8-bit states: f32 241 and 291, bf16 213 and 261)
       if (n == TILE && c.wide && (reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad)) % 32 == 0)
         step_tile<BITS, true>(c, d, t, at, n);
       else
@@ -526,9 +528,8 @@ extern "C" pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, cons
     // fetched ahead (185M elements, 8 bits: 634 us, and 660 with turns of 4 tiles)
     c.chunk = uint32_t(std::min<uint64_t>(std::max<uint64_t>(tiles / (152 * RESIDENT * 8 * WARPS), 1), 16)) * WARPS;
     c.last = i == n_tensors;
-    const cudaError_t e = n <= 16 ? launch<16>(c, items, state->bits, stream)
-                          : n <= 128 ? launch<128>(c, items, state->bits, stream)
-                                     : launch<MOST>(c, items, state->bits, stream);
+    // few tensors as fewer parameters: a launch for 9 takes the host 7.8 us, and 9.0 with all 31 KB
+    const cudaError_t e = n <= 128 ? launch<128>(c, items, state->bits, stream) : launch<MOST>(c, items, state->bits, stream);
     if (e != cudaSuccess) return ppl::rc_of(e);
   } while (i < n_tensors);
   return PP_OK;
