@@ -41,10 +41,11 @@ constexpr int CLUSTER = 8;   // blocks at most
 constexpr int MID = 512;     // threads of a block that has a part of a longer row
 constexpr int LARGE = 1024;  // and of the longest rows with a cut
 constexpr int NV_MOST = 9;   // 16-byte vectors of a thread, in registers
-// Bytes of a part in shared memory, so that three or four blocks share a
-// multiprocessor.  512 rows of 131075 bf16: 82 us in clusters of four at 72 KiB and at
-// 108, 91 in clusters of eight at 56; 2560 rows of 50001 f32: 176, 196 and 176.
-constexpr uint32_t PART_MOST = 73728;
+// Bytes of a part in shared memory, so that four blocks share a multiprocessor: 512 rows
+// of 80000 f32 61 us by six blocks, 66 by five of 62 KiB and 71 by eight; 2560 of 50001 f32
+// 175 by four, 183 by three of 65 KiB.  Three share one where one block or two then hold
+// the row: 4096 rows of 32000 f32 177 us by two blocks, 191 by three, and bf16 138 by one, 163 by two.
+constexpr uint32_t PART_MOST = 56320, PART_OF_TWO = 66048;
 constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // where a block has a multiprocessor for itself
 
 struct ProbArgs {
@@ -995,7 +996,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) plain_kernel(const Pr
   // the inputs' and the outputs' boundaries agree where their strides do
   const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
   auto probability = [&](float f, uint32_t j) { return greedy ? (j == best ? 1.f : 0.f) : (sizeof(T) == 4 ? f : ex(f)) * factor; };
-  // Elsewhere value by value, so that a warp's lie side by side: 512 rows of 131075 f16 93 us, 82 where the
+  // Elsewhere value by value, so that a warp's lie side by side: 512 rows of 131075 f16 93 us, 88 where the
   // boundaries agree (226 with the values of a vector one after the other).
   if (!wide) {
     const uint32_t from = rank * a.part;
@@ -1078,27 +1079,35 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
     a.part = each * VEC;
     return each;
   };
+  auto more = [&] {
+    while (blocks * 2 <= CLUSTER && n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID) blocks *= 2;
+  };
   if (small) {
     part();
     if (a.top_k) return launch_cut<T, 128>(a, n_rows, vectors, stream);
     return launch_in_shared(plain_kernel<T, 128>, once[0], a, n_rows, 128, vectors * 16, stream);
   }
   if (a.top_k) {
-    // as many blocks as hold the row; more while all of them run at once (64 rows of 131072 bf16: 33 us
-    // in clusters of four, one wave, and 41 of eight, two, at the time; now 19)
-    while (blocks < CLUSTER && (vectors > MID * NV_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
+    // as many blocks as hold the row, of a power of two or not (512 rows of 80000 f32: 102 us by five,
+    // 133 by eight; 2560 of 50001: 287 by three, 335 by four); more while all of them run at once (64
+    // rows of 131072 bf16: 33 us in clusters of four, one wave, and 41 of eight, two, at the time; now 19)
+    const uint32_t threads = vectors <= MID * NV_MOST * CLUSTER ? MID : LARGE;
+    blocks = std::min((vectors + threads * NV_MOST - 1) / (threads * NV_MOST), uint32_t(CLUSTER));
+    more();
     const uint32_t each = part();
     if (each <= MID * NV_MOST) return launch_cut<T, MID>(a, n_rows, each, stream);
-    // a multiprocessor a block (64 rows of 200064 f32, k = 50: 53 us, 185 in long_kernel; of 500000 bf16 77 and 651)
+    // a multiprocessor a block (64 rows of 200064 f32, k = 50: 39 us, 185 in long_kernel; of 500000 bf16 79 and 651)
     if (each <= LARGE * NV_MOST) return launch_as(cut_kernel<T, LARGE, NV_MOST>, a, n_rows, LARGE, 0, stream);
   } else {
-    while (blocks < CLUSTER && (vectors * 16 > PART_MOST * blocks || (n_rows * blocks * 2 <= 264 && vectors >= blocks * 2 * MID))) blocks *= 2;
+    const uint32_t most = (vectors <= PART_OF_TWO / 16 * 2 ? PART_OF_TWO : PART_MOST) / 16;
+    blocks = std::min((vectors + most - 1) / most, uint32_t(CLUSTER));
+    more();
     const uint32_t each = part();
-    if (each * 16 <= RESIDENT_MOST) return launch_in_shared(plain_kernel<T, MID>, once[1], a, n_rows, MID, each * 16, stream);
+    if (each <= RESIDENT_MOST / 16) return launch_in_shared(plain_kernel<T, MID>, once[1], a, n_rows, MID, each * 16, stream);
   }
   blocks = CLUSTER;
   const uint32_t each = part();
-  a.resident = each * 16 <= RESIDENT_MOST;
+  a.resident = each <= RESIDENT_MOST / 16;
   return launch_in_shared(long_kernel<T>, once[2], a, n_rows, LONG_THREADS, a.resident ? each * 16 : 0, stream);
 }
 

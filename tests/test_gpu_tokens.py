@@ -197,6 +197,20 @@ def test_probs_of_the_longest_cuts(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", FT)
+@pytest.mark.parametrize("vocab", [50001, 82003, 101001, 120007, 180011, 210001])
+def test_probs_in_clusters_of_any_size(dtype, vocab):
+    """From two blocks a row to eight."""
+    rng = np.random.default_rng(vocab)
+    x = dev(kinds_of_rows(rng, vocab)[rng.integers(0, 9, 46)], dtype)
+    k = np.exp(rng.uniform(0, np.log(vocab), 46)).astype(np.int32)
+    k[::9] = 0
+    t = rng.uniform(0.2, 3, 46).astype(np.float32)
+    t[::17] = 0
+    check(pp.token_probs(x, temperature=dev(t), top_k=dev(k)), x, t, k)
+    check(pp.token_probs(x, temperature=dev(t)), x, t)
+
+
+@pytest.mark.parametrize("dtype", FT)
 @pytest.mark.parametrize("rows,vocab", [(3, 33000), (300, 9001), (2, 131075), (610, 1027), (2, 160000)])
 def test_probs_into_rows_that_lie_otherwise(dtype, rows, vocab):
     """Results whose 16-byte boundaries are not the logits'."""
