@@ -319,8 +319,8 @@ template <class T, bool SURE, int PARTS>
 cudaError_t launch(VerifyArgs& a, uint64_t n_requests, cudaStream_t stream) {
   // a block for each half of 152 multiprocessors' room at least, if with only 2048 tokens
   // each; beyond that as long as a block has 16384 tokens, for its steps cost it as
-  // much time as some thousands of them (256 x 50001: two blocks a request 16 us, four 18;
-  // 512 x 131075: four 75 us, two 98)
+  // much time as some thousands of them (256 x 50001: two blocks a request 15 us, four 17;
+  // 512 x 131075: four 75 us, two 80, three and five 77, eight 83)
   uint32_t blocks = 1;
   while (blocks < CLUSTER && n_requests * blocks < 1025 && a.n_vocab / (blocks * 2) >= (n_requests * blocks < 304 ? 2048 : 16384)) blocks *= 2;
   a.blocks = blocks;
