@@ -649,6 +649,7 @@ __device__ __noinline__ Cut cut_of_all(const T* in, uint32_t from, uint32_t size
       all_sync<THREADS>();  // and every block has read what it needs of the others
       high = warp_max(sh.wf[0][lane % WARPS]);
       reach = -warp_max(-sh.wf[1][lane % WARPS]);
+      row_sync<THREADS>();  // all have read wf, which the caller writes next: where the step is kept whole no other barrier comes between
       return cut_among<P>(sh, entries, left, high, reach, part.all);
     }
     all_sync<THREADS>();  // the counts are read
