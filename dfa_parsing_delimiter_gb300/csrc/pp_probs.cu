@@ -8,8 +8,8 @@
 //   plain_kernel  rows without a cut.  Parts lie in shared memory; largest value,
 //                 sum of exponentials relative to it, one exchange of the two
 //                 through distributed shared memory, probabilities.  2560 rows of
-//                 50001 f32: 176 us (5.8 TB/s; with the parts in registers, two
-//                 blocks a multiprocessor, 213), 512 of 131075 bf16: 82.
+//                 50001 f32: 173 us (5.9 TB/s; with the parts in registers, two
+//                 blocks a multiprocessor, 213 at the time), 512 of 131075 bf16: 73.
 //   cut_kernel    rows with a cut.  Parts lie in registers (in shared memory the
 //                 steps below read them again each time: 512 rows of 131075 f16 111
 //                 us instead of 104, 64 rows of 131072 bf16 24 instead of 19).  At
@@ -831,12 +831,11 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS *
   const uint32_t tie = cut.least << P::LOW, over = (cut.least + 1) << P::LOW;
   const float from_tie = tie > KEY_LOST ? float_of(tie) : -3.402823466e38f, from_over = over > KEY_LOST ? float_of(over) : INFINITY;
   auto kept = [&](float f, uint32_t j) { return f >= from_over || (f >= from_tie && j <= cut.last); };
-  // 2^64 times share(f, m, c), which no exponential within a float's range of 1 leaves
+  // share(f, m, c), with what only an infinite m needs out of the way
   const bool endless = m == INFINITY;
   auto ex = [&](float f, uint32_t j) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaxf(fmaf(fmaf(f, 0.5f, -0.5f * m), c, 64.f), -200.f)));
-    if (endless) e = f == m ? 0x1p64f : 0.f;
+    float e = exp2f(fmaxf(fmaf(f, 0.5f, -0.5f * m) * c, -200.f));
+    if (endless) e = f == m ? 1.f : 0.f;
     return !some || kept(f, j) ? e : 0.f;
   };
   float s = 0.f;
@@ -944,31 +943,31 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) plain_kernel(const Pr
   if (lane == 0) wmax[warp] = m;
   __syncthreads();
   m = warp_max(wmax[lane % WARPS]);
-  // 2^64 times share(f, m, c), which no exponential within a float's range of 1 leaves
-  const bool endless = m == INFINITY;
+  // share(f, m, c) for a finite m.  Nothing is added to an exponent to keep small numbers within a float's
+  // range: beside 64 the likeliest tokens would lose 3 bits.
   const float half = -0.5f * m;
-  auto ex = [&](float f) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaxf(fmaf(fmaf(f, 0.5f, half), c, 64.f), -200.f)));
-    return endless ? (f == m ? 0x1p64f : 0.f) : e;
-  };
+  auto exponent = [&](float f) { return fmaxf(fmaf(f, 0.5f, half) * c, -200.f); };
+  const bool endless = m == INFINITY;
   float s = 0.f;
   uint32_t first = ~0u;
   if (greedy) {
     for (int i = 0; i < n; ++i)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) first = to_f(x[i * THREADS].v[k]) == m ? min(first, begin + i * STEP + k) : first;
+  } else if (endless) {
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s += to_f(x[i * THREADS].v[k]) == m ? 1.f : 0.f;
   } else {
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
-      Vec v = x[i * THREADS];
+      const Vec v = x[i * THREADS];
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const float e = ex(to_f(v.v[k]));
+        float e;  // below 2^-126: 0, beside a 1 in the sum
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(exponent(to_f(v.v[k]))));
         s += e;
-        if constexpr (sizeof(T) == 4) v.v[k] = e;
       }
-      if constexpr (sizeof(T) == 4) x[i * THREADS] = v;  // in the values' place
     }
   }
   s = warp_add(s);
@@ -996,37 +995,43 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) plain_kernel(const Pr
   const float factor = total > 0.f ? share(m, top, c) / total : 0.f;
   // the inputs' and the outputs' boundaries agree where their strides do
   const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
-  auto probability = [&](float f, uint32_t j) { return greedy ? (j == best ? 1.f : 0.f) : (sizeof(T) == 4 ? f : ex(f)) * factor; };
-  // Elsewhere value by value, so that a warp's lie side by side: 512 rows of 131075 f16 93 us, 88 where the
-  // boundaries agree (226 with the values of a vector one after the other).
-  if (!wide) {
-    const uint32_t from = rank * a.part;
-    const T* y = reinterpret_cast<const T*>(raw);
-    __syncthreads();
+  auto write = [&](auto&& probability) {
+    // Elsewhere value by value, so that a warp's lie side by side: 512 rows of 131075 f16 93 us, 88 where the
+    // boundaries agree (226 with the values of a vector one after the other).
+    if (!wide) {
+      const uint32_t from = rank * a.part;
+      const T* y = reinterpret_cast<const T*>(raw);
+      __syncthreads();
 #pragma unroll 4
-    for (uint32_t j = max(from, shift) + threadIdx.x; j < to; j += THREADS) out[j - shift] = probability(to_f(y[j - from]), j);
-    return;
-  }
-  float* q = out + (int64_t(begin) - shift);
-#pragma unroll 2
-  for (int i = 0; i < n; ++i, q += STEP) {
-    const Vec v = x[i * THREADS];
-    float p[VEC];
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) p[k] = probability(to_f(v.v[k]), begin + i * STEP + k);
-    if (i >= full && i < whole) {
-      if constexpr (VEC == 8)
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]), "f"(p[4]),
-                     "f"(p[5]), "f"(p[6]), "f"(p[7]) : "memory");
-      else
-        *reinterpret_cast<float4*>(q) = make_float4(p[0], p[1], p[2], p[3]);
-    } else {
-      const uint32_t j = begin + i * STEP;
-#pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        if (j + k >= shift && j + k < all) q[k] = p[k];
+      for (uint32_t j = max(from, shift) + threadIdx.x; j < to; j += THREADS) out[j - shift] = probability(to_f(y[j - from]), j);
+      return;
     }
-  }
+    float* q = out + (int64_t(begin) - shift);
+#pragma unroll 2
+    for (int i = 0; i < n; ++i, q += STEP) {
+      const Vec v = x[i * THREADS];
+      float p[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) p[k] = probability(to_f(v.v[k]), begin + i * STEP + k);
+      if (i >= full && i < whole) {
+        if constexpr (VEC == 8)
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]), "f"(p[4]),
+                       "f"(p[5]), "f"(p[6]), "f"(p[7]) : "memory");
+        else
+          *reinterpret_cast<float4*>(q) = make_float4(p[0], p[1], p[2], p[3]);
+      } else {
+        const uint32_t j = begin + i * STEP;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+          if (j + k >= shift && j + k < all) q[k] = p[k];
+      }
+    }
+  };
+  // each kind of row with loops of its own (one loop for all three, its values' exponentials kept in their place
+  // where they are floats: 2560 x 50001 f32 179 us, 512 x 131075 bf16 88)
+  if (greedy) write([&](float, uint32_t j) { return j == best ? 1.f : 0.f; });
+  else if (endless) write([&](float f, uint32_t) { return f == m ? factor : 0.f; });
+  else write([&](float f, uint32_t) { return exp2f(exponent(f)) * factor; });
 }
 
 template <class K>
