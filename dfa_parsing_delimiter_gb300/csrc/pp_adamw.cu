@@ -209,7 +209,10 @@ __device__ __forceinline__ uint2 encode(float* x, const uint32_t* random, uint32
   if (e == 255) return make_uint2(0, 0);
   if (field > MOST) {
 #pragma unroll
-    for (int k = 0; k < EACH; ++k) x[k] *= pow2(127 + MOST - field);
+    for (int k = 0; k < EACH; ++k) {
+      const float y = x[k] * pow2(127 + MOST - field);
+      x[k] = TOP == TOP_V && x[k] > 0.f ? fmaxf(y, 0x1p-149f) : y;  // a square that is above 0 stays so, for the code below
+    }
   }
   const float scale = pow2(127 + TOP - min(field, MOST));
   // A multiply-add where an addition and a shift would do: logic runs at half the rate.
