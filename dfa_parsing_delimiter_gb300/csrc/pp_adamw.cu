@@ -265,8 +265,10 @@ __device__ __forceinline__ void write_codes(uint8_t* p, uint32_t lane, uint32_t 
 // The square root and the quotient of the step are each within 2^-22 of their
 // values, as is the rate: what a parameter changes by is exact to 20 bits or so.
 // FLUSH: numbers below 2^-126 count as zero, which takes fewer instructions (185M
-// elements, 8 bits: 597 us, 615 without) and makes no difference to a root of 2^-63
-// beside an eps of 2^-40 or more.
+// elements, 8 bits: 597 us, 615 without).  Of a square that is a root of 2^-63,
+// times 1 / sqrt(1 - beta2^t), at most 2^-22 of an eps of 2^-41 times that and more.  A rate
+// times a mean below 2^-126 is lost, or has lost bits without FLUSH: what it would change is 2^-126
+// over the divisor.
 template <bool FLUSH>
 __device__ __forceinline__ float root_of(float x) {
   float y;
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) adamw_kernel(const __grid_c
   d.rate = d.lr / -expm1f(float(step) * c.log_b1);
   d.root = 1.f / sqrtf(-expm1f(float(step) * c.log_b2));
   d.key = mix(mix(c.seed) + uint32_t(step));
-  d.flush = c.eps >= 0x1p-40f;
+  d.flush = c.eps >= d.root * 0x1p-41f;
   // a block takes c.chunk tiles a turn, for which a tensor is looked up once
   for (uint32_t chunk = blockIdx.x * c.chunk; chunk < c.n_tiles; chunk += gridDim.x * c.chunk) {
     uint32_t i = 0;  // the last tensor that begins at or before the chunk

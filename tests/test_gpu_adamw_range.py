@@ -40,3 +40,39 @@ def test_a_small_square_beside_a_large_one_is_not_zero(top, nearest):
     before = w.clone()
     pp.adamw_step([w], [torch.zeros_like(grad)], s, betas=(0.5, 0.5), lr=1e-3)
     assert torch.isfinite(w).all() and ((w - before).abs() <= 1.0).all()
+
+
+def changes(m, v, t, lr, betas, eps):
+    """What parameters change by in 64 bits, and what they are off at most: 2^-19 of
+    themselves, 2^-126, and 2^-126 over the divisor where the rate times the mean is less than that."""
+    rate = np.float64(lr) / (1 - betas[0] ** t)
+    below = np.sqrt(v / (1 - betas[1] ** t)) + np.float64(np.float32(eps))
+    with np.errstate(divide="ignore", invalid="ignore"):
+        change = np.where(m == 0, 0.0, rate * m / below)
+        lost = np.where(np.abs(rate * m) < 2.0 ** -126, 2.0 ** -126 / below, 0.0)
+    return change, 2.0 ** -19 * np.abs(change) + 2.0 ** -126 + np.where(m == 0, 0.0, lost)
+
+
+def one_step(grad, lr, betas, eps, t=1):
+    """(what parameters of 0 became, the states as 32 bits hold them)"""
+    w = torch.zeros(grad.size, device="cuda")
+    s = pp.adamw_state([w])
+    s.step.fill_(t - 1)
+    pp.adamw_step([w], [torch.from_numpy(grad).cuda()], s, lr=lr, betas=betas, eps=eps, weight_decay=0.0)
+    m, v = wide(s.exp_avg)[:grad.size], wide(s.exp_avg_sq)[:grad.size]
+    x, y = R.step32(np.zeros_like(grad), np.zeros_like(grad), grad.astype(np.float64), *betas)
+    assert np.array_equal(m, x.astype(np.float64)) and np.array_equal(v, y.astype(np.float64))
+    return wide(w), m, v
+
+
+@pytest.mark.parametrize("beta2", [0.9, 0.99, 0.999, 0.9999, 0.999999])
+@pytest.mark.parametrize("eps", [2.0 ** -41, 2.0 ** -40, 2.0 ** -39, 2.0 ** -36, 2.0 ** -31, 1e-8])
+def test_subnormal_squares_beside_eps(eps, beta2):
+    """The first step, whose 1 / sqrt(1 - beta2) makes the root of a square larger."""
+    size = np.linspace(-64.0, -60.0, 1001) - 0.5 * np.log2(1 - beta2)
+    grad = (2.0 ** size).astype(np.float32)
+    grad[::2] *= -1
+    got, m, v = one_step(grad, 1.0, (0.9, beta2), eps)
+    assert v.min() < 2.0 ** -126 < v.max()
+    change, most = changes(m, v, 1, 1.0, (0.9, beta2), eps)
+    assert (np.abs(got + change) <= most).all(), (np.abs(got + change) / np.abs(change)).max()
