@@ -851,8 +851,9 @@ typedef struct {
  *   m = beta1 m + (1 - beta1) g
  *   v = beta2 v + (1 - beta2) g g          (each product and sum rounded)
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * (what p changes by: within 2^-19 of itself, or 2^-126) and t becomes the steps done.  p is read from d_master and written to it where
- * there is one, and rounded once to the parameter's type.  8-bit states are
+ * (what p changes by: within 2^-19 of itself, or 2^-126; where lr / (1 - beta1^t) m is
+ * below 2^-126 it may count as 0) and t becomes the steps done.  p is read from
+ * d_master and written to it where there is one, and rounded once to the parameter's type.  8-bit states are
  * rounded up or down with chances by which they are right on average: 16 bits of a
  * hash of the seed, t and the element's place, for each of the two, are added
  * below a code's last bit.  (To nearest, a beta2 of 0.999 would never move v:

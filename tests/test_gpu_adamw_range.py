@@ -76,3 +76,16 @@ def test_subnormal_squares_beside_eps(eps, beta2):
     assert v.min() < 2.0 ** -126 < v.max()
     change, most = changes(m, v, 1, 1.0, (0.9, beta2), eps)
     assert (np.abs(got + change) <= most).all(), (np.abs(got + change) / np.abs(change)).max()
+
+
+@pytest.mark.parametrize("t", [1, 2, 50, 4000])
+@pytest.mark.parametrize("eps", [1e-12, 2.0 ** -41, 1e-10, 1e-8, 1e-3])
+@pytest.mark.parametrize("lr", [1e-3, 1.0, 1e-20])
+def test_means_near_the_least_numbers(lr, eps, t):
+    """Gradients from subnormal numbers up, of which the changes are what pp.h says."""
+    size = np.linspace(-148.0, -20.0, 3001)
+    grad = (2.0 ** size).astype(np.float32)
+    grad[::2] *= -1
+    got, m, v = one_step(grad, lr, (0.9, 0.999), eps, t)
+    change, most = changes(m, v, t, lr, (0.9, 0.999), eps)
+    assert (np.abs(got + change) <= most).all(), (np.abs(got + change) - most).max()
