@@ -86,12 +86,17 @@ class AdamWState:
         return [flat[a:a + n].view(s) for a, n, s in zip(self.first, self.sizes, self.shapes)]
 
     def state_dict(self) -> dict:
-        """The state's tensors by name, as `load` takes them."""
+        """The state's tensors by name, as `load` takes them; of 8-bit states also
+        how they are rounded, `seed` (int64) and `nearest` (bool), on the host."""
         names = ("exp_avg", "exp_avg_sq", "exp_avg_exponent", "exp_avg_sq_exponent", "master", "step")
-        return {k: getattr(self, k) for k in names if getattr(self, k) is not None}
+        d = {k: getattr(self, k) for k in names if getattr(self, k) is not None}
+        if self.bits == 8:
+            d.update(seed=torch.tensor(self.seed), nearest=torch.tensor(self.nearest))
+        return d
 
     def load(self, **tensors) -> None:
-        """Copies tensors of state_dict's names into the state (None: that one stays)."""
+        """Copies tensors of state_dict's names into the state (None, or not given:
+        that one stays).  A captured graph keeps the seed that it was captured with."""
         mine = self.state_dict()
         tensors = {k: t for k, t in tensors.items() if t is not None}
         for k, t in tensors.items():
@@ -99,7 +104,12 @@ class AdamWState:
             _need(t.shape == mine[k].shape and t.dtype == mine[k].dtype,
                   f"{k}: want {tuple(mine[k].shape)} of {mine[k].dtype}, got {tuple(t.shape)} of {t.dtype}")
         for k, t in tensors.items():
-            mine[k].copy_(t)
+            if k == "seed":
+                self.seed = int(t) & 0xFFFFFFFF
+            elif k == "nearest":
+                self.nearest = bool(t)
+            else:
+                mine[k].copy_(t)
 
     def _struct(self) -> AdamWStateStruct:
         return AdamWStateStruct(*[None if t is None else t.data_ptr() for t in (
@@ -108,7 +118,8 @@ class AdamWState:
 
     def values(self, dtype=torch.float32, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         """(exp_avg, exp_avg_sq) as numbers, flat: what 8-bit codes stand for
-        (exactly in float32 and bfloat16), or the 32-bit ones in `dtype`."""
+        (exactly in float32 and bfloat16), or the 32-bit ones in `dtype` (in
+        float32 the state's own tensors, which the next step changes)."""
         _need(dtype in FTYPE, "dtype: want float32, float16 or bfloat16")
         if self.bits == 32:
             with _on_stream(stream):
