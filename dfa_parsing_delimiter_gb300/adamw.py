@@ -11,7 +11,6 @@ do not fit raise ValueError, errors of the library RuntimeError.
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 from torch.autograd.graph import increment_version
@@ -19,6 +18,7 @@ from torch.autograd.graph import increment_version
 from . import lm
 from .lm import FTYPE, _call, _need, _new, _on_stream
 
+_MOST = torch.finfo(torch.float32).max
 BLOCK = 256  # elements that share an exponent; each tensor's state begins at a multiple
 _vp, _u64, _i32, _f32, _f64 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32, ctypes.c_float, ctypes.c_double
 
@@ -184,9 +184,9 @@ def adamw_step(params, grads, state: AdamWState, lr=1e-3, betas=(0.9, 0.999), ep
     if isinstance(lr, torch.Tensor):
         lr, lr_at = 0.0, _number(lr, like, "lr")
     else:
-        _need(0.0 <= lr < math.inf, f"lr: want a number from 0 on, got {lr}")
+        _need(0.0 <= lr <= _MOST, f"lr: want a number from 0 on that 32 bits hold, got {lr}")
     _need(0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0, f"betas: want numbers from 0 to below 1, got {betas}")
-    _need(0.0 <= eps < math.inf, f"eps: want a number from 0 on, got {eps}")
+    _need(0.0 <= eps <= _MOST, f"eps: want a number from 0 on that 32 bits hold, got {eps}")
     c = lm._lib()
     scale_at, skip_at = _number(grad_scale, like, "grad_scale"), _number(skip, like, "skip")
     _call(c.adamw, "pp_adamw", like, stream, params, grads, state.sizes, state.first, weight_decay, like.get_device(),

@@ -480,8 +480,8 @@ extern "C" pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, cons
                           const pp_adamw_opts* o, cudaStream_t stream) {
   if (!state_ok(state) || !o || (n_tensors && !tensors)) return PP_EINVAL;
   if (!state->d_counters || !ppl::aligned(state->d_counters, 4) || !ppl::aligned(state->d_master, 16)) return PP_EINVAL;
-  if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) || !(o->eps >= 0) || !std::isfinite(o->eps)) return PP_EINVAL;
-  if (!o->d_lr && !(o->lr >= 0 && std::isfinite(o->lr))) return PP_EINVAL;
+  if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) || !(o->eps >= 0) || !std::isfinite(float(o->eps))) return PP_EINVAL;
+  if (!o->d_lr && !(o->lr >= 0 && std::isfinite(float(o->lr)))) return PP_EINVAL;
   if (!ppl::aligned(o->d_lr, 4) || !ppl::aligned(o->d_grad_scale, 4) || !ppl::aligned(o->d_skip, 4)) return PP_EINVAL;
   if (state->n / TILE >= ppl::MAX_DIM) return PP_ETOOLARGE;
   for (size_t i = 0; i < n_tensors; ++i) {

@@ -5,6 +5,7 @@
  * plain numbers; all call libpp, whose functions init() is given (lm.py). */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <math.h>
 
 #include "pp.h"
 
@@ -279,6 +280,10 @@ static PyObject* adamw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     const int fine = !PyErr_Occurred() && tensor_of(p, v[5], e->n, &e->d_param, &e->param_type) &&
                      tensor_of(g, v[5], e->n, &grad, &e->grad_type);
     if (PyErr_Occurred()) goto done;
+    if (!isfinite(e->weight_decay)) {
+      PyErr_Format(PyExc_ValueError, "weight_decay: want a number that 32 bits hold (tensor %zd)", i);
+      goto done;
+    }
     if (!fine) {
       PyErr_Format(PyExc_ValueError, "params and grads: want %llu contiguous elements of float32, float16 or bfloat16 on the state's device (tensor %zd)", (unsigned long long)e->n, i);
       goto done;

@@ -861,8 +861,8 @@ typedef struct {
  *   tensors         host, read before the call returns; the tensors' parameters and
  *                   states must not overlap, nor their gradients.
  *   state, opts     host; see above.  Calls for one state must not run at once.
- * Returns PP_EINVAL for bad arguments (lr and eps below 0 or not finite, a beta
- * outside [0, 1), states off 16 bytes), PP_ETOOLARGE for a state of 2^39 - 2^24
+ * Returns PP_EINVAL for bad arguments (lr and eps below 0 or not finite in 32 bits, a
+ * beta outside [0, 1), states off 16 bytes), PP_ETOOLARGE for a state of 2^39 - 2^24
  * elements or more, PP_ECUDA on CUDA errors.  No scratch.
  */
 pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, const pp_adamw_state* state,
