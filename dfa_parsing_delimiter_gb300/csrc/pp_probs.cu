@@ -829,27 +829,40 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS *
   // Kept, in floats: above all that tie, or of those that tie up to the last place.  (KEY_LOST
   // and what is beyond infinity's key make NaN, which nothing reaches.)
   const uint32_t tie = cut.least << P::LOW, over = (cut.least + 1) << P::LOW;
-  const float from_tie = tie > KEY_LOST ? float_of(tie) : -3.402823466e38f, from_over = over > KEY_LOST ? float_of(over) : INFINITY;
+  float from_tie = tie > KEY_LOST ? float_of(tie) : -3.402823466e38f, from_over = over > KEY_LOST ? float_of(over) : INFINITY;
   auto kept = [&](float f, uint32_t j) { return f >= from_over || (f >= from_tie && j <= cut.last); };
-  // share(f, m, c), with what only an infinite m needs out of the way
-  const bool endless = m == INFINITY;
-  auto ex = [&](float f, uint32_t j) {
-    float e = exp2f(fmaxf(fmaf(f, 0.5f, -0.5f * m) * c, -200.f));
-    if (endless) e = f == m ? 1.f : 0.f;
-    return !some || kept(f, j) ? e : 0.f;
-  };
+  float half = -0.5f * m;
+  if (m == INFINITY && !greedy) {  // the infinities that are kept become 0, the rest -infinity, and the largest 0
+    part.change([&](float f, uint32_t j) { return f == m && kept(f, j) ? 0.f : -INFINITY; });
+    half = 0.f;
+    from_tie = -3.402823466e38f;
+    from_over = INFINITY;
+    cut.last = ~0u;
+  }
+  // share(f, m, c), where all are kept and where not: loops for each (512 rows of 131075 bf16 without a cut 86 us, and
+  // 102 where every value is compared)
+  auto of_all = [&](float f, uint32_t) { return fmaxf(fmaf(f, 0.5f, half) * c, -200.f); };
+  auto of_kept = [&](float f, uint32_t j) { return kept(f, j) ? of_all(f, j) : -200.f; };
   float s = 0.f;
   uint32_t first = ~0u;
+  auto sum = [&](auto&& exponent) {
+    if constexpr (sizeof(T) == 4) {  // in the values' place
+      part.change([&](float f, uint32_t j) {
+        const float e = exp2f(exponent(f, j));
+        s += e;
+        return e;
+      });
+    } else {
+      part.each([&](float f, uint32_t j) {
+        float e;  // below 2^-126: 0, beside a 1 in the sum
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(exponent(f, j)));
+        s += e;
+      });
+    }
+  };
   if (greedy) part.each([&](float f, uint32_t j) { first = f == m ? min(first, j) : first; });
-  else if constexpr (sizeof(T) == 4) {  // in the values' place
-    part.change([&](float f, uint32_t j) {
-      const float e = ex(f, j);
-      s += e;
-      return e;
-    });
-  } else {
-    part.each([&](float f, uint32_t j) { s += ex(f, j); });
-  }
+  else if (some) sum(of_kept);
+  else sum(of_all);
   s = warp_add(s);
   first = __reduce_min_sync(~0u, first);
   if (lane == 0) sh.wf[1][warp] = s, sh.wu[warp] = first;
@@ -881,13 +894,17 @@ __global__ void __launch_bounds__(THREADS* GROUPS_OF<THREADS>, 1024 / (THREADS *
     return;
   }
   const float factor = total > 0.f ? share(m, top, c) / total : 0.f;
-  part.write(out, [&](int i, float* p) {
+  auto write = [&](auto&& exponent) {
+    part.write(out, [&](int i, float* p) {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const float f = to_f(part.x[i].v[k]);
-      p[k] = (sizeof(T) == 4 ? f : ex(f, part.at(i) + k)) * factor;
-    }
-  });
+      for (int k = 0; k < VEC; ++k) {
+        const float f = to_f(part.x[i].v[k]);
+        p[k] = (sizeof(T) == 4 ? f : exp2f(exponent(f, part.at(i) + k))) * factor;
+      }
+    });
+  };
+  if (sizeof(T) == 2 && some) write(of_kept);
+  else write(of_all);
 }
 
 // ------------------------------------------------------------ rows without a cut

@@ -136,3 +136,23 @@ def test_probabilities_that_are_subnormal(dtype):
     assert (got[0, :2440] > 0).all()  # 97.6 below, over a sum of 25.5: 2^-145.5
     wide = torch.cat([x[0], numbers(60000, -100.0).to(dtype)])[None]
     check(pp.token_probs(wide), wide, 1.0)
+
+
+@pytest.mark.parametrize("dtype", FT)
+@pytest.mark.parametrize("rows,vocab", [(1, 32000), (610, 4600), (9, 20011), (3, 131075), (2, 280003)])
+def test_infinities_in_long_cuts(dtype, rows, vocab):
+    """More infinities than the lists hold: the lowest of them share alike, in cuts that end
+    among them and in cuts beyond."""
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    x = torch.randn(rows, vocab, generator=g, device="cuda").to(dtype)
+    x[:, 3::2] = np.inf
+    x[:, 5::7] = -np.inf
+    many = int((x[0] == np.inf).sum())
+    for k in (0, many - 100, many, many + 100, vocab // 4):
+        got = pp.token_probs(x, top_k=torch.full((rows,), k, dtype=torch.int32, device="cuda"),
+                             temperature=torch.full((rows,), 0.5, device="cuda"))
+        keep = x == np.inf
+        if 0 < k < many:
+            keep &= torch.cumsum(keep, 1) <= k
+        p = keep.double() / keep.sum(1, keepdim=True)
+        assert ((got > 0) == keep).all() and ((got.double() - p).abs() <= 4 * U * p).all()
