@@ -5,14 +5,14 @@
 // once.  Nothing is read twice and nothing is shared between tiles but the
 // step's constants.  With 32-bit states it is bound by memory, 20 to 28 bytes an
 // element: 131072 x 2048 f32 1125 us (6.7 TB/s; with accesses of 16 bytes, not
-// 32, 1220), 35M bf16 with 32-bit copies 142 us (6.3 TB/s).
+// 32, 1220), 32M bf16 with 32-bit copies 142 us (6.3 TB/s).
 //
 // With 8-bit states a tile is also what shares an exponent: the largest one is a
 // warp reduction, and the codes come from the registers that the step left.  It is
 // bound by instructions (some 85 an element, half of them logic, which runs at half
 // the rate: hashing, codes in and out) and by loads that too few warps wait for:
-// 185M elements of f32 with bf16 gradients 597 us together with 165 for reading the
-// states' values back (floors 380 and 165).  What got it there: the next tile
+// 159M elements of f32 with bf16 gradients 443 us (floor 327), and 154 for reading the
+// states' values back (140).  What got both there, 597 us together: the next tile
 // fetched into the cache ahead (634 us, without 705), arithmetic on two floats at a
 // time (615), roots and quotients that flush (597), multiply-adds for shifts and
 // additions (714 with them and approximate quotients, 906 before).
@@ -33,7 +33,7 @@ using ppl::to_f;
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int TILE = PP_ADAMW_BLOCK, EACH = TILE / 32;  // elements of a warp and of a lane
-// Blocks that a multiprocessor holds (185M, 8 bits: 714 us, 746 with five, 835 with three, at the time)
+// Blocks that a multiprocessor holds (159M, 8 bits: 714 us, 746 with five, 835 with three, at the time)
 // and that a launch has for each.
 constexpr int RESIDENT = 4, BLOCKS = 8;
 
@@ -264,8 +264,8 @@ __device__ __forceinline__ void write_codes(uint8_t* p, uint32_t lane, uint32_t 
 
 // The square root and the quotient of the step are each within 2^-22 of their
 // values, as is the rate: what a parameter changes by is exact to 20 bits or so.
-// FLUSH: numbers below 2^-126 count as zero, which takes fewer instructions (185M
-// elements, 8 bits: 597 us, 615 without).  Of a square that is a root of 2^-63,
+// FLUSH: numbers below 2^-126 count as zero, which takes fewer instructions (159M
+// elements, 8 bits, and their values: 597 us, 615 without).  Of a square that is a root of 2^-63,
 // times 1 / sqrt(1 - beta2^t), at most 2^-22 of an eps of 2^-41 times that and more.  A rate
 // times a mean below 2^-126 is lost, or has lost bits without FLUSH: what it would change is 2^-126
 // over the divisor.
@@ -530,7 +530,7 @@ extern "C" pp_rc pp_adamw(const pp_adamw_tensor* tensors, size_t n_tensors, cons
     c.n_items = n;
     c.n_tiles = uint32_t(tiles);
     // up to 16 tiles a warp and turn, and eight turns a resident block: the next tile of a turn is
-    // fetched ahead (185M elements, 8 bits: 634 us, and 660 with turns of 4 tiles)
+    // fetched ahead (159M elements, 8 bits, and their values: 634 us, and 660 with turns of 4 tiles)
     c.chunk = uint32_t(std::min<uint64_t>(std::max<uint64_t>(tiles / (152 * RESIDENT * 8 * WARPS), 1), 16)) * WARPS;
     c.last = i == n_tensors;
     // few tensors as fewer parameters: a launch for 9 takes the host 7.8 us, and 9.0 with all 31 KB

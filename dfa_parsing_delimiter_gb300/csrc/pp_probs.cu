@@ -21,7 +21,7 @@
 //                 Bound by the latency of a block's steps one after the other (some
 //                 twenty barriers, three of them of the cluster).
 //   long_kernel   rows that eight blocks cannot hold: the steps read them again
-//                 (64 rows of 900001 bf16 290 us, with a cut 1100).
+//                 (64 rows of 900001 bf16 297 us, with a cut 1130).
 //
 // Which tokens are kept is exact, whatever 32 bits make of the exponentials.
 #include <algorithm>
@@ -42,9 +42,10 @@ constexpr int MID = 512;     // threads of a block that has a part of a longer r
 constexpr int LARGE = 1024;  // and of the longest rows with a cut
 constexpr int NV_MOST = 9;   // 16-byte vectors of a thread, in registers
 // Bytes of a part in shared memory, so that four blocks share a multiprocessor: 512 rows
-// of 80000 f32 61 us by six blocks, 66 by five of 62 KiB and 71 by eight; 2560 of 50001 f32
-// 175 by four, 183 by three of 65 KiB.  Three share one where one block or two then hold
-// the row: 4096 rows of 32000 f32 177 us by two blocks, 191 by three, and bf16 138 by one, 163 by two.
+// of 80000 f32 60 us by six blocks, 65 by five of 62 KiB and 71 by eight; 2560 of 50001 f32
+// 173 by four, 182 by three of 65 KiB; but 512 of 131075 f32 107 by eight and 104 by seven
+// of 73 KiB.  Three share one where one block or two then hold the row: 4096 rows of 32000
+// f32 174 us by two blocks, 190 by three, and bf16 123 by one, 140 by two.
 constexpr uint32_t PART_MOST = 56320, PART_OF_TWO = 66048;
 constexpr uint32_t RESIDENT_MOST = 200 * 1024;  // where a block has a multiprocessor for itself
 
@@ -262,7 +263,7 @@ constexpr int entries_of(int threads) { return threads > 128 ? 4 : 8; }  // list
 // Groups that begin together run the same instructions at nearly the same
 // time, which matters here: the code is long and straight, and warps at other
 // places in it wait for one another's instructions (8192 rows of 5000 bf16: 162 us
-// four to a block, 184 in blocks of their own, at the time; now 105).
+// four to a block, 184 in blocks of their own, at the time; now 108).
 template <int THREADS>
 __device__ __forceinline__ uint32_t tid() { return threadIdx.x % THREADS; }
 template <int THREADS>
@@ -1013,8 +1014,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) plain_kernel(const Pr
   // the inputs' and the outputs' boundaries agree where their strides do
   const bool wide = (reinterpret_cast<uintptr_t>(out) / 4 - shift) % VEC == 0;
   auto write = [&](auto&& probability) {
-    // Elsewhere value by value, so that a warp's lie side by side: 512 rows of 131075 f16 93 us, 88 where the
-    // boundaries agree (226 with the values of a vector one after the other).
+    // Elsewhere value by value, so that a warp's lie side by side: 512 rows of 131075 f16 81 us, 72 where the
+    // boundaries agree (226 with the values of a vector one after the other, at the time).
     if (!wide) {
       const uint32_t from = rank * a.part;
       const T* y = reinterpret_cast<const T*>(raw);
@@ -1093,7 +1094,7 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
   static ppi::DeviceOnce once[3];
   const uint32_t vectors = (a.n_vocab + 2 * VEC - 2) / VEC;  // at any alignment
   // Short rows, and enough of them to fill the device: 128 threads each (8192 rows of 5000 bf16
-  // with a cut: 105 us; with a block of 512 threads each 206, at 128 then 184).
+  // with a cut: 108 us; with a block of 512 threads each 206, at 128 then 184).
   const bool small = vectors <= 128 * NV_MOST && (n_rows >= 608 || vectors <= 256);
   uint32_t blocks = 1;
   auto part = [&] {
@@ -1119,7 +1120,7 @@ cudaError_t launch(ProbArgs& a, uint64_t n_rows, cudaStream_t stream) {
     more();
     const uint32_t each = part();
     if (each <= MID * NV_MOST) return launch_cut<T, MID>(a, n_rows, each, stream);
-    // a multiprocessor a block (64 rows of 200064 f32, k = 50: 39 us, 185 in long_kernel; of 500000 bf16 79 and 651)
+    // a multiprocessor a block (64 rows of 200064 f32, k = 50: 38 us, 185 in long_kernel; of 500000 bf16 81 and 651)
     if (each <= LARGE * NV_MOST) return launch_as(cut_kernel<T, LARGE, NV_MOST>, a, n_rows, LARGE, 0, stream);
   } else {
     const uint32_t most = (vectors <= PART_OF_TWO / 16 * 2 ? PART_OF_TWO : PART_MOST) / 16;
